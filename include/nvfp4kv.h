@@ -16,6 +16,10 @@
  *   - contiguous quantize / dequantize with the same block rule
  *       ("flashinfer.quantization" index: "FP4 KV Cache Quantization", nvfp4_kv_quantize,
  *        nvfp4_kv_dequantize)
+ * and, additions of this library, the operators of a decode step that works on such a cache:
+ *   - norm and rotation of the query and key rows with the append in the same pass
+ *   - bounds of each page's keys, and the pages that they promise the largest scores for
+ *   - attention of one new token per request, over all pages or over selected ones
  *
  * Number formats: E2M1 codes (grid {0,0.5,1,1.5,2,3,4,6}, 4 bits, two per byte, element
  * 2k in the low nibble); E4M3 (e4m3fn) block scales stored as bytes, one per 16
@@ -63,6 +67,9 @@ extern "C" {
 /* Bytes of the optional `workspace` of the bulk-copy kernels (see the conventions). */
 #define NVFP4_WORKSPACE_BYTES 16
 
+/* Bytes at the start of an attention workspace that are zero between calls. */
+#define NVFP4_COUNTER_BYTES 16384
+
 /* Return codes. */
 typedef int32_t nvfp4_status;
 #define NVFP4_OK 0
@@ -70,6 +77,7 @@ typedef int32_t nvfp4_status;
 #define NVFP4_ERR_UNSUPPORTED 2 /* a valid request this library does not implement */
 #define NVFP4_ERR_ALIGNMENT 3   /* a pointer or stride breaks the stated alignment */
 #define NVFP4_ERR_CUDA 4        /* the CUDA runtime reported an error at launch */
+#define NVFP4_ERR_INTERNAL 5    /* the host ran out of memory inside the call */
 
 /* Element types of fp16/bf16 tensors. */
 #define NVFP4_F16 0
@@ -420,6 +428,159 @@ nvfp4_status nvfp4_4over6_code(const nvfp4_4over6_config* recipe, int64_t* code)
  * one that packs an invalid recipe, returns NVFP4_ERR_INVALID_ARG. */
 nvfp4_status nvfp4_4over6_from_code(int64_t code, int32_t* is_4over6,
                                     nvfp4_4over6_config* recipe);
+
+/* ---- the operators of a decode step over a paged NVFP4 cache ------------------------------ */
+
+/* Normalize and rotate a step's query and key rows, and quantize-append its key and value rows,
+ * in one pass (one launch). For the rows x of head_dim D of token i, weights w of its tensor:
+ *   r = 1 / sqrt(sum(x^2) * (1/D) + eps);  y = (x * r) * w
+ *   pairs (a, b) of the first rotary_dim elements of y become (a c - b s, b c + a s)
+ * with c = cos_sin[positions[i]][k] and s = cos_sin[positions[i]][rotary_dim/2 + k] for pair k:
+ * elements (k, k + rotary_dim/2), or (2k, 2k+1) when rotary_interleaved. Rounded once to dtype.
+ * Query rows go to query_out. The rounded key rows and the value rows are quantized and
+ * written as nvfp4_quantize_append_paged writes them (same rule, same bytes).
+ * Every operation is binary32 and rounded once. The sum of squares runs in a fixed order, so
+ * the codes are reproducible: groups of eight, t[i] += t[i+4], t[i+2], t[i+1]; the two groups
+ * that rotate together (j and j + rotary_dim/16, past rotary_dim 2j and 2j+1) are added; the
+ * D/16 sums, filled up with zeros to a power of two n, t[i] += t[i + n/2], ....
+ *   query, key, value  device, rows of num_qo_heads (query) or num_kv_heads heads of D
+ *                      elements; a token's row is `*_row_stride` elements after the previous
+ *                      one (slices of one projection's output, for instance). 16-byte aligned,
+ *                      strides a multiple of 8 elements.
+ *   q_weight, k_weight device [D] of dtype, 16-byte aligned, or NULL: that tensor is not
+ *                      normalized.
+ *   eps                finite, >= 0.
+ *   cos_sin            device float [num_positions, rotary_dim], 16-byte aligned: cosines in the
+ *                      first half of a row, sines in the second. NULL with rotary_dim 0: no
+ *                      rotation. A token whose position is outside the table is reported
+ *                      (NVFP4_DEV_BAD_POSITION) and nothing of it is written.
+ *   rotary_dim         a multiple of 16, at most D.
+ *   k_scale_dev, v_scale_dev  the global decode scales in device memory, or both NULL: then
+ *                      k_scale and v_scale are used.
+ *   query_out          device, rows as query's with query_out_row_stride; may be query itself
+ *                      (same stride), and must overlap neither key nor value.
+ *   The other arguments are those of nvfp4_quantize_append_paged.
+ * Requirements: head_dim a multiple of 16, at most 512. */
+nvfp4_status nvfp4_qk_norm_rope_append_paged(
+    const void* query, const void* key, const void* value, int32_t dtype, int64_t nnz,
+    int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, int64_t query_row_stride,
+    int64_t key_row_stride, int64_t value_row_stride, const void* q_weight,
+    const void* k_weight, float eps, const float* cos_sin, int64_t num_positions,
+    int32_t rotary_dim, int32_t rotary_interleaved, const int32_t* batch_indices,
+    const int32_t* positions, nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache,
+    int32_t page_size, int32_t kv_layout, const int32_t* kv_indices, int64_t num_kv_indices,
+    const int32_t* kv_indptr, const int32_t* kv_last_page_len, int32_t batch_size,
+    float k_scale, float v_scale, const float* k_scale_dev, const float* v_scale_dev,
+    const nvfp4_4over6_config* recipe, void* query_out, int64_t query_out_row_stride,
+    int32_t* dev_status, void* stream);
+
+/* Element-wise bounds of the keys of pages: for every logical page of request b that holds a
+ * position of [first_positions[b], seq_lens[b]), with its physical page p and its live slots
+ * t (positions below seq_lens[b]):
+ *   key_bounds[p, h, 0, d] = min_t e2m1 * S,   key_bounds[p, h, 1, d] = max_t e2m1 * S
+ * (exact in binary16; the global scale, a positive factor, is left out). Slots past a
+ * request's end are not read into the bounds, whatever they hold.
+ *   first_positions  device int32 [batch_size], or NULL: all pages. A decode step passes the
+ *                    positions that it has written, and one page of each request is redone.
+ *   key_bounds       device float16 [k_cache.num_pages, num_kv_heads, 2, head_dim],
+ *                    contiguous, 16-byte aligned.
+ *   The other arguments are those of nvfp4_dequantize_paged. */
+nvfp4_status nvfp4_page_key_bounds(nvfp4_paged_cache k_cache, int32_t page_size,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t kv_layout,
+                                   const void* block_tables, int32_t table_dtype,
+                                   int32_t max_pages_per_request, const int32_t* seq_lens,
+                                   const int32_t* first_positions, int32_t batch_size,
+                                   void* key_bounds, int32_t* dev_status, void* stream);
+
+/* Bytes of the workspace of nvfp4_select_pages. */
+nvfp4_status nvfp4_select_pages_workspace_bytes(int32_t batch_size, int32_t num_kv_heads,
+                                                int32_t max_pages_per_request, int64_t* bytes);
+
+/* The pages that a query should read, for each request b and KV head h. A logical page j of
+ * ceil(seq_lens[b] / page_size) has the score
+ *   max over the query heads g of h:  sum_d (max(q_d, 0) hi_d + min(q_d, 0) lo_d)
+ * with (lo, hi) = key_bounds of its physical page: an upper bound of q . k on the page. The
+ * first num_sink_pages and the last num_recent_pages pages come before all others. The
+ * max_selected highest are selected (ties: the lower page); they are written in ascending
+ * order.
+ * The score's products are exact in binary32; its sum runs in a fixed order, so the selection
+ * is reproducible: in groups of eight, ((p0 + p2) + p4) + p6 and ((p1 + p3) + p5) + p7, the two
+ * added; the D/8 group sums, filled up with zeros to a power of two n, t[i] += t[i + n/2], ....
+ * A page whose table entry is outside the pool is reported (NVFP4_DEV_BAD_PAGE) and comes last.
+ * Infinities and NaN in the query or the bounds are out of contract.
+ *   query          device, rows of num_qo_heads heads of head_dim elements of dtype,
+ *                  query_row_stride elements apart; 16-byte aligned, stride a multiple of 8.
+ *   key_bounds     device float16 [num_pages, num_kv_heads, 2, head_dim] (see above).
+ *   selected_pages device int32 [batch_size, num_kv_heads, max_selected]: logical pages,
+ *                  ascending; -1 past the count.
+ *   num_selected   device int32 [batch_size, num_kv_heads].
+ *   workspace      device, workspace_bytes >= nvfp4_select_pages_workspace_bytes, 16-byte
+ *                  aligned; holds anything; one call at a time.
+ * Requirements: num_qo_heads a multiple of num_kv_heads, head_dim a multiple of 16 and at most
+ * 256, max_selected >= 1, num_sink_pages, num_recent_pages >= 0. */
+nvfp4_status nvfp4_select_pages(const void* query, int32_t dtype, int64_t query_row_stride,
+                                int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+                                const void* key_bounds, int64_t num_pages, int32_t page_size,
+                                const void* block_tables, int32_t table_dtype,
+                                int32_t max_pages_per_request, const int32_t* seq_lens,
+                                int32_t batch_size, int32_t max_selected,
+                                int32_t num_sink_pages, int32_t num_recent_pages,
+                                int32_t* selected_pages, int32_t* num_selected,
+                                int32_t* dev_status, void* workspace, int64_t workspace_bytes,
+                                void* stream);
+
+/* Bytes of the workspace of the two attention calls. */
+nvfp4_status nvfp4_paged_attention_workspace_bytes(int32_t num_qo_heads, int32_t num_kv_heads,
+                                                   int32_t head_dim, int64_t* bytes);
+
+/* Attention of one new token per request over a paged NVFP4 cache. For request b, query head i
+ * of KV head h = i / (num_qo_heads / num_kv_heads), over the live positions t of the request:
+ *   x_t = sm_scale * k_scale * sum_d q_d K[t, d]     (K, V: e2m1 * S)
+ *   with logits_soft_cap c > 0:  x_t = c tanh(x_t / c)
+ *   out = v_scale * sum_t exp(x_t) V[t, :] / sum_t exp(x_t),   lse = log sum_t exp(x_t)
+ * Live are the positions t < seq_lens[b]; with window_left >= 0 only those with
+ * t >= seq_lens[b] - 1 - window_left. Positions on a page outside the pool are left out
+ * (NVFP4_DEV_BAD_PAGE). A request with no live position gets out = 0 and lse = -inf. What the
+ * slots past a request's end hold is of no consequence. The new token's own key and value are
+ * in the cache already (append first).
+ * Scores and sums are binary32; K and V are exact; a weight exp(x_t - m) is rounded to
+ * binary16 before it multiplies V. The result does not depend on scheduling.
+ *   query         device [batch_size, num_qo_heads, head_dim] of dtype, tokens query_row_stride
+ *                 elements apart; 16-byte aligned, stride a multiple of 8.
+ *   out           device, contiguous [batch_size, num_qo_heads, head_dim] of dtype, 16-byte
+ *                 aligned.
+ *   lse           device float [batch_size, num_qo_heads], or NULL.
+ *   workspace     device, workspace_bytes >= nvfp4_paged_attention_workspace_bytes, 16-byte
+ *                 aligned. Its first NVFP4_COUNTER_BYTES bytes are zero before its first use
+ *                 and left zero by every call, whatever its sizes; the rest holds anything.
+ *                 One call at a time (as the work-distribution workspace).
+ *   The other arguments are those of nvfp4_dequantize_paged.
+ * Requirements: num_qo_heads a multiple of num_kv_heads, head_dim a multiple of 16 and at most
+ * 256, sm_scale finite, logits_soft_cap finite and >= 0. */
+nvfp4_status nvfp4_paged_attention_decode(
+    const void* query, int32_t dtype, int64_t query_row_stride, int32_t num_qo_heads,
+    nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache, int32_t page_size,
+    int32_t num_kv_heads, int32_t head_dim, int32_t kv_layout, const void* block_tables,
+    int32_t table_dtype, int32_t max_pages_per_request, const int32_t* seq_lens,
+    int32_t batch_size, const float* k_scale, const float* v_scale, float sm_scale,
+    float logits_soft_cap, int32_t window_left, void* out, float* lse, int32_t* dev_status,
+    void* workspace, int64_t workspace_bytes, void* stream);
+
+/* nvfp4_paged_attention_decode over selected pages: request b's KV head h attends to the live
+ * positions (t < seq_lens[b]) of its logical pages selected_pages[b, h, 0 .. num_selected[b,
+ * h]) only (nvfp4_select_pages). An entry outside [0, max_pages_per_request) is left out and
+ * reported (NVFP4_DEV_BAD_PAGE); an entry given twice counts twice.
+ *   selected_pages  device int32 [batch_size, num_kv_heads, max_selected].
+ *   num_selected    device int32 [batch_size, num_kv_heads], clamped to [0, max_selected]. */
+nvfp4_status nvfp4_sparse_paged_attention_decode(
+    const void* query, int32_t dtype, int64_t query_row_stride, int32_t num_qo_heads,
+    nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache, int32_t page_size,
+    int32_t num_kv_heads, int32_t head_dim, int32_t kv_layout, const void* block_tables,
+    int32_t table_dtype, int32_t max_pages_per_request, const int32_t* seq_lens,
+    int32_t batch_size, const int32_t* selected_pages, const int32_t* num_selected,
+    int32_t max_selected, const float* k_scale, const float* v_scale, float sm_scale,
+    float logits_soft_cap, void* out, float* lse, int32_t* dev_status, void* workspace,
+    int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

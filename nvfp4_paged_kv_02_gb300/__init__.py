@@ -16,6 +16,13 @@ Operations (FlashInfer documentation pages):
   nvfp4_kv_dequantize            (contiguous tensors, linear block scales)
   nvfp4_4over6_code,           "flashinfer.quantization" index, NVFP4 4over6 Recipes
   nvfp4_4over6_from_code         (the recipe as one int64)
+
+Operators of a decode step over such a cache (additions of this library):
+  nvfp4_qk_norm_rope_append_paged      per-head RMS norm and rotation of q and k, and the append
+  nvfp4_page_key_bounds                element-wise bounds of each page's keys
+  nvfp4_select_pages                   the pages whose bounds promise the largest scores
+  nvfp4_paged_attention_decode         attention of one new token per request
+  nvfp4_sparse_paged_attention_decode  the same over selected pages
 """
 
 from __future__ import annotations
@@ -35,18 +42,21 @@ __all__ = [
     "nvfp4_make_global_scale", "nvfp4_quantize_append_paged", "nvfp4_dequantize_paged",
     "nvfp4_materialize_fp8", "nvfp4_materialize_fp8_out_pages", "NVFP4KVMaterializer",
     "paged_caches", "LIB_PATH", "nvfp4_kv_quantize", "nvfp4_kv_dequantize",
-    "nvfp4_4over6_code", "nvfp4_4over6_from_code",
+    "nvfp4_4over6_code", "nvfp4_4over6_from_code", "nvfp4_qk_norm_rope_append_paged",
+    "nvfp4_page_key_bounds", "nvfp4_select_pages", "nvfp4_paged_attention_decode",
+    "nvfp4_sparse_paged_attention_decode",
 ]
 
 LIB_PATH = _build.LIB_PATH
 
-OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_CUDA = 0, 1, 2, 3, 4
+OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_CUDA, ERR_INTERNAL = 0, 1, 2, 3, 4, 5
 F16, BF16 = 0, 1
 NHD, HND = 0, 1
 SF_LINEAR, SF_INTERLEAVED4 = 0, 1  # materialize V block-scale layouts
 I32, I64 = 0, 1
 DEV_BAD_BATCH, DEV_BAD_POSITION, DEV_BAD_PAGE, DEV_LEN_CLAMPED, DEV_BAD_OUT_PAGE = 1, 2, 4, 8, 16
 DEV_TIMEOUT, DEV_BAD_SCALE = 32, 64
+COUNTER_BYTES = 16384  # zero bytes at the start of an attention workspace
 
 
 class NVFP4KVError(RuntimeError):
@@ -145,6 +155,29 @@ def load() -> ctypes.CDLL:
         L.nvfp4_kv_quantize.argtypes = [vp, i32, i64, i32, i64, vp, vp, vp, vp, vp, vp, vp]
         L.nvfp4_kv_dequantize.restype = i32
         L.nvfp4_kv_dequantize.argtypes = [vp, vp, i64, i32, vp, vp, i32, vp, vp, vp]
+        L.nvfp4_qk_norm_rope_append_paged.restype = i32
+        L.nvfp4_qk_norm_rope_append_paged.argtypes = [
+            vp, vp, vp, i32, i64, i32, i32, i32, i64, i64, i64, vp, vp, f32, vp, i64, i32, i32, vp,
+            vp, _Cache, _Cache, i32, i32, vp, i64, vp, vp, i32, f32, f32, vp, vp, vp, vp, i64, vp, vp]
+        L.nvfp4_page_key_bounds.restype = i32
+        L.nvfp4_page_key_bounds.argtypes = [
+            _Cache, i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, vp, vp, vp]
+        L.nvfp4_select_pages_workspace_bytes.restype = i32
+        L.nvfp4_select_pages_workspace_bytes.argtypes = [i32, i32, i32, vp]
+        L.nvfp4_select_pages.restype = i32
+        L.nvfp4_select_pages.argtypes = [
+            vp, i32, i64, i32, i32, i32, vp, i64, i32, vp, i32, i32, vp, i32, i32, i32, i32, vp, vp,
+            vp, vp, i64, vp]
+        L.nvfp4_paged_attention_workspace_bytes.restype = i32
+        L.nvfp4_paged_attention_workspace_bytes.argtypes = [i32, i32, i32, vp]
+        L.nvfp4_paged_attention_decode.restype = i32
+        L.nvfp4_paged_attention_decode.argtypes = [
+            vp, i32, i64, i32, _Cache, _Cache, i32, i32, i32, i32, vp, i32, i32, vp, i32, vp, vp, f32,
+            f32, i32, vp, vp, vp, vp, i64, vp]
+        L.nvfp4_sparse_paged_attention_decode.restype = i32
+        L.nvfp4_sparse_paged_attention_decode.argtypes = [
+            vp, i32, i64, i32, _Cache, _Cache, i32, i32, i32, i32, vp, i32, i32, vp, i32, vp, vp, i32,
+            vp, vp, f32, f32, vp, vp, vp, vp, i64, vp]
         _lib = L
         return L
 
@@ -566,3 +599,302 @@ def nvfp4_4over6_from_code(code: int) -> Optional[NVFP44Over6Config]:
     return NVFP44Over6Config(e4m3_max=float(c.e4m3_max),
                              err_mode="MSE" if c.err_mode == 1 else "MAE",
                              err_use_fast_math=bool(c.err_use_fast_math))
+
+
+# ---- the operators of a decode step -----------------------------------------------------------
+
+def _addr(t: torch.Tensor, dtype, device: torch.device, what: str) -> int:
+    """Address of a contiguous tensor of the given dtype on `device`."""
+    if t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor on {device}")
+    return t.data_ptr()
+
+
+def _device(t: torch.Tensor) -> torch.device:
+    device = t.device
+    if device.type != "cuda":
+        raise ValueError("nvfp4 ops take CUDA tensors only")
+    return device
+
+
+def _rows(t: torch.Tensor, dtype, device: torch.device, what: str, heads: Optional[int] = None,
+          head_dim: Optional[int] = None) -> int:
+    """Checks rows [n, heads, head_dim] whose heads and elements are contiguous; their stride."""
+    if t.dtype != dtype or t.device != device or t.dim() != 3:
+        raise ValueError(f"{what} must be a [n, heads, head_dim] {dtype} tensor on {device}")
+    n, h, d = t.shape
+    sn, sh, sd = t.stride()
+    if (heads is not None and h != heads) or (head_dim is not None and d != head_dim):
+        raise ValueError(f"{what} must have {heads} heads of {head_dim} elements")
+    if sd != 1 or (sh != d and h > 1):
+        raise ValueError(f"{what} must have contiguous heads and elements")
+    return sn if n > 1 else h * d
+
+
+def _status_ptr(t: Optional[torch.Tensor], device: torch.device) -> Optional[int]:
+    return None if t is None else _addr(t, torch.int32, device, "dev_status")
+
+
+def _block_tables(t: torch.Tensor, batch: int, device: torch.device):
+    if t.dim() != 2 or t.shape[0] != batch or t.dtype not in (torch.int32, torch.int64) \
+            or t.device != device or not t.is_contiguous():
+        raise ValueError(f"block_tables must be a contiguous [{batch}, max_pages] int32/int64 tensor on {device}")
+    return t.data_ptr(), I64 if t.dtype == torch.int64 else I32, t.shape[1]
+
+
+def _cache_on(data: torch.Tensor, sf: torch.Tensor, device: torch.device) -> Tuple[_Cache, torch.Size]:
+    """The C form of one cache and its code tensor's shape, checked as _one_cache checks it."""
+    c = _one_cache(data, sf)
+    if data.device != device or sf.device != device or sf.shape[:3] != data.shape[:3] \
+            or sf.shape[3] * 8 != data.shape[3]:
+        raise ValueError(f"codes [pages, ., ., D/2] and scales [pages, ., ., D/16] must match, on {device}")
+    return c._c(), data.shape
+
+
+def _caches_on(paged_kv_cache, kv_cache_sf, layout: int, device: torch.device):
+    """(K, V, page_size, heads, head_dim) of a tuple or stacked cache."""
+    if not isinstance(paged_kv_cache, (tuple, list)):
+        d, s = paged_kv_cache, kv_cache_sf
+        if d.dim() != 5 or s.dim() != 5 or d.shape[1] != 2 or s.shape[1] != 2:
+            raise ValueError("a stacked cache is 5-D with K/V on the second dimension")
+        paged_kv_cache, kv_cache_sf = d.unbind(1), s.unbind(1)
+    kc, ks = _cache_on(paged_kv_cache[0], kv_cache_sf[0], device)
+    vc, vs = _cache_on(paged_kv_cache[1], kv_cache_sf[1], device)
+    if ks[1:] != vs[1:]:
+        raise ValueError("the K and V caches must have the same page shape")
+    if layout == NHD:
+        return kc, vc, ks[1], ks[2], ks[3] * 2
+    return kc, vc, ks[2], ks[1], ks[3] * 2
+
+
+# Workspaces of the attention and selection calls, one per (device, stream) as above; a larger one takes
+# its place when a call needs it. A call that is being captured gets its own from the graph's memory, so
+# that a graph never depends on what later calls do with these.
+_scratch = {}
+
+
+def _scratch_for(device: torch.device, stream: int, nbytes: int, zeroed: int) -> torch.Tensor:
+    """At least nbytes of device memory whose first `zeroed` bytes are zero between calls."""
+    key = (device.index, stream, zeroed)
+    capturing = torch.cuda.is_current_stream_capturing()
+    t = None if capturing else _scratch.get(key)
+    if t is None or t.numel() < nbytes:
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if zeroed:
+            t[:zeroed].zero_()
+        if not capturing:
+            _scratch[key] = t
+    return t
+
+
+def _raw_stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def nvfp4_qk_norm_rope_append_paged(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                                    q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+                                    cos_sin: Optional[torch.Tensor], batch_indices: torch.Tensor,
+                                    positions: torch.Tensor, paged_kv_cache, kv_cache_sf,
+                                    kv_indices: torch.Tensor, kv_indptr: torch.Tensor,
+                                    kv_last_page_len: Optional[torch.Tensor], k_scale, v_scale,
+                                    kv_layout: str = "NHD", eps: float = 1e-6,
+                                    rotary_interleaved: bool = False,
+                                    nvfp4_4over6: Optional[NVFP44Over6Config] = None,
+                                    out: Optional[torch.Tensor] = None,
+                                    dev_status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """RMS norm of each head's query and key rows (weights q_weight, k_weight [D]; None: no norm),
+    rotation by cos_sin[position] (float32 [positions, rotary_dim]: cosines, then sines; None: no
+    rotation), and quantize-append of the key and value rows, in one launch. query [nnz, Hq, D], key
+    and value [nnz, H, D] may be slices of one tensor. Returns the query rows (`out`, which may be
+    `query`). The other arguments are those of nvfp4_quantize_append_paged."""
+    device, dt = _device(query), query.dtype
+    code = _dtype_code(dt)
+    layout = _layout(kv_layout)
+    kc, vc, ps, H, D = _caches_on(paged_kv_cache, kv_cache_sf, layout, device)
+    q_stride = _rows(query, dt, device, "query", None, D)
+    k_stride = _rows(key, dt, device, "key", H, D)
+    v_stride = _rows(value, dt, device, "value", H, D)
+    nnz, Hq = query.shape[0], query.shape[1]
+    if key.shape[0] != nnz or value.shape[0] != nnz or batch_indices.numel() != nnz or positions.numel() != nnz:
+        raise ValueError("query, key, value, batch_indices and positions must have as many rows")
+    for w in (q_weight, k_weight):
+        if w is not None and w.numel() != D:
+            raise ValueError("a norm's weights must have head_dim elements")
+    npos, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    if out is None:
+        out = torch.empty((nnz, Hq, D), dtype=dt, device=device)
+        o_stride = Hq * D
+    else:
+        o_stride = _rows(out, dt, device, "out", Hq, D)
+        if out.shape[0] != nnz:
+            raise ValueError("out must have query's shape")
+    i32 = torch.int32
+    B = kv_indptr.numel() - 1
+    if kv_last_page_len is not None and kv_last_page_len.numel() < B:
+        raise ValueError("kv_last_page_len must have one entry per request")
+    ks = vs = 1.0
+    k_dev = v_dev = None
+    if isinstance(k_scale, torch.Tensor) or isinstance(v_scale, torch.Tensor):
+        for s in (k_scale, v_scale):
+            if not isinstance(s, torch.Tensor) or s.dtype != torch.float32 or s.numel() < 1 or s.device != device:
+                raise ValueError("device scales must both be float32 CUDA tensors")
+        k_dev, v_dev = k_scale.data_ptr(), v_scale.data_ptr()
+    else:
+        ks, vs = float(k_scale), float(v_scale)
+    _check("nvfp4_qk_norm_rope_append_paged", load().nvfp4_qk_norm_rope_append_paged(
+        query.data_ptr(), key.data_ptr(), value.data_ptr(), code, nnz, Hq, H, D, q_stride, k_stride,
+        v_stride, None if q_weight is None else _addr(q_weight, dt, device, "q_weight"),
+        None if k_weight is None else _addr(k_weight, dt, device, "k_weight"), eps,
+        None if cos_sin is None else _addr(cos_sin, torch.float32, device, "cos_sin"), npos, rot,
+        int(bool(rotary_interleaved)), _addr(batch_indices, i32, device, "batch_indices"),
+        _addr(positions, i32, device, "positions"), kc, vc, ps, layout,
+        _addr(kv_indices, i32, device, "kv_indices"), kv_indices.numel(),
+        _addr(kv_indptr, i32, device, "kv_indptr"),
+        None if kv_last_page_len is None else _addr(kv_last_page_len, i32, device, "kv_last_page_len"),
+        B, ks, vs, k_dev, v_dev, _recipe(nvfp4_4over6), out.data_ptr(), o_stride,
+        _status_ptr(dev_status, device), _raw_stream(device)))
+    return out
+
+
+def nvfp4_page_key_bounds(k_cache: torch.Tensor, k_block_scales: torch.Tensor,
+                          block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                          key_bounds: torch.Tensor, first_positions: Optional[torch.Tensor] = None,
+                          kv_layout: str = "NHD", dev_status: Optional[torch.Tensor] = None) -> None:
+    """Write the element-wise (min, max) of e2m1 * block_scale over the live slots of each request's
+    pages into key_bounds [num_pages, H, 2, D] float16: the pages that hold a position from
+    first_positions on (None: all of them)."""
+    device = _device(k_cache)
+    layout = _layout(kv_layout)
+    kc, shape = _cache_on(k_cache, k_block_scales, device)
+    ps, H = (shape[1], shape[2]) if layout == NHD else (shape[2], shape[1])
+    D = shape[3] * 2
+    B = seq_lens.numel()
+    if key_bounds.shape != (shape[0], H, 2, D):
+        raise ValueError("key_bounds must be [num_pages, num_kv_heads, 2, head_dim]")
+    if first_positions is not None and first_positions.numel() != B:
+        raise ValueError("first_positions must have one entry per request")
+    table, table_dtype, width = _block_tables(block_tables, B, device)
+    _check("nvfp4_page_key_bounds", load().nvfp4_page_key_bounds(
+        kc, ps, H, D, layout, table, table_dtype, width,
+        _addr(seq_lens, torch.int32, device, "seq_lens"),
+        None if first_positions is None else _addr(first_positions, torch.int32, device, "first_positions"),
+        B, _addr(key_bounds, torch.float16, device, "key_bounds"), _status_ptr(dev_status, device),
+        _raw_stream(device)))
+
+
+def nvfp4_select_pages(query: torch.Tensor, key_bounds: torch.Tensor, block_tables: torch.Tensor,
+                       seq_lens: torch.Tensor, page_size: int, max_selected: int,
+                       num_sink_pages: int = 1, num_recent_pages: int = 1,
+                       out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                       dev_status: Optional[torch.Tensor] = None):
+    """The logical pages of each (request, KV head) with the largest upper bound of q . k, the first
+    num_sink_pages and last num_recent_pages always among them. query [B, Hq, D]; key_bounds from
+    nvfp4_page_key_bounds. Returns (selected_pages int32 [B, H, max_selected], ascending and -1 past the
+    count; num_selected int32 [B, H])."""
+    device, dt = _device(query), query.dtype
+    code = _dtype_code(dt)
+    if key_bounds.dim() != 4 or key_bounds.shape[2] != 2:
+        raise ValueError("key_bounds must be [num_pages, num_kv_heads, 2, head_dim]")
+    P, H, _, D = key_bounds.shape
+    stride = _rows(query, dt, device, "query", None, D)
+    B, Hq = query.shape[0], query.shape[1]
+    if seq_lens.numel() != B:
+        raise ValueError("seq_lens must have one entry per request")
+    table, table_dtype, width = _block_tables(block_tables, B, device)
+    if out is None:
+        selected = torch.empty((B, H, max_selected), dtype=torch.int32, device=device)
+        count = torch.empty((B, H), dtype=torch.int32, device=device)
+    else:
+        selected, count = out
+        if selected.shape != (B, H, max_selected) or count.shape != (B, H):
+            raise ValueError("out must be ([B, H, max_selected], [B, H]) int32 tensors")
+    lib = load()
+    need = ctypes.c_int64()
+    _check("nvfp4_select_pages_workspace_bytes",
+           lib.nvfp4_select_pages_workspace_bytes(B, H, width, ctypes.byref(need)))
+    stream = _raw_stream(device)
+    ws = _scratch_for(device, stream, need.value, 0)
+    _check("nvfp4_select_pages", lib.nvfp4_select_pages(
+        query.data_ptr(), code, stride, Hq, H, D, _addr(key_bounds, torch.float16, device, "key_bounds"),
+        P, page_size, table, table_dtype, width, _addr(seq_lens, torch.int32, device, "seq_lens"), B,
+        max_selected, num_sink_pages, num_recent_pages,
+        _addr(selected, torch.int32, device, "selected_pages"), _addr(count, torch.int32, device, "num_selected"),
+        _status_ptr(dev_status, device), ws.data_ptr(), ws.numel(), stream))
+    return selected, count
+
+
+def _attention(fn: str, query, paged_kv_cache, kv_cache_sf, block_tables, seq_lens, selection, k_scale,
+               v_scale, kv_layout, sm_scale, soft_cap, window_left, out, lse, dev_status):
+    device, dt = _device(query), query.dtype
+    code = _dtype_code(dt)
+    layout = _layout(kv_layout)
+    kc, vc, ps, H, D = _caches_on(paged_kv_cache, kv_cache_sf, layout, device)
+    stride = _rows(query, dt, device, "query", None, D)
+    B, Hq = query.shape[0], query.shape[1]
+    if seq_lens.numel() != B:
+        raise ValueError("seq_lens must have one entry per request")
+    table, table_dtype, width = _block_tables(block_tables, B, device)
+    for s in (k_scale, v_scale):
+        if s.dtype != torch.float32 or s.numel() < 1 or s.device != device:
+            raise ValueError("k_scale/v_scale must be float32 CUDA tensors")
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=dt, device=device)
+    elif out.shape != (B, Hq, D):
+        raise ValueError("out must be [batch, num_qo_heads, head_dim]")
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
+    elif lse.shape != (B, Hq):
+        raise ValueError("lse must be [batch, num_qo_heads]")
+    lib = load()
+    need = ctypes.c_int64()
+    _check("nvfp4_paged_attention_workspace_bytes",
+           lib.nvfp4_paged_attention_workspace_bytes(Hq, H, D, ctypes.byref(need)))
+    stream = _raw_stream(device)
+    ws = _scratch_for(device, stream, need.value, COUNTER_BYTES)
+    head = (query.data_ptr(), code, stride, Hq, kc, vc, ps, H, D, layout, table, table_dtype, width,
+            _addr(seq_lens, torch.int32, device, "seq_lens"), B)
+    scales = (k_scale.data_ptr(), v_scale.data_ptr(), D ** -0.5 if sm_scale is None else sm_scale, soft_cap)
+    tail = (_addr(out, dt, device, "out"), _addr(lse, torch.float32, device, "lse"),
+            _status_ptr(dev_status, device), ws.data_ptr(), ws.numel(), stream)
+    if selection is None:
+        _check(fn, lib.nvfp4_paged_attention_decode(*head, *scales, window_left, *tail))
+    else:
+        selected, count = selection
+        if selected.dim() != 3 or selected.shape[:2] != (B, H) or count.shape != (B, H):
+            raise ValueError("selected_pages must be [B, H, max_selected] and num_selected [B, H]")
+        _check(fn, lib.nvfp4_sparse_paged_attention_decode(
+            *head, _addr(selected, torch.int32, device, "selected_pages"),
+            _addr(count, torch.int32, device, "num_selected"), selected.shape[2], *scales, *tail))
+    return out, lse
+
+
+def nvfp4_paged_attention_decode(query: torch.Tensor, paged_kv_cache, kv_cache_sf,
+                                 block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                                 k_scale: torch.Tensor, v_scale: torch.Tensor, kv_layout: str = "NHD",
+                                 sm_scale: Optional[float] = None, logits_soft_cap: float = 0.0,
+                                 window_left: int = -1, out: Optional[torch.Tensor] = None,
+                                 lse: Optional[torch.Tensor] = None,
+                                 dev_status: Optional[torch.Tensor] = None):
+    """Attention of one new token per request, query [B, Hq, D], over the paged cache's first
+    seq_lens[b] positions (the last window_left + 1 of them when window_left >= 0). k_scale, v_scale: the
+    global decode scales, 1-element float32 CUDA tensors; sm_scale: D ** -0.5 unless given. Returns (out
+    [B, Hq, D], lse float32 [B, Hq], natural logarithm); a request without positions gets 0 and -inf."""
+    return _attention("nvfp4_paged_attention_decode", query, paged_kv_cache, kv_cache_sf, block_tables,
+                      seq_lens, None, k_scale, v_scale, kv_layout, sm_scale, logits_soft_cap,
+                      window_left, out, lse, dev_status)
+
+
+def nvfp4_sparse_paged_attention_decode(query: torch.Tensor, paged_kv_cache, kv_cache_sf,
+                                        block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                                        selected_pages: torch.Tensor, num_selected: torch.Tensor,
+                                        k_scale: torch.Tensor, v_scale: torch.Tensor,
+                                        kv_layout: str = "NHD", sm_scale: Optional[float] = None,
+                                        logits_soft_cap: float = 0.0,
+                                        out: Optional[torch.Tensor] = None,
+                                        lse: Optional[torch.Tensor] = None,
+                                        dev_status: Optional[torch.Tensor] = None):
+    """nvfp4_paged_attention_decode over the first num_selected[b, h] logical pages of
+    selected_pages[b, h] for each KV head (nvfp4_select_pages)."""
+    return _attention("nvfp4_sparse_paged_attention_decode", query, paged_kv_cache, kv_cache_sf,
+                      block_tables, seq_lens, (selected_pages, num_selected), k_scale, v_scale,
+                      kv_layout, sm_scale, logits_soft_cap, -1, out, lse, dev_status)

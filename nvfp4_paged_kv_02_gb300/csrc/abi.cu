@@ -9,6 +9,7 @@
 #include <sstream>
 #include <unordered_map>
 
+#include "attention.h"
 #include "internal.h"
 
 namespace nvfp4 {
@@ -709,6 +710,395 @@ NVFP4_EXPORT nvfp4_status nvfp4_materializer_run(
   a.workspace = workspace;
   const MaterializeLaunch c{m->bulk, m->max_batch_size, m->smem_bytes, m->grid};
   return launch_materialize_prepared(a, c, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ---- the operators of a decode step -------------------------------------------------------
+
+namespace {
+
+// No exception leaves a C entry: the only ones that can arise are the host's out-of-memory
+// from message strings and caches.
+template <typename F>
+nvfp4_status guarded(F body) noexcept {
+  try {
+    clear_error();
+    return body();
+  } catch (...) {
+    return NVFP4_ERR_INTERNAL;
+  }
+}
+
+nvfp4_status check_dtype(const std::string& f, int32_t dtype) {
+  if (dtype != NVFP4_F16 && dtype != NVFP4_BF16)
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": dtype must be NVFP4_F16 or NVFP4_BF16");
+  return NVFP4_OK;
+}
+
+nvfp4_status check_query_heads(const std::string& f, int32_t Hq, int32_t H) {
+  if (H < 1 || Hq < 1 || Hq % H != 0)
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": num_qo_heads must be a positive multiple of num_kv_heads");
+  return NVFP4_OK;
+}
+
+// Block tables and lengths, as far as the host sees them.
+nvfp4_status check_tables(const std::string& f, int32_t table_dtype, int32_t max_pages,
+                          int32_t batch_size) {
+  if (table_dtype != NVFP4_I32 && table_dtype != NVFP4_I64)
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": table_dtype must be NVFP4_I32 or NVFP4_I64");
+  if (batch_size < 0 || max_pages < 0) return fail(NVFP4_ERR_INVALID_ARG, f + ": negative size");
+  if (batch_size > kMaxScanBatch) return fail(NVFP4_ERR_UNSUPPORTED, f + ": batch_size above 16384");
+  return NVFP4_OK;
+}
+
+nvfp4_status check_rows(const std::string& f, const char* name, const void* p, int64_t stride,
+                        int64_t row) {
+  if (!p) return fail(NVFP4_ERR_INVALID_ARG, f + ": " + name + " is null");
+  if (stride < row) return fail(NVFP4_ERR_INVALID_ARG, f + ": " + name + " rows overlap: the row stride must cover heads * head_dim elements");
+  if (!aligned(p, 16) || stride % 8 != 0)
+    return fail(NVFP4_ERR_ALIGNMENT, f + ": " + name + " must be 16-byte aligned with a row stride that is a multiple of 8 elements");
+  return NVFP4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+NVFP4_EXPORT nvfp4_status nvfp4_qk_norm_rope_append_paged(
+    const void* query, const void* key, const void* value, int32_t dtype, int64_t nnz,
+    int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, int64_t query_row_stride,
+    int64_t key_row_stride, int64_t value_row_stride, const void* q_weight,
+    const void* k_weight, float eps, const float* cos_sin, int64_t num_positions,
+    int32_t rotary_dim, int32_t rotary_interleaved, const int32_t* batch_indices,
+    const int32_t* positions, nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache,
+    int32_t page_size, int32_t kv_layout, const int32_t* kv_indices, int64_t num_kv_indices,
+    const int32_t* kv_indptr, const int32_t* kv_last_page_len, int32_t batch_size,
+    float k_scale, float v_scale, const float* k_scale_dev, const float* v_scale_dev,
+    const nvfp4_4over6_config* recipe, void* query_out, int64_t query_out_row_stride,
+    int32_t* dev_status, void* stream) {
+  return guarded([&]() -> nvfp4_status {
+    const char* fn = "nvfp4_qk_norm_rope_append_paged";
+    const std::string f(fn);
+    if (nvfp4_status st = check_recipe(recipe)) return st;
+    if (nvfp4_status st = check_geometry(fn, page_size, num_kv_heads, head_dim, kv_layout)) return st;
+    if (nvfp4_status st = check_dtype(f, dtype)) return st;
+    if (num_qo_heads < 1) return fail(NVFP4_ERR_INVALID_ARG, f + ": num_qo_heads must be >= 1");
+    if (head_dim > 512) return fail(NVFP4_ERR_UNSUPPORTED, f + ": head_dim above 512");
+    if (nnz < 0 || batch_size < 0 || num_positions < 0)
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": negative size");
+    if (!(std::isfinite(eps) && eps >= 0.0f)) return fail(NVFP4_ERR_INVALID_ARG, f + ": eps must be finite and >= 0");
+    if (rotary_dim < 0 || rotary_dim % 16 != 0 || rotary_dim > head_dim)
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": rotary_dim must be a multiple of 16 between 0 and head_dim");
+    if (rotary_interleaved != 0 && rotary_interleaved != 1)
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": rotary_interleaved must be 0 or 1");
+    if ((k_scale_dev == nullptr) != (v_scale_dev == nullptr))
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": give both scales in device memory or both by value");
+    if (!k_scale_dev && (!(std::isfinite(k_scale) && k_scale > 0.0f) || !(std::isfinite(v_scale) && v_scale > 0.0f)))
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": k_scale and v_scale must be positive finite");
+    if (!aligned(k_scale_dev, 4) || !aligned(v_scale_dev, 4))
+      return fail(NVFP4_ERR_ALIGNMENT, f + ": device scales must be 4-byte aligned");
+    if (nvfp4_status st = check_cache(fn, "k_cache", k_cache, page_size, num_kv_heads, head_dim)) return st;
+    if (nvfp4_status st = check_cache(fn, "v_cache", v_cache, page_size, num_kv_heads, head_dim)) return st;
+    if (nnz == 0) return NVFP4_OK;
+    const int64_t q_row = static_cast<int64_t>(num_qo_heads) * head_dim;
+    const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+    if (nvfp4_status st = check_rows(f, "query", query, query_row_stride, q_row)) return st;
+    if (nvfp4_status st = check_rows(f, "key", key, key_row_stride, kv_row)) return st;
+    if (nvfp4_status st = check_rows(f, "value", value, value_row_stride, kv_row)) return st;
+    if (nvfp4_status st = check_rows(f, "query_out", query_out, query_out_row_stride, q_row)) return st;
+    if (query_out == query && query_out_row_stride != query_row_stride)
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": query_out in place needs query's row stride");
+    if (!batch_indices || !positions || !kv_indptr || (!kv_indices && num_kv_indices > 0) ||
+        (rotary_dim > 0 && !cos_sin))
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": null device pointer");
+    if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(cos_sin, 16))
+      return fail(NVFP4_ERR_ALIGNMENT, f + ": weights and cos_sin must be 16-byte aligned");
+    if (batch_size == 0) return fail(NVFP4_ERR_INVALID_ARG, f + ": rows given but batch_size is 0");
+    if (num_kv_indices < 0) return fail(NVFP4_ERR_INVALID_ARG, f + ": num_kv_indices must be >= 0");
+    if (num_qo_heads + 2 * static_cast<int64_t>(num_kv_heads) > INT32_MAX / 2 ||
+        nnz > (int64_t(1) << 40) / (num_qo_heads + 2 * static_cast<int64_t>(num_kv_heads)))
+      return fail(NVFP4_ERR_UNSUPPORTED, f + ": more than 2^40 rows");
+    NormRopeArgs a{};
+    a.ap.k = static_cast<const uint8_t*>(key);
+    a.ap.v = static_cast<const uint8_t*>(value);
+    a.ap.k_row_bytes = key_row_stride * 2;
+    a.ap.v_row_bytes = value_row_stride * 2;
+    a.ap.nnz = nnz;
+    a.ap.H = num_kv_heads;
+    a.ap.D = head_dim;
+    a.ap.nb = head_dim / 16;
+    a.ap.div_ps = make_div(page_size);
+    a.ap.batch_indices = batch_indices;
+    a.ap.positions = positions;
+    a.ap.kc = k_cache;
+    a.ap.vc = v_cache;
+    a.ap.ps = page_size;
+    a.ap.layout = kv_layout;
+    a.ap.kv_indices = kv_indices;
+    a.ap.num_kv_indices = num_kv_indices;
+    a.ap.kv_indptr = kv_indptr;
+    a.ap.kv_last_page_len = kv_last_page_len;
+    a.ap.batch_size = batch_size;
+    a.ap.gs[0] = k_scale;
+    a.ap.gs[1] = v_scale;
+    a.ap.gs_dev[0] = k_scale_dev;
+    a.ap.gs_dev[1] = v_scale_dev;
+    a.ap.cap_a = nvfp4_e4m3_max(recipe);
+    a.ap.neg_zero = 0x80000000u;
+    a.ap.status = dev_status;
+    a.q = static_cast<const uint8_t*>(query);
+    a.q_row_bytes = query_row_stride * 2;
+    a.q_out = static_cast<uint8_t*>(query_out);
+    a.q_out_row_bytes = query_out_row_stride * 2;
+    a.Hq = num_qo_heads;
+    a.div_rows = make_div(num_qo_heads + 2 * static_cast<int64_t>(num_kv_heads));
+    a.q_weight = static_cast<const uint8_t*>(q_weight);
+    a.k_weight = static_cast<const uint8_t*>(k_weight);
+    a.eps = eps;
+    a.inv_d = static_cast<float>(1.0 / head_dim);
+    a.cos_sin = cos_sin;
+    a.num_positions = num_positions;
+    a.rotary_dim = rotary_dim;
+    a.interleaved = rotary_interleaved;
+    while ((16 << a.log2_T) < head_dim) ++a.log2_T;
+    int mode = 0;
+    if (recipe) mode = 1 + (recipe->err_mode == NVFP4_ERR_MSE ? 1 : 0) + (recipe->err_use_fast_math ? 2 : 0);
+    return launch_norm_rope_append(a, dtype == NVFP4_BF16, mode, static_cast<cudaStream_t>(stream));
+  });
+}
+
+NVFP4_EXPORT nvfp4_status nvfp4_page_key_bounds(
+    nvfp4_paged_cache k_cache, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
+    int32_t kv_layout, const void* block_tables, int32_t table_dtype,
+    int32_t max_pages_per_request, const int32_t* seq_lens, const int32_t* first_positions,
+    int32_t batch_size, void* key_bounds, int32_t* dev_status, void* stream) {
+  return guarded([&]() -> nvfp4_status {
+    const char* fn = "nvfp4_page_key_bounds";
+    const std::string f(fn);
+    if (nvfp4_status st = check_geometry(fn, page_size, num_kv_heads, head_dim, kv_layout)) return st;
+    if (nvfp4_status st = check_tables(f, table_dtype, max_pages_per_request, batch_size)) return st;
+    if (nvfp4_status st = check_cache(fn, "k_cache", k_cache, page_size, num_kv_heads, head_dim)) return st;
+    if (batch_size == 0 || max_pages_per_request == 0) return NVFP4_OK;
+    if (!block_tables || !seq_lens || (!key_bounds && k_cache.num_pages > 0))
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": null device pointer");
+    if (!aligned(key_bounds, 16)) return fail(NVFP4_ERR_ALIGNMENT, f + ": key_bounds must be 16-byte aligned");
+    BoundsArgs a{};
+    a.kc = k_cache;
+    a.ps = page_size;
+    a.H = num_kv_heads;
+    a.D = head_dim;
+    a.layout = kv_layout;
+    a.B = batch_size;
+    a.table64 = table_dtype == NVFP4_I64;
+    a.div_ps = make_div(page_size);
+    a.block_tables = block_tables;
+    a.max_pages = max_pages_per_request;
+    a.seq_lens = seq_lens;
+    a.first_positions = first_positions;
+    a.bounds = static_cast<uint16_t*>(key_bounds);
+    a.status = dev_status;
+    return launch_page_key_bounds(a, static_cast<cudaStream_t>(stream));
+  });
+}
+
+NVFP4_EXPORT nvfp4_status nvfp4_select_pages_workspace_bytes(int32_t batch_size,
+                                                             int32_t num_kv_heads,
+                                                             int32_t max_pages_per_request,
+                                                             int64_t* bytes) {
+  return guarded([&]() -> nvfp4_status {
+    if (batch_size < 0 || num_kv_heads < 1 || max_pages_per_request < 0 || !bytes)
+      return fail(NVFP4_ERR_INVALID_ARG, "nvfp4_select_pages_workspace_bytes: bad size or null output pointer");
+    *bytes = select_workspace_bytes(batch_size, num_kv_heads, max_pages_per_request);
+    return NVFP4_OK;
+  });
+}
+
+NVFP4_EXPORT nvfp4_status nvfp4_select_pages(
+    const void* query, int32_t dtype, int64_t query_row_stride, int32_t num_qo_heads,
+    int32_t num_kv_heads, int32_t head_dim, const void* key_bounds, int64_t num_pages,
+    int32_t page_size, const void* block_tables, int32_t table_dtype,
+    int32_t max_pages_per_request, const int32_t* seq_lens, int32_t batch_size,
+    int32_t max_selected, int32_t num_sink_pages, int32_t num_recent_pages,
+    int32_t* selected_pages, int32_t* num_selected, int32_t* dev_status, void* workspace,
+    int64_t workspace_bytes, void* stream) {
+  return guarded([&]() -> nvfp4_status {
+    const char* fn = "nvfp4_select_pages";
+    const std::string f(fn);
+    if (nvfp4_status st = check_geometry(fn, page_size, num_kv_heads, head_dim, NVFP4_NHD)) return st;
+    if (nvfp4_status st = check_dtype(f, dtype)) return st;
+    if (nvfp4_status st = check_query_heads(f, num_qo_heads, num_kv_heads)) return st;
+    if (head_dim > kAttnMaxHeadDim) return fail(NVFP4_ERR_UNSUPPORTED, f + ": head_dim above 256");
+    if (nvfp4_status st = check_tables(f, table_dtype, max_pages_per_request, batch_size)) return st;
+    if (max_selected < 1) return fail(NVFP4_ERR_INVALID_ARG, f + ": max_selected must be >= 1");
+    if (num_pages < 0 || num_sink_pages < 0 || num_recent_pages < 0)
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": negative size");
+    if (static_cast<int64_t>(batch_size) * num_kv_heads > INT32_MAX)
+      return fail(NVFP4_ERR_UNSUPPORTED, f + ": more than 2^31 - 1 lists");
+    if (batch_size == 0) return NVFP4_OK;
+    if (nvfp4_status st = check_rows(f, "query", query, query_row_stride,
+                                     static_cast<int64_t>(num_qo_heads) * head_dim)) return st;
+    if (!seq_lens || !selected_pages || !num_selected || (!block_tables && max_pages_per_request > 0) ||
+        (!key_bounds && num_pages > 0))
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": null device pointer");
+    if (!aligned(key_bounds, 16)) return fail(NVFP4_ERR_ALIGNMENT, f + ": key_bounds must be 16-byte aligned");
+    const int64_t need = select_workspace_bytes(batch_size, num_kv_heads, max_pages_per_request);
+    if (workspace_bytes < need || (need > 0 && !workspace))
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": the workspace is smaller than nvfp4_select_pages_workspace_bytes");
+    if (!aligned(workspace, 16)) return fail(NVFP4_ERR_ALIGNMENT, f + ": workspace must be 16-byte aligned");
+    SelectArgs a{};
+    a.q = static_cast<const uint8_t*>(query);
+    a.q_row_bytes = query_row_stride * 2;
+    a.bf16 = dtype == NVFP4_BF16;
+    a.Hq = num_qo_heads;
+    a.H = num_kv_heads;
+    a.G = num_qo_heads / num_kv_heads;
+    a.D = head_dim;
+    a.ps = page_size;
+    a.B = batch_size;
+    a.table64 = table_dtype == NVFP4_I64;
+    a.bounds = static_cast<const uint16_t*>(key_bounds);
+    a.num_pages = num_pages;
+    a.block_tables = block_tables;
+    a.max_pages = max_pages_per_request;
+    a.seq_lens = seq_lens;
+    a.k = max_selected;
+    a.sink = num_sink_pages;
+    a.recent = num_recent_pages;
+    a.selected = selected_pages;
+    a.num_selected = num_selected;
+    a.scores = static_cast<uint32_t*>(workspace);
+    a.status = dev_status;
+    return launch_select_pages(a, static_cast<cudaStream_t>(stream));
+  });
+}
+
+NVFP4_EXPORT nvfp4_status nvfp4_paged_attention_workspace_bytes(int32_t num_qo_heads,
+                                                                int32_t num_kv_heads,
+                                                                int32_t head_dim, int64_t* bytes) {
+  return guarded([&]() -> nvfp4_status {
+    const std::string f("nvfp4_paged_attention_workspace_bytes");
+    if (nvfp4_status st = check_query_heads(f, num_qo_heads, num_kv_heads)) return st;
+    if (head_dim < 16 || head_dim % 16 != 0)
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": head_dim must be a positive multiple of 16");
+    if (head_dim > kAttnMaxHeadDim) return fail(NVFP4_ERR_UNSUPPORTED, f + ": head_dim above 256");
+    if (!bytes) return fail(NVFP4_ERR_INVALID_ARG, f + ": bytes is null");
+    *bytes = attention_workspace_bytes(num_qo_heads, num_kv_heads, head_dim);
+    return NVFP4_OK;
+  });
+}
+
+}  // extern "C"
+
+namespace {
+
+// Shared body of the two attention entry points.
+nvfp4_status attention_impl(
+    const char* fn, const void* query, int32_t dtype, int64_t query_row_stride,
+    int32_t num_qo_heads, const nvfp4_paged_cache& k_cache, const nvfp4_paged_cache& v_cache,
+    int32_t page_size, int32_t num_kv_heads, int32_t head_dim, int32_t kv_layout,
+    const void* block_tables, int32_t table_dtype, int32_t max_pages, const int32_t* seq_lens,
+    int32_t batch_size, bool sparse, const int32_t* selected, const int32_t* num_selected,
+    int32_t max_selected, const float* k_scale, const float* v_scale, float sm_scale,
+    float soft_cap, int32_t window_left, void* out, float* lse, int32_t* dev_status,
+    void* workspace, int64_t workspace_bytes, void* stream) {
+  const std::string f(fn);
+  if (nvfp4_status st = check_geometry(fn, page_size, num_kv_heads, head_dim, kv_layout)) return st;
+  if (nvfp4_status st = check_dtype(f, dtype)) return st;
+  if (nvfp4_status st = check_query_heads(f, num_qo_heads, num_kv_heads)) return st;
+  if (head_dim > kAttnMaxHeadDim) return fail(NVFP4_ERR_UNSUPPORTED, f + ": head_dim above 256");
+  if (nvfp4_status st = check_tables(f, table_dtype, max_pages, batch_size)) return st;
+  if (sparse && max_selected < 1) return fail(NVFP4_ERR_INVALID_ARG, f + ": max_selected must be >= 1");
+  if (!std::isfinite(sm_scale)) return fail(NVFP4_ERR_INVALID_ARG, f + ": sm_scale must be finite");
+  if (!(std::isfinite(soft_cap) && soft_cap >= 0.0f))
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": logits_soft_cap must be finite and >= 0");
+  if (nvfp4_status st = check_cache(fn, "k_cache", k_cache, page_size, num_kv_heads, head_dim)) return st;
+  if (nvfp4_status st = check_cache(fn, "v_cache", v_cache, page_size, num_kv_heads, head_dim)) return st;
+  if (batch_size == 0) return NVFP4_OK;
+  const int64_t row = static_cast<int64_t>(num_qo_heads) * head_dim;
+  if (nvfp4_status st = check_rows(f, "query", query, query_row_stride, row)) return st;
+  if (nvfp4_status st = check_rows(f, "out", out, row, row)) return st;
+  if (!seq_lens || !k_scale || !v_scale || (!block_tables && max_pages > 0) ||
+      (sparse && (!selected || !num_selected)))
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": null device pointer");
+  if (!aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(lse, 4))
+    return fail(NVFP4_ERR_ALIGNMENT, f + ": scales and lse must be 4-byte aligned");
+  const int64_t need = attention_workspace_bytes(num_qo_heads, num_kv_heads, head_dim);
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": the workspace is smaller than nvfp4_paged_attention_workspace_bytes");
+  if (!aligned(workspace, 16)) return fail(NVFP4_ERR_ALIGNMENT, f + ": workspace must be 16-byte aligned");
+  AttentionArgs a{};
+  a.q = static_cast<const uint8_t*>(query);
+  a.q_row_bytes = query_row_stride * 2;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.ps = page_size;
+  a.Hq = num_qo_heads;
+  a.H = num_kv_heads;
+  a.G = num_qo_heads / num_kv_heads;
+  a.D = head_dim;
+  a.layout = kv_layout;
+  a.B = batch_size;
+  a.bf16 = dtype == NVFP4_BF16;
+  a.table64 = table_dtype == NVFP4_I64;
+  a.div_ps = make_div(page_size);
+  a.block_tables = block_tables;
+  a.max_pages = max_pages;
+  a.seq_lens = seq_lens;
+  a.selected = sparse ? selected : nullptr;
+  a.num_selected = num_selected;
+  a.max_selected = max_selected;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.sm_scale = sm_scale;
+  a.soft_cap = soft_cap;
+  a.window_left = window_left;
+  a.out = static_cast<uint8_t*>(out);
+  a.lse = lse;
+  a.status = dev_status;
+  a.workspace = workspace;
+  return launch_attention(a, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+NVFP4_EXPORT nvfp4_status nvfp4_paged_attention_decode(
+    const void* query, int32_t dtype, int64_t query_row_stride, int32_t num_qo_heads,
+    nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache, int32_t page_size,
+    int32_t num_kv_heads, int32_t head_dim, int32_t kv_layout, const void* block_tables,
+    int32_t table_dtype, int32_t max_pages_per_request, const int32_t* seq_lens,
+    int32_t batch_size, const float* k_scale, const float* v_scale, float sm_scale,
+    float logits_soft_cap, int32_t window_left, void* out, float* lse, int32_t* dev_status,
+    void* workspace, int64_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    return attention_impl("nvfp4_paged_attention_decode", query, dtype, query_row_stride,
+                          num_qo_heads, k_cache, v_cache, page_size, num_kv_heads, head_dim,
+                          kv_layout, block_tables, table_dtype, max_pages_per_request, seq_lens,
+                          batch_size, false, nullptr, nullptr, 0, k_scale, v_scale, sm_scale,
+                          logits_soft_cap, window_left, out, lse, dev_status, workspace,
+                          workspace_bytes, stream);
+  });
+}
+
+NVFP4_EXPORT nvfp4_status nvfp4_sparse_paged_attention_decode(
+    const void* query, int32_t dtype, int64_t query_row_stride, int32_t num_qo_heads,
+    nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache, int32_t page_size,
+    int32_t num_kv_heads, int32_t head_dim, int32_t kv_layout, const void* block_tables,
+    int32_t table_dtype, int32_t max_pages_per_request, const int32_t* seq_lens,
+    int32_t batch_size, const int32_t* selected_pages, const int32_t* num_selected,
+    int32_t max_selected, const float* k_scale, const float* v_scale, float sm_scale,
+    float logits_soft_cap, void* out, float* lse, int32_t* dev_status, void* workspace,
+    int64_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    return attention_impl("nvfp4_sparse_paged_attention_decode", query, dtype, query_row_stride,
+                          num_qo_heads, k_cache, v_cache, page_size, num_kv_heads, head_dim,
+                          kv_layout, block_tables, table_dtype, max_pages_per_request, seq_lens,
+                          batch_size, true, selected_pages, num_selected, max_selected, k_scale,
+                          v_scale, sm_scale, logits_soft_cap, -1, out, lse, dev_status,
+                          workspace, workspace_bytes, stream);
+  });
 }
 
 }  // extern "C"

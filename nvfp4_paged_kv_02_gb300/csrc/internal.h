@@ -70,6 +70,26 @@ struct AppendArgs {
 nvfp4_status launch_append(const AppendArgs& a, bool bf16, int mode, bool vec256,
                            cudaStream_t stream);
 
+// ---- norm, rotation and append -----------------------------------------------------------
+struct NormRopeArgs {
+  AppendArgs ap;  // the key and value rows and where they go
+  const uint8_t* q;
+  int64_t q_row_bytes;
+  uint8_t* q_out;
+  int64_t q_out_row_bytes;
+  int32_t Hq;
+  Div div_rows;  // query, key and value rows of a token
+  const uint8_t* q_weight;  // null: that tensor is not normalized
+  const uint8_t* k_weight;
+  float eps, inv_d;
+  const float* cos_sin;  // [num_positions, rotary_dim]
+  int64_t num_positions;
+  int32_t rotary_dim, interleaved;
+  int32_t log2_T;  // lanes of a row
+};
+nvfp4_status launch_norm_rope_append(const NormRopeArgs& a, bool bf16, int mode,
+                                     cudaStream_t stream);
+
 // ---- dequantize --------------------------------------------------------------------------
 struct DequantArgs {
   nvfp4_paged_cache kc, vc;
