@@ -1009,6 +1009,8 @@ nvfp4_status attention_impl(
   if (head_dim > kAttnMaxHeadDim) return fail(NVFP4_ERR_UNSUPPORTED, f + ": head_dim above 256");
   if (nvfp4_status st = check_tables(f, table_dtype, max_pages, batch_size)) return st;
   if (sparse && max_selected < 1) return fail(NVFP4_ERR_INVALID_ARG, f + ": max_selected must be >= 1");
+  if (sparse && static_cast<int64_t>(max_selected) * page_size > (int64_t(1) << 30))
+    return fail(NVFP4_ERR_UNSUPPORTED, f + ": max_selected * page_size above 2^30");
   if (!std::isfinite(sm_scale)) return fail(NVFP4_ERR_INVALID_ARG, f + ": sm_scale must be finite");
   if (!(std::isfinite(soft_cap) && soft_cap >= 0.0f))
     return fail(NVFP4_ERR_INVALID_ARG, f + ": logits_soft_cap must be finite and >= 0");

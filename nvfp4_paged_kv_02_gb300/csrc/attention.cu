@@ -4,135 +4,855 @@
 //   x_t = sm_scale * gs_k * sum_d q[d] (e2m1 * S)_K[t, d]      (soft cap c: c tanh(x_t / c))
 //   out = gs_v * sum_t exp(x_t - m) (e2m1 * S)_V[t, :] / l,    m = max x_t, l = sum exp(x_t - m)
 //   lse = m + log(l)
-// in one pass with a running maximum and sum; statistics and sums are binary32, e2m1 * S is
-// exact. No live token: out = 0, lse = -inf.
+// in one pass with a running maximum and sum. No live token: out = 0, lse = -inf.
+//
+// What bounds it is reading the cache: 9/8 byte for an element of K and of V together, against
+// 4 G operations, so at the measured copy bandwidth an SM has to take in about 42 elements a
+// clock. A tile that goes through shared memory as binary16 for tcgen05.mma would have to be
+// decoded to registers and written back first; mma.sync takes the decoded registers as they
+// are, and its 1024 multiply-adds a clock and SM (measured) are three times what G <= 8 needs.
+// The budget is instructions: about 3 a lane and element, of which decoding, scaling and
+// multiplying take 1.7.
+//
+// Work. A unit is 32 tokens of one (request, KV head, chunk of up to 8 NT query heads). All
+// units of a launch, in that order, are cut into equal runs, one for each CTA, so that ragged
+// lengths balance and one long request fills the GPU; the lengths are read on the device. In a
+// run, the four warps take the units of a segment (request, head, chunk) in turn and are joined
+// in shared memory at its end. A segment that several CTAs share is joined by the last of them
+// to finish (a counter), always in the order of the runs: results do not depend on timing.
+//
+// A warp's units come through its own ring of stages (cp.async, no barrier with other warps).
+// Rows that are not live are zero-filled, never read, and masked.
+//
+// Scores. S^T = K Q^T by m16n8k16: A is K (16 tokens), B is Q^T (8 heads). Lane (r, c) = (lane
+// / 4, lane % 4) holds elements 16 NW c .. 16 NW (c + 1) of its two rows; Q is laid out to
+// match (any order of d serves, as long as both have it). e2m1 * S is exact in binary16. A
+// query row is scaled by a power of two, so that its largest element is in [2^14, 2^15), and
+// is then exact in binary16 down to 2^-38 of that element.
+// Weights. p = 2^(x log2 e - m + 15), at most 2^15, rounded to binary16 (2^-11 relative, down
+// to 2^-29 of the largest weight) for the second product; their sum is binary32.
+// Output. O^T = V^T P^T: A is V^T (16 of d), B is P^T, which movmatrix makes of S^T. A
+// fragment pairs tokens, codes pair elements of d, so nibbles of two tokens are interleaved
+// before they are decoded.
 #include "attention.h"
 
 #include <cfloat>
+#include <type_traits>
 
 namespace nvfp4 {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kMaxPerLane = kAttnMaxHeadDim / 64;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnit = 32;     // tokens
+constexpr int kMinUnits = 4;  // of a CTA's run: one for each warp
+constexpr int kMaxCtasPerSm = 4;
+constexpr float kWeightBias = 15.0f;
+constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float f32_of16(const uint8_t* p, bool bf16) {
-  const uint32_t w = *reinterpret_cast<const uint16_t*>(p);
-  return bf16 ? __uint_as_float(w << 16) : f32_from_f16_lo(w);
+// ---- instructions ------------------------------------------------------------------------
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool live) {
+  const int n = live ? BYTES : 0;  // 0: nothing is read, the destination is zero-filled
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ float2 code_pair(uint32_t byte, float s) {
-  uint32_t h[4];
-  f16x2x4_from_e2m1x8(byte, h[0], h[1], h[2], h[3]);
-  return make_float2(f32_from_f16_lo(h[0]) * s, f32_from_f16_hi(h[0]) * s);
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float scale_of(uint32_t byte) {
-  return f32_from_f16_lo(f16x2_from_e4m3x2(byte));
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 
-// One warp for each (request, query head); its lanes share the head dimension.
-__global__ void __launch_bounds__(kWarps * 32) attention_kernel(const AttentionArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (item >= static_cast<int64_t>(a.B) * a.Hq) return;
-  const int32_t b = static_cast<int32_t>(item / a.Hq), hq = static_cast<int32_t>(item % a.Hq);
-  const int32_t h = hq / a.G, nbytes = a.D / 2;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// c tanh(x / c) by 1 - 2 / (e^(2x/c) + 1): absolute error a few 2^-24 of c.
+__device__ __forceinline__ float soft_capped(float x, float cap) {
+  const float e = ex2(x / cap * (2.0f * kLog2e));
+  return cap * (1.0f - 2.0f / (e + 1.0f));
+}
+
+// ---- which units ---------------------------------------------------------------------------
+
+// The live range of request b: tokens [lo, len).
+struct Span {
+  int32_t lo, len;
+};
+__device__ __forceinline__ Span span_of(const AttentionArgs& a, int32_t b) {
   const int64_t reach = a.max_pages * a.ps;
-  int64_t len = __ldg(a.seq_lens + b);
-  if (len > reach) {
-    if (lane == 0) flag(a.status, NVFP4_DEV_LEN_CLAMPED);
-    len = reach;
-  }
-  const int64_t lo = a.window_left >= 0 ? max(int64_t(0), len - 1 - a.window_left) : 0;
-  int64_t n = len;  // positions walked: tokens, or slots of the selected pages
-  if (a.selected) n = static_cast<int64_t>(min(max(__ldg(a.num_selected + b * a.H + h), 0), a.max_selected)) * a.ps;
-
-  float q[2 * kMaxPerLane], o[2 * kMaxPerLane], m = -INFINITY, l = 0.0f;
-  for (int u = 0; u < kMaxPerLane; ++u) {
-    const int byte = lane + 32 * u;
-    const uint8_t* p = a.q + b * a.q_row_bytes + (static_cast<int64_t>(hq) * a.D + 2 * byte) * 2;
-    q[2 * u] = byte < nbytes ? f32_of16(p, a.bf16) : 0.0f;
-    q[2 * u + 1] = byte < nbytes ? f32_of16(p + 2, a.bf16) : 0.0f;
-    o[2 * u] = o[2 * u + 1] = 0.0f;
-  }
-  // the query's power of two moves into the scale, so that no product overflows
-  float top = 0.0f;
-  for (int u = 0; u < 2 * kMaxPerLane; ++u) top = fmaxf(top, fabsf(q[u]));
-  for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
-  const int e = top > 0.0f && top < INFINITY ? ilogbf(top) : 0;
-  for (int u = 0; u < 2 * kMaxPerLane; ++u) q[u] = ldexpf(q[u], -e);
-  const float scale = ldexpf(a.sm_scale, e) * __ldg(a.k_scale);
-  for (int64_t i = a.selected ? 0 : lo; i < n; ++i) {
-    int64_t col = i / a.ps, t = i;
-    const int32_t slot = static_cast<int32_t>(i - col * a.ps);
-    if (a.selected) {
-      col = __ldg(a.selected + (static_cast<int64_t>(b) * a.H + h) * a.max_selected + col);
-      if (col < 0 || col >= a.max_pages) {
-        if (lane == 0) flag(a.status, NVFP4_DEV_BAD_PAGE);
-        continue;
-      }
-      t = col * a.ps + slot;
-    }
-    if (t >= len) continue;
-    const int64_t at = b * a.max_pages + col;
-    const int64_t page = a.table64 ? reinterpret_cast<const int64_t*>(a.block_tables)[at]
-                                   : reinterpret_cast<const int32_t*>(a.block_tables)[at];
-    if (page < 0 || page >= a.kc.num_pages || page >= a.vc.num_pages) {
-      if (lane == 0) flag(a.status, NVFP4_DEV_BAD_PAGE);
-      continue;
-    }
-    const int64_t r = a.layout == NVFP4_NHD ? static_cast<int64_t>(slot) * a.H + h
-                                            : static_cast<int64_t>(h) * a.ps + slot;
-    const uint8_t* kd = a.kc.data + page * a.kc.data_page_stride + r * nbytes;
-    const uint8_t* ks = a.kc.sf + page * a.kc.sf_page_stride + r * (a.D / 16);
-    const uint8_t* vd = a.vc.data + page * a.vc.data_page_stride + r * nbytes;
-    const uint8_t* vs = a.vc.sf + page * a.vc.sf_page_stride + r * (a.D / 16);
-    float x = 0.0f;
-    for (int u = 0; u < kMaxPerLane; ++u) {
-      const int byte = lane + 32 * u;
-      if (byte < nbytes) {
-        const float2 k = code_pair(kd[byte], scale_of(ks[byte / 8]));
-        x += q[2 * u] * k.x + q[2 * u + 1] * k.y;
-      }
-    }
-    for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, s);
-    x *= scale;
-    if (a.soft_cap > 0.0f) x = a.soft_cap * tanhf(x / a.soft_cap);
-    const float m2 = fmaxf(m, x), f = m2 == -INFINITY ? 1.0f : __expf(m - m2);
-    const float p = m2 == -INFINITY ? 0.0f : __expf(x - m2);
-    m = m2;
-    l = l * f + p;
-    for (int u = 0; u < kMaxPerLane; ++u) {
-      const int byte = lane + 32 * u;
-      if (byte < nbytes) {
-        const float2 v = code_pair(vd[byte], scale_of(vs[byte / 8]));
-        o[2 * u] = o[2 * u] * f + p * v.x;
-        o[2 * u + 1] = o[2 * u + 1] * f + p * v.y;
-      }
-    }
-  }
-  const float inv = l == 0.0f ? 0.0f : __ldg(a.v_scale) / l;
-  for (int u = 0; u < kMaxPerLane; ++u) {
-    const int byte = lane + 32 * u;
-    if (byte < nbytes) {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + ((static_cast<int64_t>(b) * a.Hq + hq) * a.D + 2 * byte) * 2);
-      *dst = a.bf16 ? bf16x2_from_f32(o[2 * u] * inv, o[2 * u + 1] * inv)
-                    : f16x2_from_f32(o[2 * u] * inv, o[2 * u + 1] * inv);
-    }
-  }
-  if (a.lse && lane == 0) a.lse[static_cast<int64_t>(b) * a.Hq + hq] = l == 0.0f ? -INFINITY : m + logf(l);
+  const int32_t n = max(__ldg(a.seq_lens + b), 0);
+  Span s;
+  s.len = n > reach ? static_cast<int32_t>(reach) : n;
+  s.lo = a.window_left >= 0 ? max(0, s.len - 1 - a.window_left) : 0;
+  return s;
 }
+
+// Units of one (request, head): of its tokens, or of the slots of its selected pages.
+__device__ __forceinline__ int32_t units_of(const AttentionArgs& a, int32_t b, int32_t h) {
+  if (a.selected) {
+    const int32_t n = min(max(__ldg(a.num_selected + static_cast<int64_t>(b) * a.H + h), 0), a.max_selected);
+    return (n * a.ps + kUnit - 1) / kUnit;
+  }
+  const Span s = span_of(a, b);
+  return s.len > 0 ? (s.len - 1) / kUnit + 1 - s.lo / kUnit : 0;
+}
+
+__device__ __forceinline__ int64_t units_of_request(const AttentionArgs& a, int32_t b) {
+  int64_t n = 0;
+  if (a.selected) {
+    for (int32_t h = 0; h < a.H; ++h) n += units_of(a, b, h);
+  } else {
+    n = static_cast<int64_t>(units_of(a, b, 0)) * a.H;
+  }
+  return n * a.chunks;
+}
+
+// cum[b] = units of the requests up to b; every thread calls it, ends with a barrier.
+__device__ __forceinline__ void scan_units(const AttentionArgs& a, int64_t* cum, int64_t* s_warp) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int lo = tid * per, hi = min(a.B, lo + per);
+  int64_t local = 0;
+  for (int b = lo; b < hi; ++b) {
+    local += units_of_request(a, b);
+    cum[b] = local;
+  }
+  int64_t v = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  int64_t before = v - local;
+  for (int w = 0; w < warp; ++w) before += s_warp[w];
+  for (int b = lo; b < hi; ++b) cum[b] += before;
+  __syncthreads();
+}
+
+// One (request, head, chunk of query heads) and where its units are among all units.
+struct Segment {
+  int32_t b, h, chunk, units;
+  int64_t start;
+};
+
+__device__ __forceinline__ Segment find_segment(const AttentionArgs& a, const int64_t* cum, int64_t unit) {
+  int32_t lo = 0, hi = a.B - 1;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (cum[mid] > unit) hi = mid;
+    else lo = mid + 1;
+  }
+  Segment s{lo, 0, 0, 0, lo > 0 ? cum[lo - 1] : 0};
+  for (;;) {
+    s.units = units_of(a, s.b, s.h);
+    const int64_t head = static_cast<int64_t>(s.units) * a.chunks;
+    if (unit < s.start + head || s.h + 1 == a.H) break;
+    s.start += head;
+    ++s.h;
+  }
+  if (s.units > 0) s.chunk = static_cast<int32_t>((unit - s.start) / s.units);
+  s.start += static_cast<int64_t>(s.chunk) * s.units;
+  return s;
+}
+
+// The next segment that has units (the caller knows that there is one).
+__device__ __forceinline__ void next_segment(const AttentionArgs& a, Segment& s) {
+  s.start += s.units;
+  if (++s.chunk < a.chunks) return;
+  s.chunk = 0;
+  do {
+    if (++s.h == a.H) {
+      s.h = 0;
+      ++s.b;
+    }
+    s.units = s.b < a.B ? units_of(a, s.b, s.h) : 1;
+  } while (s.units == 0);
+}
+
+// ---- one warp's stages ---------------------------------------------------------------------
+
+// Physical order of eight tokens in a fragment. With it and the swizzle below, the reads of K
+// (rows by lane / 4) and of V (rows by 2 (lane % 4)) both touch every bank once.
+__device__ __forceinline__ int token_of(int k) { return k < 4 ? k : k ^ 1; }
+
+template <int NW>
+struct Tile {
+  static constexpr int kRow = 32 * NW;       // bytes of a row of codes, D rounded up to 64 NW
+  static constexpr int kScales = 4 * NW;     // bytes of its scales
+  static constexpr int kV = kUnit * kRow;    // V's codes
+  static constexpr int kKs = 2 * kUnit * kRow;
+  static constexpr int kVs = kKs + kUnit * kScales;
+  static constexpr int kMask = kVs + kUnit * kScales;
+  static constexpr int kBytes = (kMask + 4 + 15) / 16 * 16;
+  // 16-byte chunks of row t are exchanged so that a fragment's rows spread over the banks
+  __host__ __device__ static constexpr int swizzle(int t) { return NW == 2 ? t & 2 : (NW == 4 ? t & 7 : 0); }
+};
+
+constexpr int kStages = 3;
+
+// The codes of this lane's block of 16 elements, scaled: eight pairs.
+__device__ __forceinline__ void decode16(uint32_t w0, uint32_t w1, uint32_t S2, uint32_t v[8]) {
+  f16x2x4_from_e2m1x8(w0, v[0], v[1], v[2], v[3]);
+  f16x2x4_from_e2m1x8(w1, v[4], v[5], v[6], v[7]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = hmul2_rn(v[i], S2);
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+
+// ---- the kernel ------------------------------------------------------------------------------
+
+// NW: words of codes that a lane holds of a V row (D <= 64 NW). NT: eights of query heads.
+// FULL: D = 64 NW and scale rows that cp.async can copy; otherwise any D, and scales of any
+// alignment, which go through registers.
+template <int NW, int NT, bool FULL>
+__global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs a) {
+  using T = Tile<NW>;
+  constexpr int NS = kStages;
+  constexpr int kHeads = 8 * NT;
+  constexpr int kPitch = 64 * NW + 4;  // floats of a row of O in shared memory
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t s_scan[kWarps];
+  __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads], s_f[kWarps][kHeads], s_top[kHeads], s_sum[kHeads];
+  __shared__ int s_last;
+  float* s_o = reinterpret_cast<float*>(smem + kWarps * NS * T::kBytes);  // [kWarps][kHeads][kPitch]
+  int64_t* cum = reinterpret_cast<int64_t*>(s_o + kWarps * kHeads * kPitch);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane >> 2, c = lane & 3;
+  const int D = FULL ? 64 * NW : a.D;
+  scan_units(a, cum, s_scan);
+
+  // heads without live tokens: zeros
+  for (int32_t b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const int64_t reach = a.max_pages * a.ps;
+    if (tid == 0 && __ldg(a.seq_lens + b) > reach) flag(a.status, NVFP4_DEV_LEN_CLAMPED);
+    if (!a.selected && units_of(a, b, 0) > 0) continue;
+    for (int32_t h = 0; h < a.H; ++h) {
+      if (units_of(a, b, h) > 0) continue;
+      const int64_t row = static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(h) * a.G;
+      uint2* o = reinterpret_cast<uint2*>(a.out + row * D * 2);
+      for (int i = tid; i < a.G * D / 4; i += kThreads) o[i] = make_uint2(0, 0);
+      for (int i = tid; i < a.G && a.lse; i += kThreads) a.lse[row + i] = -INFINITY;
+    }
+  }
+
+  const int64_t total = cum[a.B - 1];
+  const int64_t want = (total + kMinUnits - 1) / kMinUnits;
+  const int64_t ncta = want < gridDim.x ? want : gridDim.x;
+  if (blockIdx.x >= ncta) return;
+  const int64_t c0 = total * blockIdx.x / ncta, c1 = total * (blockIdx.x + 1) / ncta;
+
+  const uint32_t ring = smem_addr(smem) + warp * NS * T::kBytes;
+  uint8_t* const ring_p = smem + warp * NS * T::kBytes;
+  if (!FULL) {
+    // what lies between D and 64 NW stays zero: no copy writes there
+    for (int i = lane; i < NS * T::kBytes / 16; i += 32) reinterpret_cast<uint4*>(ring_p)[i] = uint4{};
+    __syncwarp();
+  }
+
+  // -- the producer: this warp's units, one looked up ahead of its copies --
+  Segment ps = find_segment(a, cum, c0);
+  Segment cs = ps;  // the consumer's
+  auto portion = [&](const Segment& s, int32_t& u, int32_t& end) {
+    u = static_cast<int32_t>(max(c0 - s.start, int64_t(0)));
+    end = static_cast<int32_t>(min(c1 - s.start, static_cast<int64_t>(s.units)));
+  };
+  int32_t pu, pend;
+  portion(ps, pu, pend);
+  pu += warp;
+  auto settle = [&] {  // to a unit of this warp, or past the run's end (pu >= pend)
+    while (pu >= pend && ps.start + ps.units < c1) {
+      next_segment(a, ps);
+      portion(ps, pu, pend);
+      pu += warp;
+    }
+  };
+  settle();
+  int32_t lk_page = -1, lk_row = 0;  // this lane's row of the unit looked up
+  bool lk_unit = false;
+  auto look_up = [&] {
+    lk_page = -1;
+    lk_unit = pu < pend;
+    if (!lk_unit) return;
+    const Span sp = span_of(a, ps.b);
+    int64_t col;
+    int32_t slot;
+    bool live;
+    if (a.selected) {
+      const int64_t list = static_cast<int64_t>(ps.b) * a.H + ps.h;
+      const int32_t p = pu * kUnit + lane;
+      const int32_t i = static_cast<int32_t>(div_q32(p, a.div_ps));
+      slot = p - i * a.ps;
+      live = i < min(__ldg(a.num_selected + list), a.max_selected);
+      col = live ? __ldg(a.selected + list * a.max_selected + i) : 0;
+      if (col < 0 || col >= a.max_pages) {
+        flag(a.status, NVFP4_DEV_BAD_PAGE);
+        live = false;
+      }
+      live = live && col * a.ps + slot < sp.len;
+    } else {
+      const int64_t t = (static_cast<int64_t>(sp.lo / kUnit) + pu) * kUnit + lane;
+      live = t >= sp.lo && t < sp.len;
+      col = live ? div_q32(static_cast<int32_t>(t), a.div_ps) : 0;
+      slot = static_cast<int32_t>(t - col * a.ps);
+    }
+    if (live) {
+      const int64_t at = ps.b * a.max_pages + col;
+      const int64_t page = a.table64 ? __ldg(static_cast<const int64_t*>(a.block_tables) + at)
+                                     : __ldg(static_cast<const int32_t*>(a.block_tables) + at);
+      lk_row = a.layout == NVFP4_NHD ? slot * a.H + ps.h : ps.h * a.ps + slot;
+      if (page >= 0 && page < a.pool_pages) lk_page = static_cast<int32_t>(page);
+      else flag(a.status, NVFP4_DEV_BAD_PAGE);
+    }
+  };
+  look_up();
+
+  // !FULL: scale bytes on their way to the stage of the unit issued last
+  uint32_t pk[4], pv[4];
+  int pend_stage = -1;
+  const int nb = D / 16;
+  auto put_scales = [&] {
+    if (FULL || pend_stage < 0) return;
+    uint8_t* st = ring_p + pend_stage * T::kBytes;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      *reinterpret_cast<uint32_t*>(st + T::kKs + lane * T::kScales + 4 * i) = pk[i];
+      *reinterpret_cast<uint32_t*>(st + T::kVs + lane * T::kScales + 4 * i) = pv[i];
+    }
+  };
+  // Copies of the unit looked up into stage s, then the look-up of the next one.
+  auto issue = [&](int s) {
+    if (!FULL) put_scales();
+    if (lk_unit) {
+      const uint32_t st = ring + s * T::kBytes;
+      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, lk_page >= 0);
+      if (lane == 0) *reinterpret_cast<uint32_t*>(ring_p + s * T::kBytes + T::kMask) = mask;
+      const bool live = lk_page >= 0;
+      const int64_t page = live ? lk_page : 0;
+      const uint8_t* ks = a.kc.sf + page * a.kc.sf_page_stride + static_cast<int64_t>(live ? lk_row : 0) * nb;
+      const uint8_t* vs = a.vc.sf + page * a.vc.sf_page_stride + static_cast<int64_t>(live ? lk_row : 0) * nb;
+      const uint32_t ksd = st + T::kKs + lane * T::kScales, vsd = st + T::kVs + lane * T::kScales;
+      if (FULL) {
+        constexpr int kPart = NW == 3 ? 4 : 4 * NW;
+#pragma unroll
+        for (int i = 0; i < T::kScales / kPart; ++i) {
+          cp_async<kPart>(ksd + i * kPart, ks + i * kPart, live);
+          cp_async<kPart>(vsd + i * kPart, vs + i * kPart, live);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NW; ++i) pk[i] = pv[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 4 * NW; ++i) {
+          if (live && i < nb) {
+            pk[i / 4] |= static_cast<uint32_t>(__ldg(ks + i)) << (8 * (i % 4));
+            pv[i / 4] |= static_cast<uint32_t>(__ldg(vs + i)) << (8 * (i % 4));
+          }
+        }
+        pend_stage = s;
+      }
+      auto row_copy = [&](int row, int off, auto bytes) {
+        constexpr int B = decltype(bytes)::value;
+        const int32_t pg = __shfl_sync(0xFFFFFFFFu, lk_page, row);
+        const int32_t rw = __shfl_sync(0xFFFFFFFFu, lk_row, row);
+        const bool ok = pg >= 0;
+        const int64_t in = static_cast<int64_t>(ok ? rw : 0) * (D / 2) + off;
+        const int64_t p = ok ? pg : 0;
+        const uint32_t dst = st + row * T::kRow + (((off >> 4) ^ T::swizzle(row)) << 4) + (off & 15);
+        cp_async<B>(dst, a.kc.data + p * a.kc.data_page_stride + in, ok);
+        cp_async<B>(dst + T::kV, a.vc.data + p * a.vc.data_page_stride + in, ok);
+      };
+      if (FULL) {
+        constexpr int kChunks = 2 * NW;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int k = i * 32 + lane;
+          row_copy(k / kChunks, k % kChunks * 16, std::integral_constant<int, 16>{});
+        }
+      } else {
+        const int chunks = D / 16;  // of 8 bytes
+        for (int i = 0; i < chunks; ++i) {
+          const int k = i * 32 + lane;
+          row_copy(k / chunks, k % chunks * 8, std::integral_constant<int, 8>{});
+        }
+      }
+      pu += kWarps;
+      settle();
+      look_up();
+    } else {
+      pend_stage = -1;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < NS - 1; ++s) issue(s);
+
+  // -- the consumer --
+  const float gk = __ldg(a.k_scale), gv = __ldg(a.v_scale);
+  const int t0 = token_of(r);                    // this lane's K rows: t0 and t0 + 8
+  const int v0 = token_of(2 * c), v1 = token_of(2 * c + 1);  // its V rows, and 8 more
+  int stage = 0, refill = NS - 1;
+  for (;;) {
+    // the segment's query heads
+    const int head0 = cs.chunk * a.chunk_heads;
+    const int heads = min(a.chunk_heads, a.G - head0);
+    const int64_t q_row = static_cast<int64_t>(cs.h) * a.G + head0;
+    uint32_t qf[NT][4 * NW][2];
+    float factor[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int head = 8 * nt + r;
+      const uint8_t* q = a.q + cs.b * a.q_row_bytes + ((q_row + head) * D + 16 * NW * c) * 2;
+      float top = 0.0f;
+      uint32_t w[8 * NW];
+#pragma unroll
+      for (int i = 0; i < 2 * NW; ++i) {
+        const bool in = head < heads && 16 * NW * c + 8 * i < D;
+        const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(q) + i) : uint4{};
+        w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 8 * NW; ++i) {
+        const float lo = a.bf16 ? __uint_as_float(w[i] << 16) : f32_from_f16_lo(w[i]);
+        const float hi = a.bf16 ? f32_from_bf16_hi(w[i]) : f32_from_f16_hi(w[i]);
+        top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      const int e = top > 0.0f && top <= FLT_MAX ? ilogbf(top) - 14 : 0;
+      // 2^-e as two factors: it may be out of range by itself
+      const float f1 = __int_as_float((127 - e / 2) << 23), f2 = __int_as_float((127 - (e - e / 2)) << 23);
+#pragma unroll
+      for (int i = 0; i < 8 * NW; ++i) {
+        const float lo = a.bf16 ? __uint_as_float(w[i] << 16) : f32_from_f16_lo(w[i]);
+        const float hi = a.bf16 ? f32_from_bf16_hi(w[i]) : f32_from_f16_hi(w[i]);
+        qf[nt][i >> 1][i & 1] = f16x2_from_f32(lo * f1 * f2, hi * f1 * f2);
+      }
+      const float f = ldexpf(a.sm_scale, e) * gk;
+      factor[nt][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * c);
+      factor[nt][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * c + 4);
+      if (a.soft_cap == 0.0f) {
+        factor[nt][0] *= kLog2e;
+        factor[nt][1] *= kLog2e;
+      }
+    }
+    float o[NT][NW][4][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[nt][w][i][k] = 0.0f;
+    }
+
+    int32_t cu, cend;
+    portion(cs, cu, cend);
+    const bool whole = cu == 0 && cend == cs.units;
+    for (cu += warp; cu < cend; cu += kWarps) {
+      cp_async_wait<NS - 2>();
+      __syncwarp();
+      issue(refill);
+      const uint8_t* st = ring_p + stage * T::kBytes;
+      refill = stage;
+      stage = stage + 1 == NS ? 0 : stage + 1;
+      const uint32_t mask = *reinterpret_cast<const uint32_t*>(st + T::kMask);
+
+      float x[2][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[mt][nt][k] = 0.0f;
+        // rows t0 + 16 mt and + 8: 8 NW bytes each, NW scales each
+        uint32_t kw[2][2 * NW], S2[2][NW];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int t = 16 * mt + 8 * p + t0;
+          const uint8_t* row = st + t * T::kRow;
+          const uint8_t* sr = st + T::kKs + t * T::kScales + NW * c;
+          if (NW == 1) {
+            const uint2 v = *reinterpret_cast<const uint2*>(row + 8 * c);
+            kw[p][0] = v.x; kw[p][1] = v.y;
+            const uint32_t s = *sr;
+            S2[p][0] = f16x2_from_e4m3x2(s * 0x0101u);
+          } else if (NW == 3) {
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+              const uint2 v = *reinterpret_cast<const uint2*>(row + 8 * NW * c + 8 * i);
+              kw[p][2 * i] = v.x; kw[p][2 * i + 1] = v.y;
+              S2[p][i] = f16x2_from_e4m3x2(static_cast<uint32_t>(sr[i]) * 0x0101u);
+            }
+          } else {
+            const uint32_t s = NW == 2 ? static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sr))
+                                       : *reinterpret_cast<const uint32_t*>(sr);
+#pragma unroll
+            for (int i = 0; i < NW / 2; ++i) {
+              const uint4 v = *reinterpret_cast<const uint4*>(row + (((NW / 2 * c + i) ^ T::swizzle(t)) << 4));
+              kw[p][4 * i] = v.x; kw[p][4 * i + 1] = v.y; kw[p][4 * i + 2] = v.z; kw[p][4 * i + 3] = v.w;
+              const uint32_t s2 = f16x2_from_e4m3x2(i == 0 ? s : s >> 16);
+              S2[p][2 * i] = prmt(s2, 0u, 0x1010u);
+              S2[p][2 * i + 1] = prmt(s2, 0u, 0x3232u);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+          uint32_t k0[8], k1[8];
+          decode16(kw[0][2 * i], kw[0][2 * i + 1], S2[0][i], k0);
+          decode16(kw[1][2 * i], kw[1][2 * i + 1], S2[1][i], k1);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t f[4] = {k0[2 * j], k1[2 * j], k0[2 * j + 1], k1[2 * j + 1]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(x[mt][nt], f, qf[nt][4 * i + j][0], qf[nt][4 * i + j][1]);
+          }
+        }
+      }
+      // x[mt][nt][2 p + k]: token 16 mt + 8 p + t0, head 8 nt + 2 c + k
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float v = x[mt][nt][k] * factor[nt][k & 1];
+            if (a.soft_cap > 0.0f) v = soft_capped(v, a.soft_cap) * kLog2e;
+            x[mt][nt][k] = v;
+          }
+      if (mask != 0xFFFFFFFFu) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            if (!(mask >> (16 * mt + 8 * p + t0) & 1u)) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) x[mt][nt][2 * p] = x[mt][nt][2 * p + 1] = -INFINITY;
+            }
+      }
+      bool grew = false;
+      float top[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float v = fmaxf(fmaxf(x[0][nt][k], x[0][nt][k + 2]), fmaxf(x[1][nt][k], x[1][nt][k + 2]));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+          top[nt][k] = v;
+          grew = grew || v > m[nt][k];
+        }
+      if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float m2 = fmaxf(m[nt][k], top[nt][k]);
+            const float f = m2 == -INFINITY ? 1.0f : ex2(m[nt][k] - m2);
+            m[nt][k] = m2;
+            l[nt][k] *= f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[nt][w][i][k] *= f;
+                o[nt][w][i][k + 2] *= f;
+              }
+          }
+      }
+      uint32_t pb[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float off0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0] - kWeightBias;
+        const float off1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1] - kWeightBias;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const float p0 = ex2(x[mt][nt][2 * p] - off0), p1 = ex2(x[mt][nt][2 * p + 1] - off1);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            pb[mt][nt][p] = transpose8x8(f16x2_from_f32(p0, p1));
+          }
+      }
+      // V: tokens v0, v1 (k = 2c, 2c + 1) and 8 more, words NW r .. of each row
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t vw[4][NW], S01[NW], S23[NW];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const int t = 16 * mt + (p >= 2 ? 8 : 0) + ((p & 1) ? v1 : v0);
+          const uint8_t* row = st + T::kV + t * T::kRow;
+          if (NW == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(row + (((r >> 1) ^ T::swizzle(t)) << 4) + 8 * (r & 1));
+            vw[p][0] = v.x; vw[p][1 % NW] = v.y;
+          } else if (NW == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(row + ((r ^ T::swizzle(t)) << 4));
+            vw[p][0] = v.x; vw[p][1 % NW] = v.y; vw[p][2 % NW] = v.z; vw[p][3 % NW] = v.w;
+          } else {
+#pragma unroll
+            for (int w = 0; w < NW; ++w) vw[p][w] = *reinterpret_cast<const uint32_t*>(row + 4 * (NW * r + w));
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          if ((NW == 2 || NW == 4) && (w & 1)) {  // two words to a block
+            S01[w] = S01[w - 1 < 0 ? 0 : w - 1];
+            S23[w] = S23[w - 1 < 0 ? 0 : w - 1];
+            continue;
+          }
+          const uint8_t* sr = st + T::kVs + 16 * mt * T::kScales + ((NW * r + w) >> 1);
+          const uint32_t s0 = sr[v0 * T::kScales], s1 = sr[v1 * T::kScales];
+          const uint32_t s2 = sr[(v0 + 8) * T::kScales], s3 = sr[(v1 + 8) * T::kScales];
+          S01[w] = f16x2_from_e4m3x2(s0 | (s1 << 8));
+          S23[w] = f16x2_from_e4m3x2(s2 | (s3 << 8));
+        }
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          constexpr uint32_t kLow = 0x0F0F0F0Fu;
+          uint32_t x01[4], y01[4], x23[4], y23[4];
+          const uint32_t e01 = (vw[0][w] & kLow) | ((vw[1][w] << 4) & ~kLow);
+          const uint32_t o01 = ((vw[0][w] >> 4) & kLow) | (vw[1][w] & ~kLow);
+          const uint32_t e23 = (vw[2][w] & kLow) | ((vw[3][w] << 4) & ~kLow);
+          const uint32_t o23 = ((vw[2][w] >> 4) & kLow) | (vw[3][w] & ~kLow);
+          f16x2x4_from_e2m1x8(e01, x01[0], x01[1], x01[2], x01[3]);
+          f16x2x4_from_e2m1x8(o01, y01[0], y01[1], y01[2], y01[3]);
+          f16x2x4_from_e2m1x8(e23, x23[0], x23[1], x23[2], x23[3]);
+          f16x2x4_from_e2m1x8(o23, y23[0], y23[1], y23[2], y23[3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t f[4] = {hmul2_rn(x01[i], S01[w]), hmul2_rn(y01[i], S01[w]),
+                                   hmul2_rn(x23[i], S23[w]), hmul2_rn(y23[i], S23[w])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][w][i], f, pb[mt][nt][0], pb[mt][nt][1]);
+          }
+        }
+      }
+    }
+
+    // -- the four warps' parts, joined --
+    // o[nt][w][i][k], [k + 2]: head 8 nt + 2 c + k, d = 8 (NW r + w) + 2 i, + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float s = l[nt][k];
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 4);
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+        const int head = 8 * nt + 2 * c + k;
+        if (r == 0) {
+          s_m[warp][head] = m[nt][k];
+          s_l[warp][head] = s;
+        }
+        float4* dst = reinterpret_cast<float4*>(s_o + (warp * kHeads + head) * kPitch + 8 * NW * r);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          dst[2 * w] = make_float4(o[nt][w][0][k], o[nt][w][0][k + 2], o[nt][w][1][k], o[nt][w][1][k + 2]);
+          dst[2 * w + 1] = make_float4(o[nt][w][2][k], o[nt][w][2][k + 2], o[nt][w][3][k], o[nt][w][3][k + 2]);
+        }
+      }
+    __syncthreads();
+    // factors of the four parts and the joined maximum and sum, by the first threads
+    auto join_stats = [&] {
+      if (tid < kHeads) {
+        float M = -INFINITY, L = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][tid]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = s_m[w][tid] == -INFINITY ? 0.0f : ex2(s_m[w][tid] - M);
+          s_f[w][tid] = f;
+          L += f * s_l[w][tid];
+        }
+        s_top[tid] = M;
+        s_sum[tid] = L;
+      }
+      __syncthreads();
+    };
+    auto joined = [&](int head, int d) {
+      float4 v{0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kHeads + head) * kPitch + d);
+        const float f = s_f[w][head];
+        v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
+      }
+      return v;
+    };
+    auto write_out = [&] {
+      const int64_t row = static_cast<int64_t>(cs.b) * a.Hq + q_row;
+      for (int i = tid; i < heads * D / 4; i += kThreads) {
+        const int head = i / (D / 4), d = i % (D / 4) * 4;
+        const float4 v = joined(head, d);
+        const float f = s_sum[head] == 0.0f ? 0.0f : gv / s_sum[head];
+        uint2 w;
+        w.x = a.bf16 ? bf16x2_from_f32(v.x * f, v.y * f) : f16x2_from_f32(v.x * f, v.y * f);
+        w.y = a.bf16 ? bf16x2_from_f32(v.z * f, v.w * f) : f16x2_from_f32(v.z * f, v.w * f);
+        *reinterpret_cast<uint2*>(a.out + ((row + head) * D + d) * 2) = w;
+      }
+      if (a.lse && tid < heads)
+        a.lse[row + tid] = s_sum[tid] == 0.0f ? -INFINITY
+                                              : (s_top[tid] - kWeightBias) * (1.0f / kLog2e) + logf(s_sum[tid]);
+    };
+    join_stats();
+    if (whole) {
+      write_out();
+    } else {
+      // this run's part of a segment that others share; slot 0 of a CTA if the segment began before
+      // its run, else slot 1
+      constexpr int kSlot = kHeads * (64 * NW + 2);
+      float* const parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + NVFP4_COUNTER_BYTES);
+      const int64_t first = ((cs.start + 1) * ncta - 1) / total;
+      const int64_t last = ((cs.start + cs.units) * ncta - 1) / total;
+      float* part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (cs.start >= c0 ? 1 : 0)) * kSlot;
+      for (int i = tid; i < heads * D / 4; i += kThreads) {
+        const int head = i / (D / 4), d = i % (D / 4) * 4;
+        __stcg(reinterpret_cast<float4*>(part + head * (64 * NW) + d), joined(head, d));
+      }
+      if (tid < heads) {
+        __stcg(part + kHeads * 64 * NW + tid, s_top[tid]);
+        __stcg(part + kHeads * 64 * NW + kHeads + tid, s_sum[tid]);
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        uint32_t* counter = static_cast<uint32_t*>(a.workspace) + first;
+        s_last = atomicAdd(counter, 1u) == static_cast<uint32_t>(last - first);
+        if (s_last) *counter = 0;
+        __threadfence();
+      }
+      __syncthreads();
+      if (s_last) {
+        // the last of them: warp w adds up the parts first + w, first + w + 4, ...
+        auto part_of = [&](int64_t i) {
+          return parts + (2 * i + (i == first ? 1 : 0)) * kSlot;
+        };
+        for (int head = lane; head < heads; head += 32) {
+          float M = -INFINITY;
+          for (int64_t i = first + warp; i <= last; i += kWarps) M = fmaxf(M, __ldcg(part_of(i) + kHeads * 64 * NW + head));
+          float L = 0.0f;
+          for (int64_t i = first + warp; i <= last; i += kWarps) {
+            const float mi = __ldcg(part_of(i) + kHeads * 64 * NW + head);
+            if (mi != -INFINITY) L += ex2(mi - M) * __ldcg(part_of(i) + kHeads * 64 * NW + kHeads + head);
+          }
+          s_m[warp][head] = M;
+          s_l[warp][head] = L;
+        }
+        __syncwarp();
+        for (int k = lane; k < heads * D / 4; k += 32) {
+          const int head = k / (D / 4), d = k % (D / 4) * 4;
+          const float M = s_m[warp][head];
+          float4 v{0, 0, 0, 0};
+#pragma unroll 4
+          for (int64_t i = first + warp; i <= last; i += kWarps) {
+            const float* p = part_of(i);
+            const float mi = __ldcg(p + kHeads * 64 * NW + head);
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(p + head * (64 * NW) + d));
+            const float f = mi == -INFINITY ? 0.0f : ex2(mi - M);
+            v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
+          }
+          *reinterpret_cast<float4*>(s_o + (warp * kHeads + head) * kPitch + d) = v;
+        }
+        __syncthreads();
+        join_stats();
+        write_out();
+      }
+    }
+    if (cs.start + cs.units >= c1) break;
+    next_segment(a, cs);
+    __syncthreads();  // the buffers of the join are free again
+  }
+  cp_async_wait<0>();
+}
+
+template <int NW, int NT, bool FULL>
+nvfp4_status launch_t(const AttentionArgs& a, cudaStream_t stream) {
+  const auto kern = attention_kernel<NW, NT, FULL>;
+  const size_t smem = kWarps * kStages * Tile<NW>::kBytes + kWarps * 8 * NT * (64 * NW + 4) * 4 +
+                      static_cast<size_t>(a.B) * 8;
+  if (nvfp4_status st = set_dynamic_smem(reinterpret_cast<const void*>(kern), smem, "nvfp4_paged_attention_decode"))
+    return st;
+  int per_sm = blocks_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem);
+  if (per_sm > kMaxCtasPerSm) per_sm = kMaxCtasPerSm;
+  const int64_t cap = static_cast<int64_t>(sm_count()) * per_sm;
+  const int64_t reach = a.selected ? static_cast<int64_t>(a.max_selected) * a.ps : a.max_pages * a.ps;
+  const int64_t most = static_cast<int64_t>(a.B) * a.H * a.chunks * ((reach + kUnit - 1) / kUnit + 1);
+  const int64_t need = (most + kMinUnits - 1) / kMinUnits;
+  const int grid = static_cast<int>(need < cap ? (need < 1 ? 1 : need) : cap);
+  kern<<<grid, kThreads, smem, stream>>>(a);
+  return check_launch("nvfp4_paged_attention_decode");
+}
+
+template <int NW, int NT>
+nvfp4_status launch_f(const AttentionArgs& a, bool full, cudaStream_t s) {
+  return full ? launch_t<NW, NT, true>(a, s) : launch_t<NW, NT, false>(a, s);
+}
+
+// Query heads that one pass over the cache serves: eight, or sixteen where the accumulators of
+// sixteen fit the registers (D <= 128).
+int eights_of(int G, int D) { return G > 8 && D <= 128 ? 2 : 1; }
 
 }  // namespace
 
-int64_t attention_workspace_bytes(int32_t, int32_t, int32_t) { return NVFP4_COUNTER_BYTES; }
+int64_t attention_workspace_bytes(int32_t Hq, int32_t H, int32_t D) {
+  const int64_t nw = (D + 63) / 64, heads = 8 * eights_of(Hq / H, D);
+  const int64_t slot = heads * (64 * nw + 2) * 4;
+  return NVFP4_COUNTER_BYTES + 2 * slot * kMaxCtasPerSm * sm_count();
+}
 
-nvfp4_status launch_attention(const AttentionArgs& a, cudaStream_t stream) {
-  const int64_t items = static_cast<int64_t>(a.B) * a.Hq;
-  const int grid = static_cast<int>((items + kWarps - 1) / kWarps);
-  attention_kernel<<<grid, kWarps * 32, 0, stream>>>(a);
-  return check_launch("nvfp4_paged_attention_decode");
+nvfp4_status launch_attention(AttentionArgs a, cudaStream_t stream) {
+  const int nt = eights_of(a.G, a.D), nw = (a.D + 63) / 64;
+  a.chunks = (a.G + 8 * nt - 1) / (8 * nt);
+  a.chunk_heads = (a.G + a.chunks - 1) / a.chunks;
+  a.pool_pages = a.kc.num_pages < a.vc.num_pages ? a.kc.num_pages : a.vc.num_pages;
+  if (a.pool_pages > INT32_MAX) a.pool_pages = INT32_MAX;
+  if (sm_count() * kMaxCtasPerSm * 4 > NVFP4_COUNTER_BYTES)
+    return fail(NVFP4_ERR_UNSUPPORTED, "nvfp4_paged_attention_decode: more SMs than counters");
+  // the scale rows' copies: 4 nw bytes (nw = 3: 4 at a time), aligned to that
+  const uintptr_t part = nw == 3 ? 4 : 4 * nw;
+  auto al = [&](const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % part == 0 && stride % part == 0; };
+  const bool full = a.D % 64 == 0 && al(a.kc.sf, a.kc.sf_page_stride) && al(a.vc.sf, a.vc.sf_page_stride);
+  switch (nw * 2 + nt) {
+    case 3: return launch_f<1, 1>(a, full, stream);
+    case 4: return launch_f<1, 2>(a, full, stream);
+    case 5: return launch_f<2, 1>(a, full, stream);
+    case 6: return launch_f<2, 2>(a, full, stream);
+    case 7: return launch_f<3, 1>(a, full, stream);
+    default: return launch_f<4, 1>(a, full, stream);
+  }
 }
 
 }  // namespace nvfp4

@@ -30,10 +30,13 @@ struct AttentionArgs {
   float* lse;  // may be null
   int32_t* status;
   void* workspace;
+  // set at launch
+  int32_t chunks, chunk_heads;  // passes over a KV head's query heads, and the heads of one
+  int64_t pool_pages;           // pages that both caches have
 };
 // Device memory that a launch needs, whatever the lengths.
 int64_t attention_workspace_bytes(int32_t Hq, int32_t H, int32_t D);
-nvfp4_status launch_attention(const AttentionArgs& a, cudaStream_t stream);
+nvfp4_status launch_attention(AttentionArgs a, cudaStream_t stream);
 
 struct BoundsArgs {
   nvfp4_paged_cache kc;
