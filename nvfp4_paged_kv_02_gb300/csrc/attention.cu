@@ -47,6 +47,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;     // tokens
 constexpr int kMinUnits = 4;  // of a CTA's run: one for each warp
 constexpr int kMaxCtasPerSm = 4;
+constexpr int kSegmentCost = 2;
 constexpr float kWeightBias = 15.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -117,24 +118,28 @@ __device__ __forceinline__ int32_t units_of(const AttentionArgs& a, int32_t b, i
   return s.len > 0 ? (s.len - 1) / kUnit + 1 - s.lo / kUnit : 0;
 }
 
-__device__ __forceinline__ int64_t units_of_request(const AttentionArgs& a, int32_t b) {
+// What a segment counts for when the runs are cut: its units, and kSegmentCost for its queries,
+// its join and its output. Those trailing places of a segment hold no work.
+__device__ __forceinline__ int32_t places_of(int32_t units) { return units > 0 ? units + kSegmentCost : 0; }
+
+__device__ __forceinline__ int64_t places_of_request(const AttentionArgs& a, int32_t b) {
   int64_t n = 0;
   if (a.selected) {
-    for (int32_t h = 0; h < a.H; ++h) n += units_of(a, b, h);
+    for (int32_t h = 0; h < a.H; ++h) n += places_of(units_of(a, b, h));
   } else {
-    n = static_cast<int64_t>(units_of(a, b, 0)) * a.H;
+    n = static_cast<int64_t>(places_of(units_of(a, b, 0))) * a.H;
   }
   return n * a.chunks;
 }
 
-// cum[b] = units of the requests up to b; every thread calls it, ends with a barrier.
-__device__ __forceinline__ void scan_units(const AttentionArgs& a, int64_t* cum, int64_t* s_warp) {
+// cum[b] = places of the requests up to b; every thread calls it, ends with a barrier.
+__device__ __forceinline__ void scan_places(const AttentionArgs& a, int64_t* cum, int64_t* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.B + kThreads - 1) / kThreads;
   const int lo = tid * per, hi = min(a.B, lo + per);
   int64_t local = 0;
   for (int b = lo; b < hi; ++b) {
-    local += units_of_request(a, b);
+    local += places_of_request(a, b);
     cum[b] = local;
   }
   int64_t v = local;
@@ -151,35 +156,36 @@ __device__ __forceinline__ void scan_units(const AttentionArgs& a, int64_t* cum,
   __syncthreads();
 }
 
-// One (request, head, chunk of query heads) and where its units are among all units.
+// One (request, head, chunk of query heads), and the place of its first unit relative to the
+// run's first.
 struct Segment {
-  int32_t b, h, chunk, units;
-  int64_t start;
+  int32_t b, h, chunk, units, start;
 };
 
-__device__ __forceinline__ Segment find_segment(const AttentionArgs& a, const int64_t* cum, int64_t unit) {
+__device__ __forceinline__ Segment find_segment(const AttentionArgs& a, const int64_t* cum, int64_t place) {
   int32_t lo = 0, hi = a.B - 1;
   while (lo < hi) {
     const int32_t mid = (lo + hi) >> 1;
-    if (cum[mid] > unit) hi = mid;
+    if (cum[mid] > place) hi = mid;
     else lo = mid + 1;
   }
-  Segment s{lo, 0, 0, 0, lo > 0 ? cum[lo - 1] : 0};
+  Segment s{lo, 0, 0, 0, 0};
+  int64_t start = lo > 0 ? cum[lo - 1] : 0;
   for (;;) {
     s.units = units_of(a, s.b, s.h);
-    const int64_t head = static_cast<int64_t>(s.units) * a.chunks;
-    if (unit < s.start + head || s.h + 1 == a.H) break;
-    s.start += head;
+    const int64_t head = static_cast<int64_t>(places_of(s.units)) * a.chunks;
+    if (place < start + head || s.h + 1 == a.H) break;
+    start += head;
     ++s.h;
   }
-  if (s.units > 0) s.chunk = static_cast<int32_t>((unit - s.start) / s.units);
-  s.start += static_cast<int64_t>(s.chunk) * s.units;
+  if (s.units > 0) s.chunk = static_cast<int32_t>((place - start) / places_of(s.units));
+  s.start = static_cast<int32_t>(start + static_cast<int64_t>(s.chunk) * places_of(s.units) - place);
   return s;
 }
 
 // The next segment that has units (the caller knows that there is one).
 __device__ __forceinline__ void next_segment(const AttentionArgs& a, Segment& s) {
-  s.start += s.units;
+  s.start += places_of(s.units);
   if (++s.chunk < a.chunks) return;
   s.chunk = 0;
   do {
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
   const int D = FULL ? 64 * NW : a.D;
-  scan_units(a, cum, s_scan);
+  scan_places(a, cum, s_scan);
 
   // heads without live tokens: zeros
   for (int32_t b = blockIdx.x; b < a.B; b += gridDim.x) {
@@ -267,7 +273,8 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
   const int64_t want = (total + kMinUnits - 1) / kMinUnits;
   const int64_t ncta = want < gridDim.x ? want : gridDim.x;
   if (blockIdx.x >= ncta) return;
-  const int64_t c0 = total * blockIdx.x / ncta, c1 = total * (blockIdx.x + 1) / ncta;
+  const int64_t c0 = total * blockIdx.x / ncta;
+  const int32_t run = static_cast<int32_t>(total * (blockIdx.x + 1) / ncta - c0);  // places
 
   const uint32_t ring = smem_addr(smem) + warp * NS * T::kBytes;
   uint8_t* const ring_p = smem + warp * NS * T::kBytes;
@@ -278,58 +285,65 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
   }
 
   // -- the producer: this warp's units, one looked up ahead of its copies --
-  Segment ps = find_segment(a, cum, c0);
-  Segment cs = ps;  // the consumer's
+  Segment cs = find_segment(a, cum, c0);  // the consumer's segment
+  Segment ps = cs;                        // the producer's
+  // the units [u, end) of a segment that lie in this run
   auto portion = [&](const Segment& s, int32_t& u, int32_t& end) {
-    u = static_cast<int32_t>(max(c0 - s.start, int64_t(0)));
-    end = static_cast<int32_t>(min(c1 - s.start, static_cast<int64_t>(s.units)));
+    u = max(-s.start, 0);
+    end = min(run - s.start, s.units);
   };
+  auto more = [&](const Segment& s) { return s.start + places_of(s.units) < run; };
   int32_t pu, pend;
-  portion(ps, pu, pend);
-  pu += warp;
+  Span span;            // the producer's request
+  int32_t slots = 0;    // slots of its selected pages
+  const uint8_t* list;  // its row of the page table
+  auto enter = [&] {
+    portion(ps, pu, pend);
+    pu += warp;
+    span = span_of(a, ps.b);
+    list = static_cast<const uint8_t*>(a.block_tables) + (ps.b * a.max_pages << (a.table64 ? 3 : 2));
+    if (a.selected)
+      slots = min(max(__ldg(a.num_selected + static_cast<int64_t>(ps.b) * a.H + ps.h), 0), a.max_selected) * a.ps;
+  };
+  enter();
   auto settle = [&] {  // to a unit of this warp, or past the run's end (pu >= pend)
-    while (pu >= pend && ps.start + ps.units < c1) {
+    while (pu >= pend && more(ps)) {
       next_segment(a, ps);
-      portion(ps, pu, pend);
-      pu += warp;
+      enter();
     }
   };
   settle();
-  int32_t lk_page = -1, lk_row = 0;  // this lane's row of the unit looked up
-  bool lk_unit = false;
+  // This lane's row of the unit looked up. The table's entry stays as it was loaded until the
+  // copies are issued, so that nothing waits for it here.
+  int32_t lk_lo = 0, lk_hi = 0, lk_row = 0;
+  bool lk_unit = false, lk_live = false;
   auto look_up = [&] {
-    lk_page = -1;
+    lk_live = false;
     lk_unit = pu < pend;
     if (!lk_unit) return;
-    const Span sp = span_of(a, ps.b);
-    int64_t col;
-    int32_t slot;
-    bool live;
+    int32_t col, slot;
     if (a.selected) {
-      const int64_t list = static_cast<int64_t>(ps.b) * a.H + ps.h;
       const int32_t p = pu * kUnit + lane;
-      const int32_t i = static_cast<int32_t>(div_q32(p, a.div_ps));
+      const int32_t i = div_q32(p, a.div_ps);
       slot = p - i * a.ps;
-      live = i < min(__ldg(a.num_selected + list), a.max_selected);
-      col = live ? __ldg(a.selected + list * a.max_selected + i) : 0;
+      lk_live = p < slots;
+      col = lk_live ? __ldg(a.selected + (static_cast<int64_t>(ps.b) * a.H + ps.h) * a.max_selected + i) : 0;
       if (col < 0 || col >= a.max_pages) {
         flag(a.status, NVFP4_DEV_BAD_PAGE);
-        live = false;
+        lk_live = false;
       }
-      live = live && col * a.ps + slot < sp.len;
+      lk_live = lk_live && static_cast<int64_t>(col) * a.ps + slot < span.len;
     } else {
-      const int64_t t = (static_cast<int64_t>(sp.lo / kUnit) + pu) * kUnit + lane;
-      live = t >= sp.lo && t < sp.len;
-      col = live ? div_q32(static_cast<int32_t>(t), a.div_ps) : 0;
-      slot = static_cast<int32_t>(t - col * a.ps);
+      const uint32_t t = (static_cast<uint32_t>(span.lo / kUnit) + pu) * kUnit + lane;
+      lk_live = t >= static_cast<uint32_t>(span.lo) && t < static_cast<uint32_t>(span.len);
+      col = lk_live ? div_q32(static_cast<int32_t>(t), a.div_ps) : 0;
+      slot = static_cast<int32_t>(t) - col * a.ps;
     }
-    if (live) {
-      const int64_t at = ps.b * a.max_pages + col;
-      const int64_t page = a.table64 ? __ldg(static_cast<const int64_t*>(a.block_tables) + at)
-                                     : __ldg(static_cast<const int32_t*>(a.block_tables) + at);
+    if (lk_live) {
+      const int32_t* entry = reinterpret_cast<const int32_t*>(list + (static_cast<int64_t>(col) << (a.table64 ? 3 : 2)));
+      lk_lo = __ldg(entry);
+      if (a.table64) lk_hi = __ldg(entry + 1);
       lk_row = a.layout == NVFP4_NHD ? slot * a.H + ps.h : ps.h * a.ps + slot;
-      if (page >= 0 && page < a.pool_pages) lk_page = static_cast<int32_t>(page);
-      else flag(a.status, NVFP4_DEV_BAD_PAGE);
     }
   };
   look_up();
@@ -352,6 +366,12 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
     if (!FULL) put_scales();
     if (lk_unit) {
       const uint32_t st = ring + s * T::kBytes;
+      int32_t lk_page = -1;
+      if (lk_live) {
+        const int64_t page = a.table64 ? (static_cast<int64_t>(lk_hi) << 32) | static_cast<uint32_t>(lk_lo) : lk_lo;
+        if (page >= 0 && page < a.pool_pages) lk_page = static_cast<int32_t>(page);
+        else flag(a.status, NVFP4_DEV_BAD_PAGE);
+      }
       const uint32_t mask = __ballot_sync(0xFFFFFFFFu, lk_page >= 0);
       if (lane == 0) *reinterpret_cast<uint32_t*>(ring_p + s * T::kBytes + T::kMask) = mask;
       const bool live = lk_page >= 0;
@@ -378,29 +398,43 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
         }
         pend_stage = s;
       }
-      auto row_copy = [&](int row, int off, auto bytes) {
-        constexpr int B = decltype(bytes)::value;
+      // (a row that is not live is copied as zeros: its address is the pool's start)
+      auto row_at = [&](int row, int& bytes, const uint8_t*& k, const uint8_t*& v) {
         const int32_t pg = __shfl_sync(0xFFFFFFFFu, lk_page, row);
         const int32_t rw = __shfl_sync(0xFFFFFFFFu, lk_row, row);
-        const bool ok = pg >= 0;
-        const int64_t in = static_cast<int64_t>(ok ? rw : 0) * (D / 2) + off;
-        const int64_t p = ok ? pg : 0;
-        const uint32_t dst = st + row * T::kRow + (((off >> 4) ^ T::swizzle(row)) << 4) + (off & 15);
-        cp_async<B>(dst, a.kc.data + p * a.kc.data_page_stride + in, ok);
-        cp_async<B>(dst + T::kV, a.vc.data + p * a.vc.data_page_stride + in, ok);
+        bytes = pg >= 0;
+        const int64_t p = bytes ? pg : 0;
+        const int64_t in = static_cast<int64_t>(bytes ? rw : 0) * (D / 2);
+        k = a.kc.data + p * a.kc.data_page_stride + in;
+        v = a.vc.data + p * a.vc.data_page_stride + in;
       };
+      int ok;
+      const uint8_t *kp, *vp;
       if (FULL) {
-        constexpr int kChunks = 2 * NW;
+        // two lanes to a row: each copy takes whole 32-byte sectors, and a lane has few rows
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          const int k = i * 32 + lane;
-          row_copy(k / kChunks, k % kChunks * 16, std::integral_constant<int, 16>{});
+        for (int g = 0; g < 2; ++g) {
+          const int row = 16 * g + (lane >> 1);
+          row_at(row, ok, kp, vp);
+          const uint32_t dst = st + row * T::kRow;
+          const int sw = T::swizzle(row);
+          kp += 16 * (lane & 1);
+          vp += 16 * (lane & 1);
+#pragma unroll
+          for (int j = 0; j < NW; ++j) {
+            const uint32_t at = dst + (((2 * j + (lane & 1)) ^ sw) << 4);
+            cp_async<16>(at, kp + 32 * j, ok);
+            cp_async<16>(at + T::kV, vp + 32 * j, ok);
+          }
         }
       } else {
         const int chunks = D / 16;  // of 8 bytes
         for (int i = 0; i < chunks; ++i) {
-          const int k = i * 32 + lane;
-          row_copy(k / chunks, k % chunks * 8, std::integral_constant<int, 8>{});
+          const int k = i * 32 + lane, row = k / chunks, off = k % chunks * 8;
+          row_at(row, ok, kp, vp);
+          const uint32_t at = st + row * T::kRow + (((off >> 4) ^ T::swizzle(row)) << 4) + (off & 15);
+          cp_async<8>(at, kp + off, ok);
+          cp_async<8>(at + T::kV, vp + off, ok);
         }
       }
       pu += kWarps;
@@ -419,49 +453,59 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
   const int t0 = token_of(r);                    // this lane's K rows: t0 and t0 + 8
   const int v0 = token_of(2 * c), v1 = token_of(2 * c + 1);  // its V rows, and 8 more
   int stage = 0, refill = NS - 1;
+  uint32_t raw[NT][8 * NW];  // the coming segment's query rows, as they are
+  auto load_queries = [&](const Segment& s) {
+    const int head0 = s.chunk * a.chunk_heads, heads = min(a.chunk_heads, a.G - head0);
+    const uint8_t* q = a.q + s.b * a.q_row_bytes +
+                       ((static_cast<int64_t>(s.h) * a.G + head0 + r) * D + 16 * NW * c) * 2;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2 * NW; ++i) {
+        const bool in = 8 * nt + r < heads && 16 * NW * c + 8 * i < D;
+        const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(q + 16 * nt * D) + i) : uint4{};
+        raw[nt][4 * i] = x.x; raw[nt][4 * i + 1] = x.y; raw[nt][4 * i + 2] = x.z; raw[nt][4 * i + 3] = x.w;
+      }
+  };
+  load_queries(cs);
   for (;;) {
     // the segment's query heads
     const int head0 = cs.chunk * a.chunk_heads;
     const int heads = min(a.chunk_heads, a.G - head0);
     const int64_t q_row = static_cast<int64_t>(cs.h) * a.G + head0;
     uint32_t qf[NT][4 * NW][2];
-    float factor[NT][2];
+    float factor[NT][2];  // base-2 logarithm units of a score (before the cap: natural ones)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int head = 8 * nt + r;
-      const uint8_t* q = a.q + cs.b * a.q_row_bytes + ((q_row + head) * D + 16 * NW * c) * 2;
       float top = 0.0f;
-      uint32_t w[8 * NW];
-#pragma unroll
-      for (int i = 0; i < 2 * NW; ++i) {
-        const bool in = head < heads && 16 * NW * c + 8 * i < D;
-        const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(q) + i) : uint4{};
-        w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
-      }
 #pragma unroll
       for (int i = 0; i < 8 * NW; ++i) {
-        const float lo = a.bf16 ? __uint_as_float(w[i] << 16) : f32_from_f16_lo(w[i]);
-        const float hi = a.bf16 ? f32_from_bf16_hi(w[i]) : f32_from_f16_hi(w[i]);
+        const uint32_t w = raw[nt][i];
+        const float lo = a.bf16 ? __uint_as_float(w << 16) : f32_from_f16_lo(w);
+        const float hi = a.bf16 ? f32_from_bf16_hi(w) : f32_from_f16_hi(w);
         top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
       }
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
       const int e = top > 0.0f && top <= FLT_MAX ? ilogbf(top) - 14 : 0;
-      // 2^-e as two factors: it may be out of range by itself
-      const float f1 = __int_as_float((127 - e / 2) << 23), f2 = __int_as_float((127 - (e - e / 2)) << 23);
+      float f = ldexpf(a.sm_scale, e) * gk;
+      // 2^-e as two factors (it may be out of range by itself), with f's sign: f is not negative
+      // from here on, and a maximum of scores is one of logits; f = 0 is a query of zeros
+      float f1 = __int_as_float((127 - e / 2) << 23);
+      const float f2 = __int_as_float((127 - (e - e / 2)) << 23);
+      if (f < 0.0f) f1 = -f1;
+      if (f == 0.0f) f1 = 0.0f;
+      f = f == 0.0f ? 1.0f : fabsf(f);
 #pragma unroll
       for (int i = 0; i < 8 * NW; ++i) {
-        const float lo = a.bf16 ? __uint_as_float(w[i] << 16) : f32_from_f16_lo(w[i]);
-        const float hi = a.bf16 ? f32_from_bf16_hi(w[i]) : f32_from_f16_hi(w[i]);
+        const uint32_t w = raw[nt][i];
+        const float lo = a.bf16 ? __uint_as_float(w << 16) : f32_from_f16_lo(w);
+        const float hi = a.bf16 ? f32_from_bf16_hi(w) : f32_from_f16_hi(w);
         qf[nt][i >> 1][i & 1] = f16x2_from_f32(lo * f1 * f2, hi * f1 * f2);
       }
-      const float f = ldexpf(a.sm_scale, e) * gk;
+      if (a.soft_cap == 0.0f) f *= kLog2e;
       factor[nt][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * c);
       factor[nt][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * c + 4);
-      if (a.soft_cap == 0.0f) {
-        factor[nt][0] *= kLog2e;
-        factor[nt][1] *= kLog2e;
-      }
     }
     float o[NT][NW][4][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -475,6 +519,12 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[nt][w][i][k] = 0.0f;
     }
+
+    float unit[NT][2];  // what turns x into base-2 logarithms
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) unit[nt][k] = a.soft_cap > 0.0f ? kLog2e : factor[nt][k];
 
     int32_t cu, cend;
     portion(cs, cu, cend);
@@ -541,16 +591,15 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
         }
       }
       // x[mt][nt][2 p + k]: token 16 mt + 8 p + t0, head 8 nt + 2 c + k
+      if (a.soft_cap > 0.0f) {
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float v = x[mt][nt][k] * factor[nt][k & 1];
-            if (a.soft_cap > 0.0f) v = soft_capped(v, a.soft_cap) * kLog2e;
-            x[mt][nt][k] = v;
-          }
+            for (int k = 0; k < 4; ++k)
+              x[mt][nt][k] = soft_capped(x[mt][nt][k] * factor[nt][k & 1], a.soft_cap);
+      }
       if (mask != 0xFFFFFFFFu) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -571,8 +620,8 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
           v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
           v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
-          top[nt][k] = v;
-          grew = grew || v > m[nt][k];
+          top[nt][k] = v * unit[nt][k];
+          grew = grew || top[nt][k] > m[nt][k];
         }
       if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
@@ -595,13 +644,14 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
       uint32_t pb[2][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float off0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0] - kWeightBias;
-        const float off1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1] - kWeightBias;
+        const float off0 = m[nt][0] == -INFINITY ? 0.0f : kWeightBias - m[nt][0];
+        const float off1 = m[nt][1] == -INFINITY ? 0.0f : kWeightBias - m[nt][1];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
-            const float p0 = ex2(x[mt][nt][2 * p] - off0), p1 = ex2(x[mt][nt][2 * p + 1] - off1);
+            const float p0 = ex2(__fmaf_rn(x[mt][nt][2 * p], unit[nt][0], off0));
+            const float p1 = ex2(__fmaf_rn(x[mt][nt][2 * p + 1], unit[nt][1], off1));
             l[nt][0] += p0;
             l[nt][1] += p1;
             pb[mt][nt][p] = transpose8x8(f16x2_from_f32(p0, p1));
@@ -662,6 +712,18 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
       }
     }
 
+    // the next segment's queries arrive while this one is joined
+    const Segment done = cs;
+    const bool last_segment = !more(cs);
+    if (!last_segment) {
+      next_segment(a, cs);
+      load_queries(cs);
+    }
+    if (done.start + done.units <= 0) {  // the run begins in the segment's empty places
+      if (last_segment) break;
+      continue;
+    }
+
     // -- the four warps' parts, joined --
     // o[nt][w][i][k], [k + 2]: head 8 nt + 2 c + k, d = 8 (NW r + w) + 2 i, + 1
 #pragma unroll
@@ -713,7 +775,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
       return v;
     };
     auto write_out = [&] {
-      const int64_t row = static_cast<int64_t>(cs.b) * a.Hq + q_row;
+      const int64_t row = static_cast<int64_t>(done.b) * a.Hq + q_row;
       for (int i = tid; i < heads * D / 4; i += kThreads) {
         const int head = i / (D / 4), d = i % (D / 4) * 4;
         const float4 v = joined(head, d);
@@ -735,9 +797,11 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
       // its run, else slot 1
       constexpr int kSlot = kHeads * (64 * NW + 2);
       float* const parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + NVFP4_COUNTER_BYTES);
-      const int64_t first = ((cs.start + 1) * ncta - 1) / total;
-      const int64_t last = ((cs.start + cs.units) * ncta - 1) / total;
-      float* part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (cs.start >= c0 ? 1 : 0)) * kSlot;
+      // (run i begins at place total * i / ncta)
+      const int64_t start = c0 + done.start;
+      const int64_t first = ((start + 1) * ncta - 1) / total;
+      const int64_t last = ((start + done.units) * ncta - 1) / total;
+      float* part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (done.start >= 0 ? 1 : 0)) * kSlot;
       for (int i = tid; i < heads * D / 4; i += kThreads) {
         const int head = i / (D / 4), d = i % (D / 4) * 4;
         __stcg(reinterpret_cast<float4*>(part + head * (64 * NW) + d), joined(head, d));
@@ -791,8 +855,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
         write_out();
       }
     }
-    if (cs.start + cs.units >= c1) break;
-    next_segment(a, cs);
+    if (last_segment) break;
     __syncthreads();  // the buffers of the join are free again
   }
   cp_async_wait<0>();
