@@ -45,6 +45,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;     // tokens
+constexpr int kHalves = kUnit / 32;
+constexpr int kTiles = kUnit / 16;  // of 16 tokens
 constexpr int kMinUnits = 4;  // of a CTA's run: one for each warp
 constexpr int kMaxCtasPerSm = 4;
 constexpr int kSegmentCost = 2;
@@ -68,7 +70,7 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -77,7 +79,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 
@@ -211,7 +213,7 @@ struct Tile {
   static constexpr int kKs = 2 * kUnit * kRow;
   static constexpr int kVs = kKs + kUnit * kScales;
   static constexpr int kMask = kVs + kUnit * kScales;
-  static constexpr int kBytes = (kMask + 4 + 15) / 16 * 16;
+  static constexpr int kBytes = kMask + 16;
   // 16-byte chunks of row t are exchanged so that a fragment's rows spread over the banks
   __host__ __device__ static constexpr int swizzle(int t) { return NW == 2 ? t & 2 : (NW == 4 ? t & 7 : 0); }
 };
@@ -238,7 +240,7 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 // FULL: D = 64 NW and scale rows that cp.async can copy; otherwise any D, and scales of any
 // alignment, which go through registers.
 template <int NW, int NT, bool FULL>
-__global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs a) {
+__global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attention_kernel(const AttentionArgs a) {
   using T = Tile<NW>;
   constexpr int NS = kStages;
   constexpr int kHeads = 8 * NT;
@@ -313,128 +315,138 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
     }
   };
   settle();
-  // This lane's row of the unit looked up. The table's entry stays as it was loaded until the
-  // copies are issued, so that nothing waits for it here.
-  int32_t lk_lo = 0, lk_hi = 0, lk_row = 0;
-  bool lk_unit = false, lk_live = false;
+  // This lane's rows of the unit looked up. The table's entries stay as they were loaded until
+  // the copies are issued, so that nothing waits for them here.
+  int32_t lk_lo[kHalves], lk_hi[kHalves], lk_row[kHalves];
+  bool lk_unit = false, lk_live[kHalves];
   auto look_up = [&] {
-    lk_live = false;
     lk_unit = pu < pend;
-    if (!lk_unit) return;
-    int32_t col, slot;
-    if (a.selected) {
-      const int32_t p = pu * kUnit + lane;
-      const int32_t i = div_q32(p, a.div_ps);
-      slot = p - i * a.ps;
-      lk_live = p < slots;
-      col = lk_live ? __ldg(a.selected + (static_cast<int64_t>(ps.b) * a.H + ps.h) * a.max_selected + i) : 0;
-      if (col < 0 || col >= a.max_pages) {
-        flag(a.status, NVFP4_DEV_BAD_PAGE);
-        lk_live = false;
+#pragma unroll
+    for (int g = 0; g < kHalves; ++g) {
+      lk_live[g] = false;
+      lk_lo[g] = lk_hi[g] = lk_row[g] = 0;
+      if (!lk_unit) continue;
+      int32_t col, slot;
+      if (a.selected) {
+        const int32_t p = pu * kUnit + 32 * g + lane;
+        const int32_t i = div_q32(p, a.div_ps);
+        slot = p - i * a.ps;
+        lk_live[g] = p < slots;
+        col = lk_live[g] ? __ldg(a.selected + (static_cast<int64_t>(ps.b) * a.H + ps.h) * a.max_selected + i) : 0;
+        if (col < 0 || col >= a.max_pages) {
+          flag(a.status, NVFP4_DEV_BAD_PAGE);
+          lk_live[g] = false;
+        }
+        lk_live[g] = lk_live[g] && static_cast<int64_t>(col) * a.ps + slot < span.len;
+      } else {
+        const uint32_t t = (static_cast<uint32_t>(span.lo / kUnit) + pu) * kUnit + 32 * g + lane;
+        lk_live[g] = t >= static_cast<uint32_t>(span.lo) && t < static_cast<uint32_t>(span.len);
+        col = lk_live[g] ? div_q32(static_cast<int32_t>(t), a.div_ps) : 0;
+        slot = static_cast<int32_t>(t) - col * a.ps;
       }
-      lk_live = lk_live && static_cast<int64_t>(col) * a.ps + slot < span.len;
-    } else {
-      const uint32_t t = (static_cast<uint32_t>(span.lo / kUnit) + pu) * kUnit + lane;
-      lk_live = t >= static_cast<uint32_t>(span.lo) && t < static_cast<uint32_t>(span.len);
-      col = lk_live ? div_q32(static_cast<int32_t>(t), a.div_ps) : 0;
-      slot = static_cast<int32_t>(t) - col * a.ps;
-    }
-    if (lk_live) {
-      const int32_t* entry = reinterpret_cast<const int32_t*>(list + (static_cast<int64_t>(col) << (a.table64 ? 3 : 2)));
-      lk_lo = __ldg(entry);
-      if (a.table64) lk_hi = __ldg(entry + 1);
-      lk_row = a.layout == NVFP4_NHD ? slot * a.H + ps.h : ps.h * a.ps + slot;
+      if (lk_live[g]) {
+        const int32_t* entry = reinterpret_cast<const int32_t*>(list + (static_cast<int64_t>(col) << (a.table64 ? 3 : 2)));
+        lk_lo[g] = __ldg(entry);
+        if (a.table64) lk_hi[g] = __ldg(entry + 1);
+        lk_row[g] = a.layout == NVFP4_NHD ? slot * a.H + ps.h : ps.h * a.ps + slot;
+      }
     }
   };
   look_up();
 
   // !FULL: scale bytes on their way to the stage of the unit issued last
-  uint32_t pk[4], pv[4];
+  uint32_t pk[kHalves][NW], pv[kHalves][NW];
   int pend_stage = -1;
   const int nb = D / 16;
   auto put_scales = [&] {
-    if (FULL || pend_stage < 0) return;
+    if (pend_stage < 0) return;
     uint8_t* st = ring_p + pend_stage * T::kBytes;
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      *reinterpret_cast<uint32_t*>(st + T::kKs + lane * T::kScales + 4 * i) = pk[i];
-      *reinterpret_cast<uint32_t*>(st + T::kVs + lane * T::kScales + 4 * i) = pv[i];
-    }
+    for (int g = 0; g < kHalves; ++g)
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        *reinterpret_cast<uint32_t*>(st + T::kKs + (32 * g + lane) * T::kScales + 4 * i) = pk[g][i];
+        *reinterpret_cast<uint32_t*>(st + T::kVs + (32 * g + lane) * T::kScales + 4 * i) = pv[g][i];
+      }
   };
   // Copies of the unit looked up into stage s, then the look-up of the next one.
   auto issue = [&](int s) {
     if (!FULL) put_scales();
     if (lk_unit) {
       const uint32_t st = ring + s * T::kBytes;
-      int32_t lk_page = -1;
-      if (lk_live) {
-        const int64_t page = a.table64 ? (static_cast<int64_t>(lk_hi) << 32) | static_cast<uint32_t>(lk_lo) : lk_lo;
-        if (page >= 0 && page < a.pool_pages) lk_page = static_cast<int32_t>(page);
-        else flag(a.status, NVFP4_DEV_BAD_PAGE);
-      }
-      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, lk_page >= 0);
-      if (lane == 0) *reinterpret_cast<uint32_t*>(ring_p + s * T::kBytes + T::kMask) = mask;
-      const bool live = lk_page >= 0;
-      const int64_t page = live ? lk_page : 0;
-      const uint8_t* ks = a.kc.sf + page * a.kc.sf_page_stride + static_cast<int64_t>(live ? lk_row : 0) * nb;
-      const uint8_t* vs = a.vc.sf + page * a.vc.sf_page_stride + static_cast<int64_t>(live ? lk_row : 0) * nb;
-      const uint32_t ksd = st + T::kKs + lane * T::kScales, vsd = st + T::kVs + lane * T::kScales;
-      if (FULL) {
-        constexpr int kPart = NW == 3 ? 4 : 4 * NW;
 #pragma unroll
-        for (int i = 0; i < T::kScales / kPart; ++i) {
-          cp_async<kPart>(ksd + i * kPart, ks + i * kPart, live);
-          cp_async<kPart>(vsd + i * kPart, vs + i * kPart, live);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < NW; ++i) pk[i] = pv[i] = 0;
-#pragma unroll
-        for (int i = 0; i < 4 * NW; ++i) {
-          if (live && i < nb) {
-            pk[i / 4] |= static_cast<uint32_t>(__ldg(ks + i)) << (8 * (i % 4));
-            pv[i / 4] |= static_cast<uint32_t>(__ldg(vs + i)) << (8 * (i % 4));
+      for (int g = 0; g < kHalves; ++g) {
+        uint32_t page = 0, rw = 0;  // (a row that is not live is copied as zeros)
+        bool live = false;
+        if (lk_live[g]) {
+          const int64_t entry = a.table64 ? (static_cast<int64_t>(lk_hi[g]) << 32) | static_cast<uint32_t>(lk_lo[g]) : lk_lo[g];
+          if (entry >= 0 && entry < a.pool_pages) {
+            live = true;
+            page = static_cast<uint32_t>(entry);
+            rw = lk_row[g];
+          } else {
+            flag(a.status, NVFP4_DEV_BAD_PAGE);
           }
         }
-        pend_stage = s;
-      }
-      // (a row that is not live is copied as zeros: its address is the pool's start)
-      auto row_at = [&](int row, int& bytes, const uint8_t*& k, const uint8_t*& v) {
-        const int32_t pg = __shfl_sync(0xFFFFFFFFu, lk_page, row);
-        const int32_t rw = __shfl_sync(0xFFFFFFFFu, lk_row, row);
-        bytes = pg >= 0;
-        const int64_t p = bytes ? pg : 0;
-        const int64_t in = static_cast<int64_t>(bytes ? rw : 0) * (D / 2);
-        k = a.kc.data + p * a.kc.data_page_stride + in;
-        v = a.vc.data + p * a.vc.data_page_stride + in;
-      };
-      int ok;
-      const uint8_t *kp, *vp;
-      if (FULL) {
-        // two lanes to a row: each copy takes whole 32-byte sectors, and a lane has few rows
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, live);
+        if (lane == 0) *reinterpret_cast<uint32_t*>(ring_p + s * T::kBytes + T::kMask + 4 * g) = mask;
+        const uint8_t* ks = a.kc.sf + static_cast<uint64_t>(page) * a.k_sf_stride + static_cast<uint64_t>(rw) * nb;
+        const uint8_t* vs = a.vc.sf + static_cast<uint64_t>(page) * a.v_sf_stride + static_cast<uint64_t>(rw) * nb;
+        const uint32_t ksd = st + T::kKs + (32 * g + lane) * T::kScales;
+        const uint32_t vsd = st + T::kVs + (32 * g + lane) * T::kScales;
+        if (FULL) {
+          constexpr int kPart = NW == 3 ? 4 : 4 * NW;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int row = 16 * g + (lane >> 1);
-          row_at(row, ok, kp, vp);
-          const uint32_t dst = st + row * T::kRow;
-          const int sw = T::swizzle(row);
-          kp += 16 * (lane & 1);
-          vp += 16 * (lane & 1);
-#pragma unroll
-          for (int j = 0; j < NW; ++j) {
-            const uint32_t at = dst + (((2 * j + (lane & 1)) ^ sw) << 4);
-            cp_async<16>(at, kp + 32 * j, ok);
-            cp_async<16>(at + T::kV, vp + 32 * j, ok);
+          for (int i = 0; i < T::kScales / kPart; ++i) {
+            cp_async<kPart>(ksd + i * kPart, ks + i * kPart, live);
+            cp_async<kPart>(vsd + i * kPart, vs + i * kPart, live);
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NW; ++i) pk[g][i] = pv[g][i] = 0;
+#pragma unroll
+          for (int i = 0; i < 4 * NW; ++i) {
+            if (live && i < nb) {
+              pk[g][i / 4] |= static_cast<uint32_t>(__ldg(ks + i)) << (8 * (i % 4));
+              pv[g][i / 4] |= static_cast<uint32_t>(__ldg(vs + i)) << (8 * (i % 4));
+            }
+          }
+          pend_stage = s;
         }
-      } else {
-        const int chunks = D / 16;  // of 8 bytes
-        for (int i = 0; i < chunks; ++i) {
-          const int k = i * 32 + lane, row = k / chunks, off = k % chunks * 8;
-          row_at(row, ok, kp, vp);
-          const uint32_t at = st + row * T::kRow + (((off >> 4) ^ T::swizzle(row)) << 4) + (off & 15);
-          cp_async<8>(at, kp + off, ok);
-          cp_async<8>(at + T::kV, vp + off, ok);
+        const uint8_t *kp, *vp;
+        auto row_at = [&](int row) {
+          const uint32_t pg = __shfl_sync(0xFFFFFFFFu, page, row);
+          const uint32_t r2 = __shfl_sync(0xFFFFFFFFu, rw, row);
+          kp = a.kc.data + static_cast<uint64_t>(pg) * a.k_stride + static_cast<uint64_t>(r2) * (D / 2);
+          vp = a.vc.data + static_cast<uint64_t>(pg) * a.v_stride + static_cast<uint64_t>(r2) * (D / 2);
+        };
+        if (FULL) {
+          // two lanes to a row: each copy takes whole 32-byte sectors, and a lane has few rows
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int row = 16 * i + (lane >> 1);
+            row_at(row);
+            const bool ok = mask >> row & 1u;
+            const uint32_t dst = st + (32 * g + row) * T::kRow;
+            const int sw = T::swizzle(row);
+#pragma unroll
+            for (int j = 0; j < NW; ++j) {
+              const uint32_t at = dst + (((2 * j + (lane & 1)) ^ sw) << 4);
+              const int off = 16 * (lane & 1) + 32 * j;
+              cp_async<16>(at, kp + off, ok);
+              cp_async<16>(at + T::kV, vp + off, ok);
+            }
+          }
+        } else {
+          const int chunks = D / 16;  // of 8 bytes
+          for (int i = 0; i < chunks; ++i) {
+            const int k = i * 32 + lane, row = k / chunks, off = k % chunks * 8;
+            row_at(row);
+            const bool ok = mask >> row & 1u;
+            const uint32_t at = st + (32 * g + row) * T::kRow + (((off >> 4) ^ T::swizzle(row)) << 4) + (off & 15);
+            cp_async<8>(at, kp + off, ok);
+            cp_async<8>(at + T::kV, vp + off, ok);
+          }
         }
       }
       pu += kWarps;
@@ -536,11 +548,13 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
       const uint8_t* st = ring_p + stage * T::kBytes;
       refill = stage;
       stage = stage + 1 == NS ? 0 : stage + 1;
-      const uint32_t mask = *reinterpret_cast<const uint32_t*>(st + T::kMask);
-
-      float x[2][NT][4];
+      uint32_t mask[kHalves];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+      for (int g = 0; g < kHalves; ++g) mask[g] = *reinterpret_cast<const uint32_t*>(st + T::kMask + 4 * g);
+
+      float x[kTiles][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < kTiles; ++mt) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -593,22 +607,23 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
       // x[mt][nt][2 p + k]: token 16 mt + 8 p + t0, head 8 nt + 2 c + k
       if (a.soft_cap > 0.0f) {
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               x[mt][nt][k] = soft_capped(x[mt][nt][k] * factor[nt][k & 1], a.soft_cap);
       }
-      if (mask != 0xFFFFFFFFu) {
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+      for (int g = 0; g < kHalves; ++g) {
+        if (mask[g] == 0xFFFFFFFFu) continue;
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
-            if (!(mask >> (16 * mt + 8 * p + t0) & 1u)) {
+        for (int k = 0; k < 4; ++k)
+          if (!(mask[g] >> (8 * k + t0) & 1u)) {
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) x[mt][nt][2 * p] = x[mt][nt][2 * p + 1] = -INFINITY;
-            }
+            for (int nt = 0; nt < NT; ++nt)
+              x[2 * g + k / 2][nt][k % 2 * 2] = x[2 * g + k / 2][nt][k % 2 * 2 + 1] = -INFINITY;
+          }
       }
       bool grew = false;
       float top[NT][2];
@@ -616,7 +631,9 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float v = fmaxf(fmaxf(x[0][nt][k], x[0][nt][k + 2]), fmaxf(x[1][nt][k], x[1][nt][k + 2]));
+          float v = fmaxf(x[0][nt][k], x[0][nt][k + 2]);
+#pragma unroll
+          for (int mt = 1; mt < kTiles; ++mt) v = fmaxf(v, fmaxf(x[mt][nt][k], x[mt][nt][k + 2]));
           v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
           v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
@@ -641,13 +658,13 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
               }
           }
       }
-      uint32_t pb[2][NT][2];
+      uint32_t pb[kTiles][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float off0 = m[nt][0] == -INFINITY ? 0.0f : kWeightBias - m[nt][0];
         const float off1 = m[nt][1] == -INFINITY ? 0.0f : kWeightBias - m[nt][1];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             const float p0 = ex2(__fmaf_rn(x[mt][nt][2 * p], unit[nt][0], off0));
@@ -659,7 +676,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionArgs
       }
       // V: tokens v0, v1 (k = 2c, 2c + 1) and 8 more, words NW r .. of each row
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+      for (int mt = 0; mt < kTiles; ++mt) {
         uint32_t vw[4][NW], S01[NW], S23[NW];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
@@ -902,6 +919,13 @@ nvfp4_status launch_attention(AttentionArgs a, cudaStream_t stream) {
   a.chunk_heads = (a.G + a.chunks - 1) / a.chunks;
   a.pool_pages = a.kc.num_pages < a.vc.num_pages ? a.kc.num_pages : a.vc.num_pages;
   if (a.pool_pages > INT32_MAX) a.pool_pages = INT32_MAX;
+  const int64_t strides[4] = {a.kc.data_page_stride, a.vc.data_page_stride, a.kc.sf_page_stride, a.vc.sf_page_stride};
+  for (int64_t s : strides)
+    if (s > static_cast<int64_t>(UINT32_MAX)) return fail(NVFP4_ERR_UNSUPPORTED, "nvfp4_paged_attention_decode: a page stride above 4 GiB");
+  a.k_stride = static_cast<uint32_t>(strides[0]);
+  a.v_stride = static_cast<uint32_t>(strides[1]);
+  a.k_sf_stride = static_cast<uint32_t>(strides[2]);
+  a.v_sf_stride = static_cast<uint32_t>(strides[3]);
   if (sm_count() * kMaxCtasPerSm * 4 > NVFP4_COUNTER_BYTES)
     return fail(NVFP4_ERR_UNSUPPORTED, "nvfp4_paged_attention_decode: more SMs than counters");
   // the scale rows' copies: 4 nw bytes (nw = 3: 4 at a time), aligned to that
