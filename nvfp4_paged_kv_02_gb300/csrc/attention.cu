@@ -29,8 +29,9 @@
 // match (any order of d serves, as long as both have it). e2m1 * S is exact in binary16. A
 // query row is scaled by a power of two, so that its largest element is in [2^14, 2^15), and
 // is then exact in binary16 down to 2^-38 of that element.
-// Weights. p = 2^(x log2 e - m + 15), at most 2^15, rounded to binary16 (2^-11 relative, down
-// to 2^-29 of the largest weight) for the second product; their sum is binary32.
+// Weights. p = 2^(x log2 e - m + 8) <= 2^15 (m may lag behind the maximum by 7), rounded to
+// binary16 for the second product: 2^-11 relative, and below 2^-14, that is 2^-22 of the weight
+// at m, an absolute 2^-25. Their sum is binary32.
 // Output. O^T = V^T P^T: A is V^T (16 of d), B is P^T, which movmatrix makes of S^T. A
 // fragment pairs tokens, codes pair elements of d, so nibbles of two tokens are interleaved
 // before they are decoded.
@@ -50,7 +51,8 @@ constexpr int kTiles = kUnit / 16;  // of 16 tokens
 constexpr int kMinUnits = 4;  // of a CTA's run: one for each warp
 constexpr int kMaxCtasPerSm = 4;
 constexpr int kSegmentCost = 2;
-constexpr float kWeightBias = 15.0f;
+constexpr float kWeightBias = 8.0f;
+constexpr float kSlack = 7.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ---- instructions ------------------------------------------------------------------------
@@ -158,6 +160,22 @@ __device__ __forceinline__ void scan_places(const AttentionArgs& a, int64_t* cum
   __syncthreads();
 }
 
+// a / b, by 32-bit division where both are small.
+__device__ __forceinline__ int64_t quotient64(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// The cut of `total` places into n runs: the first `more` runs have per + 1 places.
+struct Cut {
+  int64_t per, more;
+  __device__ __forceinline__ int64_t begin(int64_t run) const { return run * per + min(run, more); }
+  __device__ __forceinline__ int64_t run_of(int64_t place) const {
+    const int64_t edge = more * (per + 1);
+    return place < edge ? quotient64(place, per + 1) : more + quotient64(place - edge, per);
+  }
+};
+
 // One (request, head, chunk of query heads), and the place of its first unit relative to the
 // run's first.
 struct Segment {
@@ -173,14 +191,20 @@ __device__ __forceinline__ Segment find_segment(const AttentionArgs& a, const in
   }
   Segment s{lo, 0, 0, 0, 0};
   int64_t start = lo > 0 ? cum[lo - 1] : 0;
-  for (;;) {
-    s.units = units_of(a, s.b, s.h);
+  s.units = units_of(a, s.b, 0);
+  if (a.selected) {
+    for (;;) {
+      const int64_t head = static_cast<int64_t>(places_of(s.units)) * a.chunks;
+      if (place < start + head || s.h + 1 == a.H) break;
+      start += head;
+      s.units = units_of(a, s.b, ++s.h);
+    }
+  } else {
     const int64_t head = static_cast<int64_t>(places_of(s.units)) * a.chunks;
-    if (place < start + head || s.h + 1 == a.H) break;
-    start += head;
-    ++s.h;
+    s.h = static_cast<int32_t>(quotient64(place - start, head));
+    start += s.h * head;
   }
-  if (s.units > 0) s.chunk = static_cast<int32_t>((place - start) / places_of(s.units));
+  if (a.chunks > 1) s.chunk = static_cast<int32_t>(quotient64(place - start, places_of(s.units)));
   s.start = static_cast<int32_t>(start + static_cast<int64_t>(s.chunk) * places_of(s.units) - place);
   return s;
 }
@@ -257,26 +281,33 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
   const int D = FULL ? 64 * NW : a.D;
   scan_places(a, cum, s_scan);
 
-  // heads without live tokens: zeros
-  for (int32_t b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const int64_t reach = a.max_pages * a.ps;
-    if (tid == 0 && __ldg(a.seq_lens + b) > reach) flag(a.status, NVFP4_DEV_LEN_CLAMPED);
-    if (!a.selected && units_of(a, b, 0) > 0) continue;
-    for (int32_t h = 0; h < a.H; ++h) {
-      if (units_of(a, b, h) > 0) continue;
-      const int64_t row = static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(h) * a.G;
-      uint2* o = reinterpret_cast<uint2*>(a.out + row * D * 2);
-      for (int i = tid; i < a.G * D / 4; i += kThreads) o[i] = make_uint2(0, 0);
-      for (int i = tid; i < a.G && a.lse; i += kThreads) a.lse[row + i] = -INFINITY;
+  // heads without live tokens get zeros
+  auto write_zeros = [&] {
+    for (int32_t b = blockIdx.x; b < a.B; b += gridDim.x) {
+      const int64_t reach = a.max_pages * a.ps;
+      if (tid == 0 && __ldg(a.seq_lens + b) > reach) flag(a.status, NVFP4_DEV_LEN_CLAMPED);
+      if (!a.selected && units_of(a, b, 0) > 0) continue;
+      for (int32_t h = 0; h < a.H; ++h) {
+        if (units_of(a, b, h) > 0) continue;
+        const int64_t row = static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(h) * a.G;
+        uint2* o = reinterpret_cast<uint2*>(a.out + row * D * 2);
+        for (int i = tid; i < a.G * D / 4; i += kThreads) o[i] = make_uint2(0, 0);
+        for (int i = tid; i < a.G && a.lse; i += kThreads) a.lse[row + i] = -INFINITY;
+      }
     }
-  }
-
+  };
   const int64_t total = cum[a.B - 1];
   const int64_t want = (total + kMinUnits - 1) / kMinUnits;
   const int64_t ncta = want < gridDim.x ? want : gridDim.x;
-  if (blockIdx.x >= ncta) return;
-  const int64_t c0 = total * blockIdx.x / ncta;
-  const int32_t run = static_cast<int32_t>(total * (blockIdx.x + 1) / ncta - c0);  // places
+  if (blockIdx.x >= ncta) {
+    write_zeros();
+    return;
+  }
+  Cut cut;
+  cut.per = quotient64(total, ncta);
+  cut.more = total - cut.per * ncta;
+  const int64_t c0 = cut.begin(blockIdx.x);
+  const int32_t run = static_cast<int32_t>(cut.per + (blockIdx.x < cut.more ? 1 : 0));  // places
 
   const uint32_t ring = smem_addr(smem) + warp * NS * T::kBytes;
   uint8_t* const ring_p = smem + warp * NS * T::kBytes;
@@ -286,9 +317,25 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
     __syncwarp();
   }
 
-  // -- the producer: this warp's units, one looked up ahead of its copies --
   Segment cs = find_segment(a, cum, c0);  // the consumer's segment
-  Segment ps = cs;                        // the producer's
+  uint32_t raw[NT][8 * NW];  // the coming segment's query rows, as they are
+  auto load_queries = [&](const Segment& s) {
+    const int head0 = s.chunk * a.chunk_heads, heads = min(a.chunk_heads, a.G - head0);
+    const uint8_t* q = a.q + s.b * a.q_row_bytes +
+                       ((static_cast<int64_t>(s.h) * a.G + head0 + r) * D + 16 * NW * c) * 2;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2 * NW; ++i) {
+        const bool in = 8 * nt + r < heads && 16 * NW * c + 8 * i < D;
+        const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(q + 16 * nt * D) + i) : uint4{};
+        raw[nt][4 * i] = x.x; raw[nt][4 * i + 1] = x.y; raw[nt][4 * i + 2] = x.z; raw[nt][4 * i + 3] = x.w;
+      }
+  };
+  load_queries(cs);
+
+  Segment ps = cs;  // the producer's segment
+  // -- the producer: this warp's units, one looked up ahead of its copies --
   // the units [u, end) of a segment that lie in this run
   auto portion = [&](const Segment& s, int32_t& u, int32_t& end) {
     u = max(-s.start, 0);
@@ -465,21 +512,6 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
   const int t0 = token_of(r);                    // this lane's K rows: t0 and t0 + 8
   const int v0 = token_of(2 * c), v1 = token_of(2 * c + 1);  // its V rows, and 8 more
   int stage = 0, refill = NS - 1;
-  uint32_t raw[NT][8 * NW];  // the coming segment's query rows, as they are
-  auto load_queries = [&](const Segment& s) {
-    const int head0 = s.chunk * a.chunk_heads, heads = min(a.chunk_heads, a.G - head0);
-    const uint8_t* q = a.q + s.b * a.q_row_bytes +
-                       ((static_cast<int64_t>(s.h) * a.G + head0 + r) * D + 16 * NW * c) * 2;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2 * NW; ++i) {
-        const bool in = 8 * nt + r < heads && 16 * NW * c + 8 * i < D;
-        const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(q + 16 * nt * D) + i) : uint4{};
-        raw[nt][4 * i] = x.x; raw[nt][4 * i + 1] = x.y; raw[nt][4 * i + 2] = x.z; raw[nt][4 * i + 3] = x.w;
-      }
-  };
-  load_queries(cs);
   for (;;) {
     // the segment's query heads
     const int head0 = cs.chunk * a.chunk_heads;
@@ -625,8 +657,10 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
               x[2 * g + k / 2][nt][k % 2 * 2] = x[2 * g + k / 2][nt][k % 2 * 2 + 1] = -INFINITY;
           }
       }
-      bool grew = false;
+      // The maximum follows the scores only when one is more than kSlack above it: until then a
+      // weight is at most 2^(kWeightBias + kSlack), which binary16 holds.
       float top[NT][2];
+      bool grew = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -634,18 +668,19 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
           float v = fmaxf(x[0][nt][k], x[0][nt][k + 2]);
 #pragma unroll
           for (int mt = 1; mt < kTiles; ++mt) v = fmaxf(v, fmaxf(x[mt][nt][k], x[mt][nt][k + 2]));
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
           top[nt][k] = v * unit[nt][k];
-          grew = grew || top[nt][k] > m[nt][k];
+          grew = grew || top[nt][k] > m[nt][k] + kSlack;
         }
       if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float m2 = fmaxf(m[nt][k], top[nt][k]);
+            float m2 = top[nt][k];
+            m2 = fmaxf(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 4));
+            m2 = fmaxf(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 8));
+            m2 = fmaxf(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 16));
+            m2 = fmaxf(m2, m[nt][k]);
             const float f = m2 == -INFINITY ? 1.0f : ex2(m[nt][k] - m2);
             m[nt][k] = m2;
             l[nt][k] *= f;
@@ -810,60 +845,78 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
     if (whole) {
       write_out();
     } else {
-      // this run's part of a segment that others share; slot 0 of a CTA if the segment began before
-      // its run, else slot 1
-      constexpr int kSlot = kHeads * (64 * NW + 2);
+      // this run's part of a segment that others share; slot 0 of a run if the segment began before
+      // it, else slot 1
+      constexpr int kStats = kHeads * 64 * NW, kSlot = kStats + 2 * kHeads;
       float* const parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + NVFP4_COUNTER_BYTES);
-      // (run i begins at place total * i / ncta)
       const int64_t start = c0 + done.start;
-      const int64_t first = ((start + 1) * ncta - 1) / total;
-      const int64_t last = ((start + done.units) * ncta - 1) / total;
-      float* part = parts + (2 * static_cast<int64_t>(blockIdx.x) + (done.start >= 0 ? 1 : 0)) * kSlot;
+      const int32_t first = static_cast<int32_t>(cut.run_of(start));
+      const int32_t last = static_cast<int32_t>(cut.run_of(start + done.units - 1));
+      auto part_of = [&](int32_t i) { return parts + (2 * static_cast<int64_t>(i) + (i == first ? 1 : 0)) * kSlot; };
+      float* part = part_of(blockIdx.x);
       for (int i = tid; i < heads * D / 4; i += kThreads) {
         const int head = i / (D / 4), d = i % (D / 4) * 4;
         __stcg(reinterpret_cast<float4*>(part + head * (64 * NW) + d), joined(head, d));
       }
       if (tid < heads) {
-        __stcg(part + kHeads * 64 * NW + tid, s_top[tid]);
-        __stcg(part + kHeads * 64 * NW + kHeads + tid, s_sum[tid]);
+        __stcg(part + kStats + tid, s_top[tid]);
+        __stcg(part + kStats + kHeads + tid, s_sum[tid]);
       }
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
+        // releases what the CTA wrote (the barrier puts it before) and acquires what others released
         uint32_t* counter = static_cast<uint32_t*>(a.workspace) + first;
-        s_last = atomicAdd(counter, 1u) == static_cast<uint32_t>(last - first);
+        uint32_t before;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+        s_last = before == static_cast<uint32_t>(last - first);
         if (s_last) *counter = 0;
-        __threadfence();
       }
       __syncthreads();
       if (s_last) {
-        // the last of them: warp w adds up the parts first + w, first + w + 4, ...
-        auto part_of = [&](int64_t i) {
-          return parts + (2 * i + (i == first ? 1 : 0)) * kSlot;
-        };
-        for (int head = lane; head < heads; head += 32) {
-          float M = -INFINITY;
-          for (int64_t i = first + warp; i <= last; i += kWarps) M = fmaxf(M, __ldcg(part_of(i) + kHeads * 64 * NW + head));
-          float L = 0.0f;
-          for (int64_t i = first + warp; i <= last; i += kWarps) {
-            const float mi = __ldcg(part_of(i) + kHeads * 64 * NW + head);
-            if (mi != -INFINITY) L += ex2(mi - M) * __ldcg(part_of(i) + kHeads * 64 * NW + kHeads + head);
+        // The last of them adds all up, in the runs' order. Loads go out kBatch at a time: this is a
+        // chain of trips to L2. A warp takes every fourth part.
+        constexpr int kBatch = 8;
+        for (int head = lane; head < kHeads; head += 32) {
+          float M = -INFINITY, L = 0.0f;
+          for (int32_t i0 = first + warp; i0 <= last; i0 += kBatch * kWarps) {
+            float mi[kBatch], li[kBatch], top = M;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const int32_t i = i0 + k * kWarps;
+              const bool in = i <= last && head < heads;
+              mi[k] = in ? __ldcg(part_of(i) + kStats + head) : -INFINITY;
+              li[k] = in ? __ldcg(part_of(i) + kStats + kHeads + head) : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) top = fmaxf(top, mi[k]);
+            if (top == -INFINITY) continue;
+            L *= ex2(M - top);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) L += ex2(mi[k] - top) * li[k];
+            M = top;
           }
           s_m[warp][head] = M;
           s_l[warp][head] = L;
         }
         __syncwarp();
-        for (int k = lane; k < heads * D / 4; k += 32) {
-          const int head = k / (D / 4), d = k % (D / 4) * 4;
+        for (int k0 = lane; k0 < heads * D / 4; k0 += 32) {
+          const int head = k0 / (D / 4), d = k0 % (D / 4) * 4;
           const float M = s_m[warp][head];
           float4 v{0, 0, 0, 0};
-#pragma unroll 4
-          for (int64_t i = first + warp; i <= last; i += kWarps) {
-            const float* p = part_of(i);
-            const float mi = __ldcg(p + kHeads * 64 * NW + head);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(p + head * (64 * NW) + d));
-            const float f = mi == -INFINITY ? 0.0f : ex2(mi - M);
-            v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
+          for (int32_t i0 = first + warp; i0 <= last; i0 += kBatch * kWarps) {
+            float mi[kBatch];
+            float4 x[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const int32_t i = i0 + k * kWarps;
+              mi[k] = i <= last ? __ldcg(part_of(i) + kStats + head) : -INFINITY;
+              x[k] = i <= last ? __ldcg(reinterpret_cast<const float4*>(part_of(i) + head * (64 * NW) + d)) : float4{};
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const float f = mi[k] == -INFINITY ? 0.0f : ex2(mi[k] - M);
+              v.x += f * x[k].x; v.y += f * x[k].y; v.z += f * x[k].z; v.w += f * x[k].w;
+            }
           }
           *reinterpret_cast<float4*>(s_o + (warp * kHeads + head) * kPitch + d) = v;
         }
@@ -876,6 +929,7 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
     __syncthreads();  // the buffers of the join are free again
   }
   cp_async_wait<0>();
+  write_zeros();
 }
 
 template <int NW, int NT, bool FULL>
