@@ -46,7 +46,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;     // tokens
-constexpr int kHalves = kUnit / 32;
 constexpr int kTiles = kUnit / 16;  // of 16 tokens
 constexpr int kMinUnits = 4;  // of a CTA's run: one for each warp
 constexpr int kMaxCtasPerSm = 4;
@@ -260,26 +259,40 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 
 // ---- the kernel ------------------------------------------------------------------------------
 
+// How a unit's rows come to shared memory.
+//   kBulk: the rows of a head are contiguous inside a page (HND, or one head): a bulk copy for each
+//          tensor and page, about a third of the instructions of kRows. Needs D = 64 NW, page_size a
+//          multiple of 4, scales aligned to 16 bytes.
+//   kRows: cp.async of 16 bytes. D = 64 NW, scale rows aligned to their size (NW = 3: to 4 bytes).
+//   kAny:  any D, scales of any alignment (through registers).
+enum { kAny, kRows, kBulk };
+
+__device__ __forceinline__ int round4(int n) { return (n + 3) & ~3; }
+
 // NW: words of codes that a lane holds of a V row (D <= 64 NW). NT: eights of query heads.
-// FULL: D = 64 NW and scale rows that cp.async can copy; otherwise any D, and scales of any
-// alignment, which go through registers.
-template <int NW, int NT, bool FULL>
-__global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attention_kernel(const AttentionArgs a) {
+template <int NW, int NT, int PATH>
+__global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attention_kernel(const AttentionArgs a) {
   using T = Tile<NW>;
   constexpr int NS = kStages;
   constexpr int kHeads = 8 * NT;
   constexpr int kPitch = 64 * NW + 4;  // floats of a row of O in shared memory
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t s_full[kWarps * NS];  // kBulk: a stage's bytes have arrived
   __shared__ int64_t s_scan[kWarps];
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads], s_f[kWarps][kHeads], s_top[kHeads], s_sum[kHeads];
-  __shared__ int s_last;
+  __shared__ struct { int32_t b, h, chunk, first, last, join; } s_shared[2];  // segments shared with other runs
   float* s_o = reinterpret_cast<float*>(smem + kWarps * NS * T::kBytes);  // [kWarps][kHeads][kPitch]
   int64_t* cum = reinterpret_cast<int64_t*>(s_o + kWarps * kHeads * kPitch);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
-  const int D = FULL ? 64 * NW : a.D;
-  scan_places(a, cum, s_scan);
+  const int D = PATH == kAny ? a.D : 64 * NW;
+  uint64_t* const full = s_full + warp * NS;
+  if (PATH == kBulk && tid == 0) {
+    for (int s = 0; s < kWarps * NS; ++s) mbar_init(s_full + s, 1);
+    fence_mbar_init();
+  }
+  scan_places(a, cum, s_scan);  // ends with a barrier
 
   // heads without live tokens get zeros
   auto write_zeros = [&] {
@@ -311,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
 
   const uint32_t ring = smem_addr(smem) + warp * NS * T::kBytes;
   uint8_t* const ring_p = smem + warp * NS * T::kBytes;
-  if (!FULL) {
+  if (PATH == kAny) {
     // what lies between D and 64 NW stays zero: no copy writes there
     for (int i = lane; i < NS * T::kBytes / 16; i += 32) reinterpret_cast<uint4*>(ring_p)[i] = uint4{};
     __syncwarp();
@@ -362,147 +375,165 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
     }
   };
   settle();
-  // This lane's rows of the unit looked up. The table's entries stay as they were loaded until
-  // the copies are issued, so that nothing waits for them here.
-  int32_t lk_lo[kHalves], lk_hi[kHalves], lk_row[kHalves];
-  bool lk_unit = false, lk_live[kHalves];
+  // What this lane has looked up of the next unit. The table's entry stays as it was loaded
+  // until the copies are issued, so that nothing waits for it here.
+  //   kBulk: lane 4 i + k copies tensor k (codes of K and V, scales of K and V) of the unit's
+  //   i-th page: the rows [lk_row, lk_row + lk_count) of a head, contiguous there, as one bulk copy.
+  //   Otherwise lane i looks up row i, which the lanes then copy 16 (or 8) bytes at a time.
+  int32_t lk_lo = 0, lk_hi = 0, lk_count = 0;
+  uint32_t lk_row = 0, lk_at = 0, lk_live = ~0u;  // (lk_live: rows that the window leaves)
+  bool lk_unit = false;
+  auto load_entry = [&](int32_t col) {
+    const int32_t* entry = reinterpret_cast<const int32_t*>(list + (static_cast<int64_t>(col) << (a.table64 ? 3 : 2)));
+    lk_lo = __ldg(entry);
+    if (a.table64) lk_hi = __ldg(entry + 1);
+  };
   auto look_up = [&] {
     lk_unit = pu < pend;
-#pragma unroll
-    for (int g = 0; g < kHalves; ++g) {
-      lk_live[g] = false;
-      lk_lo[g] = lk_hi[g] = lk_row[g] = 0;
-      if (!lk_unit) continue;
-      int32_t col, slot;
-      if (a.selected) {
-        const int32_t p = pu * kUnit + 32 * g + lane;
-        const int32_t i = div_q32(p, a.div_ps);
-        slot = p - i * a.ps;
-        lk_live[g] = p < slots;
-        col = lk_live[g] ? __ldg(a.selected + (static_cast<int64_t>(ps.b) * a.H + ps.h) * a.max_selected + i) : 0;
-        if (col < 0 || col >= a.max_pages) {
-          flag(a.status, NVFP4_DEV_BAD_PAGE);
-          lk_live[g] = false;
-        }
-        lk_live[g] = lk_live[g] && static_cast<int64_t>(col) * a.ps + slot < span.len;
-      } else {
-        const uint32_t t = (static_cast<uint32_t>(span.lo / kUnit) + pu) * kUnit + 32 * g + lane;
-        lk_live[g] = t >= static_cast<uint32_t>(span.lo) && t < static_cast<uint32_t>(span.len);
-        col = lk_live[g] ? div_q32(static_cast<int32_t>(t), a.div_ps) : 0;
-        slot = static_cast<int32_t>(t) - col * a.ps;
-      }
-      if (lk_live[g]) {
-        const int32_t* entry = reinterpret_cast<const int32_t*>(list + (static_cast<int64_t>(col) << (a.table64 ? 3 : 2)));
-        lk_lo[g] = __ldg(entry);
-        if (a.table64) lk_hi[g] = __ldg(entry + 1);
-        lk_row[g] = a.layout == NVFP4_NHD ? slot * a.H + ps.h : ps.h * a.ps + slot;
-      }
+    lk_count = 0;
+    if (!lk_unit) return;
+    // position of the unit: a token, or a slot of the selected pages
+    const int32_t p0 = static_cast<int32_t>(static_cast<uint32_t>((a.selected ? 0 : span.lo / kUnit) + pu) * kUnit);
+    const int32_t end = a.selected ? slots : span.len;
+    if (PATH == kBulk) lk_live = !a.selected && span.lo > p0 ? ~0u << (span.lo - p0) : ~0u;
+    int32_t p, n, col;
+    if (PATH == kBulk) {
+      col = div_q32(p0, a.div_ps) + (lane >> 2);
+      const int64_t from = static_cast<int64_t>(col) * a.ps;  // the page's positions
+      p = static_cast<int32_t>(max(from, static_cast<int64_t>(p0)));
+      n = static_cast<int32_t>(min(min(from + a.ps, static_cast<int64_t>(p0) + kUnit), static_cast<int64_t>(end)) - p);
+    } else {
+      p = p0 + lane;
+      col = div_q32(p, a.div_ps);
+      n = p < end && p >= (a.selected ? 0 : span.lo) ? 1 : 0;
     }
+    if (n <= 0) return;
+    const int32_t slot = p - col * a.ps;
+    if (a.selected) {
+      col = __ldg(a.selected + (static_cast<int64_t>(ps.b) * a.H + ps.h) * a.max_selected + col);
+      if (col < 0 || col >= a.max_pages) {
+        flag(a.status, NVFP4_DEV_BAD_PAGE);
+        return;
+      }
+      n = static_cast<int32_t>(min(static_cast<int64_t>(n), span.len - static_cast<int64_t>(col) * a.ps - slot));
+      if (n <= 0) return;
+    }
+    load_entry(col);
+    lk_row = a.layout == NVFP4_NHD ? slot * a.H + ps.h : ps.h * a.ps + slot;
+    lk_at = p - p0;
+    lk_count = n;
   };
   look_up();
 
-  // !FULL: scale bytes on their way to the stage of the unit issued last
-  uint32_t pk[kHalves][NW], pv[kHalves][NW];
-  int pend_stage = -1;
+  // The rows of a page of the unit that are copied: whole groups of four, so that a copy of scales
+  // is a multiple of 16 bytes (the page has them: page_size is a multiple of four there).
+  const int kind = lane & 3;
+  const uint8_t* const bulk_base = kind == 0 ? a.kc.data : (kind == 1 ? a.vc.data : (kind == 2 ? a.kc.sf : a.vc.sf));
+  const uint32_t bulk_stride = kind == 0 ? a.k_stride : (kind == 1 ? a.v_stride : (kind == 2 ? a.k_sf_stride : a.v_sf_stride));
+  const uint32_t bulk_row = kind < 2 ? T::kRow : T::kScales;
+  const uint32_t bulk_at = kind == 0 ? 0 : (kind == 1 ? T::kV : (kind == 2 ? T::kKs : T::kVs));
+
+  // kAny: scale bytes on their way to the stage of the unit issued last
+  uint32_t pk[NW], pv[NW];
+  int carried_stage = -1;
   const int nb = D / 16;
   auto put_scales = [&] {
-    if (pend_stage < 0) return;
-    uint8_t* st = ring_p + pend_stage * T::kBytes;
+    if (carried_stage < 0) return;
+    uint8_t* st = ring_p + carried_stage * T::kBytes + lane * T::kScales;
 #pragma unroll
-    for (int g = 0; g < kHalves; ++g)
-#pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        *reinterpret_cast<uint32_t*>(st + T::kKs + (32 * g + lane) * T::kScales + 4 * i) = pk[g][i];
-        *reinterpret_cast<uint32_t*>(st + T::kVs + (32 * g + lane) * T::kScales + 4 * i) = pv[g][i];
-      }
+    for (int w = 0; w < NW; ++w) {
+      *reinterpret_cast<uint32_t*>(st + T::kKs + 4 * w) = pk[w];
+      *reinterpret_cast<uint32_t*>(st + T::kVs + 4 * w) = pv[w];
+    }
   };
+  uint32_t parity = 0, flight = 0;  // of the stages: their barriers' phase, and copies not waited for
+  bool gave_up = false;             // a wait ran out: nothing more is copied
+  bool stall = PATH == kBulk && a.pipe.stall != 0;  // test control: withhold the first unit
   // Copies of the unit looked up into stage s, then the look-up of the next one.
   auto issue = [&](int s) {
-    if (!FULL) put_scales();
-    if (lk_unit) {
+    if (PATH == kAny) put_scales();
+    if (lk_unit && !gave_up) {
       const uint32_t st = ring + s * T::kBytes;
-#pragma unroll
-      for (int g = 0; g < kHalves; ++g) {
-        uint32_t page = 0, rw = 0;  // (a row that is not live is copied as zeros)
-        bool live = false;
-        if (lk_live[g]) {
-          const int64_t entry = a.table64 ? (static_cast<int64_t>(lk_hi[g]) << 32) | static_cast<uint32_t>(lk_lo[g]) : lk_lo[g];
-          if (entry >= 0 && entry < a.pool_pages) {
-            live = true;
-            page = static_cast<uint32_t>(entry);
-            rw = lk_row[g];
-          } else {
-            flag(a.status, NVFP4_DEV_BAD_PAGE);
-          }
-        }
-        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, live);
-        if (lane == 0) *reinterpret_cast<uint32_t*>(ring_p + s * T::kBytes + T::kMask + 4 * g) = mask;
+      uint32_t page = static_cast<uint32_t>(lk_lo);
+      int32_t n = lk_count;
+      if (n > 0 && (page >= a.pool_pages || (a.table64 && lk_hi != 0))) {
+        flag(a.status, NVFP4_DEV_BAD_PAGE);
+        n = 0;
+      }
+      uint32_t mask;
+      if (PATH == kBulk) {
+        mask = n > 0 ? (n >= 32 ? ~0u : (1u << n) - 1u) << lk_at : 0u;
+        mask = __reduce_or_sync(0xFFFFFFFFu, mask) & lk_live;
+        const uint32_t bytes = n > 0 ? static_cast<uint32_t>(round4(n)) * bulk_row : 0u;
+        const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, bytes);
+        if (lane == 0 && !stall) mbar_arrive_expect_tx(full + s, all);
+        __syncwarp();
+        if (bytes > 0 && !stall)
+          bulk_g2s(ring_p + s * T::kBytes + bulk_at + lk_at * bulk_row,
+                   bulk_base + static_cast<uint64_t>(page) * bulk_stride + static_cast<uint64_t>(lk_row) * bulk_row, bytes,
+                   full + s);
+        stall = false;
+        flight |= 1u << s;
+      } else {
+        const bool live = n > 0;
+        if (!live) page = 0;  // (a row that is not live is copied as zeros)
+        const uint32_t rw = live ? lk_row : 0;
+        mask = __ballot_sync(0xFFFFFFFFu, live);
         const uint8_t* ks = a.kc.sf + static_cast<uint64_t>(page) * a.k_sf_stride + static_cast<uint64_t>(rw) * nb;
         const uint8_t* vs = a.vc.sf + static_cast<uint64_t>(page) * a.v_sf_stride + static_cast<uint64_t>(rw) * nb;
-        const uint32_t ksd = st + T::kKs + (32 * g + lane) * T::kScales;
-        const uint32_t vsd = st + T::kVs + (32 * g + lane) * T::kScales;
-        if (FULL) {
+        const uint32_t ksd = st + T::kKs + lane * T::kScales, vsd = st + T::kVs + lane * T::kScales;
+        if (PATH == kRows) {
           constexpr int kPart = NW == 3 ? 4 : 4 * NW;
 #pragma unroll
-          for (int i = 0; i < T::kScales / kPart; ++i) {
-            cp_async<kPart>(ksd + i * kPart, ks + i * kPart, live);
-            cp_async<kPart>(vsd + i * kPart, vs + i * kPart, live);
+          for (int w = 0; w < T::kScales / kPart; ++w) {
+            cp_async<kPart>(ksd + w * kPart, ks + w * kPart, live);
+            cp_async<kPart>(vsd + w * kPart, vs + w * kPart, live);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < NW; ++i) pk[g][i] = pv[g][i] = 0;
+          for (int w = 0; w < NW; ++w) pk[w] = pv[w] = 0;
 #pragma unroll
-          for (int i = 0; i < 4 * NW; ++i) {
-            if (live && i < nb) {
-              pk[g][i / 4] |= static_cast<uint32_t>(__ldg(ks + i)) << (8 * (i % 4));
-              pv[g][i / 4] |= static_cast<uint32_t>(__ldg(vs + i)) << (8 * (i % 4));
+          for (int w = 0; w < 4 * NW; ++w) {
+            if (live && w < nb) {
+              pk[w / 4] |= static_cast<uint32_t>(__ldg(ks + w)) << (8 * (w % 4));
+              pv[w / 4] |= static_cast<uint32_t>(__ldg(vs + w)) << (8 * (w % 4));
             }
           }
-          pend_stage = s;
         }
-        const uint8_t *kp, *vp;
-        auto row_at = [&](int row) {
+        auto copy = [&](int row, int off, auto bytes) {
+          constexpr int B = decltype(bytes)::value;
           const uint32_t pg = __shfl_sync(0xFFFFFFFFu, page, row);
-          const uint32_t r2 = __shfl_sync(0xFFFFFFFFu, rw, row);
-          kp = a.kc.data + static_cast<uint64_t>(pg) * a.k_stride + static_cast<uint64_t>(r2) * (D / 2);
-          vp = a.vc.data + static_cast<uint64_t>(pg) * a.v_stride + static_cast<uint64_t>(r2) * (D / 2);
+          const uint64_t in = static_cast<uint64_t>(__shfl_sync(0xFFFFFFFFu, rw, row)) * (D / 2) + off;
+          const bool ok = mask >> row & 1u;
+          const uint32_t at = st + row * T::kRow + (((off >> 4) ^ (PATH == kBulk ? 0 : T::swizzle(row))) << 4) + (off & 15);
+          cp_async<B>(at, a.kc.data + static_cast<uint64_t>(pg) * a.k_stride + in, ok);
+          cp_async<B>(at + T::kV, a.vc.data + static_cast<uint64_t>(pg) * a.v_stride + in, ok);
         };
-        if (FULL) {
-          // two lanes to a row: each copy takes whole 32-byte sectors, and a lane has few rows
+        if (PATH == kRows) {
+          constexpr int kChunks = 2 * NW;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int row = 16 * i + (lane >> 1);
-            row_at(row);
-            const bool ok = mask >> row & 1u;
-            const uint32_t dst = st + (32 * g + row) * T::kRow;
-            const int sw = T::swizzle(row);
-#pragma unroll
-            for (int j = 0; j < NW; ++j) {
-              const uint32_t at = dst + (((2 * j + (lane & 1)) ^ sw) << 4);
-              const int off = 16 * (lane & 1) + 32 * j;
-              cp_async<16>(at, kp + off, ok);
-              cp_async<16>(at + T::kV, vp + off, ok);
-            }
+          for (int i = 0; i < kChunks; ++i) {
+            const int k = i * 32 + lane;
+            copy(k / kChunks, k % kChunks * 16, std::integral_constant<int, 16>{});
           }
         } else {
-          const int chunks = D / 16;  // of 8 bytes
-          for (int i = 0; i < chunks; ++i) {
-            const int k = i * 32 + lane, row = k / chunks, off = k % chunks * 8;
-            row_at(row);
-            const bool ok = mask >> row & 1u;
-            const uint32_t at = st + (32 * g + row) * T::kRow + (((off >> 4) ^ T::swizzle(row)) << 4) + (off & 15);
-            cp_async<8>(at, kp + off, ok);
-            cp_async<8>(at + T::kV, vp + off, ok);
-          }
+          // eight rows at a time, four lanes to a row
+          for (int i = 0; i < 4; ++i)
+            for (int w = 0; w < nb; w += 4) {
+              const int off = min(w + (lane & 3), nb - 1) * 8;  // (the last chunk again, rather than none)
+              copy(8 * i + (lane >> 2), off, std::integral_constant<int, 8>{});
+            }
         }
       }
+      if (lane == 0) *reinterpret_cast<uint32_t*>(ring_p + s * T::kBytes + T::kMask) = mask;
+      carried_stage = s;
       pu += kWarps;
       settle();
       look_up();
     } else {
-      pend_stage = -1;
+      carried_stage = -1;
     }
-    cp_async_commit();
+    if (PATH != kBulk) cp_async_commit();
   };
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s) issue(s);
@@ -511,6 +542,55 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
   const float gk = __ldg(a.k_scale), gv = __ldg(a.v_scale);
   const int t0 = token_of(r);                    // this lane's K rows: t0 and t0 + 8
   const int v0 = token_of(2 * c), v1 = token_of(2 * c + 1);  // its V rows, and 8 more
+  // factors of the four parts and the joined maximum and sum, by the first threads
+  auto join_stats = [&] {
+    if (tid < kHeads) {
+      float M = -INFINITY, L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][tid]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = s_m[w][tid] == -INFINITY ? 0.0f : ex2(s_m[w][tid] - M);
+        s_f[w][tid] = f;
+        L += f * s_l[w][tid];
+      }
+      s_top[tid] = M;
+      s_sum[tid] = L;
+    }
+    __syncthreads();
+  };
+  auto joined = [&](int head, int d) {
+    float4 v{0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kHeads + head) * kPitch + d);
+      const float f = s_f[w][head];
+      v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
+    }
+    return v;
+  };
+  auto write_out = [&](int64_t row, int heads) {
+    for (int i = tid; i < heads * D / 4; i += kThreads) {
+      const int head = i / (D / 4), d = i % (D / 4) * 4;
+      const float4 v = joined(head, d);
+      const float f = s_sum[head] == 0.0f ? 0.0f : gv / s_sum[head];
+      uint2 w;
+      w.x = a.bf16 ? bf16x2_from_f32(v.x * f, v.y * f) : f16x2_from_f32(v.x * f, v.y * f);
+      w.y = a.bf16 ? bf16x2_from_f32(v.z * f, v.w * f) : f16x2_from_f32(v.z * f, v.w * f);
+      *reinterpret_cast<uint2*>(a.out + ((row + head) * D + d) * 2) = w;
+    }
+    if (a.lse && tid < heads)
+      a.lse[row + tid] = s_sum[tid] == 0.0f ? -INFINITY
+                                            : (s_top[tid] - kWeightBias) * (1.0f / kLog2e) + logf(s_sum[tid]);
+  };
+  // Parts of shared segments: run i's slot 0 if the segment began before the run, else its slot 1.
+  constexpr int kStats = kHeads * 64 * NW, kSlot = kStats + 2 * kHeads;
+  float* const parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + NVFP4_COUNTER_BYTES);
+  auto part_of = [&](int32_t i, int32_t first) {
+    return parts + (2 * static_cast<int64_t>(i) + (i == first ? 1 : 0)) * kSlot;
+  };
+  uint32_t arrived0 = 0, arrived1 = 0;
+  int shared = 0;
   int stage = 0, refill = NS - 1;
   for (;;) {
     // the segment's query heads
@@ -574,15 +654,35 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
     portion(cs, cu, cend);
     const bool whole = cu == 0 && cend == cs.units;
     for (cu += warp; cu < cend; cu += kWarps) {
-      cp_async_wait<NS - 2>();
+      if (PATH != kBulk) {
+        cp_async_wait<NS - 2>();
+      } else if (!gave_up) {
+        if (__all_sync(0xFFFFFFFFu, mbar_wait(full + stage, parity >> stage & 1u, a.pipe.wait_limit))) {
+          parity ^= 1u << stage;
+          flight &= ~(1u << stage);
+        } else {  // what follows is computed from whatever is there, and reported
+          gave_up = true;
+          flag(a.status, NVFP4_DEV_TIMEOUT);
+        }
+      }
       __syncwarp();
       issue(refill);
-      const uint8_t* st = ring_p + stage * T::kBytes;
+      uint8_t* const st = ring_p + stage * T::kBytes;
       refill = stage;
       stage = stage + 1 == NS ? 0 : stage + 1;
-      uint32_t mask[kHalves];
+      const uint32_t mask = *reinterpret_cast<const uint32_t*>(st + T::kMask);
+      if (PATH == kBulk && mask != 0xFFFFFFFFu) {
+        // rows that are not live came as they are, or not at all: their scales become zeros
+        if (!(mask >> lane & 1u)) {
 #pragma unroll
-      for (int g = 0; g < kHalves; ++g) mask[g] = *reinterpret_cast<const uint32_t*>(st + T::kMask + 4 * g);
+          for (int w = 0; w < NW; ++w) {
+            *reinterpret_cast<uint32_t*>(st + T::kKs + lane * T::kScales + 4 * w) = 0;
+            *reinterpret_cast<uint32_t*>(st + T::kVs + lane * T::kScales + 4 * w) = 0;
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copies
+        __syncwarp();
+      }
 
       float x[kTiles][NT][4];
 #pragma unroll
@@ -615,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
                                        : *reinterpret_cast<const uint32_t*>(sr);
 #pragma unroll
             for (int i = 0; i < NW / 2; ++i) {
-              const uint4 v = *reinterpret_cast<const uint4*>(row + (((NW / 2 * c + i) ^ T::swizzle(t)) << 4));
+              const uint4 v = *reinterpret_cast<const uint4*>(row + (((NW / 2 * c + i) ^ (PATH == kBulk ? 0 : T::swizzle(t))) << 4));
               kw[p][4 * i] = v.x; kw[p][4 * i + 1] = v.y; kw[p][4 * i + 2] = v.z; kw[p][4 * i + 3] = v.w;
               const uint32_t s2 = f16x2_from_e4m3x2(i == 0 ? s : s >> 16);
               S2[p][2 * i] = prmt(s2, 0u, 0x1010u);
@@ -646,15 +746,12 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
             for (int k = 0; k < 4; ++k)
               x[mt][nt][k] = soft_capped(x[mt][nt][k] * factor[nt][k & 1], a.soft_cap);
       }
-#pragma unroll
-      for (int g = 0; g < kHalves; ++g) {
-        if (mask[g] == 0xFFFFFFFFu) continue;
+      if (mask != 0xFFFFFFFFu) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (!(mask[g] >> (8 * k + t0) & 1u)) {
+          if (!(mask >> (8 * k + t0) & 1u)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              x[2 * g + k / 2][nt][k % 2 * 2] = x[2 * g + k / 2][nt][k % 2 * 2 + 1] = -INFINITY;
+            for (int nt = 0; nt < NT; ++nt) x[k / 2][nt][k % 2 * 2] = x[k / 2][nt][k % 2 * 2 + 1] = -INFINITY;
           }
       }
       // The maximum follows the scores only when one is more than kSlack above it: until then a
@@ -718,10 +815,10 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
           const int t = 16 * mt + (p >= 2 ? 8 : 0) + ((p & 1) ? v1 : v0);
           const uint8_t* row = st + T::kV + t * T::kRow;
           if (NW == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(row + (((r >> 1) ^ T::swizzle(t)) << 4) + 8 * (r & 1));
+            const uint2 v = *reinterpret_cast<const uint2*>(row + (((r >> 1) ^ (PATH == kBulk ? 0 : T::swizzle(t))) << 4) + 8 * (r & 1));
             vw[p][0] = v.x; vw[p][1 % NW] = v.y;
           } else if (NW == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(row + ((r ^ T::swizzle(t)) << 4));
+            const uint4 v = *reinterpret_cast<const uint4*>(row + ((r ^ (PATH == kBulk ? 0 : T::swizzle(t))) << 4));
             vw[p][0] = v.x; vw[p][1 % NW] = v.y; vw[p][2 % NW] = v.z; vw[p][3 % NW] = v.w;
           } else {
 #pragma unroll
@@ -799,61 +896,16 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
         }
       }
     __syncthreads();
-    // factors of the four parts and the joined maximum and sum, by the first threads
-    auto join_stats = [&] {
-      if (tid < kHeads) {
-        float M = -INFINITY, L = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][tid]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = s_m[w][tid] == -INFINITY ? 0.0f : ex2(s_m[w][tid] - M);
-          s_f[w][tid] = f;
-          L += f * s_l[w][tid];
-        }
-        s_top[tid] = M;
-        s_sum[tid] = L;
-      }
-      __syncthreads();
-    };
-    auto joined = [&](int head, int d) {
-      float4 v{0, 0, 0, 0};
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kHeads + head) * kPitch + d);
-        const float f = s_f[w][head];
-        v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
-      }
-      return v;
-    };
-    auto write_out = [&] {
-      const int64_t row = static_cast<int64_t>(done.b) * a.Hq + q_row;
-      for (int i = tid; i < heads * D / 4; i += kThreads) {
-        const int head = i / (D / 4), d = i % (D / 4) * 4;
-        const float4 v = joined(head, d);
-        const float f = s_sum[head] == 0.0f ? 0.0f : gv / s_sum[head];
-        uint2 w;
-        w.x = a.bf16 ? bf16x2_from_f32(v.x * f, v.y * f) : f16x2_from_f32(v.x * f, v.y * f);
-        w.y = a.bf16 ? bf16x2_from_f32(v.z * f, v.w * f) : f16x2_from_f32(v.z * f, v.w * f);
-        *reinterpret_cast<uint2*>(a.out + ((row + head) * D + d) * 2) = w;
-      }
-      if (a.lse && tid < heads)
-        a.lse[row + tid] = s_sum[tid] == 0.0f ? -INFINITY
-                                              : (s_top[tid] - kWeightBias) * (1.0f / kLog2e) + logf(s_sum[tid]);
-    };
     join_stats();
     if (whole) {
-      write_out();
+      write_out(static_cast<int64_t>(done.b) * a.Hq + q_row, heads);
     } else {
-      // this run's part of a segment that others share; slot 0 of a run if the segment began before
-      // it, else slot 1
-      constexpr int kStats = kHeads * 64 * NW, kSlot = kStats + 2 * kHeads;
-      float* const parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + NVFP4_COUNTER_BYTES);
+      // this run's part of a segment that others share: the last of them will join the parts, at its
+      // end, so that nobody waits here for the count (a run shares at most its first and its last)
       const int64_t start = c0 + done.start;
       const int32_t first = static_cast<int32_t>(cut.run_of(start));
       const int32_t last = static_cast<int32_t>(cut.run_of(start + done.units - 1));
-      auto part_of = [&](int32_t i) { return parts + (2 * static_cast<int64_t>(i) + (i == first ? 1 : 0)) * kSlot; };
-      float* part = part_of(blockIdx.x);
+      float* part = part_of(blockIdx.x, first);
       for (int i = tid; i < heads * D / 4; i += kThreads) {
         const int head = i / (D / 4), d = i % (D / 4) * 4;
         __stcg(reinterpret_cast<float4*>(part + head * (64 * NW) + d), joined(head, d));
@@ -865,76 +917,96 @@ __global__ void __launch_bounds__(kThreads, NW == 2 && NT == 1 ? 3 : 1) attentio
       __syncthreads();
       if (tid == 0) {
         // releases what the CTA wrote (the barrier puts it before) and acquires what others released
-        uint32_t* counter = static_cast<uint32_t*>(a.workspace) + first;
         uint32_t before;
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
-        s_last = before == static_cast<uint32_t>(last - first);
-        if (s_last) *counter = 0;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                     : "=r"(before) : "l"(static_cast<uint32_t*>(a.workspace) + first) : "memory");
+        if (shared == 0) arrived0 = before;
+        else arrived1 = before;
+        s_shared[shared] = {done.b, done.h, done.chunk, first, last, 0};
       }
-      __syncthreads();
-      if (s_last) {
-        // The last of them adds all up, in the runs' order. Loads go out kBatch at a time: this is a
-        // chain of trips to L2. A warp takes every fourth part.
-        constexpr int kBatch = 8;
-        for (int head = lane; head < kHeads; head += 32) {
-          float M = -INFINITY, L = 0.0f;
-          for (int32_t i0 = first + warp; i0 <= last; i0 += kBatch * kWarps) {
-            float mi[kBatch], li[kBatch], top = M;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              const int32_t i = i0 + k * kWarps;
-              const bool in = i <= last && head < heads;
-              mi[k] = in ? __ldcg(part_of(i) + kStats + head) : -INFINITY;
-              li[k] = in ? __ldcg(part_of(i) + kStats + kHeads + head) : 0.0f;
-            }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) top = fmaxf(top, mi[k]);
-            if (top == -INFINITY) continue;
-            L *= ex2(M - top);
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) L += ex2(mi[k] - top) * li[k];
-            M = top;
-          }
-          s_m[warp][head] = M;
-          s_l[warp][head] = L;
-        }
-        __syncwarp();
-        for (int k0 = lane; k0 < heads * D / 4; k0 += 32) {
-          const int head = k0 / (D / 4), d = k0 % (D / 4) * 4;
-          const float M = s_m[warp][head];
-          float4 v{0, 0, 0, 0};
-          for (int32_t i0 = first + warp; i0 <= last; i0 += kBatch * kWarps) {
-            float mi[kBatch];
-            float4 x[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              const int32_t i = i0 + k * kWarps;
-              mi[k] = i <= last ? __ldcg(part_of(i) + kStats + head) : -INFINITY;
-              x[k] = i <= last ? __ldcg(reinterpret_cast<const float4*>(part_of(i) + head * (64 * NW) + d)) : float4{};
-            }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              const float f = mi[k] == -INFINITY ? 0.0f : ex2(mi[k] - M);
-              v.x += f * x[k].x; v.y += f * x[k].y; v.z += f * x[k].z; v.w += f * x[k].w;
-            }
-          }
-          *reinterpret_cast<float4*>(s_o + (warp * kHeads + head) * kPitch + d) = v;
-        }
-        __syncthreads();
-        join_stats();
-        write_out();
-      }
+      ++shared;
     }
     if (last_segment) break;
     __syncthreads();  // the buffers of the join are free again
   }
-  cp_async_wait<0>();
+  // no copy may still be on its way when the CTA ends
+  if (PATH != kBulk) cp_async_wait<0>();
+  for (int s = 0; s < NS; ++s)
+    if (flight >> s & 1u) mbar_wait(full + s, parity >> s & 1u, a.pipe.wait_limit);
+
+  // -- shared segments whose last part was this run's --
+  if (shared > 0) {
+    if (tid == 0) {
+      for (int n = 0; n < shared; ++n)
+        if ((n == 0 ? arrived0 : arrived1) == static_cast<uint32_t>(s_shared[n].last - s_shared[n].first)) {
+          s_shared[n].join = 1;
+          static_cast<uint32_t*>(a.workspace)[s_shared[n].first] = 0;
+        }
+    }
+    __syncthreads();
+    for (int n = 0; n < shared; ++n) {
+      if (!s_shared[n].join) continue;
+      const int32_t first = s_shared[n].first, last = s_shared[n].last, head0 = s_shared[n].chunk * a.chunk_heads;
+      const int heads = min(a.chunk_heads, a.G - head0);
+      // The last of them adds all up, in the runs' order. Loads go out kBatch at a time: this is a
+      // chain of trips to L2. A warp takes every fourth part.
+      constexpr int kBatch = 8;
+      for (int head = lane; head < kHeads; head += 32) {
+        float M = -INFINITY, L = 0.0f;
+        for (int32_t i0 = first + warp; i0 <= last; i0 += kBatch * kWarps) {
+          float mi[kBatch], li[kBatch], top = M;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int32_t i = i0 + k * kWarps;
+            const bool in = i <= last && head < heads;
+            mi[k] = in ? __ldcg(part_of(i, first) + kStats + head) : -INFINITY;
+            li[k] = in ? __ldcg(part_of(i, first) + kStats + kHeads + head) : 0.0f;
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) top = fmaxf(top, mi[k]);
+          if (top == -INFINITY) continue;
+          L *= ex2(M - top);
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) L += ex2(mi[k] - top) * li[k];
+          M = top;
+        }
+        s_m[warp][head] = M;
+        s_l[warp][head] = L;
+      }
+      __syncwarp();
+      for (int k0 = lane; k0 < heads * D / 4; k0 += 32) {
+        const int head = k0 / (D / 4), d = k0 % (D / 4) * 4;
+        const float M = s_m[warp][head];
+        float4 v{0, 0, 0, 0};
+        for (int32_t i0 = first + warp; i0 <= last; i0 += kBatch * kWarps) {
+          float mi[kBatch];
+          float4 x[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const int32_t i = i0 + k * kWarps;
+            mi[k] = i <= last ? __ldcg(part_of(i, first) + kStats + head) : -INFINITY;
+            x[k] = i <= last ? __ldcg(reinterpret_cast<const float4*>(part_of(i, first) + head * (64 * NW) + d)) : float4{};
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const float f = mi[k] == -INFINITY ? 0.0f : ex2(mi[k] - M);
+            v.x += f * x[k].x; v.y += f * x[k].y; v.z += f * x[k].z; v.w += f * x[k].w;
+          }
+        }
+        *reinterpret_cast<float4*>(s_o + (warp * kHeads + head) * kPitch + d) = v;
+      }
+      __syncthreads();
+      join_stats();
+      write_out(static_cast<int64_t>(s_shared[n].b) * a.Hq + static_cast<int64_t>(s_shared[n].h) * a.G + head0, heads);
+      __syncthreads();
+    }
+  }
   write_zeros();
 }
 
-template <int NW, int NT, bool FULL>
+template <int NW, int NT, int PATH>
 nvfp4_status launch_t(const AttentionArgs& a, cudaStream_t stream) {
-  const auto kern = attention_kernel<NW, NT, FULL>;
+  const auto kern = attention_kernel<NW, NT, PATH>;
   const size_t smem = kWarps * kStages * Tile<NW>::kBytes + kWarps * 8 * NT * (64 * NW + 4) * 4 +
                       static_cast<size_t>(a.B) * 8;
   if (nvfp4_status st = set_dynamic_smem(reinterpret_cast<const void*>(kern), smem, "nvfp4_paged_attention_decode"))
@@ -951,8 +1023,12 @@ nvfp4_status launch_t(const AttentionArgs& a, cudaStream_t stream) {
 }
 
 template <int NW, int NT>
-nvfp4_status launch_f(const AttentionArgs& a, bool full, cudaStream_t s) {
-  return full ? launch_t<NW, NT, true>(a, s) : launch_t<NW, NT, false>(a, s);
+nvfp4_status launch_p(const AttentionArgs& a, int path, cudaStream_t s) {
+  switch (path) {
+    case kBulk: return launch_t<NW, NT, kBulk>(a, s);
+    case kRows: return launch_t<NW, NT, kRows>(a, s);
+    default: return launch_t<NW, NT, kAny>(a, s);
+  }
 }
 
 // Query heads that one pass over the cache serves: eight, or sixteen where the accumulators of
@@ -971,8 +1047,8 @@ nvfp4_status launch_attention(AttentionArgs a, cudaStream_t stream) {
   const int nt = eights_of(a.G, a.D), nw = (a.D + 63) / 64;
   a.chunks = (a.G + 8 * nt - 1) / (8 * nt);
   a.chunk_heads = (a.G + a.chunks - 1) / a.chunks;
-  a.pool_pages = a.kc.num_pages < a.vc.num_pages ? a.kc.num_pages : a.vc.num_pages;
-  if (a.pool_pages > INT32_MAX) a.pool_pages = INT32_MAX;
+  const int64_t pool = a.kc.num_pages < a.vc.num_pages ? a.kc.num_pages : a.vc.num_pages;
+  a.pool_pages = pool > INT32_MAX ? static_cast<uint32_t>(INT32_MAX) : static_cast<uint32_t>(pool);
   const int64_t strides[4] = {a.kc.data_page_stride, a.vc.data_page_stride, a.kc.sf_page_stride, a.vc.sf_page_stride};
   for (int64_t s : strides)
     if (s > static_cast<int64_t>(UINT32_MAX)) return fail(NVFP4_ERR_UNSUPPORTED, "nvfp4_paged_attention_decode: a page stride above 4 GiB");
@@ -982,17 +1058,21 @@ nvfp4_status launch_attention(AttentionArgs a, cudaStream_t stream) {
   a.v_sf_stride = static_cast<uint32_t>(strides[3]);
   if (sm_count() * kMaxCtasPerSm * 4 > NVFP4_COUNTER_BYTES)
     return fail(NVFP4_ERR_UNSUPPORTED, "nvfp4_paged_attention_decode: more SMs than counters");
-  // the scale rows' copies: 4 nw bytes (nw = 3: 4 at a time), aligned to that
-  const uintptr_t part = nw == 3 ? 4 : 4 * nw;
-  auto al = [&](const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % part == 0 && stride % part == 0; };
-  const bool full = a.D % 64 == 0 && al(a.kc.sf, a.kc.sf_page_stride) && al(a.vc.sf, a.vc.sf_page_stride);
+  auto scales_aligned = [&](uintptr_t n) {
+    return reinterpret_cast<uintptr_t>(a.kc.sf) % n == 0 && reinterpret_cast<uintptr_t>(a.vc.sf) % n == 0 &&
+           a.kc.sf_page_stride % n == 0 && a.vc.sf_page_stride % n == 0;
+  };
+  int path = kAny;
+  if (a.D % 64 == 0 && scales_aligned(nw == 3 ? 4 : 4 * nw)) path = kRows;
+  if (a.D % 64 == 0 && (a.layout == NVFP4_HND || a.H == 1) && a.ps % 4 == 0 && scales_aligned(16)) path = kBulk;
+  a.pipe = pipe_test_from_env();
   switch (nw * 2 + nt) {
-    case 3: return launch_f<1, 1>(a, full, stream);
-    case 4: return launch_f<1, 2>(a, full, stream);
-    case 5: return launch_f<2, 1>(a, full, stream);
-    case 6: return launch_f<2, 2>(a, full, stream);
-    case 7: return launch_f<3, 1>(a, full, stream);
-    default: return launch_f<4, 1>(a, full, stream);
+    case 3: return launch_p<1, 1>(a, path, stream);
+    case 4: return launch_p<1, 2>(a, path, stream);
+    case 5: return launch_p<2, 1>(a, path, stream);
+    case 6: return launch_p<2, 2>(a, path, stream);
+    case 7: return launch_p<3, 1>(a, path, stream);
+    default: return launch_p<4, 1>(a, path, stream);
   }
 }
 
