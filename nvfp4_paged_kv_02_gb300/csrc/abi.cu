@@ -883,6 +883,8 @@ NVFP4_EXPORT nvfp4_status nvfp4_page_key_bounds(
     if (!block_tables || !seq_lens || (!key_bounds && k_cache.num_pages > 0))
       return fail(NVFP4_ERR_INVALID_ARG, f + ": null device pointer");
     if (!aligned(key_bounds, 16)) return fail(NVFP4_ERR_ALIGNMENT, f + ": key_bounds must be 16-byte aligned");
+    if (static_cast<int64_t>(batch_size) * max_pages_per_request > INT32_MAX)
+      return fail(NVFP4_ERR_UNSUPPORTED, f + ": more than 2^31 - 1 table entries");
     BoundsArgs a{};
     a.kc = k_cache;
     a.ps = page_size;

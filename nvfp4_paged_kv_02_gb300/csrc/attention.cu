@@ -49,7 +49,7 @@ constexpr int kUnit = 32;     // tokens
 constexpr int kTiles = kUnit / 16;  // of 16 tokens
 constexpr int kMinUnits = 4;  // of a CTA's run: one for each warp
 constexpr int kMaxCtasPerSm = 4;
-constexpr int kSegmentCost = 2;
+constexpr int kSegmentCost = 6;
 constexpr float kWeightBias = 8.0f;
 constexpr float kSlack = 7.0f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -259,25 +259,16 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 
 // ---- the kernel ------------------------------------------------------------------------------
 
-// How a unit's rows come to shared memory.
-//   kBulk: the rows of a head are contiguous inside a page (HND, or one head): a bulk copy for each
-//          tensor and page, about a third of the instructions of kRows. Needs D = 64 NW, page_size a
-//          multiple of 4, scales aligned to 16 bytes.
-//   kRows: cp.async of 16 bytes. D = 64 NW, scale rows aligned to their size (NW = 3: to 4 bytes).
-//   kAny:  any D, scales of any alignment (through registers).
-enum { kAny, kRows, kBulk };
-
-__device__ __forceinline__ int round4(int n) { return (n + 3) & ~3; }
-
 // NW: words of codes that a lane holds of a V row (D <= 64 NW). NT: eights of query heads.
-template <int NW, int NT, int PATH>
+// FULL: D = 64 NW and scale rows that cp.async can copy; otherwise any D, and scales of any
+// alignment, which go through registers.
+template <int NW, int NT, bool FULL>
 __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attention_kernel(const AttentionArgs a) {
   using T = Tile<NW>;
   constexpr int NS = kStages;
   constexpr int kHeads = 8 * NT;
   constexpr int kPitch = 64 * NW + 4;  // floats of a row of O in shared memory
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t s_full[kWarps * NS];  // kBulk: a stage's bytes have arrived
   __shared__ int64_t s_scan[kWarps];
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads], s_f[kWarps][kHeads], s_top[kHeads], s_sum[kHeads];
   __shared__ struct { int32_t b, h, chunk, first, last, join; } s_shared[2];  // segments shared with other runs
@@ -286,13 +277,8 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
-  const int D = PATH == kAny ? a.D : 64 * NW;
-  uint64_t* const full = s_full + warp * NS;
-  if (PATH == kBulk && tid == 0) {
-    for (int s = 0; s < kWarps * NS; ++s) mbar_init(s_full + s, 1);
-    fence_mbar_init();
-  }
-  scan_places(a, cum, s_scan);  // ends with a barrier
+  const int D = FULL ? 64 * NW : a.D;
+  scan_places(a, cum, s_scan);
 
   // heads without live tokens get zeros
   auto write_zeros = [&] {
@@ -324,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
 
   const uint32_t ring = smem_addr(smem) + warp * NS * T::kBytes;
   uint8_t* const ring_p = smem + warp * NS * T::kBytes;
-  if (PATH == kAny) {
+  if (!FULL) {
     // what lies between D and 64 NW stays zero: no copy writes there
     for (int i = lane; i < NS * T::kBytes / 16; i += 32) reinterpret_cast<uint4*>(ring_p)[i] = uint4{};
     __syncwarp();
@@ -375,65 +361,39 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
     }
   };
   settle();
-  // What this lane has looked up of the next unit. The table's entry stays as it was loaded
-  // until the copies are issued, so that nothing waits for it here.
-  //   kBulk: lane 4 i + k copies tensor k (codes of K and V, scales of K and V) of the unit's
-  //   i-th page: the rows [lk_row, lk_row + lk_count) of a head, contiguous there, as one bulk copy.
-  //   Otherwise lane i looks up row i, which the lanes then copy 16 (or 8) bytes at a time.
-  int32_t lk_lo = 0, lk_hi = 0, lk_count = 0;
-  uint32_t lk_row = 0, lk_at = 0, lk_live = ~0u;  // (lk_live: rows that the window leaves)
-  bool lk_unit = false;
-  auto load_entry = [&](int32_t col) {
-    const int32_t* entry = reinterpret_cast<const int32_t*>(list + (static_cast<int64_t>(col) << (a.table64 ? 3 : 2)));
-    lk_lo = __ldg(entry);
-    if (a.table64) lk_hi = __ldg(entry + 1);
-  };
+  // What this lane has looked up of the next unit: its row `lane`. The table's entry stays as it
+  // was loaded until the copies are issued, so that nothing waits for it here.
+  int32_t lk_lo = 0, lk_hi = 0;
+  uint32_t lk_row = 0;
+  bool lk_unit = false, lk_live = false;
   auto look_up = [&] {
     lk_unit = pu < pend;
-    lk_count = 0;
+    lk_live = false;
     if (!lk_unit) return;
-    // position of the unit: a token, or a slot of the selected pages
-    const int32_t p0 = static_cast<int32_t>(static_cast<uint32_t>((a.selected ? 0 : span.lo / kUnit) + pu) * kUnit);
-    const int32_t end = a.selected ? slots : span.len;
-    if (PATH == kBulk) lk_live = !a.selected && span.lo > p0 ? ~0u << (span.lo - p0) : ~0u;
-    int32_t p, n, col;
-    if (PATH == kBulk) {
-      col = div_q32(p0, a.div_ps) + (lane >> 2);
-      const int64_t from = static_cast<int64_t>(col) * a.ps;  // the page's positions
-      p = static_cast<int32_t>(max(from, static_cast<int64_t>(p0)));
-      n = static_cast<int32_t>(min(min(from + a.ps, static_cast<int64_t>(p0) + kUnit), static_cast<int64_t>(end)) - p);
-    } else {
-      p = p0 + lane;
-      col = div_q32(p, a.div_ps);
-      n = p < end && p >= (a.selected ? 0 : span.lo) ? 1 : 0;
-    }
-    if (n <= 0) return;
+    // a token, or a slot of the selected pages
+    const int32_t p = static_cast<int32_t>(static_cast<uint32_t>((a.selected ? 0 : span.lo / kUnit) + pu) * kUnit + lane);
+    int32_t col = div_q32(p, a.div_ps);
     const int32_t slot = p - col * a.ps;
     if (a.selected) {
+      if (p >= slots) return;
       col = __ldg(a.selected + (static_cast<int64_t>(ps.b) * a.H + ps.h) * a.max_selected + col);
       if (col < 0 || col >= a.max_pages) {
         flag(a.status, NVFP4_DEV_BAD_PAGE);
         return;
       }
-      n = static_cast<int32_t>(min(static_cast<int64_t>(n), span.len - static_cast<int64_t>(col) * a.ps - slot));
-      if (n <= 0) return;
+      if (static_cast<int64_t>(col) * a.ps + slot >= span.len) return;
+    } else if (p < span.lo || p >= span.len) {
+      return;
     }
-    load_entry(col);
+    const int32_t* entry = reinterpret_cast<const int32_t*>(list + (static_cast<int64_t>(col) << (a.table64 ? 3 : 2)));
+    lk_lo = __ldg(entry);
+    if (a.table64) lk_hi = __ldg(entry + 1);
     lk_row = a.layout == NVFP4_NHD ? slot * a.H + ps.h : ps.h * a.ps + slot;
-    lk_at = p - p0;
-    lk_count = n;
+    lk_live = true;
   };
   look_up();
 
-  // The rows of a page of the unit that are copied: whole groups of four, so that a copy of scales
-  // is a multiple of 16 bytes (the page has them: page_size is a multiple of four there).
-  const int kind = lane & 3;
-  const uint8_t* const bulk_base = kind == 0 ? a.kc.data : (kind == 1 ? a.vc.data : (kind == 2 ? a.kc.sf : a.vc.sf));
-  const uint32_t bulk_stride = kind == 0 ? a.k_stride : (kind == 1 ? a.v_stride : (kind == 2 ? a.k_sf_stride : a.v_sf_stride));
-  const uint32_t bulk_row = kind < 2 ? T::kRow : T::kScales;
-  const uint32_t bulk_at = kind == 0 ? 0 : (kind == 1 ? T::kV : (kind == 2 ? T::kKs : T::kVs));
-
-  // kAny: scale bytes on their way to the stage of the unit issued last
+  // !FULL: scale bytes on their way to the stage of the unit issued last
   uint32_t pk[NW], pv[NW];
   int carried_stage = -1;
   const int nb = D / 16;
@@ -446,44 +406,47 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
       *reinterpret_cast<uint32_t*>(st + T::kVs + 4 * w) = pv[w];
     }
   };
-  uint32_t parity = 0, flight = 0;  // of the stages: their barriers' phase, and copies not waited for
-  bool gave_up = false;             // a wait ran out: nothing more is copied
-  bool stall = PATH == kBulk && a.pipe.stall != 0;  // test control: withhold the first unit
+  // Lanes copy 16 bytes each of consecutive rows (FULL; kRows rows at a time).
+  constexpr int kChunks = 2 * NW;
+  constexpr bool kEven = FULL && NW != 3;  // a row's chunks divide the warp
+  constexpr int kRows = 32 / kChunks;
+  const int my_row = lane / kChunks, my_chunk = lane % kChunks;
+  const uint32_t my_dst = my_row * T::kRow + ((my_chunk ^ T::swizzle(my_row)) << 4);
+  const bool same_strides = a.k_stride == a.v_stride && a.k_sf_stride == a.v_sf_stride;
   // Copies of the unit looked up into stage s, then the look-up of the next one.
   auto issue = [&](int s) {
-    if (PATH == kAny) put_scales();
-    if (lk_unit && !gave_up) {
+    if (!FULL) put_scales();
+    if (lk_unit) {
       const uint32_t st = ring + s * T::kBytes;
       uint32_t page = static_cast<uint32_t>(lk_lo);
-      int32_t n = lk_count;
-      if (n > 0 && (page >= a.pool_pages || (a.table64 && lk_hi != 0))) {
+      bool live = lk_live;
+      if (live && (page >= a.pool_pages || (a.table64 && lk_hi != 0))) {
         flag(a.status, NVFP4_DEV_BAD_PAGE);
-        n = 0;
+        live = false;
       }
-      uint32_t mask;
-      if (PATH == kBulk) {
-        mask = n > 0 ? (n >= 32 ? ~0u : (1u << n) - 1u) << lk_at : 0u;
-        mask = __reduce_or_sync(0xFFFFFFFFu, mask) & lk_live;
-        const uint32_t bytes = n > 0 ? static_cast<uint32_t>(round4(n)) * bulk_row : 0u;
-        const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, bytes);
-        if (lane == 0 && !stall) mbar_arrive_expect_tx(full + s, all);
-        __syncwarp();
-        if (bytes > 0 && !stall)
-          bulk_g2s(ring_p + s * T::kBytes + bulk_at + lk_at * bulk_row,
-                   bulk_base + static_cast<uint64_t>(page) * bulk_stride + static_cast<uint64_t>(lk_row) * bulk_row, bytes,
-                   full + s);
-        stall = false;
-        flight |= 1u << s;
+      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, live);
+      if (lane == 0) *reinterpret_cast<uint32_t*>(ring_p + s * T::kBytes + T::kMask) = mask;
+      const uint32_t ksd = st + T::kKs + lane * T::kScales, vsd = st + T::kVs + lane * T::kScales;
+      constexpr int kPart = NW == 3 ? 4 : 4 * NW;
+      if (kEven && same_strides && mask == 0xFFFFFFFFu) {
+        // the common unit: every row live, one offset for K and V
+        const uint64_t sf = static_cast<uint64_t>(page) * a.k_sf_stride + lk_row * static_cast<uint64_t>(T::kScales);
+        cp_async<kPart>(ksd, a.kc.sf + sf, true);
+        cp_async<kPart>(vsd, a.vc.sf + sf, true);
+        const uint64_t off = static_cast<uint64_t>(page) * a.k_stride + lk_row * static_cast<uint64_t>(T::kRow);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const uint64_t at = __shfl_sync(0xFFFFFFFFu, off, i * kRows + my_row) + 16 * my_chunk;
+          const uint32_t dst = st + i * kRows * T::kRow + (NW == 4 && (i & 1) ? my_dst ^ 64u : my_dst);
+          cp_async<16>(dst, a.kc.data + at, true);
+          cp_async<16>(dst + T::kV, a.vc.data + at, true);
+        }
       } else {
-        const bool live = n > 0;
         if (!live) page = 0;  // (a row that is not live is copied as zeros)
         const uint32_t rw = live ? lk_row : 0;
-        mask = __ballot_sync(0xFFFFFFFFu, live);
         const uint8_t* ks = a.kc.sf + static_cast<uint64_t>(page) * a.k_sf_stride + static_cast<uint64_t>(rw) * nb;
         const uint8_t* vs = a.vc.sf + static_cast<uint64_t>(page) * a.v_sf_stride + static_cast<uint64_t>(rw) * nb;
-        const uint32_t ksd = st + T::kKs + lane * T::kScales, vsd = st + T::kVs + lane * T::kScales;
-        if (PATH == kRows) {
-          constexpr int kPart = NW == 3 ? 4 : 4 * NW;
+        if (FULL) {
 #pragma unroll
           for (int w = 0; w < T::kScales / kPart; ++w) {
             cp_async<kPart>(ksd + w * kPart, ks + w * kPart, live);
@@ -505,19 +468,19 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
           const uint32_t pg = __shfl_sync(0xFFFFFFFFu, page, row);
           const uint64_t in = static_cast<uint64_t>(__shfl_sync(0xFFFFFFFFu, rw, row)) * (D / 2) + off;
           const bool ok = mask >> row & 1u;
-          const uint32_t at = st + row * T::kRow + (((off >> 4) ^ (PATH == kBulk ? 0 : T::swizzle(row))) << 4) + (off & 15);
+          const uint32_t at = st + row * T::kRow + (((off >> 4) ^ T::swizzle(row)) << 4) + (off & 15);
           cp_async<B>(at, a.kc.data + static_cast<uint64_t>(pg) * a.k_stride + in, ok);
           cp_async<B>(at + T::kV, a.vc.data + static_cast<uint64_t>(pg) * a.v_stride + in, ok);
         };
-        if (PATH == kRows) {
-          constexpr int kChunks = 2 * NW;
-#pragma unroll
+        if (FULL) {
+#pragma unroll 1
           for (int i = 0; i < kChunks; ++i) {
             const int k = i * 32 + lane;
             copy(k / kChunks, k % kChunks * 16, std::integral_constant<int, 16>{});
           }
         } else {
           // eight rows at a time, four lanes to a row
+#pragma unroll 1
           for (int i = 0; i < 4; ++i)
             for (int w = 0; w < nb; w += 4) {
               const int off = min(w + (lane & 3), nb - 1) * 8;  // (the last chunk again, rather than none)
@@ -525,7 +488,6 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
             }
         }
       }
-      if (lane == 0) *reinterpret_cast<uint32_t*>(ring_p + s * T::kBytes + T::kMask) = mask;
       carried_stage = s;
       pu += kWarps;
       settle();
@@ -533,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
     } else {
       carried_stage = -1;
     }
-    if (PATH != kBulk) cp_async_commit();
+    cp_async_commit();
   };
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s) issue(s);
@@ -654,35 +616,13 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
     portion(cs, cu, cend);
     const bool whole = cu == 0 && cend == cs.units;
     for (cu += warp; cu < cend; cu += kWarps) {
-      if (PATH != kBulk) {
-        cp_async_wait<NS - 2>();
-      } else if (!gave_up) {
-        if (__all_sync(0xFFFFFFFFu, mbar_wait(full + stage, parity >> stage & 1u, a.pipe.wait_limit))) {
-          parity ^= 1u << stage;
-          flight &= ~(1u << stage);
-        } else {  // what follows is computed from whatever is there, and reported
-          gave_up = true;
-          flag(a.status, NVFP4_DEV_TIMEOUT);
-        }
-      }
+      cp_async_wait<NS - 2>();
       __syncwarp();
       issue(refill);
-      uint8_t* const st = ring_p + stage * T::kBytes;
+      const uint8_t* st = ring_p + stage * T::kBytes;
       refill = stage;
       stage = stage + 1 == NS ? 0 : stage + 1;
       const uint32_t mask = *reinterpret_cast<const uint32_t*>(st + T::kMask);
-      if (PATH == kBulk && mask != 0xFFFFFFFFu) {
-        // rows that are not live came as they are, or not at all: their scales become zeros
-        if (!(mask >> lane & 1u)) {
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            *reinterpret_cast<uint32_t*>(st + T::kKs + lane * T::kScales + 4 * w) = 0;
-            *reinterpret_cast<uint32_t*>(st + T::kVs + lane * T::kScales + 4 * w) = 0;
-          }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copies
-        __syncwarp();
-      }
 
       float x[kTiles][NT][4];
 #pragma unroll
@@ -715,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
                                        : *reinterpret_cast<const uint32_t*>(sr);
 #pragma unroll
             for (int i = 0; i < NW / 2; ++i) {
-              const uint4 v = *reinterpret_cast<const uint4*>(row + (((NW / 2 * c + i) ^ (PATH == kBulk ? 0 : T::swizzle(t))) << 4));
+              const uint4 v = *reinterpret_cast<const uint4*>(row + (((NW / 2 * c + i) ^ T::swizzle(t)) << 4));
               kw[p][4 * i] = v.x; kw[p][4 * i + 1] = v.y; kw[p][4 * i + 2] = v.z; kw[p][4 * i + 3] = v.w;
               const uint32_t s2 = f16x2_from_e4m3x2(i == 0 ? s : s >> 16);
               S2[p][2 * i] = prmt(s2, 0u, 0x1010u);
@@ -815,10 +755,10 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
           const int t = 16 * mt + (p >= 2 ? 8 : 0) + ((p & 1) ? v1 : v0);
           const uint8_t* row = st + T::kV + t * T::kRow;
           if (NW == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(row + (((r >> 1) ^ (PATH == kBulk ? 0 : T::swizzle(t))) << 4) + 8 * (r & 1));
+            const uint2 v = *reinterpret_cast<const uint2*>(row + (((r >> 1) ^ T::swizzle(t)) << 4) + 8 * (r & 1));
             vw[p][0] = v.x; vw[p][1 % NW] = v.y;
           } else if (NW == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(row + ((r ^ (PATH == kBulk ? 0 : T::swizzle(t))) << 4));
+            const uint4 v = *reinterpret_cast<const uint4*>(row + ((r ^ T::swizzle(t)) << 4));
             vw[p][0] = v.x; vw[p][1 % NW] = v.y; vw[p][2 % NW] = v.z; vw[p][3 % NW] = v.w;
           } else {
 #pragma unroll
@@ -929,10 +869,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
     if (last_segment) break;
     __syncthreads();  // the buffers of the join are free again
   }
-  // no copy may still be on its way when the CTA ends
-  if (PATH != kBulk) cp_async_wait<0>();
-  for (int s = 0; s < NS; ++s)
-    if (flight >> s & 1u) mbar_wait(full + s, parity >> s & 1u, a.pipe.wait_limit);
+  cp_async_wait<0>();
 
   // -- shared segments whose last part was this run's --
   if (shared > 0) {
@@ -1004,9 +941,9 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
   write_zeros();
 }
 
-template <int NW, int NT, int PATH>
+template <int NW, int NT, bool FULL>
 nvfp4_status launch_t(const AttentionArgs& a, cudaStream_t stream) {
-  const auto kern = attention_kernel<NW, NT, PATH>;
+  const auto kern = attention_kernel<NW, NT, FULL>;
   const size_t smem = kWarps * kStages * Tile<NW>::kBytes + kWarps * 8 * NT * (64 * NW + 4) * 4 +
                       static_cast<size_t>(a.B) * 8;
   if (nvfp4_status st = set_dynamic_smem(reinterpret_cast<const void*>(kern), smem, "nvfp4_paged_attention_decode"))
@@ -1023,12 +960,8 @@ nvfp4_status launch_t(const AttentionArgs& a, cudaStream_t stream) {
 }
 
 template <int NW, int NT>
-nvfp4_status launch_p(const AttentionArgs& a, int path, cudaStream_t s) {
-  switch (path) {
-    case kBulk: return launch_t<NW, NT, kBulk>(a, s);
-    case kRows: return launch_t<NW, NT, kRows>(a, s);
-    default: return launch_t<NW, NT, kAny>(a, s);
-  }
+nvfp4_status launch_f(const AttentionArgs& a, bool full, cudaStream_t s) {
+  return full ? launch_t<NW, NT, true>(a, s) : launch_t<NW, NT, false>(a, s);
 }
 
 // Query heads that one pass over the cache serves: eight, or sixteen where the accumulators of
@@ -1058,21 +991,19 @@ nvfp4_status launch_attention(AttentionArgs a, cudaStream_t stream) {
   a.v_sf_stride = static_cast<uint32_t>(strides[3]);
   if (sm_count() * kMaxCtasPerSm * 4 > NVFP4_COUNTER_BYTES)
     return fail(NVFP4_ERR_UNSUPPORTED, "nvfp4_paged_attention_decode: more SMs than counters");
+  // scale rows are copied 4 nw bytes at a time (nw = 3: 4), aligned to that
   auto scales_aligned = [&](uintptr_t n) {
     return reinterpret_cast<uintptr_t>(a.kc.sf) % n == 0 && reinterpret_cast<uintptr_t>(a.vc.sf) % n == 0 &&
            a.kc.sf_page_stride % n == 0 && a.vc.sf_page_stride % n == 0;
   };
-  int path = kAny;
-  if (a.D % 64 == 0 && scales_aligned(nw == 3 ? 4 : 4 * nw)) path = kRows;
-  if (a.D % 64 == 0 && (a.layout == NVFP4_HND || a.H == 1) && a.ps % 4 == 0 && scales_aligned(16)) path = kBulk;
-  a.pipe = pipe_test_from_env();
+  const bool full = a.D % 64 == 0 && scales_aligned(nw == 3 ? 4 : 4 * nw);
   switch (nw * 2 + nt) {
-    case 3: return launch_p<1, 1>(a, path, stream);
-    case 4: return launch_p<1, 2>(a, path, stream);
-    case 5: return launch_p<2, 1>(a, path, stream);
-    case 6: return launch_p<2, 2>(a, path, stream);
-    case 7: return launch_p<3, 1>(a, path, stream);
-    default: return launch_p<4, 1>(a, path, stream);
+    case 3: return launch_f<1, 1>(a, full, stream);
+    case 4: return launch_f<1, 2>(a, full, stream);
+    case 5: return launch_f<2, 1>(a, full, stream);
+    case 6: return launch_f<2, 2>(a, full, stream);
+    case 7: return launch_f<3, 1>(a, full, stream);
+    default: return launch_f<4, 1>(a, full, stream);
   }
 }
 

@@ -33,7 +33,6 @@ struct AttentionArgs {
   // set at launch
   int32_t chunks, chunk_heads;  // passes over a KV head's query heads, and the heads of one
   uint32_t pool_pages;          // pages that both caches have
-  PipeTest pipe;
   uint32_t k_stride, v_stride, k_sf_stride, v_sf_stride;  // page strides, bytes
 };
 // Device memory that a launch needs, whatever the lengths.

@@ -10,6 +10,7 @@
 // chains, of the even and of the odd elements, then their sum; the D/8 group sums, filled up
 // with zeros to a power of two, add by halves (t[i] += t[i + n/2]).
 #include "attention.h"
+#include "scan.cuh"
 
 namespace nvfp4 {
 namespace {
@@ -20,185 +21,524 @@ __device__ __forceinline__ int64_t table_entry(const void* tables, int32_t is64,
 }
 
 // ---- bounds -----------------------------------------------------------------------------
+//
+// Reading the keys bounds it: 9/16 byte an element, and 4 bytes written for page_size of them.
+// A CTA takes one page, all heads, which is contiguous in either layout. A thread has one
+// 16-element block of a row (a column) and every kSlices-th slot; the slices are joined in
+// shared memory. kBatch slots of a thread are loaded before the first is decoded.
 
-constexpr int kBoundsThreads = 128;
+constexpr int kBoundsThreads = 256;
+constexpr int kBatch = 8;
 
-// A CTA walks the pages of request blockIdx.y; a thread has one 16-element block of one head.
+__device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 __global__ void __launch_bounds__(kBoundsThreads) page_key_bounds_kernel(const BoundsArgs a) {
-  const int32_t b = blockIdx.y, nb = a.D / 16;
-  int64_t len = __ldg(a.seq_lens + b);
+  extern __shared__ int32_t s_cum[];
+  // slice ts, word w (lo 0-7, hi 8-15) of column c at [ts][w][c]: c below kBoundsThreads / slices
+  __shared__ uint32_t s_part[16 * kBoundsThreads];
+  const int tid = threadIdx.x, nb = a.D / 16;
   const int64_t reach = a.max_pages * a.ps;
-  if (len > reach) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) flag(a.status, NVFP4_DEV_LEN_CLAMPED);
-    len = reach;
-  }
-  const int64_t from = a.first_positions ? max(__ldg(a.first_positions + b), 0) : 0;
-  for (int64_t col = from / a.ps + blockIdx.x; col * a.ps < len; col += gridDim.x) {
+  auto len_of = [&](int32_t b) { return min(static_cast<int64_t>(__ldg(a.seq_lens + b)), reach); };
+  auto first_of = [&](int32_t b) {  // first page
+    return a.first_positions ? div_q32(max(__ldg(a.first_positions + b), 0), a.div_ps) : 0;
+  };
+  block_inclusive_scan(s_cum, a.B, [&](int32_t b) {
+    const int64_t len = len_of(b);
+    if (blockIdx.x == 0 && __ldg(a.seq_lens + b) > reach) flag(a.status, NVFP4_DEV_LEN_CLAMPED);
+    const int32_t pages = len > 0 ? static_cast<int32_t>((len + a.ps - 1) / a.ps) : 0;
+    return max(pages - first_of(b), 0);
+  });
+  const int32_t total = s_cum[a.B - 1];
+  const int32_t columns = a.H * nb;
+  const int tile = min(columns, kBoundsThreads);        // columns at a time
+  const int slices = max(kBoundsThreads / tile, 1);     // threads of a column
+  const int col_l = a.layout == NVFP4_NHD ? tid % tile : tid / (slices * nb) * nb + tid % nb;
+  const int ts = a.layout == NVFP4_NHD ? tid / tile : tid / nb % slices;
+  // (HND: slices of one head are neighbours, so that a warp's loads are contiguous. A tile of
+  // columns then has to be whole heads; where it is not, the NHD arrangement serves.)
+  const bool by_head = a.layout == NVFP4_HND && tile % nb == 0;
+  const int my_col = by_head ? col_l : tid % tile, my_slice = by_head ? ts : tid / tile;
+
+  for (int32_t item = blockIdx.x; item < total; item += gridDim.x) {
+    const int32_t b = scan_find(s_cum, a.B, item);
+    const int32_t col = item - (b > 0 ? s_cum[b - 1] : 0) + first_of(b);
     const int64_t page = table_entry(a.block_tables, a.table64, b * a.max_pages + col);
     if (page < 0 || page >= a.kc.num_pages) {
-      if (threadIdx.x == 0) flag(a.status, NVFP4_DEV_BAD_PAGE);
+      if (tid == 0) flag(a.status, NVFP4_DEV_BAD_PAGE);
       continue;
     }
-    const int32_t n = static_cast<int32_t>(min(static_cast<int64_t>(a.ps), len - col * a.ps));
-    for (int32_t w = threadIdx.x; w < a.H * nb; w += kBoundsThreads) {
+    const int32_t n = static_cast<int32_t>(min(static_cast<int64_t>(a.ps), len_of(b) - static_cast<int64_t>(col) * a.ps));
+    const uint8_t* codes = a.kc.data + page * a.kc.data_page_stride;
+    const uint8_t* scales = a.kc.sf + page * a.kc.sf_page_stride;
+    for (int32_t c0 = 0; c0 < columns; c0 += tile) {
+      const int32_t w = c0 + my_col;
+      const bool mine = my_slice < slices && my_col < tile && w < columns;
       const int32_t h = w / nb, j = w - h * nb;
+      // block of slot t: base + t * step
+      const int64_t base = a.layout == NVFP4_NHD ? w : static_cast<int64_t>(h) * a.ps * nb + j;
+      const int32_t step = a.layout == NVFP4_NHD ? columns : nb;
       uint32_t lo[8], hi[8];
-      for (int32_t t = 0; t < n; ++t) {
-        const int64_t r = a.layout == NVFP4_NHD ? static_cast<int64_t>(t) * a.H + h
-                                                : static_cast<int64_t>(h) * a.ps + t;
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>(
-            a.kc.data + page * a.kc.data_page_stride + r * (a.D / 2)) + j);
-        const uint32_t s = __ldg(a.kc.sf + page * a.kc.sf_page_stride + r * nb + j);
-        const uint32_t S2 = f16x2_from_e4m3x2(s * 0x0101u);
-        uint32_t v[8];
-        f16x2x4_from_e2m1x8(c.x, v[0], v[1], v[2], v[3]);
-        f16x2x4_from_e2m1x8(c.y, v[4], v[5], v[6], v[7]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[e] = hmul2_rn(v[e], S2);
-          asm("min.f16x2 %0, %1, %2;" : "=r"(lo[e]) : "r"(t ? lo[e] : v[e]), "r"(v[e]));
-          asm("max.f16x2 %0, %1, %2;" : "=r"(hi[e]) : "r"(t ? hi[e] : v[e]), "r"(v[e]));
+      for (int e = 0; e < 8; ++e) {
+        lo[e] = 0x7C007C00u;  // +inf, -inf: what a slice without slots leaves
+        hi[e] = 0xFC00FC00u;
+      }
+      if (mine) {
+        for (int32_t t0 = my_slice; t0 < n; t0 += kBatch * slices) {
+          uint2 c[kBatch];
+          uint32_t s[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            // (past the end: the batch's first slot again)
+            const int32_t t = t0 + k * slices < n ? t0 + k * slices : t0;
+            const int64_t at = base + static_cast<int64_t>(t) * step;
+            c[k] = __ldg(reinterpret_cast<const uint2*>(codes) + at);
+            s[k] = __ldg(scales + at);
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const uint32_t S2 = f16x2_from_e4m3x2(s[k] * 0x0101u);
+            uint32_t v[8];
+            f16x2x4_from_e2m1x8(c[k].x, v[0], v[1], v[2], v[3]);
+            f16x2x4_from_e2m1x8(c[k].y, v[4], v[5], v[6], v[7]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              v[e] = hmul2_rn(v[e], S2);
+              lo[e] = hmin2(lo[e], v[e]);
+              hi[e] = hmax2(hi[e], v[e]);
+            }
+          }
         }
       }
-      uint4* dst = reinterpret_cast<uint4*>(a.bounds + (page * a.H + h) * 2 * a.D + 16 * j);
-      uint4* dst_hi = reinterpret_cast<uint4*>(a.bounds + ((page * a.H + h) * 2 + 1) * a.D + 16 * j);
-      dst[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      dst[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-      dst_hi[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      dst_hi[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+      __syncthreads();  // the last page's reads are done
+      if (mine) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s_part[(my_slice * 16 + e) * tile + my_col] = lo[e];
+          s_part[(my_slice * 16 + 8 + e) * tile + my_col] = hi[e];
+        }
+      }
+      __syncthreads();
+      // words of the output: [head][lo, hi][block][8 words]
+      const int32_t cols = min(tile, columns - c0);
+      for (int k = tid; k < cols * 16; k += kBoundsThreads) {
+        const int e = k & 7, cw = k >> 3;  // word of a block; (column, lo or hi)
+        const int which = cw >= cols, cl = cw - which * cols;
+        uint32_t v = s_part[(which * 8 + e) * tile + cl];
+        for (int q = 1; q < slices; ++q) {
+          const uint32_t x = s_part[(q * 16 + which * 8 + e) * tile + cl];
+          v = which ? hmax2(v, x) : hmin2(v, x);
+        }
+        const int32_t hh = (c0 + cl) / nb, jj = c0 + cl - hh * nb;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(a.bounds + ((page * a.H + hh) * 2 + which) * a.D);
+        dst[8 * jj + e] = v;
+      }
     }
   }
 }
 
-// ---- selection --------------------------------------------------------------------------
+// ---- scores -----------------------------------------------------------------------------
+//
+// A unit is 32 pages of one (request, KV head). All units are cut into equal runs, one for each
+// warp; a warp holds its query heads in registers (as positive and negative parts) and passes
+// over the pages' bounds once, T lanes to a page (T = D/8 rounded up), each lane eight elements.
+// A lane's bounds come through its own ring of stages in shared memory (cp.async; no other lane
+// reads them, so a wait is all the synchronization there is). Reading the bounds bounds it, 4 D
+// bytes a page and head; the 2 G D multiply-adds are packed two by two.
 
-constexpr int kSelectThreads = 256;
+constexpr int kScoreWarps = 4;
+constexpr int kScoreStages = 8;
 
 // Unsigned keys in the order of the scores.
 __device__ __forceinline__ uint32_t key_of(float s) {
   const uint32_t u = __float_as_uint(s + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+constexpr uint32_t kForced = 0xFFFFFFFFu;  // a page that is selected before all others
 
-// A CTA scores the pages of one (request, KV head), a page to T lanes, finds the k-th largest
-// key by its bytes, and writes the pages above it and the first ones equal to it.
-__global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const SelectArgs a) {
-  const int64_t item = blockIdx.x;
-  const int32_t b = static_cast<int32_t>(item / a.H), h = static_cast<int32_t>(item % a.H);
-  const int64_t reach = a.max_pages * a.ps;
-  int64_t len = max(__ldg(a.seq_lens + b), 0);
-  if (len > reach) {
-    if (threadIdx.x == 0 && h == 0) flag(a.status, NVFP4_DEV_LEN_CLAMPED);
-    len = reach;
-  }
-  const int64_t n = (len + a.ps - 1) / a.ps;
-  const int32_t count = static_cast<int32_t>(min(n, static_cast<int64_t>(a.k)));
-  int32_t* out = a.selected + item * a.k;
-  uint32_t* keys = a.scores + item * a.max_pages;
-  if (threadIdx.x == 0) a.num_selected[item] = count;
-  for (int32_t i = count + threadIdx.x; i < a.k; i += kSelectThreads) out[i] = -1;
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t widen2(uint32_t h) {
+  return pack2(f32_from_f16_lo(h), f32_from_f16_hi(h));
+}
 
-  const int slices = a.D / 8;
-  int T = 1;
-  while (T < slices) T *= 2;
-  const int sub = threadIdx.x % 32;  // one warp to a page; lanes take groups of eight
-  for (int64_t j = threadIdx.x / 32; j < n; j += kSelectThreads / 32) {
-    const int64_t page = table_entry(a.block_tables, a.table64, b * a.max_pages + j);
-    float best = -INFINITY;
-    if (page < 0 || page >= a.num_pages) {
-      if (sub == 0) flag(a.status, NVFP4_DEV_BAD_PAGE);
-    } else {
-      for (int32_t g = 0; g < a.G; ++g) {
-        float s = 0.0f;
-        if (sub < slices) {
-          const uint16_t* lo = a.bounds + (page * a.H + h) * 2 * a.D + 8 * sub;
-          const uint16_t* hi = lo + a.D;
-          const uint8_t* q = a.q + b * a.q_row_bytes + ((static_cast<int64_t>(h) * a.G + g) * a.D + 8 * sub) * 2;
-          float chain[2] = {0.0f, 0.0f};
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t w = reinterpret_cast<const uint16_t*>(q)[e];
-            const float x = a.bf16 ? __uint_as_float(w << 16) : f32_from_f16_lo(w);
-            chain[e & 1] = __fadd_rn(chain[e & 1], __fmul_rn(x, f32_from_f16_lo(x > 0.0f ? hi[e] : lo[e])));
-          }
-          s = __fadd_rn(chain[0], chain[1]);
+__device__ __forceinline__ int32_t pages_of(const SelectArgs& a, int32_t b) {
+  const int64_t len = min(static_cast<int64_t>(max(__ldg(a.seq_lens + b), 0)), a.max_pages * a.ps);
+  return static_cast<int32_t>((len + a.ps - 1) / a.ps);
+}
+
+template <int GC, int T>
+__global__ void __launch_bounds__(kScoreWarps * 32) page_scores_kernel(const SelectArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kPages = 32 / T;  // of an iteration
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane % T, group = lane / T;
+  int32_t* cum = reinterpret_cast<int32_t*>(smem + kScoreWarps * kScoreStages * 1024);
+  block_inclusive_scan(cum, a.B, [&](int32_t b) {
+    if (blockIdx.x == 0 && __ldg(a.seq_lens + b) > a.max_pages * a.ps) flag(a.status, NVFP4_DEV_LEN_CLAMPED);
+    return (pages_of(a, b) + 31) / 32;
+  });
+  const int64_t total = static_cast<int64_t>(cum[a.B - 1]) * a.H;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kScoreWarps;
+  const int64_t me = static_cast<int64_t>(blockIdx.x) * kScoreWarps + warp;
+  int64_t u = total * me / warps;
+  const int64_t u_end = total * (me + 1) / warps;
+  if (u >= u_end) return;
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem + warp * kScoreStages * 1024)) + lane * 16;
+
+  // the list of unit u: units run over requests, then heads, then pages
+  int32_t b = scan_find(cum, a.B, static_cast<int32_t>(u / a.H));
+  int32_t units = cum[b] - (b > 0 ? cum[b - 1] : 0);
+  int64_t in_request = u - static_cast<int64_t>(b > 0 ? cum[b - 1] : 0) * a.H;
+  int32_t h = static_cast<int32_t>(in_request / units), first = static_cast<int32_t>(in_request % units);
+
+  const bool active = 8 * sub < a.D;
+  for (;;) {
+    const int32_t n = pages_of(a, b);
+    const int32_t last = static_cast<int32_t>(min(static_cast<int64_t>(units), first + (u_end - u)));
+    uint32_t* keys = a.scores + (static_cast<int64_t>(b) * a.H + h) * a.max_pages;
+    for (int32_t g0 = 0; g0 < a.G; g0 += GC) {
+      uint64_t qp[GC][4], qn[GC][4];
+#pragma unroll
+      for (int g = 0; g < GC; ++g) {
+        uint4 w{};
+        if (active && g0 + g < a.G)
+          w = __ldg(reinterpret_cast<const uint4*>(
+              a.q + b * a.q_row_bytes + ((static_cast<int64_t>(h) * a.G + g0 + g) * a.D + 8 * sub) * 2));
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = a.bf16 ? __uint_as_float(ww[i] << 16) : f32_from_f16_lo(ww[i]);
+          const float y = a.bf16 ? f32_from_bf16_hi(ww[i]) : f32_from_f16_hi(ww[i]);
+          qp[g][i] = pack2(fmaxf(x, 0.0f), fmaxf(y, 0.0f));
+          qn[g][i] = pack2(fminf(x, 0.0f), fminf(y, 0.0f));
         }
-        for (int o = T / 2; o > 0; o /= 2) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
-        best = fmaxf(best, s);
       }
+      // iterations: kPages pages each, T of them to a unit
+      const int32_t it_end = (last - first) * T;
+      int32_t issued = 0, entry_unit = -1, entry = -1;
+      auto issue = [&] {
+        if (issued < it_end) {
+          const int32_t unit = issued / T;
+          if (unit != entry_unit) {  // the unit's 32 pages, one to a lane
+            entry_unit = unit;
+            const int32_t col = (first + unit) * 32 + lane;
+            entry = -1;
+            if (col < n) {
+              const int64_t page = table_entry(a.block_tables, a.table64, b * a.max_pages + col);
+              if (page >= 0 && page < a.num_pages) entry = static_cast<int32_t>(page);
+              else flag(a.status, NVFP4_DEV_BAD_PAGE);
+            }
+          }
+          const int32_t page = __shfl_sync(0xFFFFFFFFu, entry, issued % T * kPages + group);
+          const bool live = page >= 0 && active;
+          const uint16_t* src = a.bounds + ((static_cast<int64_t>(live ? page : 0) * a.H + h) * 2 * a.D + (live ? 8 * sub : 0));
+          const uint32_t dst = ring + issued % kScoreStages * 1024;
+          const int bytes = live ? 16 : 0;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 512), "l"(src + a.D), "r"(bytes) : "memory");
+        }
+        ++issued;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      for (int s = 0; s < kScoreStages - 1; ++s) issue();
+      float mine = -INFINITY;
+      for (int32_t it = 0; it < it_end; ++it) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kScoreStages - 2) : "memory");
+        const uint8_t* st = smem + warp * kScoreStages * 1024 + it % kScoreStages * 1024 + lane * 16;
+        const uint4 lw = *reinterpret_cast<const uint4*>(st), hw = *reinterpret_cast<const uint4*>(st + 512);
+        issue();
+        const uint64_t lo[4] = {widen2(lw.x), widen2(lw.y), widen2(lw.z), widen2(lw.w)};
+        const uint64_t hi[4] = {widen2(hw.x), widen2(hw.y), widen2(hw.z), widen2(hw.w)};
+        float v[GC];
+#pragma unroll
+        for (int g = 0; g < GC; ++g) {
+          uint64_t acc = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            fma2(acc, qp[g][i], hi[i]);
+            fma2(acc, qn[g][i], lo[i]);
+          }
+          float x, y;
+          asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(acc));
+          v[g] = __fadd_rn(x, y);
+        }
+        // Sums over the T lanes by halves. While a lane has several heads left it gives half of them
+        // to its partner and keeps the other half.
+        int cnt = GC, mine_g = 0;
+#pragma unroll
+        for (int o = T / 2; o >= 1; o /= 2) {
+          if (cnt > 1) {
+            cnt /= 2;
+            const bool up = lane & o;
+#pragma unroll
+            for (int k = 0; k < GC / 2; ++k) {
+              if (k < cnt) {
+                const float give = up ? v[k] : v[k + cnt], keep = up ? v[k + cnt] : v[k];
+                v[k] = __fadd_rn(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
+              }
+            }
+            if (up) mine_g += cnt;
+          } else {
+            v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], o));
+          }
+        }
+        // the maximum over the heads: lanes that differ in the bits that chose a head
+        float best = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < (GC > T ? GC / T : 1); ++k)
+          best = fmaxf(best, g0 + mine_g + k < a.G ? v[k] : -INFINITY);
+#pragma unroll
+        for (int o = T / 2; o >= (T > GC ? T / GC : 1); o /= 2) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+        // lane l keeps the score of the unit's page l
+        const float got = __shfl_sync(0xFFFFFFFFu, best, lane % kPages * T);
+        if (lane / kPages == it % T) mine = got;
+        if (it % T == T - 1) {
+          const int32_t j = (first + it / T) * 32 + lane;
+          if (j < n) {
+            // (a page outside the pool was copied as zeros: it comes last)
+            const int64_t page = table_entry(a.block_tables, a.table64, b * a.max_pages + j);
+            const bool bad = page < 0 || page >= a.num_pages;
+            uint32_t key = bad ? key_of(-INFINITY) : key_of(mine);
+            if (g0 > 0) key = max(key, keys[j]);
+            if (j < a.sink || j >= n - a.recent) key = kForced;
+            keys[j] = key;
+          }
+        }
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
-    if (j < a.sink || j >= n - a.recent) best = INFINITY;
-    if (sub == 0) keys[j] = key_of(best);
+    u += last - first;
+    if (u >= u_end) break;
+    first = 0;
+    if (++h == a.H) {
+      h = 0;
+      do {
+        ++b;
+        units = cum[b] - cum[b - 1];
+      } while (units == 0);
+    }
   }
-  __syncthreads();
+}
+
+// ---- selection --------------------------------------------------------------------------
+//
+// One CTA for each list. The k-th largest key is found by its digits, from the highest bit in
+// which the keys differ: a histogram of a digit in shared memory, the bin that holds the k-th,
+// and so on inside that bin, until the bin is wanted as a whole. Then one pass in page order
+// writes the pages above it and the first ones equal to it.
+
+constexpr int kSelectThreads = 512;
+constexpr int kDigit = 9, kBins = 1 << kDigit;
+constexpr int kPerThread = 16;  // keys that a thread has in registers
+
+__device__ __forceinline__ uint32_t warp_sum(uint32_t v) { return __reduce_add_sync(0xFFFFFFFFu, v); }
+
+__global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const SelectArgs a) {
+  __shared__ uint32_t s_hist[kBins], s_red[4][kSelectThreads / 32], s_bin, s_above, s_in_bin;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t item = blockIdx.x;
+  const int32_t b = static_cast<int32_t>(item / a.H);
+  const int32_t n = pages_of(a, b);
+  const int32_t count = min(n, a.k);
+  int32_t* out = a.selected + item * a.k;
+  const uint32_t* keys = a.scores + item * a.max_pages;
+  if (tid == 0) a.num_selected[item] = count;
+  for (int32_t i = count + tid; i < a.k; i += kSelectThreads) out[i] = -1;
   if (count == n) {
-    for (int64_t j = threadIdx.x; j < n; j += kSelectThreads) out[j] = static_cast<int32_t>(j);
+    for (int32_t j = tid; j < n; j += kSelectThreads) out[j] = j;
     return;
   }
-  __shared__ uint32_t s_hist[256];
-  __shared__ uint32_t s_prefix, s_want, s_base[2], s_warp[2][kSelectThreads / 32];
-  if (threadIdx.x == 0) {
-    s_prefix = 0;
-    s_want = count;  // keys still to be taken among those that share the prefix
+  // A thread's keys are neighbours, so that page order is thread order: the first tile's in
+  // registers, what is past it (a list longer than kSelectThreads * kPerThread) read again.
+  constexpr int32_t kTile = kSelectThreads * kPerThread;
+  uint32_t mine[kPerThread];
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int32_t j = tid * kPerThread + i;
+    mine[i] = j < n ? __ldcg(keys + j) : 0u;
   }
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    s_hist[threadIdx.x] = 0;
-    __syncthreads();
-    const uint32_t prefix = s_prefix, mask = shift == 24 ? 0u : ~((1u << (shift + 8)) - 1u);
-    for (int64_t j = threadIdx.x; j < n; j += kSelectThreads)
-      if ((keys[j] & mask) == prefix) atomicAdd(s_hist + ((keys[j] >> shift) & 255u), 1u);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      uint32_t want = s_want;
-      int d = 255;
-      while (s_hist[d] < want) want -= s_hist[d--];
-      s_want = want;
-      s_prefix = prefix | (static_cast<uint32_t>(d) << shift);
+  auto each = [&](auto body) {  // of this thread's keys, in page order inside a tile
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i)
+      if (tid * kPerThread + i < n) body(mine[i]);
+    for (int32_t t = kTile; t < n; t += kTile)
+      for (int i = 0; i < kPerThread; ++i) {
+        const int32_t j = t + tid * kPerThread + i;
+        if (j < n) body(__ldcg(keys + j));
+      }
+  };
+  uint32_t lo = 0xFFFFFFFFu, hi = 0, forced = 0;
+  each([&](uint32_t k) {
+    if (k == kForced) {
+      ++forced;
+    } else {
+      lo = min(lo, k);
+      hi = max(hi, k);
     }
-    __syncthreads();
+  });
+  lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+  hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+  forced = warp_sum(forced);
+  if (lane == 0) {
+    s_red[0][warp] = lo;
+    s_red[1][warp] = hi;
+    s_red[2][warp] = forced;
   }
-  // in page order: every key above the k-th, and the first s_want of those equal to it
-  const uint32_t kth = s_prefix, ties = s_want;
-  if (threadIdx.x < 2) s_base[threadIdx.x] = 0;
   __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int64_t j0 = 0; j0 < n; j0 += kSelectThreads) {
-    const int64_t j = j0 + threadIdx.x;
-    const uint32_t key = j < n ? keys[j] : 0u;
-    const bool eq = j < n && key == kth, gt = j < n && key > kth;
-    const uint32_t beq = __ballot_sync(0xFFFFFFFFu, eq), bgt = __ballot_sync(0xFFFFFFFFu, gt);
-    if (lane == 0) {
-      s_warp[0][warp] = __popc(beq);
-      s_warp[1][warp] = __popc(bgt);
+  forced = 0;
+  for (int w = 0; w < kSelectThreads / 32; ++w) {
+    lo = min(lo, s_red[0][w]);
+    hi = max(hi, s_red[1][w]);
+    forced += s_red[2][w];
+  }
+  // keys >= floor_ are taken, of those in [floor_, ceil_] the first `want` in page order
+  uint32_t floor_ = kForced, ceil_ = kForced, want = count;
+  if (forced < static_cast<uint32_t>(count)) {
+    want = count - forced;
+    // digits of key - base, `left` bits of them
+    uint32_t base = lo, left = 32 - __clz(hi - lo);
+    floor_ = lo;
+    ceil_ = hi;
+    uint32_t in_range = n - forced;
+    while (left > 0 && in_range > want) {
+      const uint32_t shift = left > kDigit ? left - kDigit : 0;
+      for (int i = tid; i < kBins; i += kSelectThreads) s_hist[i] = 0;
+      __syncthreads();
+      each([&](uint32_t k) {
+        if (k >= floor_ && k <= ceil_) {
+          // lanes of one bin add together: neighbours' scores often share it
+          atomicAdd(s_hist + ((k - base) >> shift), 1u);
+        }
+      });
+      __syncthreads();
+      // the bin of the want-th largest: bins from the top, kBins = kSelectThreads of them
+      static_assert(kBins == kSelectThreads, "one bin to a thread");
+      const uint32_t c = s_hist[kBins - 1 - tid];
+      uint32_t sum = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += x;
+      }
+      if (lane == 31) s_red[3][warp] = sum;
+      __syncthreads();
+      uint32_t before = 0;
+      for (int w = 0; w < warp; ++w) before += s_red[3][w];
+      sum += before;
+      if (sum >= want && sum - c < want) {
+        s_bin = kBins - 1 - tid;
+        s_above = sum - c;
+        s_in_bin = c;
+      }
+      __syncthreads();
+      base += s_bin << shift;
+      want -= s_above;
+      in_range = s_in_bin;
+      floor_ = base;
+      const uint32_t top = base + ((1u << shift) - 1u);
+      ceil_ = min(ceil_, top);
+      left = shift;
+      __syncthreads();
+    }
+  }
+  // One pass in page order. taken = keys above the range, and the first `want` inside it.
+  uint32_t base_above = 0, base_in = 0;
+  for (int32_t t = 0; t < n; t += kTile) {
+    uint32_t above = 0, in = 0;
+    uint32_t k[kPerThread];
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      const int32_t j = t + tid * kPerThread + i;
+      k[i] = t == 0 ? mine[i] : (j < n ? __ldcg(keys + j) : 0u);
+      if (j < n) {
+        above += k[i] > ceil_;
+        in += k[i] >= floor_ && k[i] <= ceil_;
+      }
+    }
+    uint32_t sa = above, si = in;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, sa, o), y = __shfl_up_sync(0xFFFFFFFFu, si, o);
+      if (lane >= o) {
+        sa += x;
+        si += y;
+      }
     }
     __syncthreads();
-    uint32_t neq = s_base[0], ngt = s_base[1], alleq = neq, allgt = ngt;
+    if (lane == 31) {
+      s_red[0][warp] = sa;
+      s_red[1][warp] = si;
+    }
+    __syncthreads();
+    uint32_t a_all = 0, i_all = 0, na = base_above + sa - above, ni = base_in + si - in;
     for (int w = 0; w < kSelectThreads / 32; ++w) {
       if (w < warp) {
-        neq += s_warp[0][w];
-        ngt += s_warp[1][w];
+        na += s_red[0][w];
+        ni += s_red[1][w];
       }
-      alleq += s_warp[0][w];
-      allgt += s_warp[1][w];
+      a_all += s_red[0][w];
+      i_all += s_red[1][w];
     }
-    const uint32_t below = (1u << lane) - 1u;
-    neq += __popc(beq & below);
-    ngt += __popc(bgt & below);
-    if (gt || (eq && neq < ties)) out[ngt + min(neq, ties)] = static_cast<int32_t>(j);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      s_base[0] = alleq;
-      s_base[1] = allgt;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      const int32_t j = t + tid * kPerThread + i;
+      if (j >= n) continue;
+      const bool is_above = k[i] > ceil_, is_in = k[i] >= floor_ && k[i] <= ceil_;
+      if (is_above || (is_in && ni < want)) out[na + min(ni, want)] = j;
+      na += is_above;
+      ni += is_in;
     }
-    __syncthreads();
+    base_above += a_all;
+    base_in += i_all;
   }
+}
+
+template <int GC, int T>
+nvfp4_status launch_scores(const SelectArgs& a, cudaStream_t stream) {
+  const auto kern = page_scores_kernel<GC, T>;
+  const size_t smem = kScoreWarps * kScoreStages * 1024 + static_cast<size_t>(a.B) * 4;
+  if (nvfp4_status st = set_dynamic_smem(reinterpret_cast<const void*>(kern), smem, "nvfp4_select_pages")) return st;
+  const int64_t cap = static_cast<int64_t>(sm_count()) *
+                      blocks_per_sm(reinterpret_cast<const void*>(kern), kScoreWarps * 32, smem);
+  const int64_t most = (static_cast<int64_t>(a.B) * a.H * ((a.max_pages + 31) / 32) + kScoreWarps - 1) / kScoreWarps;
+  const int grid = static_cast<int>(most < cap ? most : cap);
+  if (grid > 0) kern<<<grid, kScoreWarps * 32, smem, stream>>>(a);
+  return check_launch("nvfp4_select_pages");
+}
+
+template <int GC>
+nvfp4_status launch_scores_t(const SelectArgs& a, cudaStream_t stream) {
+  if (a.D <= 64) return launch_scores<GC, 8>(a, stream);
+  if (a.D <= 128) return launch_scores<GC, 16>(a, stream);
+  return launch_scores<GC, 32>(a, stream);
 }
 
 }  // namespace
 
 nvfp4_status launch_page_key_bounds(const BoundsArgs& a, cudaStream_t stream) {
-  const int64_t per = 8 * static_cast<int64_t>(sm_count()) / a.B + 1;
-  const int gx = static_cast<int>(a.max_pages < per ? a.max_pages : per);
-  page_key_bounds_kernel<<<dim3(gx, a.B), kBoundsThreads, 0, stream>>>(a);
+  const void* kern = reinterpret_cast<const void*>(page_key_bounds_kernel);
+  const size_t smem = static_cast<size_t>(a.B) * 4;
+  if (nvfp4_status st = set_dynamic_smem(kern, smem, "nvfp4_page_key_bounds")) return st;
+  const int64_t cap = static_cast<int64_t>(sm_count()) * blocks_per_sm(kern, kBoundsThreads, smem);
+  const int64_t most = a.B * a.max_pages;
+  const int grid = static_cast<int>(most < cap ? most : cap);
+  page_key_bounds_kernel<<<grid, kBoundsThreads, smem, stream>>>(a);
   return check_launch("nvfp4_page_key_bounds");
 }
 
@@ -207,6 +547,8 @@ int64_t select_workspace_bytes(int32_t B, int32_t H, int64_t max_pages) {
 }
 
 nvfp4_status launch_select_pages(const SelectArgs& a, cudaStream_t stream) {
+  const nvfp4_status st = a.G <= 4 ? launch_scores_t<4>(a, stream) : launch_scores_t<8>(a, stream);
+  if (st != NVFP4_OK) return st;
   select_pages_kernel<<<a.B * a.H, kSelectThreads, 0, stream>>>(a);
   return check_launch("nvfp4_select_pages");
 }
