@@ -852,7 +852,6 @@ NVFP4_EXPORT nvfp4_status nvfp4_qk_norm_rope_append_paged(
     a.q_out = static_cast<uint8_t*>(query_out);
     a.q_out_row_bytes = query_out_row_stride * 2;
     a.Hq = num_qo_heads;
-    a.div_rows = make_div(num_qo_heads + 2 * static_cast<int64_t>(num_kv_heads));
     a.q_weight = static_cast<const uint8_t*>(q_weight);
     a.k_weight = static_cast<const uint8_t*>(k_weight);
     a.eps = eps;

@@ -49,8 +49,9 @@ struct BoundsArgs {
   const int32_t* first_positions;  // may be null: 0
   uint16_t* bounds;
   int32_t* status;
+  int32_t tile, slices, pages;  // a CTA's shape, set at launch
 };
-nvfp4_status launch_page_key_bounds(const BoundsArgs& a, cudaStream_t stream);
+nvfp4_status launch_page_key_bounds(BoundsArgs a, cudaStream_t stream);
 
 struct SelectArgs {
   const uint8_t* q;

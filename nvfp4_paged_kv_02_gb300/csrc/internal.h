@@ -78,7 +78,6 @@ struct NormRopeArgs {
   uint8_t* q_out;
   int64_t q_out_row_bytes;
   int32_t Hq;
-  Div div_rows;  // query, key and value rows of a token
   const uint8_t* q_weight;  // null: that tensor is not normalized
   const uint8_t* k_weight;
   float eps, inv_d;
@@ -86,6 +85,10 @@ struct NormRopeArgs {
   int64_t num_positions;
   int32_t rotary_dim, interleaved;
   int32_t log2_T;  // lanes of a row
+  // set at launch: steps of a token's query rows and of its key (value) rows, and the parts that
+  // a token's steps are dealt out in
+  int32_t q_steps, kv_steps, parts, steps_per_part;
+  Div div_parts;
 };
 nvfp4_status launch_norm_rope_append(const NormRopeArgs& a, bool bf16, int mode,
                                      cudaStream_t stream);

@@ -18,6 +18,11 @@
 // eight elements that rotate together: groups j and j + R/16 below R/16, else 2j and 2j+1. A
 // rotation then needs no exchange, and the sum of squares is in-lane plus log2(T) shuffles. A
 // key row's 16-element blocks are put together through shared memory.
+//
+// A warp takes a token's rows a step at a time, 32/T rows of one kind to a step: first the query
+// rows, then the key rows, then the value rows. What the rows share (the table's row, the weights,
+// the page) is read once. With many tokens a warp has all steps of a token; with few, the steps
+// are dealt out so that every step has a warp. Query rows are loaded two steps at a time.
 #include "internal.h"
 #include "quantize.cuh"
 
@@ -70,6 +75,48 @@ __device__ __forceinline__ void load4(const float* p, float v[4]) {
   v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
 }
 
+// What a token's query and key rows share, in one lane: its groups, its part of the table's row.
+struct Turn {
+  int ga, gb;      // the lane's groups of eight
+  bool turns;      // they are rotated
+  float c[8], s[8];
+};
+
+template <bool BF16>
+__device__ __forceinline__ void norm_rope(const NormRopeArgs& a, const Turn& turn, uint4 wa, uint4 wb,
+                                          bool norm, int T, uint4& va, uint4& vb) {
+  float xa[8], xb[8];
+  unpack8<BF16>(va, xa);
+  unpack8<BF16>(vb, xb);
+  if (norm) {
+    float sum = __fadd_rn(sum_squares8(xa), sum_squares8(xb));
+    for (int o = T >> 1; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, o));
+    const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, a.inv_d), a.eps)));
+    float fa[8], fb[8];
+    unpack8<BF16>(wa, fa);
+    unpack8<BF16>(wb, fb);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      xa[e] = __fmul_rn(__fmul_rn(xa[e], r), fa[e]);
+      xb[e] = __fmul_rn(__fmul_rn(xb[e], r), fb[e]);
+    }
+  }
+  if (turn.turns) {
+    if (a.interleaved) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        rotate(xa[2 * e], xa[2 * e + 1], turn.c[e], turn.s[e]);
+        rotate(xb[2 * e], xb[2 * e + 1], turn.c[4 + e], turn.s[4 + e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) rotate(xa[e], xb[e], turn.c[e], turn.s[e]);
+    }
+  }
+  va = pack8<BF16>(xa);
+  vb = pack8<BF16>(xb);
+}
+
 template <bool BF16, int MODE>
 __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRopeArgs a) {
   __shared__ Tables tab;
@@ -77,104 +124,113 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
   float gs[2];
   if (!load_scales(a.ap, gs)) return;
   fill_tables<MODE>(tab, gs);
-  const TensorConsts tc[2] = {make_consts(gs[0]), make_consts(gs[1])};
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int T = 1 << a.log2_T, j = lane & (T - 1), nt = a.ap.D / 16, nr = a.rotary_dim / 16;
-  const int per_warp = 32 >> a.log2_T;
-  const int ga = j < nr ? j : 2 * j, gb = j < nr ? j + nr : 2 * j + 1;  // this lane's groups
-  const int32_t H = a.ap.H, row_kinds = a.Hq + 2 * H;
-  const int64_t rows = a.ap.nnz * row_kinds;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * per_warp;
-  for (int64_t first = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp) * per_warp;
-       first < rows; first += step) {
-    const int64_t row = first + (lane >> a.log2_T);
-    bool live = row < rows && j < nt;
-    const int64_t i = live ? div_q(row, a.div_rows) : 0;
-    const int32_t rr = live ? static_cast<int32_t>(row - i * row_kinds) : 0;
-    const int kind = rr < a.Hq ? 0 : (rr < a.Hq + H ? 1 : 2);  // query, key, value
-    const int32_t h = kind == 0 ? rr : (kind == 1 ? rr - a.Hq : rr - a.Hq - H);
+  const int per_step = 32 >> a.log2_T, slot_in_step = lane >> a.log2_T;
+  const int32_t H = a.ap.H;
+  const int64_t row = static_cast<int64_t>(a.ap.D) * 2;
+  Turn turn;
+  turn.turns = j < nr;
+  turn.ga = j < nt ? (j < nr ? j : 2 * j) : 0;
+  turn.gb = j < nt ? (j < nr ? j + nr : 2 * j + 1) : 0;
+  const int64_t items = a.ap.nnz * a.parts;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp; item < items;
+       item += static_cast<int64_t>(gridDim.x) * (kThreads / 32)) {
+    const int64_t i = div_q(item, a.div_parts);
+    const int32_t from = static_cast<int32_t>(item - i * a.parts) * a.steps_per_part;
+    const int32_t to = min(from + a.steps_per_part, a.q_steps + 2 * a.kv_steps);
     const int32_t pos = __ldg(a.ap.positions + i);
-    if (live && nr > 0 && (pos < 0 || pos >= a.num_positions)) {
-      flag(a.ap.status, NVFP4_DEV_BAD_POSITION);
-      live = false;
+    if (nr > 0 && (pos < 0 || pos >= a.num_positions)) {
+      if (lane == 0) flag(a.ap.status, NVFP4_DEV_BAD_POSITION);
+      continue;
     }
-    const uint8_t* src = kind == 0 ? a.q + i * a.q_row_bytes
-                                   : (kind == 1 ? a.ap.k + i * a.ap.k_row_bytes
-                                                : a.ap.v + i * a.ap.v_row_bytes);
-    src += static_cast<int64_t>(h) * a.ap.D * 2;
-    const int pa = kind == 2 ? 2 * j : ga, pb = kind == 2 ? 2 * j + 1 : gb;
-    uint4 va{}, vb{};
-    if (live) {
-      va = reinterpret_cast<const uint4*>(src)[pa];
-      vb = reinterpret_cast<const uint4*>(src)[pb];
-    }
-    float xa[8], xb[8];
-    unpack8<BF16>(va, xa);
-    unpack8<BF16>(vb, xb);
-    const uint8_t* w = kind == 0 ? a.q_weight : a.k_weight;
-    float sum = __fadd_rn(sum_squares8(xa), sum_squares8(xb));
-    for (int o = T >> 1; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, o));
-    if (live && kind != 2 && w != nullptr) {
-      const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, a.inv_d), a.eps)));
-      float wa[8], wb[8];
-      unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(w) + ga), wa);
-      unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(w) + gb), wb);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        xa[e] = __fmul_rn(__fmul_rn(xa[e], r), wa[e]);
-        xb[e] = __fmul_rn(__fmul_rn(xb[e], r), wb[e]);
-      }
-    }
-    if (live && kind != 2 && j < nr) {
+    if (turn.turns && from < a.q_steps + a.kv_steps) {
       const float* cs = a.cos_sin + static_cast<int64_t>(pos) * a.rotary_dim;
       const float* sn = cs + a.rotary_dim / 2;
-      float c[8], s[8];
-      if (a.interleaved) {
-        load4(cs + 4 * ga, c);
-        load4(cs + 4 * gb, c + 4);
-        load4(sn + 4 * ga, s);
-        load4(sn + 4 * gb, s + 4);
+      const int ca = a.interleaved ? 4 * turn.ga : 8 * j, cb = a.interleaved ? 4 * turn.gb : 8 * j + 4;
+      load4(cs + ca, turn.c);
+      load4(cs + cb, turn.c + 4);
+      load4(sn + ca, turn.s);
+      load4(sn + cb, turn.s + 4);
+    }
+    if (from < a.q_steps) {
+      uint4 wa{}, wb{};
+      if (a.q_weight) {
+        wa = __ldg(reinterpret_cast<const uint4*>(a.q_weight) + turn.ga);
+        wb = __ldg(reinterpret_cast<const uint4*>(a.q_weight) + turn.gb);
+      }
+      const uint8_t* src = a.q + i * a.q_row_bytes;
+      uint8_t* dst = a.q_out + i * a.q_out_row_bytes;
+      const int32_t end = min(to, a.q_steps);
+      for (int32_t step = from; step < end; step += 2) {
+        uint4 v[2][2] = {};
+        bool live[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          rotate(xa[2 * e], xa[2 * e + 1], c[e], s[e]);
-          rotate(xb[2 * e], xb[2 * e + 1], c[4 + e], s[4 + e]);
+        for (int k = 0; k < 2; ++k) {
+          const int32_t h = (step + k) * per_step + slot_in_step;
+          live[k] = step + k < end && h < a.Hq && j < nt;
+          if (live[k]) {
+            const uint4* x = reinterpret_cast<const uint4*>(src + h * row);
+            v[k][0] = x[turn.ga];
+            v[k][1] = x[turn.gb];
+          }
         }
-      } else {
-        load4(cs + 8 * j, c);
-        load4(cs + 8 * j + 4, c + 4);
-        load4(sn + 8 * j, s);
-        load4(sn + 8 * j + 4, s + 4);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) rotate(xa[e], xb[e], c[e], s[e]);
+        for (int k = 0; k < 2; ++k) {
+          if (step + k >= end) break;
+          norm_rope<BF16>(a, turn, wa, wb, a.q_weight != nullptr, T, v[k][0], v[k][1]);
+          if (live[k]) {
+            uint4* y = reinterpret_cast<uint4*>(dst + ((step + k) * per_step + slot_in_step) * row);
+            y[turn.ga] = v[k][0];
+            y[turn.gb] = v[k][1];
+          }
+        }
       }
     }
-    if (kind != 2) {
-      va = pack8<BF16>(xa);
-      vb = pack8<BF16>(xb);
+    if (to <= a.q_steps) continue;
+    const RowMeta m = resolve_row(a.ap, i);
+    uint4 wa{}, wb{};
+    if (a.k_weight && from < a.q_steps + a.kv_steps) {
+      wa = __ldg(reinterpret_cast<const uint4*>(a.k_weight) + turn.ga);
+      wb = __ldg(reinterpret_cast<const uint4*>(a.k_weight) + turn.gb);
     }
-    if (live && kind == 0) {
-      uint4* dst = reinterpret_cast<uint4*>(a.q_out + i * a.q_out_row_bytes +
-                                            static_cast<int64_t>(h) * a.ap.D * 2);
-      dst[ga] = va;
-      dst[gb] = vb;
-    }
-    if (!__any_sync(0xFFFFFFFFu, live && kind != 0)) continue;
-    uint4* buf = s_rows[warp] + (lane - j) * 2;
-    if (j < nt) {
-      buf[pa] = va;
-      buf[pb] = vb;
-    }
-    __syncwarp();
-    if (live && kind != 0) {
-      const RowMeta m = resolve_row(a.ap, i);
-      const int kv = kind - 1;
-      if (m.flags & (1 << kv)) {
+#pragma unroll 1
+    for (int32_t step = max(from, a.q_steps); step < to; ++step) {
+      const int kv = step >= a.q_steps + a.kv_steps;
+      const int32_t h = (step - a.q_steps - kv * a.kv_steps) * per_step + slot_in_step;
+      const bool live = h < H && j < nt;
+      const uint8_t* src = (kv ? a.ap.v + i * a.ap.v_row_bytes : a.ap.k + i * a.ap.k_row_bytes) + h * row;
+      uint4 lo{}, hi{};
+      if (kv) {
+        if (live) {
+          lo = reinterpret_cast<const uint4*>(src)[2 * j];
+          hi = reinterpret_cast<const uint4*>(src)[2 * j + 1];
+        }
+      } else {
+        if (live) {
+          lo = reinterpret_cast<const uint4*>(src)[turn.ga];
+          hi = reinterpret_cast<const uint4*>(src)[turn.gb];
+        }
+        norm_rope<BF16>(a, turn, wa, wb, a.k_weight != nullptr, T, lo, hi);
+        if (nr > 0) {  // groups back into blocks
+          uint4* buf = s_rows[warp] + (lane - j) * 2;
+          __syncwarp();
+          if (j < nt) {
+            buf[turn.ga] = lo;
+            buf[turn.gb] = hi;
+          }
+          __syncwarp();
+          lo = buf[2 * j];
+          hi = buf[2 * j + 1];
+        }
+      }
+      if (live && (m.flags & (1 << kv))) {
         U32x8 in;
-        const uint4 lo = buf[2 * j], hi = buf[2 * j + 1];
         in.w[0] = lo.x; in.w[1] = lo.y; in.w[2] = lo.z; in.w[3] = lo.w;
         in.w[4] = hi.x; in.w[5] = hi.y; in.w[6] = hi.z; in.w[7] = hi.w;
-        const BlockOut q = quantize_block<BF16, MODE>(in, tc[kv], tab, kv, a.ap.cap_a, a.ap.neg_zero);
+        const BlockOut q = quantize_block<BF16, MODE>(in, make_consts(kv ? gs[1] : gs[0]), tab, kv, a.ap.cap_a,
+                                                      a.ap.neg_zero);
         const nvfp4_paged_cache& c = kv ? a.ap.vc : a.ap.kc;
         const int64_t r = a.ap.layout == NVFP4_NHD ? static_cast<int64_t>(m.slot) * H + h
                                                    : static_cast<int64_t>(h) * a.ap.ps + m.slot;
@@ -183,18 +239,26 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
         c.sf[m.page * c.sf_page_stride + r * nt + j] = static_cast<uint8_t>(q.s);
       }
     }
-    __syncwarp();
   }
 }
 
 template <bool BF16, int MODE>
-nvfp4_status launch_t(const NormRopeArgs& a, cudaStream_t stream) {
+nvfp4_status launch_t(NormRopeArgs a, cudaStream_t stream) {
   const auto kern = norm_rope_append_kernel<BF16, MODE>;
-  const int64_t rows = a.ap.nnz * (a.Hq + 2 * static_cast<int64_t>(a.ap.H));
-  const int64_t per_cta = (kThreads / 32) * (32 >> a.log2_T);
-  const int64_t need = (rows + per_cta - 1) / per_cta;
   const int64_t cap = static_cast<int64_t>(sm_count()) *
                       blocks_per_sm(reinterpret_cast<const void*>(kern), kThreads, 0);
+  const int per_step = 32 >> a.log2_T;
+  a.q_steps = (a.Hq + per_step - 1) / per_step;
+  a.kv_steps = (a.ap.H + per_step - 1) / per_step;
+  // parts of a token: enough that the warps of one wave have an item each
+  const int64_t warps = cap * (kThreads / 32);
+  const int32_t steps = a.q_steps + 2 * a.kv_steps;
+  const int64_t wanted = (warps + a.ap.nnz - 1) / a.ap.nnz;
+  a.parts = static_cast<int32_t>(wanted < steps ? wanted : steps);
+  a.steps_per_part = (steps + a.parts - 1) / a.parts;
+  a.parts = (steps + a.steps_per_part - 1) / a.steps_per_part;
+  a.div_parts = make_div(a.parts);
+  const int64_t need = (a.ap.nnz * a.parts + kThreads / 32 - 1) / (kThreads / 32);
   const int grid = static_cast<int>(need < cap ? need : cap);
   kern<<<grid, kThreads, 0, stream>>>(a);
   return check_launch("nvfp4_qk_norm_rope_append_paged");

@@ -23,12 +23,13 @@ __device__ __forceinline__ int64_t table_entry(const void* tables, int32_t is64,
 // ---- bounds -----------------------------------------------------------------------------
 //
 // Reading the keys bounds it: 9/16 byte an element, and 4 bytes written for page_size of them.
-// A CTA takes one page, all heads, which is contiguous in either layout. A thread has one
-// 16-element block of a row (a column) and every kSlices-th slot; the slices are joined in
-// shared memory. kBatch slots of a thread are loaded before the first is decoded.
+// A thread has one column, a 16-element block of a head, and its slots of one page; kBatch slots
+// are loaded before the first is decoded. Pages of more than kMaxSlots slots give a column to
+// several threads, which join in shared memory.
 
 constexpr int kBoundsThreads = 256;
 constexpr int kBatch = 8;
+constexpr int kMaxSlots = 32;
 
 __device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -41,10 +42,12 @@ __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// A CTA takes `pages` items of `tile` columns in `slices` threads each (their product is at most
+// kBoundsThreads); tiles x items make its work. Thread: (item, slice, column), column fastest.
+template <bool SLICED>
 __global__ void __launch_bounds__(kBoundsThreads) page_key_bounds_kernel(const BoundsArgs a) {
   extern __shared__ int32_t s_cum[];
-  // slice ts, word w (lo 0-7, hi 8-15) of column c at [ts][w][c]: c below kBoundsThreads / slices
-  __shared__ uint32_t s_part[16 * kBoundsThreads];
+  __shared__ uint32_t s_part[SLICED ? 16 * kBoundsThreads : 1];
   const int tid = threadIdx.x, nb = a.D / 16;
   const int64_t reach = a.max_pages * a.ps;
   auto len_of = [&](int32_t b) { return min(static_cast<int64_t>(__ldg(a.seq_lens + b)), reach); };
@@ -54,37 +57,34 @@ __global__ void __launch_bounds__(kBoundsThreads) page_key_bounds_kernel(const B
   block_inclusive_scan(s_cum, a.B, [&](int32_t b) {
     const int64_t len = len_of(b);
     if (blockIdx.x == 0 && __ldg(a.seq_lens + b) > reach) flag(a.status, NVFP4_DEV_LEN_CLAMPED);
-    const int32_t pages = len > 0 ? static_cast<int32_t>((len + a.ps - 1) / a.ps) : 0;
+    const int32_t pages = len > 0 ? div_q32(static_cast<int32_t>(len - 1), a.div_ps) + 1 : 0;
     return max(pages - first_of(b), 0);
   });
   const int32_t total = s_cum[a.B - 1];
   const int32_t columns = a.H * nb;
-  const int tile = min(columns, kBoundsThreads);        // columns at a time
-  const int slices = max(kBoundsThreads / tile, 1);     // threads of a column
-  const int col_l = a.layout == NVFP4_NHD ? tid % tile : tid / (slices * nb) * nb + tid % nb;
-  const int ts = a.layout == NVFP4_NHD ? tid / tile : tid / nb % slices;
-  // (HND: slices of one head are neighbours, so that a warp's loads are contiguous. A tile of
-  // columns then has to be whole heads; where it is not, the NHD arrangement serves.)
-  const bool by_head = a.layout == NVFP4_HND && tile % nb == 0;
-  const int my_col = by_head ? col_l : tid % tile, my_slice = by_head ? ts : tid / tile;
+  const int my_col = tid % a.tile, my_slice = tid / a.tile % a.slices, my_item = tid / (a.tile * a.slices);
+  const bool in_team = my_item < a.pages;
 
-  for (int32_t item = blockIdx.x; item < total; item += gridDim.x) {
+  for (int64_t item0 = static_cast<int64_t>(blockIdx.x) * a.pages; item0 < total;
+       item0 += static_cast<int64_t>(gridDim.x) * a.pages) {
+    const int32_t item = static_cast<int32_t>(min(item0 + my_item, static_cast<int64_t>(total - 1)));
+    const bool live = in_team && item0 + my_item < total;
     const int32_t b = scan_find(s_cum, a.B, item);
     const int32_t col = item - (b > 0 ? s_cum[b - 1] : 0) + first_of(b);
-    const int64_t page = table_entry(a.block_tables, a.table64, b * a.max_pages + col);
+    int64_t page = live ? table_entry(a.block_tables, a.table64, b * a.max_pages + col) : -1;
     if (page < 0 || page >= a.kc.num_pages) {
-      if (tid == 0) flag(a.status, NVFP4_DEV_BAD_PAGE);
-      continue;
+      if (live) flag(a.status, NVFP4_DEV_BAD_PAGE);
+      page = -1;
     }
     const int32_t n = static_cast<int32_t>(min(static_cast<int64_t>(a.ps), len_of(b) - static_cast<int64_t>(col) * a.ps));
     const uint8_t* codes = a.kc.data + page * a.kc.data_page_stride;
     const uint8_t* scales = a.kc.sf + page * a.kc.sf_page_stride;
-    for (int32_t c0 = 0; c0 < columns; c0 += tile) {
+    for (int32_t c0 = 0; c0 < columns; c0 += a.tile) {
       const int32_t w = c0 + my_col;
-      const bool mine = my_slice < slices && my_col < tile && w < columns;
+      const bool mine = page >= 0 && w < columns;
       const int32_t h = w / nb, j = w - h * nb;
-      // block of slot t: base + t * step
-      const int64_t base = a.layout == NVFP4_NHD ? w : static_cast<int64_t>(h) * a.ps * nb + j;
+      // block of slot t: at + t * step
+      const int32_t at = a.layout == NVFP4_NHD ? w : h * a.ps * nb + j;
       const int32_t step = a.layout == NVFP4_NHD ? columns : nb;
       uint32_t lo[8], hi[8];
 #pragma unroll
@@ -93,16 +93,15 @@ __global__ void __launch_bounds__(kBoundsThreads) page_key_bounds_kernel(const B
         hi[e] = 0xFC00FC00u;
       }
       if (mine) {
-        for (int32_t t0 = my_slice; t0 < n; t0 += kBatch * slices) {
+        for (int32_t t0 = my_slice; t0 < n; t0 += kBatch * a.slices) {
           uint2 c[kBatch];
           uint32_t s[kBatch];
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
-            // (past the end: the batch's first slot again)
-            const int32_t t = t0 + k * slices < n ? t0 + k * slices : t0;
-            const int64_t at = base + static_cast<int64_t>(t) * step;
-            c[k] = __ldg(reinterpret_cast<const uint2*>(codes) + at);
-            s[k] = __ldg(scales + at);
+            const int32_t t = min(t0 + k * a.slices, n - 1);  // (past the end: the last slot again)
+            const int32_t blk = at + t * step;
+            c[k] = __ldg(reinterpret_cast<const uint2*>(codes) + blk);
+            s[k] = __ldg(scales + blk);
           }
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
@@ -119,28 +118,33 @@ __global__ void __launch_bounds__(kBoundsThreads) page_key_bounds_kernel(const B
           }
         }
       }
-      __syncthreads();  // the last page's reads are done
-      if (mine) {
+      if (SLICED) {
+        __syncthreads();  // what the last tile left has been read
+        if (mine) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s_part[(my_slice * 16 + e) * tile + my_col] = lo[e];
-          s_part[(my_slice * 16 + 8 + e) * tile + my_col] = hi[e];
+          for (int e = 0; e < 8; ++e) {
+            s_part[e * kBoundsThreads + tid] = lo[e];
+            s_part[(8 + e) * kBoundsThreads + tid] = hi[e];
+          }
+        }
+        __syncthreads();
+        if (mine && my_slice == 0) {
+          for (int q = 1; q < a.slices; ++q) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              lo[e] = hmin2(lo[e], s_part[e * kBoundsThreads + tid + q * a.tile]);
+              hi[e] = hmax2(hi[e], s_part[(8 + e) * kBoundsThreads + tid + q * a.tile]);
+            }
+          }
         }
       }
-      __syncthreads();
-      // words of the output: [head][lo, hi][block][8 words]
-      const int32_t cols = min(tile, columns - c0);
-      for (int k = tid; k < cols * 16; k += kBoundsThreads) {
-        const int e = k & 7, cw = k >> 3;  // word of a block; (column, lo or hi)
-        const int which = cw >= cols, cl = cw - which * cols;
-        uint32_t v = s_part[(which * 8 + e) * tile + cl];
-        for (int q = 1; q < slices; ++q) {
-          const uint32_t x = s_part[(q * 16 + which * 8 + e) * tile + cl];
-          v = which ? hmax2(v, x) : hmin2(v, x);
-        }
-        const int32_t hh = (c0 + cl) / nb, jj = c0 + cl - hh * nb;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(a.bounds + ((page * a.H + hh) * 2 + which) * a.D);
-        dst[8 * jj + e] = v;
+      if (mine && my_slice == 0) {
+        uint4* dst = reinterpret_cast<uint4*>(a.bounds + (page * a.H + h) * 2 * a.D + 16 * j);
+        uint4* dst_hi = reinterpret_cast<uint4*>(a.bounds + ((page * a.H + h) * 2 + 1) * a.D + 16 * j);
+        dst[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        dst[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+        dst_hi[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        dst_hi[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
       }
     }
   }
@@ -148,7 +152,7 @@ __global__ void __launch_bounds__(kBoundsThreads) page_key_bounds_kernel(const B
 
 // ---- scores -----------------------------------------------------------------------------
 //
-// A unit is 32 pages of one (request, KV head). All units are cut into equal runs, one for each
+// A unit is kUnitPages pages of one (request, KV head). All units are cut into equal runs, one for each
 // warp; a warp holds its query heads in registers (as positive and negative parts) and passes
 // over the pages' bounds once, T lanes to a page (T = D/8 rounded up), each lane eight elements.
 // A lane's bounds come through its own ring of stages in shared memory (cp.async; no other lane
@@ -157,6 +161,7 @@ __global__ void __launch_bounds__(kBoundsThreads) page_key_bounds_kernel(const B
 
 constexpr int kScoreWarps = 4;
 constexpr int kScoreStages = 8;
+constexpr int kUnitPages = 8;
 
 // Unsigned keys in the order of the scores.
 __device__ __forceinline__ uint32_t key_of(float s) {
@@ -183,7 +188,7 @@ __device__ __forceinline__ int32_t pages_of(const SelectArgs& a, int32_t b) {
 }
 
 template <int GC, int T>
-__global__ void __launch_bounds__(kScoreWarps * 32) page_scores_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kScoreWarps * 32, GC == 4 ? 3 : 2) page_scores_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kPages = 32 / T;  // of an iteration
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -191,7 +196,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) page_scores_kernel(const Sel
   int32_t* cum = reinterpret_cast<int32_t*>(smem + kScoreWarps * kScoreStages * 1024);
   block_inclusive_scan(cum, a.B, [&](int32_t b) {
     if (blockIdx.x == 0 && __ldg(a.seq_lens + b) > a.max_pages * a.ps) flag(a.status, NVFP4_DEV_LEN_CLAMPED);
-    return (pages_of(a, b) + 31) / 32;
+    return (pages_of(a, b) + kUnitPages - 1) / kUnitPages;
   });
   const int64_t total = static_cast<int64_t>(cum[a.B - 1]) * a.H;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kScoreWarps;
@@ -229,23 +234,24 @@ __global__ void __launch_bounds__(kScoreWarps * 32) page_scores_kernel(const Sel
           qn[g][i] = pack2(fminf(x, 0.0f), fminf(y, 0.0f));
         }
       }
-      // iterations: kPages pages each, T of them to a unit
-      const int32_t it_end = (last - first) * T;
+      // iterations: kPages pages each, kIts of them to a unit
+      constexpr int kIts = kUnitPages / kPages;
+      const int32_t it_end = (last - first) * kIts;
       int32_t issued = 0, entry_unit = -1, entry = -1;
       auto issue = [&] {
         if (issued < it_end) {
-          const int32_t unit = issued / T;
-          if (unit != entry_unit) {  // the unit's 32 pages, one to a lane
+          const int32_t unit = issued / kIts;
+          if (unit != entry_unit) {  // the unit's pages, one to a lane
             entry_unit = unit;
-            const int32_t col = (first + unit) * 32 + lane;
+            const int32_t col = (first + unit) * kUnitPages + lane;
             entry = -1;
-            if (col < n) {
+            if (lane < kUnitPages && col < n) {
               const int64_t page = table_entry(a.block_tables, a.table64, b * a.max_pages + col);
               if (page >= 0 && page < a.num_pages) entry = static_cast<int32_t>(page);
               else flag(a.status, NVFP4_DEV_BAD_PAGE);
             }
           }
-          const int32_t page = __shfl_sync(0xFFFFFFFFu, entry, issued % T * kPages + group);
+          const int32_t page = __shfl_sync(0xFFFFFFFFu, entry, issued % kIts * kPages + group);
           const bool live = page >= 0 && active;
           const uint16_t* src = a.bounds + ((static_cast<int64_t>(live ? page : 0) * a.H + h) * 2 * a.D + (live ? 8 * sub : 0));
           const uint32_t dst = ring + issued % kScoreStages * 1024;
@@ -307,10 +313,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32) page_scores_kernel(const Sel
         for (int o = T / 2; o >= (T > GC ? T / GC : 1); o /= 2) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
         // lane l keeps the score of the unit's page l
         const float got = __shfl_sync(0xFFFFFFFFu, best, lane % kPages * T);
-        if (lane / kPages == it % T) mine = got;
-        if (it % T == T - 1) {
-          const int32_t j = (first + it / T) * 32 + lane;
-          if (j < n) {
+        if (lane / kPages == it % kIts) mine = got;
+        if (it % kIts == kIts - 1) {
+          const int32_t j = (first + it / kIts) * kUnitPages + lane;
+          if (lane < kUnitPages && j < n) {
             // (a page outside the pool was copied as zeros: it comes last)
             const int64_t page = table_entry(a.block_tables, a.table64, b * a.max_pages + j);
             const bool bad = page < 0 || page >= a.num_pages;
@@ -364,19 +370,22 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     for (int32_t j = tid; j < n; j += kSelectThreads) out[j] = j;
     return;
   }
-  // A thread's keys are neighbours, so that page order is thread order: the first tile's in
-  // registers, what is past it (a list longer than kSelectThreads * kPerThread) read again.
+  // A thread's keys are neighbours, so that page order is thread order: `each_n` of them, in
+  // registers; of a list longer than kSelectThreads * kPerThread the rest is read again each time.
   constexpr int32_t kTile = kSelectThreads * kPerThread;
+  const int32_t each_n = min((n + kSelectThreads - 1) / kSelectThreads, kPerThread);
   uint32_t mine[kPerThread];
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
-    const int32_t j = tid * kPerThread + i;
-    mine[i] = j < n ? __ldcg(keys + j) : 0u;
+    const int32_t j = tid * each_n + i;
+    mine[i] = i < each_n && j < n ? __ldcg(keys + j) : 0u;
   }
-  auto each = [&](auto body) {  // of this thread's keys, in page order inside a tile
+  auto each = [&](auto body) {  // of this thread's keys
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i)
-      if (tid * kPerThread + i < n) body(mine[i]);
+    for (int i = 0; i < kPerThread; ++i) {
+      if (i >= each_n) break;
+      if (tid * each_n + i < n) body(mine[i]);
+    }
     for (int32_t t = kTile; t < n; t += kTile)
       for (int i = 0; i < kPerThread; ++i) {
         const int32_t j = t + tid * kPerThread + i;
@@ -421,10 +430,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
       for (int i = tid; i < kBins; i += kSelectThreads) s_hist[i] = 0;
       __syncthreads();
       each([&](uint32_t k) {
-        if (k >= floor_ && k <= ceil_) {
-          // lanes of one bin add together: neighbours' scores often share it
-          atomicAdd(s_hist + ((k - base) >> shift), 1u);
-        }
+        if (k >= floor_ && k <= ceil_) atomicAdd(s_hist + ((k - base) >> shift), 1u);
       });
       __syncthreads();
       // the bin of the want-th largest: bins from the top, kBins = kSelectThreads of them
@@ -464,9 +470,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     uint32_t k[kPerThread];
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
-      const int32_t j = t + tid * kPerThread + i;
+      const int32_t j = t + tid * each_n + i;
       k[i] = t == 0 ? mine[i] : (j < n ? __ldcg(keys + j) : 0u);
-      if (j < n) {
+      if (i < each_n && j < n) {
         above += k[i] > ceil_;
         in += k[i] >= floor_ && k[i] <= ceil_;
       }
@@ -497,8 +503,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     }
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
-      const int32_t j = t + tid * kPerThread + i;
-      if (j >= n) continue;
+      const int32_t j = t + tid * each_n + i;
+      if (i >= each_n || j >= n) continue;
       const bool is_above = k[i] > ceil_, is_in = k[i] >= floor_ && k[i] <= ceil_;
       if (is_above || (is_in && ni < want)) out[na + min(ni, want)] = j;
       na += is_above;
@@ -516,7 +522,7 @@ nvfp4_status launch_scores(const SelectArgs& a, cudaStream_t stream) {
   if (nvfp4_status st = set_dynamic_smem(reinterpret_cast<const void*>(kern), smem, "nvfp4_select_pages")) return st;
   const int64_t cap = static_cast<int64_t>(sm_count()) *
                       blocks_per_sm(reinterpret_cast<const void*>(kern), kScoreWarps * 32, smem);
-  const int64_t most = (static_cast<int64_t>(a.B) * a.H * ((a.max_pages + 31) / 32) + kScoreWarps - 1) / kScoreWarps;
+  const int64_t most = (static_cast<int64_t>(a.B) * a.H * ((a.max_pages + kUnitPages - 1) / kUnitPages) + kScoreWarps - 1) / kScoreWarps;
   const int grid = static_cast<int>(most < cap ? most : cap);
   if (grid > 0) kern<<<grid, kScoreWarps * 32, smem, stream>>>(a);
   return check_launch("nvfp4_select_pages");
@@ -531,14 +537,21 @@ nvfp4_status launch_scores_t(const SelectArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-nvfp4_status launch_page_key_bounds(const BoundsArgs& a, cudaStream_t stream) {
-  const void* kern = reinterpret_cast<const void*>(page_key_bounds_kernel);
+nvfp4_status launch_page_key_bounds(BoundsArgs a, cudaStream_t stream) {
+  const int32_t columns = a.H * (a.D / 16);
+  a.tile = columns < kBoundsThreads ? columns : kBoundsThreads;
+  a.slices = (a.ps + kMaxSlots - 1) / kMaxSlots;
+  const int32_t most_slices = kBoundsThreads / a.tile;
+  if (a.slices > most_slices) a.slices = most_slices;
+  a.pages = kBoundsThreads / (a.tile * a.slices);
+  const auto kern = a.slices > 1 ? page_key_bounds_kernel<true> : page_key_bounds_kernel<false>;
+  const void* f = reinterpret_cast<const void*>(kern);
   const size_t smem = static_cast<size_t>(a.B) * 4;
-  if (nvfp4_status st = set_dynamic_smem(kern, smem, "nvfp4_page_key_bounds")) return st;
-  const int64_t cap = static_cast<int64_t>(sm_count()) * blocks_per_sm(kern, kBoundsThreads, smem);
-  const int64_t most = a.B * a.max_pages;
+  if (nvfp4_status st = set_dynamic_smem(f, smem, "nvfp4_page_key_bounds")) return st;
+  const int64_t cap = static_cast<int64_t>(sm_count()) * blocks_per_sm(f, kBoundsThreads, smem);
+  const int64_t most = (a.B * a.max_pages + a.pages - 1) / a.pages;
   const int grid = static_cast<int>(most < cap ? most : cap);
-  page_key_bounds_kernel<<<grid, kBoundsThreads, smem, stream>>>(a);
+  kern<<<grid, kBoundsThreads, smem, stream>>>(a);
   return check_launch("nvfp4_page_key_bounds");
 }
 
