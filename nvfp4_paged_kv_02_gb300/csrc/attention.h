@@ -49,7 +49,10 @@ struct BoundsArgs {
   const int32_t* first_positions;  // may be null: 0
   uint16_t* bounds;
   int32_t* status;
-  int32_t tile, slices, pages;  // a CTA's shape, set at launch
+  // set at launch: a CTA's shape, and the ring's
+  int32_t tile, slices, pages, stages;
+  uint32_t code_bytes, scale_bytes, stage_bytes;
+  PipeTest pipe;
 };
 nvfp4_status launch_page_key_bounds(BoundsArgs a, cudaStream_t stream);
 
@@ -65,10 +68,11 @@ struct SelectArgs {
   int32_t k, sink, recent;
   int32_t* selected;
   int32_t* num_selected;
-  uint32_t* scores;  // workspace: [B, H, max_pages]
+  uint32_t* scores;  // workspace: [B, H, pitch]
   int32_t* status;
+  int64_t pitch;  // set at launch
 };
 int64_t select_workspace_bytes(int32_t B, int32_t H, int64_t max_pages);
-nvfp4_status launch_select_pages(const SelectArgs& a, cudaStream_t stream);
+nvfp4_status launch_select_pages(SelectArgs a, cudaStream_t stream);
 
 }  // namespace nvfp4

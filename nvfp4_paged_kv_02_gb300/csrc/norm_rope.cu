@@ -29,7 +29,7 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // Exact binary32 values of eight packed elements.
 template <bool BF16>
