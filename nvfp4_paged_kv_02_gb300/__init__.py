@@ -108,6 +108,8 @@ _lib = None
 def load() -> ctypes.CDLL:
     """Build (if stale) and load libnvfp4kv.so. Raises if it cannot be built or loaded."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -603,32 +605,34 @@ def nvfp4_4over6_from_code(code: int) -> Optional[NVFP44Over6Config]:
 
 # ---- the operators of a decode step -----------------------------------------------------------
 
+# (These calls run once per layer and step, so their checks read each tensor's properties once.)
+
 def _addr(t: torch.Tensor, dtype, device: torch.device, what: str) -> int:
     """Address of a contiguous tensor of the given dtype on `device`."""
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor on {device}")
     return t.data_ptr()
 
 
 def _device(t: torch.Tensor) -> torch.device:
-    device = t.device
-    if device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("nvfp4 ops take CUDA tensors only")
-    return device
+    return t.device
 
 
-def _rows(t: torch.Tensor, dtype, device: torch.device, what: str, heads: Optional[int] = None,
-          head_dim: Optional[int] = None) -> int:
-    """Checks rows [n, heads, head_dim] whose heads and elements are contiguous; their stride."""
-    if t.dtype != dtype or t.device != device or t.dim() != 3:
+def _rows(t: torch.Tensor, dtype, device: torch.device, what: str, heads: int, head_dim: int):
+    """Checks rows [n, heads, head_dim] (heads < 0: any number) whose heads and elements are contiguous;
+    returns (n, heads, stride, address)."""
+    shape = t.shape
+    if len(shape) != 3 or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{what} must be a [n, heads, head_dim] {dtype} tensor on {device}")
-    n, h, d = t.shape
+    n, h, d = shape
+    if d != head_dim or (h != heads and heads >= 0):
+        raise ValueError(f"{what} must have {heads if heads >= 0 else 'its'} heads of {head_dim} elements")
     sn, sh, sd = t.stride()
-    if (heads is not None and h != heads) or (head_dim is not None and d != head_dim):
-        raise ValueError(f"{what} must have {heads} heads of {head_dim} elements")
     if sd != 1 or (sh != d and h > 1):
         raise ValueError(f"{what} must have contiguous heads and elements")
-    return sn if n > 1 else h * d
+    return n, h, sn if n > 1 else h * d, t.data_ptr()
 
 
 def _status_ptr(t: Optional[torch.Tensor], device: torch.device) -> Optional[int]:
@@ -636,19 +640,31 @@ def _status_ptr(t: Optional[torch.Tensor], device: torch.device) -> Optional[int
 
 
 def _block_tables(t: torch.Tensor, batch: int, device: torch.device):
-    if t.dim() != 2 or t.shape[0] != batch or t.dtype not in (torch.int32, torch.int64) \
+    shape, dtype = t.shape, t.dtype
+    if len(shape) != 2 or shape[0] != batch or (dtype is not torch.int32 and dtype is not torch.int64) \
             or t.device != device or not t.is_contiguous():
         raise ValueError(f"block_tables must be a contiguous [{batch}, max_pages] int32/int64 tensor on {device}")
-    return t.data_ptr(), I64 if t.dtype == torch.int64 else I32, t.shape[1]
+    return t.data_ptr(), I64 if dtype is torch.int64 else I32, shape[1]
 
 
-def _cache_on(data: torch.Tensor, sf: torch.Tensor, device: torch.device) -> Tuple[_Cache, torch.Size]:
-    """The C form of one cache and its code tensor's shape, checked as _one_cache checks it."""
-    c = _one_cache(data, sf)
-    if data.device != device or sf.device != device or sf.shape[:3] != data.shape[:3] \
-            or sf.shape[3] * 8 != data.shape[3]:
+_SCALE_DTYPES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _cache_on(data: torch.Tensor, sf: torch.Tensor, device: torch.device):
+    """The C form of one cache and its code tensor's shape, with the checks of _one_cache."""
+    ds, ss = data.shape, sf.shape
+    if data.dtype is not torch.uint8 or sf.dtype not in _SCALE_DTYPES:
+        raise ValueError("paged caches are uint8 codes and uint8 / float8_e4m3fn scales")
+    if len(ds) != 4 or len(ss) != 4:
+        raise ValueError("a paged cache tensor is 4-D [pages, ., ., head_dim // 2|16]")
+    p, a, b, c = ds
+    if data.device != device or sf.device != device or ss != (p, a, b, c >> 3) or c & 7:
         raise ValueError(f"codes [pages, ., ., D/2] and scales [pages, ., ., D/16] must match, on {device}")
-    return c._c(), data.shape
+    d0, d1, d2, d3 = data.stride()
+    s0, s1, s2, s3 = sf.stride()
+    if d3 != 1 or d2 != c or d1 != b * c or s3 != 1 or s2 != c >> 3 or s1 != b * c >> 3:
+        raise ValueError("paged cache pages must be contiguous inside (page stride may be larger)")
+    return _Cache(data.data_ptr(), sf.data_ptr(), d0, s0, p), ds
 
 
 def _caches_on(paged_kv_cache, kv_cache_sf, layout: int, device: torch.device):
@@ -667,6 +683,12 @@ def _caches_on(paged_kv_cache, kv_cache_sf, layout: int, device: torch.device):
     return kc, vc, ks[2], ks[1], ks[3] * 2
 
 
+def _device_scale(s, device: torch.device) -> int:
+    if not isinstance(s, torch.Tensor) or s.dtype is not torch.float32 or s.device != device or s.numel() < 1:
+        raise ValueError("k_scale/v_scale must be float32 CUDA tensors")
+    return s.data_ptr()
+
+
 # Workspaces of the attention and selection calls, one per (device, stream) as above; a larger one takes
 # its place when a call needs it. A call that is being captured gets its own from the graph's memory, so
 # that a graph never depends on what later calls do with these.
@@ -676,7 +698,7 @@ _scratch = {}
 def _scratch_for(device: torch.device, stream: int, nbytes: int, zeroed: int) -> torch.Tensor:
     """At least nbytes of device memory whose first `zeroed` bytes are zero between calls."""
     key = (device.index, stream, zeroed)
-    capturing = torch.cuda.is_current_stream_capturing()
+    capturing = torch._C._cuda_isCurrentStreamCapturing()
     t = None if capturing else _scratch.get(key)
     if t is None or t.numel() < nbytes:
         t = torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -688,7 +710,24 @@ def _scratch_for(device: torch.device, stream: int, nbytes: int, zeroed: int) ->
 
 
 def _raw_stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+_workspace_bytes = {}
+
+
+def _bytes_for(fn: str, device: torch.device, *sizes: int) -> int:
+    """What the library's function `fn` says of these sizes, asked once for each."""
+    key = (fn, device.index, sizes)
+    n = _workspace_bytes.get(key)
+    if n is None:
+        need = ctypes.c_int64()
+        with torch.cuda.device(device):
+            _check(fn, getattr(load(), fn)(*sizes, ctypes.byref(need)))
+        n = _workspace_bytes[key] = need.value
+        if len(_workspace_bytes) > 4096:
+            _workspace_bytes.clear()
+    return n
 
 
 def nvfp4_qk_norm_rope_append_paged(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -711,22 +750,20 @@ def nvfp4_qk_norm_rope_append_paged(query: torch.Tensor, key: torch.Tensor, valu
     code = _dtype_code(dt)
     layout = _layout(kv_layout)
     kc, vc, ps, H, D = _caches_on(paged_kv_cache, kv_cache_sf, layout, device)
-    q_stride = _rows(query, dt, device, "query", None, D)
-    k_stride = _rows(key, dt, device, "key", H, D)
-    v_stride = _rows(value, dt, device, "value", H, D)
-    nnz, Hq = query.shape[0], query.shape[1]
-    if key.shape[0] != nnz or value.shape[0] != nnz or batch_indices.numel() != nnz or positions.numel() != nnz:
+    nnz, Hq, q_stride, q_ptr = _rows(query, dt, device, "query", -1, D)
+    k_rows, _, k_stride, k_ptr = _rows(key, dt, device, "key", H, D)
+    v_rows, _, v_stride, v_ptr = _rows(value, dt, device, "value", H, D)
+    if k_rows != nnz or v_rows != nnz or batch_indices.numel() != nnz or positions.numel() != nnz:
         raise ValueError("query, key, value, batch_indices and positions must have as many rows")
-    for w in (q_weight, k_weight):
-        if w is not None and w.numel() != D:
-            raise ValueError("a norm's weights must have head_dim elements")
+    if (q_weight is not None and q_weight.numel() != D) or (k_weight is not None and k_weight.numel() != D):
+        raise ValueError("a norm's weights must have head_dim elements")
     npos, rot = (0, 0) if cos_sin is None else cos_sin.shape
     if out is None:
         out = torch.empty((nnz, Hq, D), dtype=dt, device=device)
-        o_stride = Hq * D
+        o_stride, o_ptr = Hq * D, out.data_ptr()
     else:
-        o_stride = _rows(out, dt, device, "out", Hq, D)
-        if out.shape[0] != nnz:
+        o_rows, _, o_stride, o_ptr = _rows(out, dt, device, "out", Hq, D)
+        if o_rows != nnz:
             raise ValueError("out must have query's shape")
     i32 = torch.int32
     B = kv_indptr.numel() - 1
@@ -735,24 +772,23 @@ def nvfp4_qk_norm_rope_append_paged(query: torch.Tensor, key: torch.Tensor, valu
     ks = vs = 1.0
     k_dev = v_dev = None
     if isinstance(k_scale, torch.Tensor) or isinstance(v_scale, torch.Tensor):
-        for s in (k_scale, v_scale):
-            if not isinstance(s, torch.Tensor) or s.dtype != torch.float32 or s.numel() < 1 or s.device != device:
-                raise ValueError("device scales must both be float32 CUDA tensors")
-        k_dev, v_dev = k_scale.data_ptr(), v_scale.data_ptr()
+        k_dev, v_dev = _device_scale(k_scale, device), _device_scale(v_scale, device)
     else:
         ks, vs = float(k_scale), float(v_scale)
-    _check("nvfp4_qk_norm_rope_append_paged", load().nvfp4_qk_norm_rope_append_paged(
-        query.data_ptr(), key.data_ptr(), value.data_ptr(), code, nnz, Hq, H, D, q_stride, k_stride,
-        v_stride, None if q_weight is None else _addr(q_weight, dt, device, "q_weight"),
+    code = load().nvfp4_qk_norm_rope_append_paged(
+        q_ptr, k_ptr, v_ptr, code, nnz, Hq, H, D, q_stride, k_stride, v_stride,
+        None if q_weight is None else _addr(q_weight, dt, device, "q_weight"),
         None if k_weight is None else _addr(k_weight, dt, device, "k_weight"), eps,
         None if cos_sin is None else _addr(cos_sin, torch.float32, device, "cos_sin"), npos, rot,
-        int(bool(rotary_interleaved)), _addr(batch_indices, i32, device, "batch_indices"),
+        1 if rotary_interleaved else 0, _addr(batch_indices, i32, device, "batch_indices"),
         _addr(positions, i32, device, "positions"), kc, vc, ps, layout,
         _addr(kv_indices, i32, device, "kv_indices"), kv_indices.numel(),
         _addr(kv_indptr, i32, device, "kv_indptr"),
         None if kv_last_page_len is None else _addr(kv_last_page_len, i32, device, "kv_last_page_len"),
-        B, ks, vs, k_dev, v_dev, _recipe(nvfp4_4over6), out.data_ptr(), o_stride,
-        _status_ptr(dev_status, device), _raw_stream(device)))
+        B, ks, vs, k_dev, v_dev, _recipe(nvfp4_4over6), o_ptr, o_stride, _status_ptr(dev_status, device),
+        _raw_stream(device))
+    if code:
+        _check("nvfp4_qk_norm_rope_append_paged", code)
     return out
 
 
@@ -796,8 +832,7 @@ def nvfp4_select_pages(query: torch.Tensor, key_bounds: torch.Tensor, block_tabl
     if key_bounds.dim() != 4 or key_bounds.shape[2] != 2:
         raise ValueError("key_bounds must be [num_pages, num_kv_heads, 2, head_dim]")
     P, H, _, D = key_bounds.shape
-    stride = _rows(query, dt, device, "query", None, D)
-    B, Hq = query.shape[0], query.shape[1]
+    B, Hq, stride, q_ptr = _rows(query, dt, device, "query", -1, D)
     if seq_lens.numel() != B:
         raise ValueError("seq_lens must have one entry per request")
     table, table_dtype, width = _block_tables(block_tables, B, device)
@@ -808,18 +843,16 @@ def nvfp4_select_pages(query: torch.Tensor, key_bounds: torch.Tensor, block_tabl
         selected, count = out
         if selected.shape != (B, H, max_selected) or count.shape != (B, H):
             raise ValueError("out must be ([B, H, max_selected], [B, H]) int32 tensors")
-    lib = load()
-    need = ctypes.c_int64()
-    _check("nvfp4_select_pages_workspace_bytes",
-           lib.nvfp4_select_pages_workspace_bytes(B, H, width, ctypes.byref(need)))
     stream = _raw_stream(device)
-    ws = _scratch_for(device, stream, need.value, 0)
-    _check("nvfp4_select_pages", lib.nvfp4_select_pages(
-        query.data_ptr(), code, stride, Hq, H, D, _addr(key_bounds, torch.float16, device, "key_bounds"),
-        P, page_size, table, table_dtype, width, _addr(seq_lens, torch.int32, device, "seq_lens"), B,
-        max_selected, num_sink_pages, num_recent_pages,
-        _addr(selected, torch.int32, device, "selected_pages"), _addr(count, torch.int32, device, "num_selected"),
-        _status_ptr(dev_status, device), ws.data_ptr(), ws.numel(), stream))
+    ws = _scratch_for(device, stream, _bytes_for("nvfp4_select_pages_workspace_bytes", device, B, H, width), 0)
+    code = load().nvfp4_select_pages(
+        q_ptr, code, stride, Hq, H, D, _addr(key_bounds, torch.float16, device, "key_bounds"), P, page_size,
+        table, table_dtype, width, _addr(seq_lens, torch.int32, device, "seq_lens"), B, max_selected,
+        num_sink_pages, num_recent_pages, _addr(selected, torch.int32, device, "selected_pages"),
+        _addr(count, torch.int32, device, "num_selected"), _status_ptr(dev_status, device), ws.data_ptr(),
+        ws.numel(), stream)
+    if code:
+        _check("nvfp4_select_pages", code)
     return selected, count
 
 
@@ -829,42 +862,46 @@ def _attention(fn: str, query, paged_kv_cache, kv_cache_sf, block_tables, seq_le
     code = _dtype_code(dt)
     layout = _layout(kv_layout)
     kc, vc, ps, H, D = _caches_on(paged_kv_cache, kv_cache_sf, layout, device)
-    stride = _rows(query, dt, device, "query", None, D)
-    B, Hq = query.shape[0], query.shape[1]
+    B, Hq, stride, q_ptr = _rows(query, dt, device, "query", -1, D)
     if seq_lens.numel() != B:
         raise ValueError("seq_lens must have one entry per request")
     table, table_dtype, width = _block_tables(block_tables, B, device)
-    for s in (k_scale, v_scale):
-        if s.dtype != torch.float32 or s.numel() < 1 or s.device != device:
-            raise ValueError("k_scale/v_scale must be float32 CUDA tensors")
     if out is None:
         out = torch.empty((B, Hq, D), dtype=dt, device=device)
+        o_ptr = out.data_ptr()
     elif out.shape != (B, Hq, D):
         raise ValueError("out must be [batch, num_qo_heads, head_dim]")
+    else:
+        o_ptr = _addr(out, dt, device, "out")
     if lse is None:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
+        lse_ptr = lse.data_ptr()
     elif lse.shape != (B, Hq):
         raise ValueError("lse must be [batch, num_qo_heads]")
-    lib = load()
-    need = ctypes.c_int64()
-    _check("nvfp4_paged_attention_workspace_bytes",
-           lib.nvfp4_paged_attention_workspace_bytes(Hq, H, D, ctypes.byref(need)))
+    else:
+        lse_ptr = _addr(lse, torch.float32, device, "lse")
     stream = _raw_stream(device)
-    ws = _scratch_for(device, stream, need.value, COUNTER_BYTES)
-    head = (query.data_ptr(), code, stride, Hq, kc, vc, ps, H, D, layout, table, table_dtype, width,
-            _addr(seq_lens, torch.int32, device, "seq_lens"), B)
-    scales = (k_scale.data_ptr(), v_scale.data_ptr(), D ** -0.5 if sm_scale is None else sm_scale, soft_cap)
-    tail = (_addr(out, dt, device, "out"), _addr(lse, torch.float32, device, "lse"),
-            _status_ptr(dev_status, device), ws.data_ptr(), ws.numel(), stream)
+    ws = _scratch_for(device, stream, _bytes_for("nvfp4_paged_attention_workspace_bytes", device, Hq, H, D),
+                      COUNTER_BYTES)
+    lens = _addr(seq_lens, torch.int32, device, "seq_lens")
+    gk, gv = _device_scale(k_scale, device), _device_scale(v_scale, device)
+    sm = D ** -0.5 if sm_scale is None else sm_scale
+    status, ws_ptr, ws_bytes = _status_ptr(dev_status, device), ws.data_ptr(), ws.numel()
     if selection is None:
-        _check(fn, lib.nvfp4_paged_attention_decode(*head, *scales, window_left, *tail))
+        code = load().nvfp4_paged_attention_decode(
+            q_ptr, code, stride, Hq, kc, vc, ps, H, D, layout, table, table_dtype, width, lens, B, gk, gv, sm,
+            soft_cap, window_left, o_ptr, lse_ptr, status, ws_ptr, ws_bytes, stream)
     else:
         selected, count = selection
         if selected.dim() != 3 or selected.shape[:2] != (B, H) or count.shape != (B, H):
             raise ValueError("selected_pages must be [B, H, max_selected] and num_selected [B, H]")
-        _check(fn, lib.nvfp4_sparse_paged_attention_decode(
-            *head, _addr(selected, torch.int32, device, "selected_pages"),
-            _addr(count, torch.int32, device, "num_selected"), selected.shape[2], *scales, *tail))
+        code = load().nvfp4_sparse_paged_attention_decode(
+            q_ptr, code, stride, Hq, kc, vc, ps, H, D, layout, table, table_dtype, width, lens, B,
+            _addr(selected, torch.int32, device, "selected_pages"),
+            _addr(count, torch.int32, device, "num_selected"), selected.shape[2], gk, gv, sm, soft_cap, o_ptr,
+            lse_ptr, status, ws_ptr, ws_bytes, stream)
+    if code:
+        _check(fn, code)
     return out, lse
 
 

@@ -44,6 +44,7 @@ namespace {
 std::mutex g_mu;
 std::unordered_map<int, int> g_sms;
 std::unordered_map<std::string, int> g_occ;
+std::unordered_map<std::string, size_t> g_opted;
 
 int current_device() {
   int dev = 0;
@@ -89,6 +90,37 @@ int blocks_per_sm(const void* kernel, int threads, size_t smem) {
   std::lock_guard<std::mutex> lk(g_mu);
   g_occ[key.str()] = n;
   return n;
+}
+
+nvfp4_status resident_ctas(const void* kernel, int threads, size_t smem, int most_per_sm, const char* what,
+                           int64_t* ctas) {
+  struct Entry {
+    const void* kernel;
+    size_t smem;
+    int device, threads;
+    int64_t per_sm, sms;
+  };
+  static thread_local Entry kept[32];
+  static thread_local unsigned filled = 0;
+  const int dev = current_device();
+  Entry* e = nullptr;
+  for (unsigned i = 0; i < 32 && i < filled && !e; ++i)
+    if (kept[i].kernel == kernel && kept[i].smem == smem && kept[i].device == dev && kept[i].threads == threads) e = kept + i;
+  if (!e) {
+    {
+      // the opt-in is the process's: it only ever grows, so that no thread lowers another's
+      std::lock_guard<std::mutex> lk(g_mu);
+      size_t& opted = g_opted[std::to_string(dev) + ':' + std::to_string(reinterpret_cast<uintptr_t>(kernel))];
+      if (smem > opted) {
+        if (nvfp4_status st = set_dynamic_smem(kernel, smem, what)) return st;
+        opted = smem;
+      }
+    }
+    e = kept + filled++ % 32;
+    *e = Entry{kernel, smem, dev, threads, blocks_per_sm(kernel, threads, smem), sm_count()};
+  }
+  *ctas = e->sms * (e->per_sm < most_per_sm ? e->per_sm : most_per_sm);
+  return NVFP4_OK;
 }
 
 }  // namespace nvfp4

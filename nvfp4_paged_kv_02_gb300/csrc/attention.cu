@@ -946,11 +946,10 @@ nvfp4_status launch_t(const AttentionArgs& a, cudaStream_t stream) {
   const auto kern = attention_kernel<NW, NT, FULL>;
   const size_t smem = kWarps * kStages * Tile<NW>::kBytes + kWarps * 8 * NT * (64 * NW + 4) * 4 +
                       static_cast<size_t>(a.B) * 8;
-  if (nvfp4_status st = set_dynamic_smem(reinterpret_cast<const void*>(kern), smem, "nvfp4_paged_attention_decode"))
+  int64_t cap;
+  if (nvfp4_status st = resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem, kMaxCtasPerSm,
+                                      "nvfp4_paged_attention_decode", &cap))
     return st;
-  int per_sm = blocks_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem);
-  if (per_sm > kMaxCtasPerSm) per_sm = kMaxCtasPerSm;
-  const int64_t cap = static_cast<int64_t>(sm_count()) * per_sm;
   const int64_t reach = a.selected ? static_cast<int64_t>(a.max_selected) * a.ps : a.max_pages * a.ps;
   const int64_t most = static_cast<int64_t>(a.B) * a.H * a.chunks * ((reach + kUnit - 1) / kUnit + 1);
   const int64_t need = (most + kMinUnits - 1) / kMinUnits;

@@ -30,6 +30,11 @@ int sm_count();
 // (cached per kernel and device).
 int blocks_per_sm(const void* kernel, int threads, size_t smem);
 
+// Opt `kernel` in to `smem` dynamic bytes and return its resident CTAs on the whole device (at most
+// `most_per_sm` an SM); kept per thread, so that a launch in a loop pays for it once.
+nvfp4_status resident_ctas(const void* kernel, int threads, size_t smem, int most_per_sm, const char* what,
+                           int64_t* ctas);
+
 // Pipeline test control from the environment (NVFP4KV_TEST_STALL_PIPELINE=1).
 PipeTest pipe_test_from_env();
 

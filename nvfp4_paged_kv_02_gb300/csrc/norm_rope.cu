@@ -245,8 +245,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
 template <bool BF16, int MODE>
 nvfp4_status launch_t(NormRopeArgs a, cudaStream_t stream) {
   const auto kern = norm_rope_append_kernel<BF16, MODE>;
-  const int64_t cap = static_cast<int64_t>(sm_count()) *
-                      blocks_per_sm(reinterpret_cast<const void*>(kern), kThreads, 0);
+  int64_t cap;
+  if (nvfp4_status st = resident_ctas(reinterpret_cast<const void*>(kern), kThreads, 0, 32,
+                                      "nvfp4_qk_norm_rope_append_paged", &cap))
+    return st;
   const int per_step = 32 >> a.log2_T;
   a.q_steps = (a.Hq + per_step - 1) / per_step;
   a.kv_steps = (a.ap.H + per_step - 1) / per_step;

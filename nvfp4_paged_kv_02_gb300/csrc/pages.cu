@@ -656,9 +656,10 @@ template <int GC, int T>
 nvfp4_status launch_scores(const SelectArgs& a, cudaStream_t stream) {
   const auto kern = page_scores_kernel<GC, T, GC == 4 ? 2 : 1>;
   const size_t smem = kScoreWarps * kScoreBytes + static_cast<size_t>(a.B) * 4;
-  if (nvfp4_status st = set_dynamic_smem(reinterpret_cast<const void*>(kern), smem, "nvfp4_select_pages")) return st;
-  const int64_t cap = static_cast<int64_t>(sm_count()) *
-                      blocks_per_sm(reinterpret_cast<const void*>(kern), kScoreWarps * 32, smem);
+  int64_t cap;
+  if (nvfp4_status st = resident_ctas(reinterpret_cast<const void*>(kern), kScoreWarps * 32, smem, 32,
+                                      "nvfp4_select_pages", &cap))
+    return st;
   const int64_t most = (static_cast<int64_t>(a.B) * a.H * ((a.max_pages + kUnitPages - 1) / kUnitPages) + kScoreWarps - 1) / kScoreWarps;
   const int grid = static_cast<int>(most < cap ? most : cap);
   if (grid > 0) kern<<<grid, kScoreWarps * 32, smem, stream>>>(a);
@@ -697,9 +698,10 @@ nvfp4_status launch_page_key_bounds(BoundsArgs a, cudaStream_t stream) {
     smem += static_cast<size_t>(a.stages) * a.stage_bytes;
   }
   const auto kern = ring ? page_key_bounds_ring_kernel : page_key_bounds_kernel;
-  const void* f = reinterpret_cast<const void*>(kern);
-  if (nvfp4_status st = set_dynamic_smem(f, smem, "nvfp4_page_key_bounds")) return st;
-  const int64_t cap = static_cast<int64_t>(sm_count()) * blocks_per_sm(f, kBoundsThreads, smem);
+  int64_t cap;
+  if (nvfp4_status st = resident_ctas(reinterpret_cast<const void*>(kern), kBoundsThreads, smem, 32,
+                                      "nvfp4_page_key_bounds", &cap))
+    return st;
   const int64_t most = (a.B * a.max_pages + a.pages - 1) / a.pages;
   const int grid = static_cast<int>(most < cap ? most : cap);
   kern<<<grid, kBoundsThreads, smem, stream>>>(a);
