@@ -251,9 +251,19 @@ __device__ __forceinline__ void decode16(uint32_t w0, uint32_t w1, uint32_t S2, 
   for (int i = 0; i < 8; ++i) v[i] = hmul2_rn(v[i], S2);
 }
 
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+__device__ __forceinline__ uint32_t low_twice(uint32_t v) {
   uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(d) : "r"(v));
+  return d;
+}
+__device__ __forceinline__ uint32_t high_twice(uint32_t v) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(d) : "r"(v));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -412,7 +422,8 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
   constexpr int kRows = 32 / kChunks;
   const int my_row = lane / kChunks, my_chunk = lane % kChunks;
   const uint32_t my_dst = my_row * T::kRow + ((my_chunk ^ T::swizzle(my_row)) << 4);
-  const bool same_strides = a.k_stride == a.v_stride && a.k_sf_stride == a.v_sf_stride;
+  const uint8_t* const k_base = a.kc.data + 16 * my_chunk;
+  const uint8_t* const v_base = a.vc.data + 16 * my_chunk;
   // Copies of the unit looked up into stage s, then the look-up of the next one.
   auto issue = [&](int s) {
     if (!FULL) put_scales();
@@ -428,18 +439,18 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
       if (lane == 0) *reinterpret_cast<uint32_t*>(ring_p + s * T::kBytes + T::kMask) = mask;
       const uint32_t ksd = st + T::kKs + lane * T::kScales, vsd = st + T::kVs + lane * T::kScales;
       constexpr int kPart = NW == 3 ? 4 : 4 * NW;
-      if (kEven && same_strides && mask == 0xFFFFFFFFu) {
-        // the common unit: every row live, one offset for K and V
-        const uint64_t sf = static_cast<uint64_t>(page) * a.k_sf_stride + lk_row * static_cast<uint64_t>(T::kScales);
-        cp_async<kPart>(ksd, a.kc.sf + sf, true);
-        cp_async<kPart>(vsd, a.vc.sf + sf, true);
-        const uint64_t off = static_cast<uint64_t>(page) * a.k_stride + lk_row * static_cast<uint64_t>(T::kRow);
+      if (kEven && a.compact && mask == 0xFFFFFFFFu) {
+        // the common unit: every row live, one 32-bit offset for K and V, in 16 (scales: 4) bytes
+        const uint32_t sf = page * (a.k_sf_stride / 4) + lk_row * (T::kScales / 4);
+        cp_async<kPart>(ksd, a.kc.sf + sf * uint64_t(4), true);
+        cp_async<kPart>(vsd, a.vc.sf + sf * uint64_t(4), true);
+        const uint32_t off = page * (a.k_stride / 16) + lk_row * (T::kRow / 16);
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-          const uint64_t at = __shfl_sync(0xFFFFFFFFu, off, i * kRows + my_row) + 16 * my_chunk;
+          const uint64_t at = __shfl_sync(0xFFFFFFFFu, off, i * kRows + my_row) * uint64_t(16);
           const uint32_t dst = st + i * kRows * T::kRow + (NW == 4 && (i & 1) ? my_dst ^ 64u : my_dst);
-          cp_async<16>(dst, a.kc.data + at, true);
-          cp_async<16>(dst + T::kV, a.vc.data + at, true);
+          cp_async<16>(dst, k_base + at, true);
+          cp_async<16>(dst + T::kV, v_base + at, true);
         }
       } else {
         if (!live) page = 0;  // (a row that is not live is copied as zeros)
@@ -658,8 +669,8 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
               const uint4 v = *reinterpret_cast<const uint4*>(row + (((NW / 2 * c + i) ^ T::swizzle(t)) << 4));
               kw[p][4 * i] = v.x; kw[p][4 * i + 1] = v.y; kw[p][4 * i + 2] = v.z; kw[p][4 * i + 3] = v.w;
               const uint32_t s2 = f16x2_from_e4m3x2(i == 0 ? s : s >> 16);
-              S2[p][2 * i] = prmt(s2, 0u, 0x1010u);
-              S2[p][2 * i + 1] = prmt(s2, 0u, 0x3232u);
+              S2[p][2 * i] = low_twice(s2);
+              S2[p][2 * i + 1] = high_twice(s2);
             }
           }
         }
@@ -704,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
         for (int k = 0; k < 2; ++k) {
           float v = fmaxf(x[0][nt][k], x[0][nt][k + 2]);
 #pragma unroll
-          for (int mt = 1; mt < kTiles; ++mt) v = fmaxf(v, fmaxf(x[mt][nt][k], x[mt][nt][k + 2]));
+          for (int mt = 1; mt < kTiles; ++mt) v = max3(v, x[mt][nt][k], x[mt][nt][k + 2]);
           top[nt][k] = v * unit[nt][k];
           grew = grew || top[nt][k] > m[nt][k] + kSlack;
         }
@@ -775,8 +786,8 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
           const uint8_t* sr = st + T::kVs + 16 * mt * T::kScales + ((NW * r + w) >> 1);
           const uint32_t s0 = sr[v0 * T::kScales], s1 = sr[v1 * T::kScales];
           const uint32_t s2 = sr[(v0 + 8) * T::kScales], s3 = sr[(v1 + 8) * T::kScales];
-          S01[w] = f16x2_from_e4m3x2(s0 | (s1 << 8));
-          S23[w] = f16x2_from_e4m3x2(s2 | (s3 << 8));
+          S01[w] = f16x2_from_e4m3x2(s1 * 256u + s0);
+          S23[w] = f16x2_from_e4m3x2(s3 * 256u + s2);
         }
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
@@ -988,6 +999,10 @@ nvfp4_status launch_attention(AttentionArgs a, cudaStream_t stream) {
   a.v_stride = static_cast<uint32_t>(strides[1]);
   a.k_sf_stride = static_cast<uint32_t>(strides[2]);
   a.v_sf_stride = static_cast<uint32_t>(strides[3]);
+  // one offset serves K and V, and 32 bits hold it
+  a.compact = strides[0] == strides[1] && strides[2] == strides[3] && strides[2] % 4 == 0 &&
+              pool * (strides[0] / 16) <= static_cast<int64_t>(UINT32_MAX) &&
+              pool * (strides[2] / 4) <= static_cast<int64_t>(UINT32_MAX);
   if (sm_count() * kMaxCtasPerSm * 4 > NVFP4_COUNTER_BYTES)
     return fail(NVFP4_ERR_UNSUPPORTED, "nvfp4_paged_attention_decode: more SMs than counters");
   // scale rows are copied 4 nw bytes at a time (nw = 3: 4), aligned to that

@@ -34,6 +34,7 @@ struct AttentionArgs {
   int32_t chunks, chunk_heads;  // passes over a KV head's query heads, and the heads of one
   uint32_t pool_pages;          // pages that both caches have
   uint32_t k_stride, v_stride, k_sf_stride, v_sf_stride;  // page strides, bytes
+  int32_t compact;
 };
 // Device memory that a launch needs, whatever the lengths.
 int64_t attention_workspace_bytes(int32_t Hq, int32_t H, int32_t D);
