@@ -49,7 +49,7 @@ constexpr int kUnit = 32;     // tokens
 constexpr int kTiles = kUnit / 16;  // of 16 tokens
 constexpr int kMinUnits = 4;  // of a CTA's run: one for each warp
 constexpr int kMaxCtasPerSm = 4;
-constexpr int kSegmentCost = 6;
+constexpr int kSegmentCost = 9;
 constexpr float kWeightBias = 8.0f;
 constexpr float kSlack = 7.0f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -536,8 +536,9 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
     float4 v{0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kHeads + head) * kPitch + d);
       const float f = s_f[w][head];
+      if (f == 0.0f) continue;  // (a part without weights may hold anything)
+      const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kHeads + head) * kPitch + d);
       v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
     }
     return v;
@@ -896,53 +897,48 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
       if (!s_shared[n].join) continue;
       const int32_t first = s_shared[n].first, last = s_shared[n].last, head0 = s_shared[n].chunk * a.chunk_heads;
       const int heads = min(a.chunk_heads, a.G - head0);
-      // The last of them adds all up, in the runs' order. Loads go out kBatch at a time: this is a
-      // chain of trips to L2. A warp takes every fourth part.
+      // The last of them adds all up, in the runs' order, with kBatch parts' loads under way at once:
+      // this is a chain of trips to L2, at the kernel's end. Few parts: all threads go over all of
+      // them; many: every warp over a fourth.
       constexpr int kBatch = 8;
-      for (int head = lane; head < kHeads; head += 32) {
-        float M = -INFINITY, L = 0.0f;
-        for (int32_t i0 = first + warp; i0 <= last; i0 += kBatch * kWarps) {
-          float mi[kBatch], li[kBatch], top = M;
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int32_t i = i0 + k * kWarps;
-            const bool in = i <= last && head < heads;
-            mi[k] = in ? __ldcg(part_of(i, first) + kStats + head) : -INFINITY;
-            li[k] = in ? __ldcg(part_of(i, first) + kStats + kHeads + head) : 0.0f;
-          }
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) top = fmaxf(top, mi[k]);
-          if (top == -INFINITY) continue;
-          L *= ex2(M - top);
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) L += ex2(mi[k] - top) * li[k];
-          M = top;
-        }
-        s_m[warp][head] = M;
-        s_l[warp][head] = L;
-      }
-      __syncwarp();
-      for (int k0 = lane; k0 < heads * D / 4; k0 += 32) {
+      const int teams = last - first >= kBatch ? kWarps : 1;
+      const int team = teams > 1 ? warp : 0, size = kThreads / teams;
+      for (int k0 = teams > 1 ? lane : tid; k0 < heads * D / 4; k0 += size) {
         const int head = k0 / (D / 4), d = k0 % (D / 4) * 4;
-        const float M = s_m[warp][head];
+        float M = -INFINITY, L = 0.0f;
         float4 v{0, 0, 0, 0};
-        for (int32_t i0 = first + warp; i0 <= last; i0 += kBatch * kWarps) {
-          float mi[kBatch];
+        for (int32_t i0 = first + team; i0 <= last; i0 += kBatch * teams) {
+          float mi[kBatch], li[kBatch], top = M;
           float4 x[kBatch];
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
-            const int32_t i = i0 + k * kWarps;
-            mi[k] = i <= last ? __ldcg(part_of(i, first) + kStats + head) : -INFINITY;
-            x[k] = i <= last ? __ldcg(reinterpret_cast<const float4*>(part_of(i, first) + head * (64 * NW) + d)) : float4{};
+            const int32_t i = i0 + k * teams;
+            const float* p = part_of(i, first);
+            mi[k] = i <= last ? __ldcg(p + kStats + head) : -INFINITY;
+            li[k] = i <= last && d == 0 ? __ldcg(p + kStats + kHeads + head) : 0.0f;
+            x[k] = i <= last ? __ldcg(reinterpret_cast<const float4*>(p + head * (64 * NW) + d)) : float4{};
           }
 #pragma unroll
+          for (int k = 0; k < kBatch; ++k) top = fmaxf(top, mi[k]);
+          if (top == -INFINITY) continue;  // (parts without weights: zeros)
+          const float f = ex2(M - top);
+          M = top;
+          L *= f;
+          v.x *= f; v.y *= f; v.z *= f; v.w *= f;
+#pragma unroll
           for (int k = 0; k < kBatch; ++k) {
-            const float f = mi[k] == -INFINITY ? 0.0f : ex2(mi[k] - M);
-            v.x += f * x[k].x; v.y += f * x[k].y; v.z += f * x[k].z; v.w += f * x[k].w;
+            const float g = ex2(mi[k] - top);
+            L += g * li[k];
+            v.x += g * x[k].x; v.y += g * x[k].y; v.z += g * x[k].z; v.w += g * x[k].w;
           }
         }
-        *reinterpret_cast<float4*>(s_o + (warp * kHeads + head) * kPitch + d) = v;
+        *reinterpret_cast<float4*>(s_o + (team * kHeads + head) * kPitch + d) = v;
+        if (d == 0) {
+          s_m[team][head] = M;
+          s_l[team][head] = L;
+        }
       }
+      if (teams == 1 && tid >= kHeads && tid < kWarps * kHeads) s_m[tid / kHeads][tid % kHeads] = -INFINITY;
       __syncthreads();
       join_stats();
       write_out(static_cast<int64_t>(s_shared[n].b) * a.Hq + static_cast<int64_t>(s_shared[n].h) * a.G + head0, heads);
