@@ -1,9 +1,9 @@
 """GB300 (sm_103a) NVFP4 paged KV-cache operations.
 
-A thin ctypes binding over ``libnvfp4kv.so`` (C ABI in ``include/nvfp4kv.h``): it only
-turns torch tensors into pointers, strides and the current CUDA stream. Every step of the
-work runs in the library's CUDA kernels; there is no fallback of any kind, and using an op
-without the built library raises.
+A thin binding over ``libnvfp4kv.so`` (C ABI in ``include/nvfp4kv.h``), by ctypes and, for the
+decode-step calls, by a small compiled module: it only turns torch tensors into pointers, strides
+and the current CUDA stream. Every step of the work runs in the library's CUDA kernels; there is
+no fallback of any kind, and using an op without the built library raises.
 
 Operations (FlashInfer documentation pages):
   nvfp4_quantize_append_paged  "flashinfer.page.nvfp4_quantize_append_paged_kv_cache"
@@ -28,6 +28,8 @@ Operators of a decode step over such a cache (additions of this library):
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from dataclasses import dataclass
@@ -103,6 +105,7 @@ class NVFP44Over6Config:
 
 _lock = threading.Lock()
 _lib = None
+_calls_module = None
 
 
 def load() -> ctypes.CDLL:
@@ -182,6 +185,20 @@ def load() -> ctypes.CDLL:
             vp, vp, f32, f32, vp, vp, vp, vp, i64, vp]
         _lib = L
         return L
+
+
+def _calls():
+    """The module that carries the decode-step calls (built with the library)."""
+    global _calls_module
+    if _calls_module is None:
+        load()
+        with _lock:
+            if _calls_module is None:
+                loader = importlib.machinery.ExtensionFileLoader("nvfp4kv_calls", _build.CALLS_PATH)
+                _calls_module = importlib.util.module_from_spec(
+                    importlib.util.spec_from_file_location("nvfp4kv_calls", _build.CALLS_PATH, loader=loader))
+                loader.exec_module(_calls_module)
+    return _calls_module
 
 
 def _check(fn: str, code: int) -> None:
@@ -605,129 +622,23 @@ def nvfp4_4over6_from_code(code: int) -> Optional[NVFP44Over6Config]:
 
 # ---- the operators of a decode step -----------------------------------------------------------
 
-# (These calls run once per layer and step, so their checks read each tensor's properties once.)
+# These calls run once per layer and step, and small ones take the GPU less time than the argument checks
+# take in Python: they go to the library through nvfp4kv_calls (csrc/calls.cpp), which makes the checks, keeps
+# the workspaces and raises ValueError as the functions above do.
 
-def _addr(t: torch.Tensor, dtype, device: torch.device, what: str) -> int:
-    """Address of a contiguous tensor of the given dtype on `device`."""
-    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor on {device}")
-    return t.data_ptr()
-
-
-def _device(t: torch.Tensor) -> torch.device:
-    if not t.is_cuda:
-        raise ValueError("nvfp4 ops take CUDA tensors only")
-    return t.device
+def _pair(cache):
+    """(K, V) of a tuple or of a stacked 5-D tensor with K/V on the second dimension."""
+    if isinstance(cache, (tuple, list)):
+        return cache
+    if cache.dim() != 5 or cache.shape[1] != 2:
+        raise ValueError("a stacked cache is 5-D with K/V on the second dimension")
+    return cache.unbind(1)
 
 
-def _rows(t: torch.Tensor, dtype, device: torch.device, what: str, heads: int, head_dim: int):
-    """Checks rows [n, heads, head_dim] (heads < 0: any number) whose heads and elements are contiguous;
-    returns (n, heads, stride, address)."""
-    shape = t.shape
-    if len(shape) != 3 or t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{what} must be a [n, heads, head_dim] {dtype} tensor on {device}")
-    n, h, d = shape
-    if d != head_dim or (h != heads and heads >= 0):
-        raise ValueError(f"{what} must have {heads if heads >= 0 else 'its'} heads of {head_dim} elements")
-    sn, sh, sd = t.stride()
-    if sd != 1 or (sh != d and h > 1):
-        raise ValueError(f"{what} must have contiguous heads and elements")
-    return n, h, sn if n > 1 else h * d, t.data_ptr()
-
-
-def _status_ptr(t: Optional[torch.Tensor], device: torch.device) -> Optional[int]:
-    return None if t is None else _addr(t, torch.int32, device, "dev_status")
-
-
-def _block_tables(t: torch.Tensor, batch: int, device: torch.device):
-    shape, dtype = t.shape, t.dtype
-    if len(shape) != 2 or shape[0] != batch or (dtype is not torch.int32 and dtype is not torch.int64) \
-            or t.device != device or not t.is_contiguous():
-        raise ValueError(f"block_tables must be a contiguous [{batch}, max_pages] int32/int64 tensor on {device}")
-    return t.data_ptr(), I64 if dtype is torch.int64 else I32, shape[1]
-
-
-_SCALE_DTYPES = (torch.uint8, torch.float8_e4m3fn)
-
-
-def _cache_on(data: torch.Tensor, sf: torch.Tensor, device: torch.device):
-    """The C form of one cache and its code tensor's shape, with the checks of _one_cache."""
-    ds, ss = data.shape, sf.shape
-    if data.dtype is not torch.uint8 or sf.dtype not in _SCALE_DTYPES:
-        raise ValueError("paged caches are uint8 codes and uint8 / float8_e4m3fn scales")
-    if len(ds) != 4 or len(ss) != 4:
-        raise ValueError("a paged cache tensor is 4-D [pages, ., ., head_dim // 2|16]")
-    p, a, b, c = ds
-    if data.device != device or sf.device != device or ss != (p, a, b, c >> 3) or c & 7:
-        raise ValueError(f"codes [pages, ., ., D/2] and scales [pages, ., ., D/16] must match, on {device}")
-    d0, d1, d2, d3 = data.stride()
-    s0, s1, s2, s3 = sf.stride()
-    if d3 != 1 or d2 != c or d1 != b * c or s3 != 1 or s2 != c >> 3 or s1 != b * c >> 3:
-        raise ValueError("paged cache pages must be contiguous inside (page stride may be larger)")
-    return _Cache(data.data_ptr(), sf.data_ptr(), d0, s0, p), ds
-
-
-def _caches_on(paged_kv_cache, kv_cache_sf, layout: int, device: torch.device):
-    """(K, V, page_size, heads, head_dim) of a tuple or stacked cache."""
-    if not isinstance(paged_kv_cache, (tuple, list)):
-        d, s = paged_kv_cache, kv_cache_sf
-        if d.dim() != 5 or s.dim() != 5 or d.shape[1] != 2 or s.shape[1] != 2:
-            raise ValueError("a stacked cache is 5-D with K/V on the second dimension")
-        paged_kv_cache, kv_cache_sf = d.unbind(1), s.unbind(1)
-    kc, ks = _cache_on(paged_kv_cache[0], kv_cache_sf[0], device)
-    vc, vs = _cache_on(paged_kv_cache[1], kv_cache_sf[1], device)
-    if ks[1:] != vs[1:]:
-        raise ValueError("the K and V caches must have the same page shape")
-    if layout == NHD:
-        return kc, vc, ks[1], ks[2], ks[3] * 2
-    return kc, vc, ks[2], ks[1], ks[3] * 2
-
-
-def _device_scale(s, device: torch.device) -> int:
-    if not isinstance(s, torch.Tensor) or s.dtype is not torch.float32 or s.device != device or s.numel() < 1:
-        raise ValueError("k_scale/v_scale must be float32 CUDA tensors")
-    return s.data_ptr()
-
-
-# Workspaces of the attention and selection calls, one per (device, stream) as above; a larger one takes
-# its place when a call needs it. A call that is being captured gets its own from the graph's memory, so
-# that a graph never depends on what later calls do with these.
-_scratch = {}
-
-
-def _scratch_for(device: torch.device, stream: int, nbytes: int, zeroed: int) -> torch.Tensor:
-    """At least nbytes of device memory whose first `zeroed` bytes are zero between calls."""
-    key = (device.index, stream, zeroed)
-    capturing = torch._C._cuda_isCurrentStreamCapturing()
-    t = None if capturing else _scratch.get(key)
-    if t is None or t.numel() < nbytes:
-        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        if zeroed:
-            t[:zeroed].zero_()
-        if not capturing:
-            _scratch[key] = t
-    return t
-
-
-def _raw_stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-_workspace_bytes = {}
-
-
-def _bytes_for(fn: str, device: torch.device, *sizes: int) -> int:
-    """What the library's function `fn` says of these sizes, asked once for each."""
-    key = (fn, device.index, sizes)
-    n = _workspace_bytes.get(key)
-    if n is None:
-        need = ctypes.c_int64()
-        with torch.cuda.device(device):
-            _check(fn, getattr(load(), fn)(*sizes, ctypes.byref(need)))
-        n = _workspace_bytes[key] = need.value
-        if len(_workspace_bytes) > 4096:
-            _workspace_bytes.clear()
-    return n
+def _done(fn: str, result):
+    if type(result) is int:
+        _check(fn, result)
+    return result
 
 
 def nvfp4_qk_norm_rope_append_paged(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
@@ -746,50 +657,17 @@ def nvfp4_qk_norm_rope_append_paged(query: torch.Tensor, key: torch.Tensor, valu
     rotation), and quantize-append of the key and value rows, in one launch. query [nnz, Hq, D], key
     and value [nnz, H, D] may be slices of one tensor. Returns the query rows (`out`, which may be
     `query`). The other arguments are those of nvfp4_quantize_append_paged."""
-    device, dt = _device(query), query.dtype
-    code = _dtype_code(dt)
-    layout = _layout(kv_layout)
-    kc, vc, ps, H, D = _caches_on(paged_kv_cache, kv_cache_sf, layout, device)
-    nnz, Hq, q_stride, q_ptr = _rows(query, dt, device, "query", -1, D)
-    k_rows, _, k_stride, k_ptr = _rows(key, dt, device, "key", H, D)
-    v_rows, _, v_stride, v_ptr = _rows(value, dt, device, "value", H, D)
-    if k_rows != nnz or v_rows != nnz or batch_indices.numel() != nnz or positions.numel() != nnz:
-        raise ValueError("query, key, value, batch_indices and positions must have as many rows")
-    if (q_weight is not None and q_weight.numel() != D) or (k_weight is not None and k_weight.numel() != D):
-        raise ValueError("a norm's weights must have head_dim elements")
-    npos, rot = (0, 0) if cos_sin is None else cos_sin.shape
-    if out is None:
-        out = torch.empty((nnz, Hq, D), dtype=dt, device=device)
-        o_stride, o_ptr = Hq * D, out.data_ptr()
-    else:
-        o_rows, _, o_stride, o_ptr = _rows(out, dt, device, "out", Hq, D)
-        if o_rows != nnz:
-            raise ValueError("out must have query's shape")
-    i32 = torch.int32
-    B = kv_indptr.numel() - 1
-    if kv_last_page_len is not None and kv_last_page_len.numel() < B:
-        raise ValueError("kv_last_page_len must have one entry per request")
-    ks = vs = 1.0
-    k_dev = v_dev = None
-    if isinstance(k_scale, torch.Tensor) or isinstance(v_scale, torch.Tensor):
-        k_dev, v_dev = _device_scale(k_scale, device), _device_scale(v_scale, device)
-    else:
-        ks, vs = float(k_scale), float(v_scale)
-    code = load().nvfp4_qk_norm_rope_append_paged(
-        q_ptr, k_ptr, v_ptr, code, nnz, Hq, H, D, q_stride, k_stride, v_stride,
-        None if q_weight is None else _addr(q_weight, dt, device, "q_weight"),
-        None if k_weight is None else _addr(k_weight, dt, device, "k_weight"), eps,
-        None if cos_sin is None else _addr(cos_sin, torch.float32, device, "cos_sin"), npos, rot,
-        1 if rotary_interleaved else 0, _addr(batch_indices, i32, device, "batch_indices"),
-        _addr(positions, i32, device, "positions"), kc, vc, ps, layout,
-        _addr(kv_indices, i32, device, "kv_indices"), kv_indices.numel(),
-        _addr(kv_indptr, i32, device, "kv_indptr"),
-        None if kv_last_page_len is None else _addr(kv_last_page_len, i32, device, "kv_last_page_len"),
-        B, ks, vs, k_dev, v_dev, _recipe(nvfp4_4over6), o_ptr, o_stride, _status_ptr(dev_status, device),
-        _raw_stream(device))
-    if code:
-        _check("nvfp4_qk_norm_rope_append_paged", code)
-    return out
+    k, v = _pair(paged_kv_cache)
+    ks, vs = _pair(kv_cache_sf)
+    r = nvfp4_4over6
+    if r is not None:
+        c = r._c()
+        r = (c.e4m3_max, c.err_mode, c.err_use_fast_math)
+    return _done("nvfp4_qk_norm_rope_append_paged", _calls().qk_norm_rope_append(
+        query, key, value, q_weight, k_weight, cos_sin, batch_indices, positions, k, v, ks, vs, kv_indices,
+        kv_indptr, kv_last_page_len, k_scale, v_scale, _layout(kv_layout), eps, rotary_interleaved, r, out,
+        dev_status))
+
 
 
 def nvfp4_page_key_bounds(k_cache: torch.Tensor, k_block_scales: torch.Tensor,
@@ -799,23 +677,10 @@ def nvfp4_page_key_bounds(k_cache: torch.Tensor, k_block_scales: torch.Tensor,
     """Write the element-wise (min, max) of e2m1 * block_scale over the live slots of each request's
     pages into key_bounds [num_pages, H, 2, D] float16: the pages that hold a position from
     first_positions on (None: all of them)."""
-    device = _device(k_cache)
-    layout = _layout(kv_layout)
-    kc, shape = _cache_on(k_cache, k_block_scales, device)
-    ps, H = (shape[1], shape[2]) if layout == NHD else (shape[2], shape[1])
-    D = shape[3] * 2
-    B = seq_lens.numel()
-    if key_bounds.shape != (shape[0], H, 2, D):
-        raise ValueError("key_bounds must be [num_pages, num_kv_heads, 2, head_dim]")
-    if first_positions is not None and first_positions.numel() != B:
-        raise ValueError("first_positions must have one entry per request")
-    table, table_dtype, width = _block_tables(block_tables, B, device)
-    _check("nvfp4_page_key_bounds", load().nvfp4_page_key_bounds(
-        kc, ps, H, D, layout, table, table_dtype, width,
-        _addr(seq_lens, torch.int32, device, "seq_lens"),
-        None if first_positions is None else _addr(first_positions, torch.int32, device, "first_positions"),
-        B, _addr(key_bounds, torch.float16, device, "key_bounds"), _status_ptr(dev_status, device),
-        _raw_stream(device)))
+    _done("nvfp4_page_key_bounds", _calls().page_key_bounds(
+        k_cache, k_block_scales, block_tables, seq_lens, key_bounds, first_positions, _layout(kv_layout),
+        dev_status))
+
 
 
 def nvfp4_select_pages(query: torch.Tensor, key_bounds: torch.Tensor, block_tables: torch.Tensor,
@@ -827,82 +692,11 @@ def nvfp4_select_pages(query: torch.Tensor, key_bounds: torch.Tensor, block_tabl
     num_sink_pages and last num_recent_pages always among them. query [B, Hq, D]; key_bounds from
     nvfp4_page_key_bounds. Returns (selected_pages int32 [B, H, max_selected], ascending and -1 past the
     count; num_selected int32 [B, H])."""
-    device, dt = _device(query), query.dtype
-    code = _dtype_code(dt)
-    if key_bounds.dim() != 4 or key_bounds.shape[2] != 2:
-        raise ValueError("key_bounds must be [num_pages, num_kv_heads, 2, head_dim]")
-    P, H, _, D = key_bounds.shape
-    B, Hq, stride, q_ptr = _rows(query, dt, device, "query", -1, D)
-    if seq_lens.numel() != B:
-        raise ValueError("seq_lens must have one entry per request")
-    table, table_dtype, width = _block_tables(block_tables, B, device)
-    if out is None:
-        selected = torch.empty((B, H, max_selected), dtype=torch.int32, device=device)
-        count = torch.empty((B, H), dtype=torch.int32, device=device)
-    else:
-        selected, count = out
-        if selected.shape != (B, H, max_selected) or count.shape != (B, H):
-            raise ValueError("out must be ([B, H, max_selected], [B, H]) int32 tensors")
-    stream = _raw_stream(device)
-    ws = _scratch_for(device, stream, _bytes_for("nvfp4_select_pages_workspace_bytes", device, B, H, width), 0)
-    code = load().nvfp4_select_pages(
-        q_ptr, code, stride, Hq, H, D, _addr(key_bounds, torch.float16, device, "key_bounds"), P, page_size,
-        table, table_dtype, width, _addr(seq_lens, torch.int32, device, "seq_lens"), B, max_selected,
-        num_sink_pages, num_recent_pages, _addr(selected, torch.int32, device, "selected_pages"),
-        _addr(count, torch.int32, device, "num_selected"), _status_ptr(dev_status, device), ws.data_ptr(),
-        ws.numel(), stream)
-    if code:
-        _check("nvfp4_select_pages", code)
-    return selected, count
+    selected, count = (None, None) if out is None else out
+    return _done("nvfp4_select_pages", _calls().select_pages(
+        query, key_bounds, block_tables, seq_lens, page_size, max_selected, num_sink_pages, num_recent_pages,
+        selected, count, dev_status))
 
-
-def _attention(fn: str, query, paged_kv_cache, kv_cache_sf, block_tables, seq_lens, selection, k_scale,
-               v_scale, kv_layout, sm_scale, soft_cap, window_left, out, lse, dev_status):
-    device, dt = _device(query), query.dtype
-    code = _dtype_code(dt)
-    layout = _layout(kv_layout)
-    kc, vc, ps, H, D = _caches_on(paged_kv_cache, kv_cache_sf, layout, device)
-    B, Hq, stride, q_ptr = _rows(query, dt, device, "query", -1, D)
-    if seq_lens.numel() != B:
-        raise ValueError("seq_lens must have one entry per request")
-    table, table_dtype, width = _block_tables(block_tables, B, device)
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=dt, device=device)
-        o_ptr = out.data_ptr()
-    elif out.shape != (B, Hq, D):
-        raise ValueError("out must be [batch, num_qo_heads, head_dim]")
-    else:
-        o_ptr = _addr(out, dt, device, "out")
-    if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
-        lse_ptr = lse.data_ptr()
-    elif lse.shape != (B, Hq):
-        raise ValueError("lse must be [batch, num_qo_heads]")
-    else:
-        lse_ptr = _addr(lse, torch.float32, device, "lse")
-    stream = _raw_stream(device)
-    ws = _scratch_for(device, stream, _bytes_for("nvfp4_paged_attention_workspace_bytes", device, Hq, H, D),
-                      COUNTER_BYTES)
-    lens = _addr(seq_lens, torch.int32, device, "seq_lens")
-    gk, gv = _device_scale(k_scale, device), _device_scale(v_scale, device)
-    sm = D ** -0.5 if sm_scale is None else sm_scale
-    status, ws_ptr, ws_bytes = _status_ptr(dev_status, device), ws.data_ptr(), ws.numel()
-    if selection is None:
-        code = load().nvfp4_paged_attention_decode(
-            q_ptr, code, stride, Hq, kc, vc, ps, H, D, layout, table, table_dtype, width, lens, B, gk, gv, sm,
-            soft_cap, window_left, o_ptr, lse_ptr, status, ws_ptr, ws_bytes, stream)
-    else:
-        selected, count = selection
-        if selected.dim() != 3 or selected.shape[:2] != (B, H) or count.shape != (B, H):
-            raise ValueError("selected_pages must be [B, H, max_selected] and num_selected [B, H]")
-        code = load().nvfp4_sparse_paged_attention_decode(
-            q_ptr, code, stride, Hq, kc, vc, ps, H, D, layout, table, table_dtype, width, lens, B,
-            _addr(selected, torch.int32, device, "selected_pages"),
-            _addr(count, torch.int32, device, "num_selected"), selected.shape[2], gk, gv, sm, soft_cap, o_ptr,
-            lse_ptr, status, ws_ptr, ws_bytes, stream)
-    if code:
-        _check(fn, code)
-    return out, lse
 
 
 def nvfp4_paged_attention_decode(query: torch.Tensor, paged_kv_cache, kv_cache_sf,
@@ -916,9 +710,12 @@ def nvfp4_paged_attention_decode(query: torch.Tensor, paged_kv_cache, kv_cache_s
     seq_lens[b] positions (the last window_left + 1 of them when window_left >= 0). k_scale, v_scale: the
     global decode scales, 1-element float32 CUDA tensors; sm_scale: D ** -0.5 unless given. Returns (out
     [B, Hq, D], lse float32 [B, Hq], natural logarithm); a request without positions gets 0 and -inf."""
-    return _attention("nvfp4_paged_attention_decode", query, paged_kv_cache, kv_cache_sf, block_tables,
-                      seq_lens, None, k_scale, v_scale, kv_layout, sm_scale, logits_soft_cap,
-                      window_left, out, lse, dev_status)
+    k, v = _pair(paged_kv_cache)
+    ks, vs = _pair(kv_cache_sf)
+    return _done("nvfp4_paged_attention_decode", _calls().attention(
+        query, k, v, ks, vs, block_tables, seq_lens, None, None, k_scale, v_scale, _layout(kv_layout), sm_scale,
+        logits_soft_cap, window_left, out, lse, dev_status))
+
 
 
 def nvfp4_sparse_paged_attention_decode(query: torch.Tensor, paged_kv_cache, kv_cache_sf,
@@ -932,6 +729,8 @@ def nvfp4_sparse_paged_attention_decode(query: torch.Tensor, paged_kv_cache, kv_
                                         dev_status: Optional[torch.Tensor] = None):
     """nvfp4_paged_attention_decode over the first num_selected[b, h] logical pages of
     selected_pages[b, h] for each KV head (nvfp4_select_pages)."""
-    return _attention("nvfp4_sparse_paged_attention_decode", query, paged_kv_cache, kv_cache_sf,
-                      block_tables, seq_lens, (selected_pages, num_selected), k_scale, v_scale,
-                      kv_layout, sm_scale, logits_soft_cap, -1, out, lse, dev_status)
+    k, v = _pair(paged_kv_cache)
+    ks, vs = _pair(kv_cache_sf)
+    return _done("nvfp4_sparse_paged_attention_decode", _calls().attention(
+        query, k, v, ks, vs, block_tables, seq_lens, selected_pages, num_selected, k_scale, v_scale,
+        _layout(kv_layout), sm_scale, logits_soft_cap, -1, out, lse, dev_status))
