@@ -265,8 +265,13 @@ __global__ void __launch_bounds__(kBoundsThreads) page_key_bounds_ring_kernel(co
 // warp; a warp holds its query heads in registers (as positive and negative parts) and passes
 // over the pages' bounds once, T lanes to a page (T = D/8 rounded up), each lane eight elements.
 // A lane's bounds come through its own ring of stages in shared memory (cp.async; no other lane
-// reads them, so a wait is all the synchronization there is). Reading the bounds bounds it, 4 D
-// bytes a page and head; the 2 G D multiply-adds are packed two by two.
+// reads them, so a wait is all the synchronization there is). The lanes' parts of a unit's sums are
+// joined together at its end: 17 shuffles for eight pages and four heads of 128 elements, 32 if each
+// row of pages is joined by itself. Reading the bounds, 4 D bytes a page and head, is the floor;
+// instructions bound it, the 2 G D multiply-adds (packed two by two) first among them. With the
+// selection, at D = 128: 512 lists of 549 pages on average, G = 4, 31 us (2.95 TB/s of bounds); 512
+// lists of 2270 pages 138 us (4.3); 32 lists of 7200 pages, G = 8, 55 us (2.1). Two lanes to a page
+// would need no shuffles but takes 16 % longer: the rows then lie 4 D bytes apart in shared memory.
 
 constexpr int kScoreWarps = 4;
 constexpr int kScoreBytes = 8192;  // a warp's ring
@@ -303,8 +308,11 @@ __device__ __forceinline__ int32_t pages_of(const SelectArgs& a, int32_t b) {
 template <int GC, int T, int R>
 __global__ void __launch_bounds__(kScoreWarps * 32, GC == 4 ? 3 : 2) page_scores_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kPages = 32 / T, kStep = kPages * R;  // pages of a row of lanes, and of an iteration
+  constexpr int kPages = 32 / T, kStep = kPages * R;  // pages of a row of lanes, and of a step
   constexpr int kStage = 1024 * R, kStages = kScoreBytes / kStage;
+  constexpr int kRows = kUnitPages / kPages, kIts = kUnitPages / kStep;  // rows and steps of a unit
+  constexpr int kAhead = (kIts + kStages - 2) / kIts;  // units that the copies are ahead at a unit's end
+  static_assert(kIts >= 1 && (kAhead + 1) * kUnitPages <= 64 && kRows * GC == T * (GC / 4), "");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % T, group = lane / T;
   int32_t* cum = reinterpret_cast<int32_t*>(smem + kScoreWarps * kScoreBytes);
@@ -328,6 +336,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, GC == 4 ? 3 : 2) page_scores
   int32_t h = static_cast<int32_t>(in_request / units), first = static_cast<int32_t>(in_request % units);
 
   const bool active = 8 * sub < a.D;
+  const uint64_t page_bytes = static_cast<uint64_t>(a.H) * 4 * a.D;
   for (;;) {
     const int32_t n = pages_of(a, b);
     const int32_t last = static_cast<int32_t>(min(static_cast<int64_t>(units), first + (u_end - u)));
@@ -349,111 +358,105 @@ __global__ void __launch_bounds__(kScoreWarps * 32, GC == 4 ? 3 : 2) page_scores
           qn[g][i] = pack2(fminf(x, 0.0f), fminf(y, 0.0f));
         }
       }
-      // iterations: kPages pages each, kIts of them to a unit
-      constexpr int kIts = kUnitPages / kStep;
-      const int32_t it_end = (last - first) * kIts;
-      int32_t issued = 0, entry_unit = -1, entry = -1;
-      auto issue = [&] {
-        if (issued < it_end) {
-          const int32_t unit = issued / kIts;
-          if (unit != entry_unit) {  // the unit's pages, one to a lane
-            entry_unit = unit;
-            const int32_t col = (first + unit) * kUnitPages + lane;
-            entry = -1;
-            if (lane < kUnitPages && col < n) {
-              const int64_t page = table_entry(a.block_tables, a.table64, b * a.max_pages + col);
-              if (page >= 0 && page < a.num_pages) entry = static_cast<int32_t>(page);
-              else flag(a.status, NVFP4_DEV_BAD_PAGE);
-            }
-          }
-          const uint32_t dst = ring + issued % kStages * kStage;
+      // A unit's entries of the block table are read a unit before its first copy; `bad` has its pages
+      // outside the pool (copied as zeros), eight bits to a unit, the newest unit lowest.
+      const uint8_t* base = reinterpret_cast<const uint8_t*>(a.bounds + static_cast<int64_t>(h) * 2 * a.D + (active ? 8 * sub : 0));
+      const int32_t units_here = last - first;
+      int32_t to_issue = 0, entry = -1;
+      int64_t next = -1;
+      uint64_t bad = 0;
+      auto read_entry = [&](int32_t unit) {
+        next = -1;
+        if (unit < units_here && lane < kUnitPages && (first + unit) * kUnitPages + lane < n)
+          next = table_entry(a.block_tables, a.table64, b * a.max_pages + (first + unit) * kUnitPages + lane);
+      };
+      auto issue = [&](int step) {  // step `step` of unit `to_issue`
+        if (step == 0) {
+          const bool live = to_issue < units_here && lane < kUnitPages && (first + to_issue) * kUnitPages + lane < n;
+          const bool ok = next >= 0 && next < a.num_pages;
+          entry = live && ok ? static_cast<int32_t>(next) : -1;
+          const uint32_t out = __ballot_sync(0xFFFFFFFFu, live && !ok);
+          if (out && lane == 0) flag(a.status, NVFP4_DEV_BAD_PAGE);
+          bad = bad << kUnitPages | out;
+          read_entry(to_issue + 1);
+        }
+        if (to_issue < units_here) {
+          const uint32_t dst = ring + (to_issue * kIts + step) % kStages * kStage;
 #pragma unroll
           for (int q = 0; q < R; ++q) {
-            const int32_t page = __shfl_sync(0xFFFFFFFFu, entry, issued % kIts * kStep + q * kPages + group);
-            const bool live = page >= 0 && active;
-            const uint16_t* src = a.bounds + ((static_cast<int64_t>(live ? page : 0) * a.H + h) * 2 * a.D + (live ? 8 * sub : 0));
-            const int bytes = live ? 16 : 0;
+            const int32_t page = __shfl_sync(0xFFFFFFFFu, entry, step * kStep + q * kPages + group);
+            const uint8_t* src = base + static_cast<uint64_t>(max(page, 0)) * page_bytes;
+            const int bytes = page >= 0 && active ? 16 : 0;
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + q * 1024), "l"(src), "r"(bytes) : "memory");
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + q * 1024 + 512), "l"(src + a.D), "r"(bytes) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + q * 1024 + 512), "l"(src + 2 * a.D), "r"(bytes) : "memory");
           }
         }
-        ++issued;
+        if (step == kIts - 1) ++to_issue;
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      for (int s = 0; s < kStages - 1; ++s) issue();
-      float mine = -INFINITY;
-      for (int32_t it = 0; it < it_end; ++it) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-        const uint8_t* st = smem + warp * kScoreBytes + it % kStages * kStage + lane * 16;
-        uint4 lw[R], hw[R];
+      read_entry(0);
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-          lw[q] = *reinterpret_cast<const uint4*>(st + q * 1024);
-          hw[q] = *reinterpret_cast<const uint4*>(st + q * 1024 + 512);
-        }
-        issue();
-        float best[R];
+      for (int s = 0; s < kStages - 1; ++s) issue(s % kIts);
+#pragma unroll 1
+      for (int32_t unit = 0; unit < units_here; ++unit) {
+        float v[kRows * GC];  // the lane's part of each sum of the unit
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-          const uint64_t lo[4] = {widen2(lw[q].x), widen2(lw[q].y), widen2(lw[q].z), widen2(lw[q].w)};
-          const uint64_t hi[4] = {widen2(hw[q].x), widen2(hw[q].y), widen2(hw[q].z), widen2(hw[q].w)};
-          float v[GC];
+        for (int step = 0; step < kIts; ++step) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+          const uint8_t* st = smem + warp * kScoreBytes + (unit * kIts + step) % kStages * kStage + lane * 16;
+          uint4 lw[R], hw[R];
 #pragma unroll
-          for (int g = 0; g < GC; ++g) {
-            uint64_t acc = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              fma2(acc, qp[g][i], hi[i]);
-              fma2(acc, qn[g][i], lo[i]);
-            }
-            float x, y;
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(acc));
-            v[g] = __fadd_rn(x, y);
+          for (int q = 0; q < R; ++q) {
+            lw[q] = *reinterpret_cast<const uint4*>(st + q * 1024);
+            hw[q] = *reinterpret_cast<const uint4*>(st + q * 1024 + 512);
           }
-          // Sums over the T lanes by halves. While a lane has several heads left it gives half of them
-          // to its partner and keeps the other half.
-          int cnt = GC, mine_g = 0;
+          issue((step + kStages - 1) % kIts);
 #pragma unroll
-          for (int o = T / 2; o >= 1; o /= 2) {
-            if (cnt > 1) {
-              cnt /= 2;
-              const bool up = lane & o;
+          for (int q = 0; q < R; ++q) {
+            const uint64_t lo[4] = {widen2(lw[q].x), widen2(lw[q].y), widen2(lw[q].z), widen2(lw[q].w)};
+            const uint64_t hi[4] = {widen2(hw[q].x), widen2(hw[q].y), widen2(hw[q].z), widen2(hw[q].w)};
 #pragma unroll
-              for (int k = 0; k < GC / 2; ++k) {
-                if (k < cnt) {
-                  const float give = up ? v[k] : v[k + cnt], keep = up ? v[k + cnt] : v[k];
-                  v[k] = __fadd_rn(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
-                }
+            for (int g = 0; g < GC; ++g) {
+              uint64_t acc = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                fma2(acc, qp[g][i], hi[i]);
+                fma2(acc, qn[g][i], lo[i]);
               }
-              if (up) mine_g += cnt;
-            } else {
-              v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], o));
+              float x, y;
+              asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(acc));
+              v[(step * R + q) * GC + g] = __fadd_rn(x, y);
             }
           }
-          best[q] = g0 + mine_g < a.G ? v[0] : -INFINITY;
         }
-        // the maximum over the heads: lanes that differ in the bits that chose a head
+        // Sums over the T lanes by halves: a lane gives one half of its sums to its partner and keeps
+        // the other, so that at the end lane `sub` has row sub / 4 and the heads sub % 4 (of GC = 4;
+        // two heads of GC = 8). Then the maximum over the heads.
 #pragma unroll
-        for (int o = T / 2; o >= (T > GC ? T / GC : 1); o /= 2)
+        for (int s = 1; 1 << s <= T; ++s) {
+          const int o = T >> s;
+          const bool up = lane & o;
 #pragma unroll
-          for (int q = 0; q < R; ++q) best[q] = fmaxf(best[q], __shfl_xor_sync(0xFFFFFFFFu, best[q], o));
-        // lane l keeps the score of the unit's page l
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-          const float got = __shfl_sync(0xFFFFFFFFu, best[q], lane % kPages * T);
-          if (lane / kPages == it % kIts * R + q) mine = got;
-        }
-        if (it % kIts == kIts - 1) {
-          const int32_t j = (first + it / kIts) * kUnitPages + lane;
-          if (lane < kUnitPages && j < n) {
-            // (a page outside the pool was copied as zeros: it comes last)
-            const int64_t page = table_entry(a.block_tables, a.table64, b * a.max_pages + j);
-            const bool bad = page < 0 || page >= a.num_pages;
-            uint32_t key = bad ? key_of(-INFINITY) : key_of(mine);
-            if (g0 > 0) key = max(key, keys[j]);
-            if (j < a.sink || j >= n - a.recent) key = kForced;
-            keys[j] = key;
+          for (int k = 0; k < kRows * GC / 2; ++k) {
+            if (k < kRows * GC >> s) {
+              const float low = v[k], high = v[k + (kRows * GC >> s)];
+              v[k] = __fadd_rn(up ? high : low, __shfl_xor_sync(0xFFFFFFFFu, up ? low : high, o));
+            }
           }
+        }
+        float best = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < GC / 4; ++k)
+          if (g0 + (lane & 3) * (GC / 4) + k < a.G) best = fmaxf(best, v[k]);
+        best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, 2));
+        best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, 1));
+        const int p = (sub >> 2) * kPages + group;
+        const int32_t j = (first + unit) * kUnitPages + p;
+        if ((lane & 3) == 0 && j < n) {
+          uint32_t key = key_of(bad >> (kAhead * kUnitPages + p) & 1u ? -INFINITY : best);
+          if (g0 > 0) key = max(key, keys[j]);
+          if (j < a.sink || j >= n - a.recent) key = kForced;
+          keys[j] = key;
         }
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -476,25 +479,29 @@ __global__ void __launch_bounds__(kScoreWarps * 32, GC == 4 ? 3 : 2) page_scores
 // One CTA for each list. The k-th largest key is found by its digits, from the highest bit in
 // which the keys differ: a histogram of a digit in shared memory, the bin that holds the k-th,
 // and so on inside that bin, until the bin is wanted as a whole. Then one pass in page order
-// writes the pages above it and the first ones equal to it.
+// writes the pages above it and the first ones equal to it. Its barriers bound it, some 4 us a
+// wave: 512 lists of up to 1024 pages take 4.6 us less in CTAs of 128 threads than of 512 (31.0 and
+// 35.6 us with the scores), 16 lists of the same length 1.2 us more (12.0 and 10.8).
 
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 512, kShortThreads = 128;
 constexpr int kDigit = 9, kBins = 1 << kDigit;
 constexpr int kPerThread = 16;  // keys that a thread has in registers
 
-// Sum of v[0 .. warp) over the warps' totals v (one for each warp, kSelectThreads / 32 of them), and
+// Sum of v[0 .. warp) over the warps' totals v (one for each warp, THREADS / 32 of them), and
 // of all of them; every lane of a warp calls it.
+template <int THREADS>
 __device__ __forceinline__ uint32_t sum_before(const uint32_t* v, int warp, uint32_t* all) {
   const int lane = threadIdx.x & 31;
-  const uint32_t x = lane < kSelectThreads / 32 ? v[lane] : 0u;
+  const uint32_t x = lane < THREADS / 32 ? v[lane] : 0u;
   *all = __reduce_add_sync(0xFFFFFFFFu, x);
   return __reduce_add_sync(0xFFFFFFFFu, lane < warp ? x : 0u);
 }
 
 __device__ __forceinline__ uint32_t warp_sum(uint32_t v) { return __reduce_add_sync(0xFFFFFFFFu, v); }
 
-__global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const SelectArgs a) {
-  __shared__ uint32_t s_hist[kBins], s_red[4][kSelectThreads / 32], s_bin, s_above, s_in_bin;
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == kShortThreads ? 6 : 2) select_pages_kernel(const SelectArgs a) {
+  __shared__ uint32_t s_hist[kBins], s_red[4][THREADS / 32], s_bin, s_above, s_in_bin;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t item = blockIdx.x;
   const int32_t b = static_cast<int32_t>(item / a.H);
@@ -504,15 +511,15 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
   const uint32_t* keys = a.scores + item * a.pitch;
   wait_for_scores();  // (on every path: what follows this kernel in the stream follows the scores too)
   if (tid == 0) a.num_selected[item] = count;
-  for (int32_t i = count + tid; i < a.k; i += kSelectThreads) out[i] = -1;
+  for (int32_t i = count + tid; i < a.k; i += THREADS) out[i] = -1;
   if (count == n) {
-    for (int32_t j = tid; j < n; j += kSelectThreads) out[j] = j;
+    for (int32_t j = tid; j < n; j += THREADS) out[j] = j;
     return;
   }
   // A thread's keys are neighbours, so that page order is thread order: `each_n` of them, in
-  // registers; of a list longer than kSelectThreads * kPerThread the rest is read again each time.
-  constexpr int32_t kTile = kSelectThreads * kPerThread;
-  int32_t each_n = (n + kSelectThreads - 1) / kSelectThreads;
+  // registers; of a list longer than THREADS * kPerThread the rest is read again each time.
+  constexpr int32_t kTile = THREADS * kPerThread;
+  int32_t each_n = (n + THREADS - 1) / THREADS;
   each_n = each_n > 2 ? min((each_n + 3) & ~3, kPerThread) : each_n;
   uint32_t mine[kPerThread];
 #pragma unroll
@@ -557,9 +564,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     s_red[2][warp] = forced;
   }
   __syncthreads();
-  lo = __reduce_min_sync(0xFFFFFFFFu, s_red[0][lane % (kSelectThreads / 32)]);
-  hi = __reduce_max_sync(0xFFFFFFFFu, s_red[1][lane % (kSelectThreads / 32)]);
-  sum_before(s_red[2], 0, &forced);
+  lo = __reduce_min_sync(0xFFFFFFFFu, s_red[0][lane % (THREADS / 32)]);
+  hi = __reduce_max_sync(0xFFFFFFFFu, s_red[1][lane % (THREADS / 32)]);
+  sum_before<THREADS>(s_red[2], 0, &forced);
   // keys >= floor_ are taken, of those in [floor_, ceil_] the first `want` in page order
   uint32_t floor_ = kForced, ceil_ = kForced, want = count;
   if (forced < static_cast<uint32_t>(count)) {
@@ -571,16 +578,18 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     uint32_t in_range = n - forced;
     while (left > 0 && in_range > want) {
       const uint32_t shift = left > kDigit ? left - kDigit : 0;
-      for (int i = tid; i < kBins; i += kSelectThreads) s_hist[i] = 0;
+      for (int i = tid; i < kBins; i += THREADS) s_hist[i] = 0;
       __syncthreads();
       each([&](uint32_t k) {
         if (k >= floor_ && k <= ceil_) atomicAdd(s_hist + ((k - base) >> shift), 1u);
       });
       __syncthreads();
-      // the bin of the want-th largest: bins from the top, kBins = kSelectThreads of them
-      static_assert(kBins == kSelectThreads, "one bin to a thread");
-      const uint32_t c = s_hist[kBins - 1 - tid];
-      uint32_t sum = c;
+      // the bin of the want-th largest: bins from the top, kEach of them to a thread
+      constexpr int kEach = kBins / THREADS;
+      uint32_t c[kEach], own = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) own += c[i] = s_hist[kBins - 1 - (tid * kEach + i)];
+      uint32_t sum = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
@@ -589,11 +598,16 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
       if (lane == 31) s_red[3][warp] = sum;
       __syncthreads();
       uint32_t all;
-      sum += sum_before(s_red[3], warp, &all);
-      if (sum >= want && sum - c < want) {
-        s_bin = kBins - 1 - tid;
-        s_above = sum - c;
-        s_in_bin = c;
+      sum += sum_before<THREADS>(s_red[3], warp, &all);
+      sum -= own;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        if (sum < want && sum + c[i] >= want) {
+          s_bin = kBins - 1 - (tid * kEach + i);
+          s_above = sum;
+          s_in_bin = c[i];
+        }
+        sum += c[i];
       }
       __syncthreads();
       base += s_bin << shift;
@@ -636,8 +650,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     }
     __syncthreads();
     uint32_t a_all, i_all;
-    uint32_t na = base_above + sa - above + sum_before(s_red[0], warp, &a_all);
-    uint32_t ni = base_in + si - in + sum_before(s_red[1], warp, &i_all);
+    uint32_t na = base_above + sa - above + sum_before<THREADS>(s_red[0], warp, &a_all);
+    uint32_t ni = base_in + si - in + sum_before<THREADS>(s_red[1], warp, &i_all);
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       const int32_t j = t + tid * each_n + i;
@@ -720,15 +734,23 @@ nvfp4_status launch_select_pages(SelectArgs a, cudaStream_t stream) {
   const nvfp4_status st = a.G <= 4 ? launch_scores_t<4>(a, stream) : launch_scores_t<8>(a, stream);
   if (st != NVFP4_OK) return st;
   cudaLaunchConfig_t config{};
-  config.gridDim = dim3(a.B * a.H);
-  config.blockDim = dim3(kSelectThreads);
+  // lists that a small CTA holds in registers, and more of them than wide CTAs fit at once
+  int64_t wide;
+  if (nvfp4_status e = resident_ctas(reinterpret_cast<const void*>(select_pages_kernel<kSelectThreads>), kSelectThreads,
+                                     0, 32, "nvfp4_select_pages", &wide))
+    return e;
+  const int64_t lists = static_cast<int64_t>(a.B) * a.H;
+  const bool is_short = lists > wide && a.max_pages <= kShortThreads * kPerThread;
+  config.gridDim = dim3(static_cast<unsigned>(lists));
+  config.blockDim = dim3(is_short ? kShortThreads : kSelectThreads);
   config.stream = stream;
   cudaLaunchAttribute overlap{};
   overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   overlap.val.programmaticStreamSerializationAllowed = 1;
   config.attrs = &overlap;
   config.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&config, select_pages_kernel, a);
+  const cudaError_t e = cudaLaunchKernelEx(
+      &config, is_short ? select_pages_kernel<kShortThreads> : select_pages_kernel<kSelectThreads>, a);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return fail(NVFP4_ERR_CUDA, std::string("nvfp4_select_pages: ") + cudaGetErrorString(e));

@@ -135,6 +135,13 @@ def test_selection_is_equal(gpu_lib, i):
     _check_select(gpu_lib, _select_case(i, lens, H, G, D, ps, dtype), ps, k, sink, recent)
 
 
+@pytest.mark.parametrize("quant", [None, 500.0])
+def test_many_short_lists(gpu_lib, quant):
+    """More lists than wide CTAs fit at once: a small CTA to a list, the longest of 16 keys a thread."""
+    lens = [(37 * i) % 400 for i in range(398)] + [8192, 8189]
+    _check_select(gpu_lib, _select_case(5, lens, 2, 4, 16, 4, torch.float16, quant=quant), 4, 30, 1, 1)
+
+
 @pytest.mark.parametrize("k", [1, 5, 64, 200])
 def test_ties_go_to_the_lower_page(gpu_lib, k):
     _check_select(gpu_lib, _select_case(77, [3000, 700], 2, 4, 64, 4, torch.float16, quant=500.0), 4, k, 1, 1)
