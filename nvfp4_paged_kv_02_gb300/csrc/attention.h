@@ -50,9 +50,10 @@ struct BoundsArgs {
   const int32_t* first_positions;  // may be null: 0
   uint16_t* bounds;
   int32_t* status;
-  // set at launch: a CTA's shape, and the ring's
-  int32_t tile, slices, pages, stages;
+  // set at launch: a CTA's shape, or the ring's
+  int32_t pages, tile, slices, stages;
   uint32_t code_bytes, scale_bytes, stage_bytes;
+  Div div_nb, div_columns;
   PipeTest pipe;
 };
 nvfp4_status launch_page_key_bounds(BoundsArgs a, cudaStream_t stream);

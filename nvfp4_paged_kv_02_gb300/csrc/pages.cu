@@ -22,17 +22,17 @@ __device__ __forceinline__ int64_t table_entry(const void* tables, int32_t is64,
 
 // ---- bounds -----------------------------------------------------------------------------
 //
-// Reading the keys bounds it: 9/16 byte an element, and 4 bytes written for page_size of them;
-// the 40-odd instructions that a block takes come close. A thread has one column, a 16-element
-// block of a head, and slots of one page; kBatch slots are loaded before the first is decoded.
-// Pages of more than kMaxSlots slots give a column to several threads, which join in shared memory.
+// Reading the keys is the floor: 9/16 byte an element, and 4 bytes written for page_size of them. A
+// thread has one column, a 16-element block of a head, and slots of one page; kBatch slots are
+// loaded before the first is decoded. Pages of more than kMaxSlots slots give a column to several
+// threads.
 
 constexpr int kBoundsThreads = 256;
 constexpr int kBatch = 8;
 constexpr int kMaxSlots = 8;  // that a thread has of a column, where there are threads for it
 constexpr int kMaxBoundsStages = 4;
 // Shared memory of the ring: three CTAs to an SM, or what two stages of one larger page need.
-constexpr int64_t kBoundsRing = 56 * 1024, kBoundsMostRing = 160 * 1024;
+constexpr int64_t kBoundsRing = 72 * 1024, kBoundsMostRing = 160 * 1024;
 
 __device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -160,7 +160,8 @@ __device__ __forceinline__ void write_column(const BoundsArgs& a, const ColumnBo
   hi[1] = make_uint4(r.hi[4], r.hi[5], r.hi[6], r.hi[7]);
 }
 
-// Pages that cannot be copied in bulk (alignment, size): straight from global memory.
+// Pages that cannot be copied in bulk (alignment, size): straight from global memory. The threads of
+// a column join in shared memory.
 __global__ void __launch_bounds__(kBoundsThreads) page_key_bounds_kernel(const BoundsArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   int32_t* cum = reinterpret_cast<int32_t*>(smem);
@@ -187,76 +188,182 @@ __global__ void __launch_bounds__(kBoundsThreads) page_key_bounds_kernel(const B
 
 // The same from a ring of stages, each `pages` items' codes and scales in bulk copies: a page is
 // contiguous in either layout, and copies in flight are not bound by registers or by the number of
-// loads that an SM tracks. Measured 2.2 TB/s with direct loads on 200 K tokens.
-__global__ void __launch_bounds__(kBoundsThreads) page_key_bounds_ring_kernel(const BoundsArgs a) {
+// loads that an SM tracks. One warp keeps the ring filled; the others take a job at a time, 32/S
+// columns (of one page or, where it has fewer, of several) with S lanes to a column (S = 1, 2 or 4, about eight slots each), and are bound
+// to one another by the stages' barriers alone. The S lanes join by halves: one keeps the lower
+// bounds and gives the upper ones away, so that each ends with 32/S bytes of the result.
+//
+// Per 32 blocks of 16 elements: two loads, nine conversions, eight products, 16 minima and maxima.
+// They bound it: 200 K tokens of 8 heads of 128 elements in pages of 32 take 41 us (3.4 TB/s, the
+// ALU pipe two thirds busy), in pages of 16 41 us (4.0 TB/s); direct loads took them at 2.2 TB/s.
+// With a CTA-wide barrier at a stage's start and end and the join in shared memory it was 50 us,
+// with two larger CTAs to an SM and six stages 45 us.
+constexpr int kRingWarps = 8;
+constexpr int kRingPages = 32;  // most items of a stage: one to a lane
+
+template <int S>
+__device__ __forceinline__ void add_ring_slots(ColumnBounds& r, const uint2* c, const uint8_t* s, int32_t inc, int32_t n) {
+  auto add = [&](const uint2 (&w)[kBatch], const uint32_t (&f)[kBatch]) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const uint32_t S2 = f16x2_from_e4m3x2(f[k] * 0x0101u);
+      uint32_t v[8];
+      f16x2x4_from_e2m1x8(w[k].x, v[0], v[1], v[2], v[3]);
+      f16x2x4_from_e2m1x8(w[k].y, v[4], v[5], v[6], v[7]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = hmul2_rn(v[e], S2);
+        r.lo[e] = hmin2(r.lo[e], v[e]);
+        r.hi[e] = hmax2(r.hi[e], v[e]);
+      }
+    }
+  };
+  // slots 0, S, 2 S, .. below n, `inc` blocks apart
+#pragma unroll 1
+  while (n > 0) {
+    uint2 w[kBatch];
+    uint32_t f[kBatch];
+    if (n > (kBatch - 1) * S) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        w[k] = c[k * inc];
+        f[k] = s[k * inc];
+      }
+    } else {
+      const int32_t last = (n - 1) / S;  // (past the end: the last slot again)
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        w[k] = c[min(k, last) * inc];
+        f[k] = s[min(k, last) * inc];
+      }
+    }
+    add(w, f);
+    n -= kBatch * S;
+    c += kBatch * inc;
+    s += kBatch * inc;
+  }
+}
+
+template <int S>
+__global__ void __launch_bounds__((kRingWarps + 1) * 32, 3) page_key_bounds_ring_kernel(const BoundsArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ uint32_t s_part[16 * kBoundsThreads];
-  __shared__ __align__(8) uint64_t s_full[kMaxBoundsStages];
-  __shared__ BoundsItem s_item[kMaxBoundsStages][kBoundsThreads / 16];
+  __shared__ __align__(8) uint64_t s_full[kMaxBoundsStages], s_empty[kMaxBoundsStages];
+  __shared__ BoundsItem s_item[kMaxBoundsStages][kRingPages];
   int32_t* cum = reinterpret_cast<int32_t*>(smem + a.stages * a.stage_bytes);
-  const int tid = threadIdx.x;
-  if (tid == 0) {
-    for (int s = 0; s < a.stages; ++s) mbar_init(s_full + s, a.pages);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(s_full + s, a.pages);
+      mbar_init(s_empty + s, kRingWarps);
+    }
     fence_mbar_init();
   }
   const int32_t total = scan_items(a, cum), nb = a.D / 16, columns = a.H * nb;  // ends with a barrier
-  const BoundsShape me = bounds_shape(a);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * a.pages;
-  int64_t next = static_cast<int64_t>(blockIdx.x) * a.pages;  // first item of the next copies
-  bool stall = a.pipe.stall != 0;                             // test control: withhold the first stage
-  uint32_t flight = 0;                                        // stages whose copies have not been waited for
-  auto issue = [&](int s) {  // thread p < pages: item p of the stage
-    if (next >= total) return;
-    if (tid < a.pages && !stall) {
-      const BoundsItem it = find_item(a, cum, next + tid, total);
-      s_item[s][tid] = it;
-      if (it.page >= 0) {
-        uint8_t* dst = smem + s * a.stage_bytes + tid * (a.code_bytes + a.scale_bytes);
-        mbar_arrive_expect_tx(s_full + s, a.code_bytes + a.scale_bytes);
-        bulk_g2s(dst, a.kc.data + it.page * a.kc.data_page_stride, a.code_bytes, s_full + s);
-        bulk_g2s(dst + a.code_bytes, a.kc.sf + it.page * a.kc.sf_page_stride, a.scale_bytes, s_full + s);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * a.pages, from = static_cast<int64_t>(blockIdx.x) * a.pages;
+  int s = 0;
+  uint32_t phase = 0;
+  if (warp == kRingWarps) {  // the copies: lane p < pages has item p of a stage
+    const bool stall = a.pipe.stall != 0;  // test control: withhold the first stage
+    int32_t filled = 0;                    // stages filled, up to a.stages
+    for (int64_t item0 = from; item0 < total; item0 += step) {
+      const BoundsItem it = lane < a.pages ? find_item(a, cum, item0 + lane, total) : BoundsItem{-1, 0};
+      if (filled == a.stages) {
+        const bool ok = mbar_wait(s_empty + s, phase ^ 1u, a.pipe.wait_limit);
+        if (__any_sync(0xFFFFFFFFu, !ok)) {
+          if (lane == 0) flag(a.status, NVFP4_DEV_TIMEOUT);
+          break;
+        }
       } else {
-        mbar_arrive(s_full + s);
+        ++filled;
+      }
+      if (lane < a.pages && !(stall && item0 == from)) {
+        s_item[s][lane] = it;
+        if (it.page >= 0) {
+          uint8_t* dst = smem + s * a.stage_bytes + lane * (a.code_bytes + a.scale_bytes);
+          mbar_arrive_expect_tx(s_full + s, a.code_bytes + a.scale_bytes);
+          bulk_g2s(dst, a.kc.data + it.page * a.kc.data_page_stride, a.code_bytes, s_full + s);
+          bulk_g2s(dst + a.code_bytes, a.kc.sf + it.page * a.kc.sf_page_stride, a.scale_bytes, s_full + s);
+        } else {
+          mbar_arrive(s_full + s);
+        }
+      }
+      if (++s == a.stages) {
+        s = 0;
+        phase ^= 1u;
       }
     }
-    flight |= 1u << s;
-    stall = false;
-    next += step;
-  };
-  for (int s = 0; s < a.stages; ++s) issue(s);
-  uint32_t phase = 0;
-  int s = 0;
-  for (int64_t item0 = static_cast<int64_t>(blockIdx.x) * a.pages; item0 < total; item0 += step) {
+    // No copy may still be landing in this CTA's shared memory when it exits: the last fill of each
+    // stage. (Stages below s were filled in this round of the ring, those from s on in the last one.)
+    for (int q = 0; q < a.stages; ++q) {
+      if (q >= filled || (stall && q == 0)) continue;
+      mbar_wait(s_full + q, q < s ? phase : phase ^ 1u, a.pipe.wait_limit);
+    }
+    return;
+  }
+  constexpr int kColumns = 32 / S;
+  const int slice = lane / kColumns, in_group = lane % kColumns;
+  const int32_t all = a.pages * columns;  // a stage's columns
+  const bool nhd = a.layout == NVFP4_NHD;
+  const int32_t slot_step = nhd ? columns : nb;
+  for (int64_t item0 = from; item0 < total; item0 += step) {
     const bool ok = mbar_wait(s_full + s, phase, a.pipe.wait_limit);
-    if (__syncthreads_or(!ok)) {
-      if (tid == 0) flag(a.status, NVFP4_DEV_TIMEOUT);
-      break;
+    if (__any_sync(0xFFFFFFFFu, !ok)) {
+      if (lane == 0) flag(a.status, NVFP4_DEV_TIMEOUT);
+      return;
     }
-    flight &= ~(1u << s);
-    const BoundsItem it = me.item < a.pages ? s_item[s][me.item] : BoundsItem{-1, 0};
-    const uint8_t* codes = smem + s * a.stage_bytes + me.item * (a.code_bytes + a.scale_bytes);
-    for (int32_t c0 = 0; c0 < columns; c0 += a.tile) {
-      const int32_t w = c0 + me.col, h = w / nb, j = w - h * nb;
+    for (int32_t c0 = warp * kColumns; c0 < all; c0 += kRingWarps * kColumns) {
+      const int32_t p = min(div_q32(c0 + in_group, a.div_columns), a.pages - 1);
+      const int32_t w = c0 + in_group - p * columns;
+      const BoundsItem it = s_item[s][p];
       const bool mine = it.page >= 0 && w < columns;
-      ColumnBounds r;
-      clear(r);
-      if (mine)
-        add_slots(r, codes, codes + a.code_bytes, a.layout == NVFP4_NHD ? w : h * a.ps * nb + j,
-                  a.layout == NVFP4_NHD ? columns : nb, me.slice, a.slices, it.n);
-      if (a.slices > 1) join_slices(a, r, s_part, me.slice, mine);
-      if (mine && me.slice == 0) write_column(a, r, it.page, h, j);
+      if (__any_sync(0xFFFFFFFFu, mine)) {
+        const int32_t h = div_q32(w, a.div_nb), j = w - h * nb;
+        ColumnBounds r;
+        clear(r);
+        if (mine) {
+          const uint8_t* codes = smem + s * a.stage_bytes + p * (a.code_bytes + a.scale_bytes);
+          const int32_t at = (nhd ? w : h * a.ps * nb + j) + slice * slot_step;
+          add_ring_slots<S>(r, reinterpret_cast<const uint2*>(codes) + at, codes + a.code_bytes + at, S * slot_step,
+                            it.n - slice);
+        }
+        uint16_t* out = a.bounds + (it.page * a.H + h) * 2 * a.D + 16 * j;
+        if (S == 1) {
+          if (mine) write_column(a, r, it.page, h, j);
+        } else {
+          const bool upper = lane & 16;
+          uint32_t x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, upper ? r.lo[e] : r.hi[e], 16);
+            x[e] = upper ? hmax2(r.hi[e], got) : hmin2(r.lo[e], got);
+          }
+          if (upper) out += a.D;
+          if (S == 2) {
+            if (mine) {
+              reinterpret_cast<uint4*>(out)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+              reinterpret_cast<uint4*>(out)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+            }
+          } else {
+            const bool second = lane & 8;
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, second ? x[e] : x[4 + e], 8);
+              const uint32_t keep = second ? x[4 + e] : x[e];
+              y[e] = upper ? hmax2(keep, got) : hmin2(keep, got);
+            }
+            if (mine) reinterpret_cast<uint4*>(out)[second] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
     }
-    __syncthreads();  // the stage has been read
-    issue(s);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(s_empty + s);  // the stage has been read
     if (++s == a.stages) {
       s = 0;
       phase ^= 1u;
     }
   }
-  // no copy may still be landing in this CTA's shared memory when it exits (after a wait that ran
-  // out: the stages from s on have this phase, those before it the next)
-  for (int q = 0; q < a.stages; ++q)
-    if (flight >> q & 1u) mbar_wait(s_full + q, q >= s ? phase : phase ^ 1u, a.pipe.wait_limit);
 }
 
 // ---- scores -----------------------------------------------------------------------------
@@ -691,34 +798,44 @@ nvfp4_status launch_scores_t(const SelectArgs& a, cudaStream_t stream) {
 
 nvfp4_status launch_page_key_bounds(BoundsArgs a, cudaStream_t stream) {
   const int32_t columns = a.H * (a.D / 16);
-  a.tile = columns < kBoundsThreads ? columns : kBoundsThreads;
-  a.slices = (a.ps + kMaxSlots - 1) / kMaxSlots;
-  const int32_t most_slices = kBoundsThreads / a.tile;
-  if (a.slices > most_slices) a.slices = most_slices;
-  a.pages = kBoundsThreads / (a.tile * a.slices);
-  if (a.pages > kBoundsThreads / 16) a.pages = kBoundsThreads / 16;
   const int64_t codes = static_cast<int64_t>(a.ps) * a.H * (a.D / 2), scales = codes / 8;
   const bool ring = codes % 16 == 0 && scales % 16 == 0 && (codes + scales) * 2 <= kBoundsMostRing &&
                     reinterpret_cast<uintptr_t>(a.kc.sf) % 16 == 0 && a.kc.sf_page_stride % 16 == 0;
   size_t smem = static_cast<size_t>(a.B) * 4;
+  int threads = kBoundsThreads;
+  auto kern = page_key_bounds_kernel;
   if (ring) {
     a.code_bytes = static_cast<uint32_t>(codes);
     a.scale_bytes = static_cast<uint32_t>(scales);
+    const int S = a.ps < 2 * kMaxSlots ? 1 : (a.ps < 4 * kMaxSlots ? 2 : 4);
+    // a job for each warp, where the ring holds them
+    a.pages = (kRingWarps * (32 / S) + columns - 1) / columns;
+    if (a.pages > kRingPages) a.pages = kRingPages;
     while (a.pages > 1 && a.pages * (codes + scales) * 2 > kBoundsRing) --a.pages;
     a.stage_bytes = (a.pages * (a.code_bytes + a.scale_bytes) + 127) / 128 * 128;
     a.stages = static_cast<int32_t>(kBoundsRing / a.stage_bytes);
     a.stages = a.stages < 2 ? 2 : (a.stages > kMaxBoundsStages ? kMaxBoundsStages : a.stages);
     a.pipe = pipe_test_from_env();
+    a.div_nb = make_div(a.D / 16);
+    a.div_columns = make_div(columns);
     smem += static_cast<size_t>(a.stages) * a.stage_bytes;
+    threads = (kRingWarps + 1) * 32;
+    kern = S == 1 ? page_key_bounds_ring_kernel<1> : (S == 2 ? page_key_bounds_ring_kernel<2> : page_key_bounds_ring_kernel<4>);
+  } else {
+    a.tile = columns < kBoundsThreads ? columns : kBoundsThreads;
+    a.slices = (a.ps + kMaxSlots - 1) / kMaxSlots;
+    const int32_t most_slices = kBoundsThreads / a.tile;
+    if (a.slices > most_slices) a.slices = most_slices;
+    a.pages = kBoundsThreads / (a.tile * a.slices);
+    if (a.pages > kBoundsThreads / 16) a.pages = kBoundsThreads / 16;
   }
-  const auto kern = ring ? page_key_bounds_ring_kernel : page_key_bounds_kernel;
   int64_t cap;
-  if (nvfp4_status st = resident_ctas(reinterpret_cast<const void*>(kern), kBoundsThreads, smem, 32,
+  if (nvfp4_status st = resident_ctas(reinterpret_cast<const void*>(kern), threads, smem, 32,
                                       "nvfp4_page_key_bounds", &cap))
     return st;
   const int64_t most = (a.B * a.max_pages + a.pages - 1) / a.pages;
   const int grid = static_cast<int>(most < cap ? most : cap);
-  kern<<<grid, kBoundsThreads, smem, stream>>>(a);
+  kern<<<grid, threads, smem, stream>>>(a);
   return check_launch("nvfp4_page_key_bounds");
 }
 

@@ -73,6 +73,32 @@ def test_bounds_of_bad_pages_and_lengths(gpu_lib):
     assert int(st.item()) == nv.DEV_BAD_PAGE | nv.DEV_LEN_CLAMPED
 
 
+RING = [
+    # pages that bulk copies take: one, two and four lanes to a column, columns of several pages to a job
+    ([3000, 1, 0, 77], 1, 64, 8, R.HND, np.int32),
+    ([900, 31], 3, 96, 16, R.HND, np.int32),
+    ([900, 31], 3, 96, 16, R.NHD, np.int64),
+    ([700, 65, 64], 2, 80, 32, R.NHD, np.int32),
+    ([130, 700, 2], 5, 48, 64, R.HND, np.int32),
+    ([513] * 70, 2, 16, 16, R.NHD, np.int32),
+    ([20000], 4, 64, 32, R.NHD, np.int32),
+]
+
+
+@pytest.mark.parametrize("i", range(len(RING)))
+@pytest.mark.parametrize("last", [False, True])
+def test_bounds_of_pages_in_bulk_copies(gpu_lib, i, last):
+    lens, H, D, ps, layout, tdt = RING[i]
+    assert ps * H * D // 16 % 16 == 0
+    c = R.make_paged(i + 90, lens, H, D, ps, layout, table_dtype=tdt)
+    first = c.lens // 2 if last else None
+    got = _bounds(gpu_lib, c, first)
+    want = np.full(got.shape, 9.0)
+    for p, (lo, hi) in R.key_bounds(c, first).items():
+        want[p, :, 0], want[p, :, 1] = lo, hi
+    assert np.array_equal(got, want)
+
+
 def _select_case(seed, lens, H, G, D, ps, dtype, quant=None):
     rng = np.random.Generator(np.random.PCG64(seed))
     lens = np.asarray(lens, np.int32)
