@@ -98,9 +98,12 @@ class NVFP44Over6Config:
     err_mode: str = "MAE"
     err_use_fast_math: bool = False
 
-    def _c(self) -> _Config:
+    def _values(self) -> Tuple[float, int, int]:
         mode = {"MAE": 0, "MSE": 1}[self.err_mode.upper()]
-        return _Config(float(self.e4m3_max), mode, int(bool(self.err_use_fast_math)))
+        return float(self.e4m3_max), mode, int(bool(self.err_use_fast_math))
+
+    def _c(self) -> _Config:
+        return _Config(*self._values())
 
 
 _lock = threading.Lock()
@@ -659,10 +662,7 @@ def nvfp4_qk_norm_rope_append_paged(query: torch.Tensor, key: torch.Tensor, valu
     `query`). The other arguments are those of nvfp4_quantize_append_paged."""
     k, v = _pair(paged_kv_cache)
     ks, vs = _pair(kv_cache_sf)
-    r = nvfp4_4over6
-    if r is not None:
-        c = r._c()
-        r = (c.e4m3_max, c.err_mode, c.err_use_fast_math)
+    r = None if nvfp4_4over6 is None else nvfp4_4over6._values()
     return _done("nvfp4_qk_norm_rope_append_paged", _calls().qk_norm_rope_append(
         query, key, value, q_weight, k_weight, cos_sin, batch_indices, positions, k, v, ks, vs, kv_indices,
         kv_indptr, kv_last_page_len, k_scale, v_scale, _layout(kv_layout), eps, rotary_interleaved, r, out,
