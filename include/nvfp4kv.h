@@ -484,7 +484,9 @@ nvfp4_status nvfp4_qk_norm_rope_append_paged(
  *                    positions that it has written, and one page of each request is redone.
  *   key_bounds       device float16 [k_cache.num_pages, num_kv_heads, 2, head_dim],
  *                    contiguous, 16-byte aligned.
- *   The other arguments are those of nvfp4_dequantize_paged. */
+ *   dev_status       NVFP4_DEV_TIMEOUT besides the others, if a wait of the bulk-copy ring gave up.
+ *   The other arguments are those of nvfp4_dequantize_paged.
+ * Requirements: batch_size * max_pages_per_request at most 2^31 - 1. */
 nvfp4_status nvfp4_page_key_bounds(nvfp4_paged_cache k_cache, int32_t page_size,
                                    int32_t num_kv_heads, int32_t head_dim, int32_t kv_layout,
                                    const void* block_tables, int32_t table_dtype,
@@ -571,7 +573,8 @@ nvfp4_status nvfp4_paged_attention_decode(
  * h]) only (nvfp4_select_pages). An entry outside [0, max_pages_per_request) is left out and
  * reported (NVFP4_DEV_BAD_PAGE); an entry given twice counts twice.
  *   selected_pages  device int32 [batch_size, num_kv_heads, max_selected].
- *   num_selected    device int32 [batch_size, num_kv_heads], clamped to [0, max_selected]. */
+ *   num_selected    device int32 [batch_size, num_kv_heads], clamped to [0, max_selected].
+ * Requirements: those of nvfp4_paged_attention_decode, max_selected * page_size at most 2^30. */
 nvfp4_status nvfp4_sparse_paged_attention_decode(
     const void* query, int32_t dtype, int64_t query_row_stride, int32_t num_qo_heads,
     nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache, int32_t page_size,

@@ -11,8 +11,11 @@
 // clock. A tile that goes through shared memory as binary16 for tcgen05.mma would have to be
 // decoded to registers and written back first; mma.sync takes the decoded registers as they
 // are, and its 1024 multiply-adds a clock and SM (measured) are three times what G <= 8 needs.
-// The budget is instructions: about 3 a lane and element, of which decoding, scaling and
-// multiplying take 1.7.
+// The budget is instructions: some 720 of a warp for 32 tokens of 128 elements, 2.8 a lane and
+// element, of which decoding, scaling and multiplying take 1.7. On large calls they bound it, on
+// small ones the start (lengths, their scan, the first pages: 5 us) and the joins. At 8 KV heads of
+// 128: 430 K tokens of 128 requests, G = 4: 112 us (4.4 TB/s); 117 K tokens of 64 requests, G = 8:
+// 42 us (3.1); one request of 131 K tokens, G = 4: 48 us (3.2). The tensor pipe is 16 % busy.
 //
 // Work. A unit is 32 tokens of one (request, KV head, chunk of up to 8 NT query heads). All
 // units of a launch, in that order, are cut into equal runs, one for each CTA, so that ragged
