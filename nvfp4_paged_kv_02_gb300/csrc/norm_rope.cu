@@ -23,6 +23,13 @@
 // rows, then the key rows, then the value rows. What the rows share (the table's row, the weights,
 // the page) is read once. With many tokens a warp has all steps of a token; with few, the steps
 // are dealt out so that every step has a warp. Query rows are loaded two steps at a time.
+//
+// The floor is memory: the rows in, the queries and 9/16 byte a K/V element out. 32,764 tokens of 32
+// query and 8 KV heads of 128 take 160 us (bf16, full rotation, 4.4 TB/s) and 178 us (fp16, 4over6,
+// 4.0 TB/s); moving the data alone takes 119 us, and the instructions (some 150 of a warp for a step
+// of two query rows) use 63 % of the issue slots beside it. Packed arithmetic (200 us), a cp.async
+// ring (191), CTAs of 256 threads (207) and more CTAs an SM (179) do not overlap the two better. 64
+// tokens take 6.4 us.
 #include "internal.h"
 #include "quantize.cuh"
 
