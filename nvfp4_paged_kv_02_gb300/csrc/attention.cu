@@ -13,16 +13,18 @@
 // are, and its 1024 multiply-adds a clock and SM (measured) are three times what G <= 8 needs.
 // The budget is instructions: some 720 of a warp for 32 tokens of 128 elements, 2.8 a lane and
 // element, of which decoding, scaling and multiplying take 1.7. On large calls they bound it, on
-// small ones the start (lengths, their scan, the first pages: 5 us) and the joins. At 8 KV heads of
-// 128: 430 K tokens of 128 requests, G = 4: 112 us (4.4 TB/s); 117 K tokens of 64 requests, G = 8:
-// 42 us (3.1); one request of 131 K tokens, G = 4: 48 us (3.2). The tensor pipe is 16 % busy.
+// small ones the start (lengths, their scan, the first pages: 4 us), one unit's latency and the
+// joins. At 8 KV heads of 128: 430 K tokens of 128 requests, G = 4: 111 us (4.4 TB/s); 117 K tokens
+// of 64 requests, G = 8: 41 us (3.1); one request of 131 K tokens, G = 4: 47 us (3.2); 16 requests of
+// 30 tokens 7.7 us. The tensor pipe is 16 % busy.
 //
 // Work. A unit is 32 tokens of one (request, KV head, chunk of up to 8 NT query heads). All
 // units of a launch, in that order, are cut into equal runs, one for each CTA, so that ragged
 // lengths balance and one long request fills the GPU; the lengths are read on the device. In a
 // run, the four warps take the units of a segment (request, head, chunk) in turn and are joined
 // in shared memory at its end. A segment that several CTAs share is joined by the last of them
-// to finish (a counter), always in the order of the runs: results do not depend on timing.
+// to finish (a counter), always in the order of the runs: results do not depend on timing. Short
+// segments are not cut.
 //
 // A warp's units come through its own ring of stages (cp.async, no barrier with other warps).
 // Rows that are not live are zero-filled, never read, and masked.
@@ -53,6 +55,10 @@ constexpr int kTiles = kUnit / 16;  // of 16 tokens
 constexpr int kMinUnits = 4;  // of a CTA's run: one for each warp
 constexpr int kMaxCtasPerSm = 4;
 constexpr int kSegmentCost = 9;
+// A segment of so few units is the run's that it begins in: cutting it costs a join (3 us) and saves
+// less. 512 lists of 64 to 400 tokens: 15.2 us (8: 17.2), of 384: 19.3 (20.7); one request of 500
+// tokens (16 units): 9.9 us cut (16: 10.4), 32 lists of 512: 11.2 (12.7).
+constexpr int kWholeUnits = 12;
 constexpr float kWeightBias = 8.0f;
 constexpr float kSlack = 7.0f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -291,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
   const int D = FULL ? 64 * NW : a.D;
+  const float gk = __ldg(a.k_scale), gv = __ldg(a.v_scale);
   scan_places(a, cum, s_scan);
 
   // heads without live tokens get zeros
@@ -329,7 +336,16 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
     __syncwarp();
   }
 
+  auto more = [&](const Segment& s) { return s.start + places_of(s.units) < run; };
   Segment cs = find_segment(a, cum, c0);  // the consumer's segment
+  // the run begins in the segment's empty places, or in a segment that is not cut
+  if (cs.start + cs.units <= 0 || (cs.start < 0 && cs.units <= kWholeUnits)) {
+    if (!more(cs)) {
+      write_zeros();
+      return;
+    }
+    next_segment(a, cs);
+  }
   uint32_t raw[NT][8 * NW];  // the coming segment's query rows, as they are
   auto load_queries = [&](const Segment& s) {
     const int head0 = s.chunk * a.chunk_heads, heads = min(a.chunk_heads, a.G - head0);
@@ -351,9 +367,8 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
   // the units [u, end) of a segment that lie in this run
   auto portion = [&](const Segment& s, int32_t& u, int32_t& end) {
     u = max(-s.start, 0);
-    end = min(run - s.start, s.units);
+    end = s.units <= kWholeUnits ? s.units : min(run - s.start, s.units);
   };
-  auto more = [&](const Segment& s) { return s.start + places_of(s.units) < run; };
   int32_t pu, pend;
   Span span;            // the producer's request
   int32_t slots = 0;    // slots of its selected pages
@@ -515,7 +530,6 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
   for (int s = 0; s < NS - 1; ++s) issue(s);
 
   // -- the consumer --
-  const float gk = __ldg(a.k_scale), gv = __ldg(a.v_scale);
   const int t0 = token_of(r);                    // this lane's K rows: t0 and t0 + 8
   const int v0 = token_of(2 * c), v1 = token_of(2 * c + 1);  // its V rows, and 8 more
   // factors of the four parts and the joined maximum and sum, by the first threads
@@ -823,10 +837,6 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
       next_segment(a, cs);
       load_queries(cs);
     }
-    if (done.start + done.units <= 0) {  // the run begins in the segment's empty places
-      if (last_segment) break;
-      continue;
-    }
 
     // -- the four warps' parts, joined --
     // o[nt][w][i][k], [k + 2]: head 8 nt + 2 c + k, d = 8 (NW r + w) + 2 i, + 1
@@ -961,7 +971,7 @@ nvfp4_status launch_t(const AttentionArgs& a, cudaStream_t stream) {
                                       "nvfp4_paged_attention_decode", &cap))
     return st;
   const int64_t reach = a.selected ? static_cast<int64_t>(a.max_selected) * a.ps : a.max_pages * a.ps;
-  const int64_t most = static_cast<int64_t>(a.B) * a.H * a.chunks * ((reach + kUnit - 1) / kUnit + 1);
+  const int64_t most = static_cast<int64_t>(a.B) * a.H * a.chunks * ((reach + kUnit - 1) / kUnit + kSegmentCost);  // places
   const int64_t need = (most + kMinUnits - 1) / kMinUnits;
   const int grid = static_cast<int>(need < cap ? (need < 1 ? 1 : need) : cap);
   kern<<<grid, kThreads, smem, stream>>>(a);

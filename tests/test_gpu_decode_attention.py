@@ -92,6 +92,20 @@ def test_dense_matches_reference(gpu_lib, i):
     assert status == 0
 
 
+@pytest.mark.parametrize("lens,H,D", [
+    ([0, 700, 30, 390, 384, 385, 1, 416] * 12, 8, 64),   # more lists than CTAs, cut and whole ones mixed
+    ([383, 384, 385, 3000], 1, 128),                     # twelve units and one more
+    ([32 * n for n in range(15)], 2, 64),
+    ([1] * 300, 2, 32),
+])
+def test_lists_about_the_length_that_is_cut(gpu_lib, lens, H, D):
+    c = R.make_paged(len(lens), lens, H, D, 16, R.HND)
+    q = _query(2, c.B, H * 2, D, torch.float16)
+    out, lse, status = _run(gpu_lib, c, q)
+    R.check_attention(out, lse, _ref(c, q), q.dtype)
+    assert status == 0
+
+
 @pytest.mark.parametrize("layout", [R.NHD, R.HND])
 @pytest.mark.parametrize("D,off_sf,pad_sf,pad_data", [(128, 0, 16, 32), (128, 1, 3, 0), (128, 4, 4, 16),
                                                      (64, 2, 2, 0), (64, 0, 5, 48), (256, 8, 0, 0), (96, 0, 0, 16),
