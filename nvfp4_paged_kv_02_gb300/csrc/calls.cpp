@@ -2,7 +2,7 @@
 //
 // A decode step makes these calls once for each layer, and on small batches the kernels take less
 // time than Python needs to read a dozen tensors' properties and to convert the arguments (25 us a
-// call on the host, measured; 6 us here). So this module does what the rest of the binding does in
+// call on the host, measured; 5 to 8 us here). So this module does what the rest of the binding does in
 // Python: it checks shapes, types and strides, turns tensors into pointers, allocates outputs and
 // keeps the workspaces. No step of the work runs here.
 //
