@@ -19,8 +19,8 @@
 // rotation then needs no exchange, and the sum of squares is in-lane plus log2(T) shuffles. A
 // key row's 16-element blocks are put together through shared memory.
 //
-// A warp takes a token's rows a step at a time, 32/T rows of one kind to a step: first the query
-// rows, then the key rows, then the value rows. What the rows share (the table's row, the weights,
+// A warp takes a token's rows a step at a time, 32/T rows to a step: first the query rows, then the
+// key rows and the value rows (a step may hold some of both). What the rows share (the table's row, the weights,
 // the page) is read once. With many tokens a warp has all steps of a token; with few, the steps
 // are dealt out so that every step has a warp. Query rows are loaded two steps at a time.
 //
@@ -124,8 +124,13 @@ __device__ __forceinline__ void norm_rope(const NormRopeArgs& a, const Turn& tur
   vb = pack8<BF16>(xb);
 }
 
-template <bool BF16, int MODE>
-__global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRopeArgs a) {
+// MIXED: H is not a multiple of the rows of a step, and the value rows fill up the last key step: 62
+// us against 74 with key and value rows in steps of their own (32,764 tokens, one KV head of 128, fp16,
+// 4over6), 142 against 155 (six). Where steps are full, choosing by lane would cost: 184 against 162
+// (eight heads, bf16). Five CTAs to an SM serve the standard recipe's mixed steps (62 against 68 us);
+// the same cap costs the others (66 against 62).
+template <bool BF16, int MODE, bool MIXED>
+__global__ void __launch_bounds__(kThreads, MIXED && MODE == 0 ? 5 : 0) norm_rope_append_kernel(const NormRopeArgs a) {
   __shared__ Tables tab;
   __shared__ __align__(16) uint4 s_rows[kThreads / 32][64];  // a warp's rows, as groups of eight
   float gs[2];
@@ -141,18 +146,19 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
   turn.turns = j < nr;
   turn.ga = j < nt ? (j < nr ? j : 2 * j) : 0;
   turn.gb = j < nt ? (j < nr ? j + nr : 2 * j + 1) : 0;
+  const int32_t k_end = a.q_steps + (H + per_step - 1) / per_step;  // steps from here on have value rows only
   const int64_t items = a.ap.nnz * a.parts;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp; item < items;
        item += static_cast<int64_t>(gridDim.x) * (kThreads / 32)) {
     const int64_t i = div_q(item, a.div_parts);
     const int32_t from = static_cast<int32_t>(item - i * a.parts) * a.steps_per_part;
-    const int32_t to = min(from + a.steps_per_part, a.q_steps + 2 * a.kv_steps);
+    const int32_t to = min(from + a.steps_per_part, a.q_steps + a.kv_steps);
     const int32_t pos = __ldg(a.ap.positions + i);
     if (nr > 0 && (pos < 0 || pos >= a.num_positions)) {
       if (lane == 0) flag(a.ap.status, NVFP4_DEV_BAD_POSITION);
       continue;
     }
-    if (turn.turns && from < a.q_steps + a.kv_steps) {
+    if (turn.turns && from < k_end) {
       const float* cs = a.cos_sin + static_cast<int64_t>(pos) * a.rotary_dim;
       const float* sn = cs + a.rotary_dim / 2;
       const int ca = a.interleaved ? 4 * turn.ga : 8 * j, cb = a.interleaved ? 4 * turn.gb : 8 * j + 4;
@@ -198,39 +204,53 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
     if (to <= a.q_steps) continue;
     const RowMeta m = resolve_row(a.ap, i);
     uint4 wa{}, wb{};
-    if (a.k_weight && from < a.q_steps + a.kv_steps) {
+    if (a.k_weight && from < k_end) {
       wa = __ldg(reinterpret_cast<const uint4*>(a.k_weight) + turn.ga);
       wb = __ldg(reinterpret_cast<const uint4*>(a.k_weight) + turn.gb);
     }
 #pragma unroll 1
     for (int32_t step = max(from, a.q_steps); step < to; ++step) {
-      const int kv = step >= a.q_steps + a.kv_steps;
-      const int32_t h = (step - a.q_steps - kv * a.kv_steps) * per_step + slot_in_step;
-      const bool live = h < H && j < nt;
+      const int32_t w0 = (step - a.q_steps) * per_step, w = w0 + slot_in_step;  // the K rows, then the V rows
+      const int kv = (MIXED ? w : w0) >= H;
+      const int32_t h = w - kv * H;
+      const bool live = (!MIXED || w < 2 * H) && j < nt;
       const uint8_t* src = (kv ? a.ap.v + i * a.ap.v_row_bytes : a.ap.k + i * a.ap.k_row_bytes) + h * row;
       uint4 lo{}, hi{};
-      if (kv) {
+      auto load = [&](int ga, int gb) {
         if (live) {
-          lo = reinterpret_cast<const uint4*>(src)[2 * j];
-          hi = reinterpret_cast<const uint4*>(src)[2 * j + 1];
+          lo = reinterpret_cast<const uint4*>(src)[ga];
+          hi = reinterpret_cast<const uint4*>(src)[gb];
         }
-      } else {
-        if (live) {
-          lo = reinterpret_cast<const uint4*>(src)[turn.ga];
-          hi = reinterpret_cast<const uint4*>(src)[turn.gb];
-        }
-        norm_rope<BF16>(a, turn, wa, wb, a.k_weight != nullptr, T, lo, hi);
+      };
+      auto norm_key = [&](uint4& ya, uint4& yb) {
+        norm_rope<BF16>(a, turn, wa, wb, a.k_weight != nullptr, T, ya, yb);
         if (nr > 0) {  // groups back into blocks
           uint4* buf = s_rows[warp] + (lane - j) * 2;
           __syncwarp();
           if (j < nt) {
-            buf[turn.ga] = lo;
-            buf[turn.gb] = hi;
+            buf[turn.ga] = ya;
+            buf[turn.gb] = yb;
           }
           __syncwarp();
-          lo = buf[2 * j];
-          hi = buf[2 * j + 1];
+          ya = buf[2 * j];
+          yb = buf[2 * j + 1];
         }
+      };
+      if constexpr (MIXED) {
+        load(kv ? 2 * j : turn.ga, kv ? 2 * j + 1 : turn.gb);
+        if (step < k_end) {
+          uint4 ya = lo, yb = hi;
+          norm_key(ya, yb);
+          if (!kv) {
+            lo = ya;
+            hi = yb;
+          }
+        }
+      } else if (kv) {
+        load(2 * j, 2 * j + 1);
+      } else {
+        load(turn.ga, turn.gb);
+        norm_key(lo, hi);
       }
       if (live && (m.flags & (1 << kv))) {
         U32x8 in;
@@ -251,17 +271,18 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
 
 template <bool BF16, int MODE>
 nvfp4_status launch_t(NormRopeArgs a, cudaStream_t stream) {
-  const auto kern = norm_rope_append_kernel<BF16, MODE>;
+  const int per_step = 32 >> a.log2_T;
+  const auto kern = a.ap.H % per_step != 0 ? norm_rope_append_kernel<BF16, MODE, true>
+                                           : norm_rope_append_kernel<BF16, MODE, false>;
   int64_t cap;
   if (nvfp4_status st = resident_ctas(reinterpret_cast<const void*>(kern), kThreads, 0, 32,
                                       "nvfp4_qk_norm_rope_append_paged", &cap))
     return st;
-  const int per_step = 32 >> a.log2_T;
   a.q_steps = (a.Hq + per_step - 1) / per_step;
-  a.kv_steps = (a.ap.H + per_step - 1) / per_step;
+  a.kv_steps = (2 * a.ap.H + per_step - 1) / per_step;
   // parts of a token: enough that the warps of one wave have an item each
   const int64_t warps = cap * (kThreads / 32);
-  const int32_t steps = a.q_steps + 2 * a.kv_steps;
+  const int32_t steps = a.q_steps + a.kv_steps;
   const int64_t wanted = (warps + a.ap.nnz - 1) / a.ap.nnz;
   a.parts = static_cast<int32_t>(wanted < steps ? wanted : steps);
   a.steps_per_part = (steps + a.parts - 1) / a.parts;

@@ -117,9 +117,26 @@ CASES = [
 ]
 
 
+MANY = [  # a warp for all rows of a token; key and value rows in one step, or in steps of their own
+    (18, 3500, 6, 3, 64, 16, R.NHD, torch.bfloat16, 64),
+    (19, 3300, 3, 1, 128, 16, R.HND, torch.float16, 128, True, (256.0, 0, 0)),
+    (20, 3300, 2, 6, 128, 32, R.NHD, torch.bfloat16, 64, False, (256.0, 1, 1)),
+    (21, 3300, 4, 4, 128, 16, R.HND, torch.bfloat16, 128),
+]
+
+
 @pytest.mark.parametrize("i", range(len(CASES)))
 def test_same_bytes_as_norm_rotation_then_append(gpu_lib, i):
     case = Case(*CASES[i])
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got, caches = case.call(gpu_lib, status=st)
+    assert int(st.item()) == 0
+    _same(case, got, caches, case.expect())
+
+
+@pytest.mark.parametrize("i", range(len(MANY)))
+def test_many_tokens(gpu_lib, i):
+    case = Case(*MANY[i], B=20)
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
     got, caches = case.call(gpu_lib, status=st)
     assert int(st.item()) == 0
