@@ -532,14 +532,17 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
   // -- the consumer --
   const int t0 = token_of(r);                    // this lane's K rows: t0 and t0 + 8
   const int v0 = token_of(2 * c), v1 = token_of(2 * c + 1);  // its V rows, and 8 more
-  // factors of the four parts and the joined maximum and sum, by the first threads
-  auto join_stats = [&] {
+  // factors of the `parts` parts and the joined maximum and sum, by the first threads (what lies past the
+  // parts is of another segment: a NaN there must not get into the sum, not even with a factor of 0)
+  auto join_stats = [&](int parts) {
     if (tid < kHeads) {
       float M = -INFINITY, L = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][tid]);
+      for (int w = 0; w < kWarps; ++w)
+        if (w < parts) M = fmaxf(M, s_m[w][tid]);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
+        if (w >= parts) break;
         const float f = s_m[w][tid] == -INFINITY ? 0.0f : ex2(s_m[w][tid] - M);
         s_f[w][tid] = f;
         L += f * s_l[w][tid];
@@ -549,21 +552,21 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
     }
     __syncthreads();
   };
-  auto joined = [&](int head, int d) {
+  auto joined = [&](int head, int d, int parts) {
     float4 v{0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
+      if (w >= parts) break;
       const float f = s_f[w][head];
-      if (f == 0.0f) continue;  // (a part without weights may hold anything)
       const float4 x = *reinterpret_cast<const float4*>(s_o + (w * kHeads + head) * kPitch + d);
       v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
     }
     return v;
   };
-  auto write_out = [&](int64_t row, int heads) {
+  auto write_out = [&](int64_t row, int heads, int parts) {
     for (int i = tid; i < heads * D / 4; i += kThreads) {
       const int head = i / (D / 4), d = i % (D / 4) * 4;
-      const float4 v = joined(head, d);
+      const float4 v = joined(head, d, parts);
       const float f = s_sum[head] == 0.0f ? 0.0f : gv / s_sum[head];
       uint2 w;
       w.x = a.bf16 ? bf16x2_from_f32(v.x * f, v.y * f) : f16x2_from_f32(v.x * f, v.y * f);
@@ -861,9 +864,9 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
         }
       }
     __syncthreads();
-    join_stats();
+    join_stats(kWarps);
     if (whole) {
-      write_out(static_cast<int64_t>(done.b) * a.Hq + q_row, heads);
+      write_out(static_cast<int64_t>(done.b) * a.Hq + q_row, heads, kWarps);
     } else {
       // this run's part of a segment that others share: the last of them will join the parts, at its
       // end, so that nobody waits here for the count (a run shares at most its first and its last)
@@ -873,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
       float* part = part_of(blockIdx.x, first);
       for (int i = tid; i < heads * D / 4; i += kThreads) {
         const int head = i / (D / 4), d = i % (D / 4) * 4;
-        __stcg(reinterpret_cast<float4*>(part + head * (64 * NW) + d), joined(head, d));
+        __stcg(reinterpret_cast<float4*>(part + head * (64 * NW) + d), joined(head, d, kWarps));
       }
       if (tid < heads) {
         __stcg(part + kStats + tid, s_top[tid]);
@@ -951,10 +954,10 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
           s_l[team][head] = L;
         }
       }
-      if (teams == 1 && tid >= kHeads && tid < kWarps * kHeads) s_m[tid / kHeads][tid % kHeads] = -INFINITY;
       __syncthreads();
-      join_stats();
-      write_out(static_cast<int64_t>(s_shared[n].b) * a.Hq + static_cast<int64_t>(s_shared[n].h) * a.G + head0, heads);
+      join_stats(teams);
+      write_out(static_cast<int64_t>(s_shared[n].b) * a.Hq + static_cast<int64_t>(s_shared[n].h) * a.G + head0, heads,
+                teams);
       __syncthreads();
     }
   }
