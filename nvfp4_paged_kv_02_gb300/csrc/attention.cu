@@ -749,9 +749,9 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
             m2 = fmaxf(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 4));
             m2 = fmaxf(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 8));
             m2 = fmaxf(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 16));
-            m2 = fmaxf(m2, m[nt][k]);
-            const float f = m2 == -INFINITY ? 1.0f : ex2(m[nt][k] - m2);
-            m[nt][k] = m2;
+            const bool rises = m2 > m[nt][k] + kSlack;  // (by head: a result does not depend on other heads)
+            const float f = rises ? ex2(m[nt][k] - m2) : 1.0f;
+            m[nt][k] = rises ? m2 : m[nt][k];
             l[nt][k] *= f;
 #pragma unroll
             for (int w = 0; w < NW; ++w)
