@@ -542,7 +542,9 @@ nvfp4_status nvfp4_paged_attention_workspace_bytes(int32_t num_qo_heads, int32_t
  *   out = v_scale * sum_t exp(x_t) V[t, :] / sum_t exp(x_t),   lse = log sum_t exp(x_t)
  * Live are the positions t < seq_lens[b]; with window_left >= 0 only those with
  * t >= seq_lens[b] - 1 - window_left. Positions on a page outside the pool are left out
- * (NVFP4_DEV_BAD_PAGE). A request with no live position gets out = 0 and lse = -inf. What the
+ * (NVFP4_DEV_BAD_PAGE). A request with no live position gets out = 0 and lse = -inf, and so does
+ * a query head whose live scores are all -inf (an infinite query). NaN in a query head or in a
+ * live block scale shows in the outputs that the formula has it in, and in no others. What the
  * slots past a request's end hold is of no consequence. The new token's own key and value are
  * in the cache already (append first).
  * Scores and sums are binary32; K and V are exact; a weight exp(x_t - m) is rounded to

@@ -936,14 +936,16 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
           }
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) top = fmaxf(top, mi[k]);
-          if (top == -INFINITY) continue;  // (parts without weights: zeros)
-          const float f = ex2(M - top);
+          // Nothing above -inf so far: the parts hold zeros, or NaN where every score was NaN, which has to
+          // stay in the sums; a later maximum multiplies them by 0.
+          const bool none = top == -INFINITY;
+          const float f = none ? 1.0f : ex2(M - top);
           M = top;
           L *= f;
           v.x *= f; v.y *= f; v.z *= f; v.w *= f;
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
-            const float g = ex2(mi[k] - top);
+            const float g = none ? 1.0f : ex2(mi[k] - top);
             L += g * li[k];
             v.x += g * x[k].x; v.y += g * x[k].y; v.z += g * x[k].z; v.w += g * x[k].w;
           }

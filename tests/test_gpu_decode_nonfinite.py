@@ -64,3 +64,57 @@ def test_nan_in_the_last_list_of_a_run_that_joins_another(gpu_lib, D):
     for _ in range(5):
         out, lse, _ = _run(gpu_lib, c, q, dev)
         assert torch.equal(out[~bad], want[0][~bad]) and torch.equal(lse[~bad], want[1][~bad])
+
+
+@pytest.mark.parametrize("name", SHAPES)
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_nan_and_infinite_queries_show(gpu_lib, name, value):
+    """One query head of every second request: NaN, or an infinity (its scores are infinite or NaN, and
+    the largest less itself is NaN), at every length."""
+    c, q = _case(name)
+    dev = _dev(c)
+    want = _run(gpu_lib, c, q, dev)
+    q2 = q.clone()
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool, device=DEV)
+    for b in range(0, c.B, 2):
+        if value == value and c.lens[b] < 32:
+            continue  # (few keys: all of an infinite query's scores may be -inf)
+        q2[b, b % q.shape[1], 5] = value
+        hit[b, b % q.shape[1]] = True
+    out, lse, _ = _run(gpu_lib, c, q2, dev)
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(out[~hit], want[0][~hit]) and torch.equal(lse[~hit], want[1][~hit])
+
+
+def test_nan_queries_at_every_length(gpu_lib):
+    for n in (1, 31, 300, 385, 3000, 100000):
+        c = R.make_paged(n, [n], 1, 64, 16, R.NHD)
+        q = _query(n, 1, G, 64, torch.bfloat16).to(DEV)
+        q[0, 1] = float("nan")
+        out, lse, _ = _run(gpu_lib, c, q)
+        nan = torch.tensor([False, True, False, False], device=DEV)
+        assert torch.equal(torch.isnan(lse[0]), nan), n
+        assert torch.equal(torch.isnan(out[0]).all(-1), nan) and torch.equal(torch.isnan(out[0]).any(-1), nan), n
+
+
+@pytest.mark.parametrize("name", SHAPES)
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_nan_scales_show_where_they_are(gpu_lib, name, which):
+    """A NaN block scale of a live key: every query head of its KV head. Of a live value: the block's 16
+    elements of those heads' outputs, and no log-sum-exp."""
+    c, q = _case(name)
+    want = _run(gpu_lib, c, q)
+    out_nan = torch.zeros((c.B, c.H * G, c.D), dtype=torch.bool, device=DEV)
+    lse_nan = torch.zeros((c.B, c.H * G), dtype=torch.bool, device=DEV)
+    rng = np.random.Generator(np.random.PCG64(1))
+    for b in range(0, c.B, 2):
+        h, t, j = (int(rng.integers(0, n)) for n in (c.H, c.lens[b], c.D // 16))
+        (c.ks if which == "k" else c.vs)[c.tables[b, t // c.ps], h, t % c.ps, j] = 0x7F
+        heads = slice(h * G, (h + 1) * G)
+        if which == "k":
+            out_nan[b, heads], lse_nan[b, heads] = True, True
+        else:
+            out_nan[b, heads, 16 * j: 16 * j + 16] = True
+    out, lse, _ = _run(gpu_lib, c, q)
+    assert torch.equal(torch.isnan(out), out_nan) and torch.equal(torch.isnan(lse), lse_nan)
+    assert torch.equal(out[~out_nan], want[0][~out_nan]) and torch.equal(lse[~lse_nan], want[1][~lse_nan])
