@@ -486,7 +486,7 @@ nvfp4_status nvfp4_qk_norm_rope_append_paged(
  *                    contiguous, 16-byte aligned.
  *   dev_status       NVFP4_DEV_TIMEOUT besides the others, if a wait of the bulk-copy ring gave up.
  *   The other arguments are those of nvfp4_dequantize_paged.
- * Requirements: batch_size * max_pages_per_request at most 2^31 - 1. */
+ * Requirements: batch_size at most 16384, batch_size * max_pages_per_request at most 2^31 - 1. */
 nvfp4_status nvfp4_page_key_bounds(nvfp4_paged_cache k_cache, int32_t page_size,
                                    int32_t num_kv_heads, int32_t head_dim, int32_t kv_layout,
                                    const void* block_tables, int32_t table_dtype,
@@ -519,7 +519,7 @@ nvfp4_status nvfp4_select_pages_workspace_bytes(int32_t batch_size, int32_t num_
  *   workspace      device, workspace_bytes >= nvfp4_select_pages_workspace_bytes, 16-byte
  *                  aligned; holds anything; one call at a time.
  * Requirements: num_qo_heads a multiple of num_kv_heads, head_dim a multiple of 16 and at most
- * 256, max_selected >= 1, num_sink_pages, num_recent_pages >= 0. */
+ * 256, batch_size at most 16384, max_selected >= 1, num_sink_pages, num_recent_pages >= 0. */
 nvfp4_status nvfp4_select_pages(const void* query, int32_t dtype, int64_t query_row_stride,
                                 int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
                                 const void* key_bounds, int64_t num_pages, int32_t page_size,
@@ -560,7 +560,7 @@ nvfp4_status nvfp4_paged_attention_workspace_bytes(int32_t num_qo_heads, int32_t
  *                 One call at a time (as the work-distribution workspace).
  *   The other arguments are those of nvfp4_dequantize_paged.
  * Requirements: num_qo_heads a multiple of num_kv_heads, head_dim a multiple of 16 and at most
- * 256, sm_scale finite, logits_soft_cap finite and >= 0. */
+ * 256, batch_size at most 16384, sm_scale finite, logits_soft_cap finite and >= 0. */
 nvfp4_status nvfp4_paged_attention_decode(
     const void* query, int32_t dtype, int64_t query_row_stride, int32_t num_qo_heads,
     nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache, int32_t page_size,

@@ -55,6 +55,7 @@ constexpr int kTiles = kUnit / 16;  // of 16 tokens
 constexpr int kMinUnits = 4;  // of a CTA's run: one for each warp
 constexpr int kMaxCtasPerSm = 4;
 constexpr int kSegmentCost = 9;
+constexpr size_t kMostSmem = 224 * 1024;  // dynamic; the CTA's limit less its static arrays
 // A segment of so few units is the run's that it begins in: cutting it costs a join (3 us) and saves
 // less. 512 lists of 64 to 400 tokens: 15.2 us (8: 17.2), of 384: 19.3 (20.7); one request of 500
 // tokens (16 units): 9.9 us cut (16: 10.4), 32 lists of 512: 11.2 (12.7).
@@ -144,15 +145,18 @@ __device__ __forceinline__ int64_t places_of_request(const AttentionArgs& a, int
   return n * a.chunks;
 }
 
-// cum[b] = places of the requests up to b; every thread calls it, ends with a barrier.
+__host__ __device__ __forceinline__ int32_t entries(const AttentionArgs& a) { return (a.B + a.group - 1) / a.group; }
+
+// cum[e] = places of the requests up to the end of group e (a.group requests, in order); every thread
+// calls it, ends with a barrier.
 __device__ __forceinline__ void scan_places(const AttentionArgs& a, int64_t* cum, int64_t* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int lo = tid * per, hi = min(a.B, lo + per);
+  const int n = entries(a), per = (n + kThreads - 1) / kThreads;
+  const int lo = tid * per, hi = min(n, lo + per);
   int64_t local = 0;
-  for (int b = lo; b < hi; ++b) {
-    local += places_of_request(a, b);
-    cum[b] = local;
+  for (int e = lo; e < hi; ++e) {
+    for (int b = e * a.group; b < min(a.B, (e + 1) * a.group); ++b) local += places_of_request(a, b);
+    cum[e] = local;
   }
   int64_t v = local;
 #pragma unroll
@@ -164,7 +168,7 @@ __device__ __forceinline__ void scan_places(const AttentionArgs& a, int64_t* cum
   __syncthreads();
   int64_t before = v - local;
   for (int w = 0; w < warp; ++w) before += s_warp[w];
-  for (int b = lo; b < hi; ++b) cum[b] += before;
+  for (int e = lo; e < hi; ++e) cum[e] += before;
   __syncthreads();
 }
 
@@ -191,14 +195,17 @@ struct Segment {
 };
 
 __device__ __forceinline__ Segment find_segment(const AttentionArgs& a, const int64_t* cum, int64_t place) {
-  int32_t lo = 0, hi = a.B - 1;
+  int32_t lo = 0, hi = entries(a) - 1;
   while (lo < hi) {
     const int32_t mid = (lo + hi) >> 1;
     if (cum[mid] > place) hi = mid;
     else lo = mid + 1;
   }
-  Segment s{lo, 0, 0, 0, 0};
+  Segment s{lo * a.group, 0, 0, 0, 0};
   int64_t start = lo > 0 ? cum[lo - 1] : 0;
+  if (a.group > 1) {  // the request in its group
+    for (int64_t n; place >= start + (n = places_of_request(a, s.b)); ++s.b) start += n;
+  }
   s.units = units_of(a, s.b, 0);
   if (a.selected) {
     for (;;) {
@@ -315,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
       }
     }
   };
-  const int64_t total = cum[a.B - 1];
+  const int64_t total = cum[entries(a) - 1];
   const int64_t want = (total + kMinUnits - 1) / kMinUnits;
   const int64_t ncta = want < gridDim.x ? want : gridDim.x;
   if (blockIdx.x >= ncta) {
@@ -967,10 +974,14 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
 }
 
 template <int NW, int NT, bool FULL>
-nvfp4_status launch_t(const AttentionArgs& a, cudaStream_t stream) {
+nvfp4_status launch_t(AttentionArgs a, cudaStream_t stream) {
   const auto kern = attention_kernel<NW, NT, FULL>;
-  const size_t smem = kWarps * kStages * Tile<NW>::kBytes + kWarps * 8 * NT * (64 * NW + 4) * 4 +
-                      static_cast<size_t>(a.B) * 8;
+  const size_t fixed = kWarps * kStages * Tile<NW>::kBytes + kWarps * 8 * NT * (64 * NW + 4) * 4;
+  // an entry of the scan for each request; where they do not fit (above some 10,600 requests with head_dim
+  // above 192, 15,100 above 128), for two
+  a.group = 1;
+  while (fixed + entries(a) * 8 > kMostSmem) a.group *= 2;
+  const size_t smem = fixed + static_cast<size_t>(entries(a)) * 8;
   int64_t cap;
   if (nvfp4_status st = resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem, kMaxCtasPerSm,
                                       "nvfp4_paged_attention_decode", &cap))
