@@ -519,7 +519,8 @@ nvfp4_status nvfp4_select_pages_workspace_bytes(int32_t batch_size, int32_t num_
  *   workspace      device, workspace_bytes >= nvfp4_select_pages_workspace_bytes, 16-byte
  *                  aligned; holds anything; one call at a time.
  * Requirements: num_qo_heads a multiple of num_kv_heads, head_dim a multiple of 16 and at most
- * 256, batch_size at most 16384, max_selected >= 1, num_sink_pages, num_recent_pages >= 0. */
+ * 256, batch_size at most 16384, max_pages_per_request at most 2^30 and batch_size times an
+ * eighth of it at most 2^31 - 1, max_selected >= 1, num_sink_pages, num_recent_pages >= 0. */
 nvfp4_status nvfp4_select_pages(const void* query, int32_t dtype, int64_t query_row_stride,
                                 int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
                                 const void* key_bounds, int64_t num_pages, int32_t page_size,

@@ -784,6 +784,15 @@ nvfp4_status check_tables(const std::string& f, int32_t table_dtype, int32_t max
   return NVFP4_OK;
 }
 
+// The selection counts lists, groups of eight pages and a request's pages in 32 bits, its workspace's bytes in 64.
+nvfp4_status check_select_size(const std::string& f, int64_t batch_size, int64_t H, int64_t max_pages) {
+  if (batch_size * H > INT32_MAX) return fail(NVFP4_ERR_UNSUPPORTED, f + ": more than 2^31 - 1 lists");
+  if (max_pages > (int64_t(1) << 30)) return fail(NVFP4_ERR_UNSUPPORTED, f + ": max_pages_per_request above 2^30");
+  if (batch_size * ((max_pages + 7) / 8) > INT32_MAX || batch_size * H > (int64_t(1) << 60) / (max_pages + 8))
+    return fail(NVFP4_ERR_UNSUPPORTED, f + ": batch_size * max_pages_per_request is too large");
+  return NVFP4_OK;
+}
+
 nvfp4_status check_rows(const std::string& f, const char* name, const void* p, int64_t stride,
                         int64_t row) {
   if (!p) return fail(NVFP4_ERR_INVALID_ARG, f + ": " + name + " is null");
@@ -942,6 +951,9 @@ NVFP4_EXPORT nvfp4_status nvfp4_select_pages_workspace_bytes(int32_t batch_size,
   return guarded([&]() -> nvfp4_status {
     if (batch_size < 0 || num_kv_heads < 1 || max_pages_per_request < 0 || !bytes)
       return fail(NVFP4_ERR_INVALID_ARG, "nvfp4_select_pages_workspace_bytes: bad size or null output pointer");
+    if (nvfp4_status st = check_select_size("nvfp4_select_pages_workspace_bytes", batch_size, num_kv_heads,
+                                            max_pages_per_request))
+      return st;
     *bytes = select_workspace_bytes(batch_size, num_kv_heads, max_pages_per_request);
     return NVFP4_OK;
   });
@@ -966,8 +978,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_select_pages(
     if (max_selected < 1) return fail(NVFP4_ERR_INVALID_ARG, f + ": max_selected must be >= 1");
     if (num_pages < 0 || num_sink_pages < 0 || num_recent_pages < 0)
       return fail(NVFP4_ERR_INVALID_ARG, f + ": negative size");
-    if (static_cast<int64_t>(batch_size) * num_kv_heads > INT32_MAX)
-      return fail(NVFP4_ERR_UNSUPPORTED, f + ": more than 2^31 - 1 lists");
+    if (nvfp4_status st = check_select_size(f, batch_size, num_kv_heads, max_pages_per_request)) return st;
     if (batch_size == 0) return NVFP4_OK;
     if (nvfp4_status st = check_rows(f, "query", query, query_row_stride,
                                      static_cast<int64_t>(num_qo_heads) * head_dim)) return st;

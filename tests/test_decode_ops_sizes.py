@@ -1,0 +1,39 @@
+"""Sizes whose counters inside the kernels would pass 32 bits are refused on the host (CPU: nothing is
+launched, the addresses are made up)."""
+import ctypes
+
+import pytest
+
+import nvfp4_paged_kv_02_gb300 as nv
+from tests.test_decode_ops_refusals import UNS, attend, err, select
+
+TABLE = 2 ** 31 - 1
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return nv.load()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=1, maxp=TABLE),                       # a request's pages and a pass over them
+    dict(B=1, maxp=2 ** 30 + 1),
+    dict(B=16384, maxp=2 ** 20 + 1),             # groups of eight pages of all requests
+    dict(B=17, maxp=2 ** 30),
+    dict(B=16, maxp=2 ** 30),
+])
+def test_select_refuses_what_it_cannot_count(lib, kw):
+    bytes_ = ctypes.c_int64(-1)
+    assert select(lib, wsb=2 ** 62, **kw) == UNS
+    assert "max_pages_per_request" in err(lib)
+    assert lib.nvfp4_select_pages_workspace_bytes(kw["B"], 8, kw["maxp"], ctypes.byref(bytes_)) == UNS
+    assert bytes_.value == -1
+
+
+def test_select_workspace_bytes_do_not_wrap(lib):
+    n = ctypes.c_int64(-1)
+    assert lib.nvfp4_select_pages_workspace_bytes(1, 2 ** 31 - 1, 2 ** 30, ctypes.byref(n)) == UNS and n.value == -1
+    assert lib.nvfp4_select_pages_workspace_bytes(2 ** 31 - 1, 2, 8, ctypes.byref(n)) == UNS
+    assert lib.nvfp4_select_pages_workspace_bytes(1, 2 ** 26, 2 ** 30, ctypes.byref(n)) == nv.OK
+    assert n.value == 2 ** 58
+    assert lib.nvfp4_select_pages_workspace_bytes(15, 8, 2 ** 30, ctypes.byref(n)) == nv.OK
