@@ -1061,6 +1061,11 @@ nvfp4_status attention_impl(
   if (nvfp4_status st = check_cache(fn, "k_cache", k_cache, page_size, num_kv_heads, head_dim)) return st;
   if (nvfp4_status st = check_cache(fn, "v_cache", v_cache, page_size, num_kv_heads, head_dim)) return st;
   if (batch_size == 0) return NVFP4_OK;
+  // A CTA counts its places (units of 32 tokens and nine more of each list) in 32 bits.
+  const int64_t reach = sparse ? static_cast<int64_t>(max_selected) * page_size
+                               : static_cast<int64_t>(max_pages) * page_size;
+  if (reach / 32 + 10 > (int64_t(1) << 38) / (static_cast<int64_t>(batch_size) * num_qo_heads))
+    return fail(NVFP4_ERR_UNSUPPORTED, f + ": batch_size * num_qo_heads * positions above 2^43");
   const int64_t row = static_cast<int64_t>(num_qo_heads) * head_dim;
   if (nvfp4_status st = check_rows(f, "query", query, query_row_stride, row)) return st;
   if (nvfp4_status st = check_rows(f, "out", out, row, row)) return st;

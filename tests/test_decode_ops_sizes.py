@@ -37,3 +37,17 @@ def test_select_workspace_bytes_do_not_wrap(lib):
     assert lib.nvfp4_select_pages_workspace_bytes(1, 2 ** 26, 2 ** 30, ctypes.byref(n)) == nv.OK
     assert n.value == 2 ** 58
     assert lib.nvfp4_select_pages_workspace_bytes(15, 8, 2 ** 30, ctypes.byref(n)) == nv.OK
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=16384, maxp=TABLE), dict(B=16384, maxp=2 ** 20), dict(B=16384, S=2 ** 24, sel=1 << 20),
+])
+def test_attention_refuses_what_it_cannot_count(lib, kw):
+    assert attend(lib, **kw) == UNS
+    assert "2^43" in err(lib)
+
+
+def test_attention_counts_every_list_of_a_wide_batch(lib):
+    # below the limit the next check answers (here: no query)
+    assert attend(lib, q=None, B=16384, maxp=2 ** 19 - 2 ** 10) == nv.ERR_INVALID_ARG and "query" in err(lib)
+    assert attend(lib, q=None, B=1, maxp=TABLE) == nv.ERR_INVALID_ARG and "query" in err(lib)
