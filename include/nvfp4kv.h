@@ -478,8 +478,9 @@ nvfp4_status nvfp4_qk_norm_rope_append_paged(
  * position of [first_positions[b], seq_lens[b]), with its physical page p and its live slots
  * t (positions below seq_lens[b]):
  *   key_bounds[p, h, 0, d] = min_t e2m1 * S,   key_bounds[p, h, 1, d] = max_t e2m1 * S
- * (exact in binary16; the global scale, a positive factor, is left out). Slots past a
- * request's end are not read into the bounds, whatever they hold.
+ * (exact in binary16; the global scale, a positive factor, is left out). A NaN block scale of a
+ * live slot makes the 16 bounds of its block NaN. Slots past a request's end are not read into
+ * the bounds, whatever they hold.
  *   first_positions  device int32 [batch_size], or NULL: all pages. A decode step passes the
  *                    positions that it has written, and one page of each request is redone.
  *   key_bounds       device float16 [k_cache.num_pages, num_kv_heads, 2, head_dim],

@@ -34,14 +34,15 @@ constexpr int kMaxBoundsStages = 4;
 // Shared memory of the ring: three CTAs to an SM, or what two stages of one larger page need.
 constexpr int64_t kBoundsRing = 72 * 1024, kBoundsMostRing = 160 * 1024;
 
+// (NaN if either is)
 __device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
