@@ -145,17 +145,16 @@ __device__ __forceinline__ int64_t places_of_request(const AttentionArgs& a, int
   return n * a.chunks;
 }
 
-__host__ __device__ __forceinline__ int32_t entries(const AttentionArgs& a) { return (a.B + a.group - 1) / a.group; }
-
-// cum[e] = places of the requests up to the end of group e (a.group requests, in order); every thread
-// calls it, ends with a barrier.
+// cum[e] = places of the requests up to the end of group e (of 1 << a.log2_group in order, a.groups of
+// them); every thread calls it, ends with a barrier.
 __device__ __forceinline__ void scan_places(const AttentionArgs& a, int64_t* cum, int64_t* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = entries(a), per = (n + kThreads - 1) / kThreads;
-  const int lo = tid * per, hi = min(n, lo + per);
+  const int per = (a.groups + kThreads - 1) / kThreads;
+  const int lo = tid * per, hi = min(a.groups, lo + per);
   int64_t local = 0;
   for (int e = lo; e < hi; ++e) {
-    for (int b = e * a.group; b < min(a.B, (e + 1) * a.group); ++b) local += places_of_request(a, b);
+    local += places_of_request(a, e << a.log2_group);
+    for (int b = (e << a.log2_group) + 1; b < min(a.B, (e + 1) << a.log2_group); ++b) local += places_of_request(a, b);
     cum[e] = local;
   }
   int64_t v = local;
@@ -195,15 +194,15 @@ struct Segment {
 };
 
 __device__ __forceinline__ Segment find_segment(const AttentionArgs& a, const int64_t* cum, int64_t place) {
-  int32_t lo = 0, hi = entries(a) - 1;
+  int32_t lo = 0, hi = a.groups - 1;
   while (lo < hi) {
     const int32_t mid = (lo + hi) >> 1;
     if (cum[mid] > place) hi = mid;
     else lo = mid + 1;
   }
-  Segment s{lo * a.group, 0, 0, 0, 0};
+  Segment s{lo << a.log2_group, 0, 0, 0, 0};
   int64_t start = lo > 0 ? cum[lo - 1] : 0;
-  if (a.group > 1) {  // the request in its group
+  if (a.log2_group > 0) {  // the request in its group
     for (int64_t n; place >= start + (n = places_of_request(a, s.b)); ++s.b) start += n;
   }
   s.units = units_of(a, s.b, 0);
@@ -322,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
       }
     }
   };
-  const int64_t total = cum[entries(a) - 1];
+  const int64_t total = cum[a.groups - 1];
   const int64_t want = (total + kMinUnits - 1) / kMinUnits;
   const int64_t ncta = want < gridDim.x ? want : gridDim.x;
   if (blockIdx.x >= ncta) {
@@ -979,9 +978,9 @@ nvfp4_status launch_t(AttentionArgs a, cudaStream_t stream) {
   const size_t fixed = kWarps * kStages * Tile<NW>::kBytes + kWarps * 8 * NT * (64 * NW + 4) * 4;
   // an entry of the scan for each request; where they do not fit (above some 10,600 requests with head_dim
   // above 192, 15,100 above 128), for two
-  a.group = 1;
-  while (fixed + entries(a) * 8 > kMostSmem) a.group *= 2;
-  const size_t smem = fixed + static_cast<size_t>(entries(a)) * 8;
+  a.groups = a.B;
+  while (fixed + static_cast<size_t>(a.groups) * 8 > kMostSmem) a.groups = (a.B + (1 << ++a.log2_group) - 1) >> a.log2_group;
+  const size_t smem = fixed + static_cast<size_t>(a.groups) * 8;
   int64_t cap;
   if (nvfp4_status st = resident_ctas(reinterpret_cast<const void*>(kern), kThreads, smem, kMaxCtasPerSm,
                                       "nvfp4_paged_attention_decode", &cap))

@@ -35,7 +35,7 @@ struct AttentionArgs {
   uint32_t pool_pages;          // pages that both caches have
   uint32_t k_stride, v_stride, k_sf_stride, v_sf_stride;  // page strides, bytes
   int32_t compact;
-  int32_t group;  // requests to an entry of the scan
+  int32_t groups, log2_group;  // entries of the scan, and the requests to one
 };
 // Device memory that a launch needs, whatever the lengths.
 int64_t attention_workspace_bytes(int32_t Hq, int32_t H, int32_t D);
