@@ -509,7 +509,8 @@ nvfp4_status nvfp4_select_pages_workspace_bytes(int32_t batch_size, int32_t num_
  * The score's products are exact in binary32; its sum runs in a fixed order, so the selection
  * is reproducible: in groups of eight, ((p0 + p2) + p4) + p6 and ((p1 + p3) + p5) + p7, the two
  * added; the D/8 group sums, filled up with zeros to a power of two n, t[i] += t[i + n/2], ....
- * A page whose table entry is outside the pool is reported (NVFP4_DEV_BAD_PAGE) and comes last.
+ * A page whose table entry is outside the pool is reported (NVFP4_DEV_BAD_PAGE) and comes last,
+ * forced or not.
  * Infinities and NaN in the query or the bounds are out of contract.
  *   query          device, rows of num_qo_heads heads of head_dim elements of dtype,
  *                  query_row_stride elements apart; 16-byte aligned, stride a multiple of 8.

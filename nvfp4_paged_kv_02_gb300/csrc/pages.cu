@@ -561,9 +561,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32, GC == 4 ? 3 : 2) page_scores
         const int p = (sub >> 2) * kPages + group;
         const int32_t j = (first + unit) * kUnitPages + p;
         if ((lane & 3) == 0 && j < n) {
-          uint32_t key = key_of(bad >> (kAhead * kUnitPages + p) & 1u ? -INFINITY : best);
+          const bool outside = bad >> (kAhead * kUnitPages + p) & 1u;
+          uint32_t key = key_of(outside ? -INFINITY : best);
           if (g0 > 0) key = max(key, keys[j]);
-          if (j < a.sink || j >= n - a.recent) key = kForced;
+          if (!outside && (j < a.sink || j >= n - a.recent)) key = kForced;
           keys[j] = key;
         }
       }
