@@ -480,7 +480,10 @@ nvfp4_status nvfp4_qk_norm_rope_append_paged(
  *   key_bounds[p, h, 0, d] = min_t e2m1 * S,   key_bounds[p, h, 1, d] = max_t e2m1 * S
  * (exact in binary16; the global scale, a positive factor, is left out). A NaN block scale of a
  * live slot makes the 16 bounds of its block NaN. Slots past a request's end are not read into
- * the bounds, whatever they hold.
+ * the bounds, whatever they hold. Requests may share pages whose slots are live for all of them
+ * (a common prompt's full pages). A page that is live up to different slots for two requests of
+ * one call gets the bounds of either, element by element: a page's last slots belong to one
+ * request, as for the append, which would write the next one.
  *   first_positions  device int32 [batch_size], or NULL: all pages. A decode step passes the
  *                    positions that it has written, and one page of each request is redone.
  *   key_bounds       device float16 [k_cache.num_pages, num_kv_heads, 2, head_dim],

@@ -676,7 +676,8 @@ def nvfp4_page_key_bounds(k_cache: torch.Tensor, k_block_scales: torch.Tensor,
                           kv_layout: str = "NHD", dev_status: Optional[torch.Tensor] = None) -> None:
     """Write the element-wise (min, max) of e2m1 * block_scale over the live slots of each request's
     pages into key_bounds [num_pages, H, 2, D] float16: the pages that hold a position from
-    first_positions on (None: all of them)."""
+    first_positions on (None: all of them). Requests may share full pages; a partly filled one belongs
+    to one request of a call."""
     _done("nvfp4_page_key_bounds", _calls().page_key_bounds(
         k_cache, k_block_scales, block_tables, seq_lens, key_bounds, first_positions, _layout(kv_layout),
         dev_status))
