@@ -119,7 +119,7 @@ def load() -> ctypes.CDLL:
     with _lock:
         if _lib is not None:
             return _lib
-        path = _build.build()
+        path = _build.build_library()
         L = ctypes.CDLL(path)
         vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
         L.nvfp4_abi_version.restype = i32
@@ -191,16 +191,18 @@ def load() -> ctypes.CDLL:
 
 
 def _calls():
-    """The module that carries the decode-step calls (built with the library)."""
+    """The module that carries the decode-step calls. Builds it if stale; the other operations do not need it."""
     global _calls_module
     if _calls_module is None:
         load()
         with _lock:
             if _calls_module is None:
-                loader = importlib.machinery.ExtensionFileLoader("nvfp4kv_calls", _build.CALLS_PATH)
-                _calls_module = importlib.util.module_from_spec(
-                    importlib.util.spec_from_file_location("nvfp4kv_calls", _build.CALLS_PATH, loader=loader))
-                loader.exec_module(_calls_module)
+                path = _build.build_calls()
+                loader = importlib.machinery.ExtensionFileLoader("nvfp4kv_calls", path)
+                module = importlib.util.module_from_spec(
+                    importlib.util.spec_from_file_location("nvfp4kv_calls", path, loader=loader))
+                loader.exec_module(module)
+                _calls_module = module
     return _calls_module
 
 

@@ -3,7 +3,8 @@ that carries the decode-step calls from torch tensors to the library (calls.cpp,
 
 Each translation unit under csrc/ is compiled in parallel, then linked into one shared
 library next to this file. A stamp of the sources and flags skips rebuilds when nothing
-changed.
+changed. The library needs nvcc alone (`python _build.py library`); the module has its own
+stamp, and its failure leaves the library in place.
 """
 
 from __future__ import annotations
@@ -58,61 +59,105 @@ def _calls_link(obj: str, out: str) -> list:
             f"-L{HERE}", "-l:" + os.path.basename(LIB_PATH), "-Wl,-rpath,$ORIGIN"]
 
 
-def _stamp() -> str:
-    import torch
+def _digest(names: list, *more: str) -> str:
     h = hashlib.sha256()
-    h.update(f"{torch.__version__} {sysconfig.get_python_version()}".encode())
-    for name in SOURCES + HEADERS + [CALLS_SOURCE]:
+    for name in names:
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode() + f.read())
     with open(os.path.join(ROOT, "include", "nvfp4kv.h"), "rb") as f:
         h.update(f.read())
-    h.update(" ".join(NVCC_FLAGS).encode())
+    h.update(" ".join(more).encode())
     return h.hexdigest()
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if stale) and return the path of libnvfp4kv.so."""
-    stamp = _stamp()
-    stamp_file = os.path.join(BUILD_DIR, "stamp")
-    if not force and os.path.exists(LIB_PATH) and os.path.exists(CALLS_PATH) and os.path.exists(stamp_file):
-        with open(stamp_file) as f:
-            if f.read() == stamp:
-                return LIB_PATH
+def _library_stamp() -> str:
+    return _digest(SOURCES + HEADERS, *NVCC_FLAGS)
+
+
+def _calls_stamp() -> str:
+    import torch
+    return _digest([CALLS_SOURCE], torch.__version__, sysconfig.get_python_version(), *_calls_command())
+
+
+def _is_current(path: str, stamp_file: str, stamp: str) -> bool:
+    if not (os.path.exists(path) and os.path.exists(stamp_file)):
+        return False
+    with open(stamp_file) as f:
+        return f.read() == stamp
+
+
+def _run(cmd: list, what: str, verbose: bool = False) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed on {what}:\n{r.stdout}\n{r.stderr}")
+    if verbose and r.stderr:
+        print(r.stderr)
+
+
+def _obj(src: str) -> str:
+    return os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
+
+
+def _put(path: str, tmp: str, stamp_file: str, stamp: str) -> None:
+    os.replace(tmp, path)
+    with open(stamp_file, "w") as f:
+        f.write(stamp)
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compile the C-ABI library (if stale) and return its path. It needs nvcc alone."""
+    stamp, stamp_file = _library_stamp(), os.path.join(BUILD_DIR, "stamp")
+    if not force and _is_current(LIB_PATH, stamp_file, stamp):
+        return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     exe = nvcc()
 
     def compile_one(src: str) -> str:
-        obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-        if src == CALLS_SOURCE:
-            cmd = [*_calls_command(), "-o", obj]
-        else:
-            cmd = [exe, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
-            if verbose:
-                cmd += ["-Xptxas", "-v"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{cmd[0]} failed on {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose and r.stderr:
-            print(r.stderr)
-        return obj
+        _run([exe, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", _obj(src),
+              *(["-Xptxas", "-v"] if verbose else [])], src, verbose)
+        return _obj(src)
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        *objs, calls = ex.map(compile_one, SOURCES + [CALLS_SOURCE])
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+        objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB_PATH + ".tmp"
-    r = subprocess.run([exe, "-shared", *ARCH, "-o", tmp, *objs], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
-    tmp = CALLS_PATH + ".tmp"
-    r = subprocess.run(_calls_link(calls, tmp), capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS_PATH)
-    with open(stamp_file, "w") as f:
-        f.write(stamp)
+    _run([exe, "-shared", *ARCH, "-o", tmp, *objs], "the library's link")
+    _put(LIB_PATH, tmp, stamp_file, stamp)
     return LIB_PATH
 
 
-if __name__ == "__main__":
-    print(build(force=True, verbose=True))
+def _compile_calls() -> None:
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    _run([*_calls_command(), "-o", _obj(CALLS_SOURCE)], CALLS_SOURCE)
+
+
+def build_calls(force: bool = False, compiled: bool = False) -> str:
+    """Compile the decode-step calls' module (if stale) against this interpreter's and this torch's headers,
+    and return its path; the library comes first. `compiled`: its object file is up to date."""
+    stamp, stamp_file = _calls_stamp(), os.path.join(BUILD_DIR, "stamp_calls")
+    if not force and _is_current(CALLS_PATH, stamp_file, stamp):
+        return CALLS_PATH
+    build_library()
+    if not compiled:
+        _compile_calls()
+    tmp = CALLS_PATH + ".tmp"
+    _run(_calls_link(_obj(CALLS_SOURCE), tmp), "the calls' link")
+    _put(CALLS_PATH, tmp, stamp_file, stamp)
+    return CALLS_PATH
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile what is stale of the library and the calls' module, side by side, and return the library's path.
+    The library is there even where the module cannot be compiled (which raises)."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        stale = force or not _is_current(CALLS_PATH, os.path.join(BUILD_DIR, "stamp_calls"), _calls_stamp())
+        calls = ex.submit(_compile_calls) if stale else None
+        build_library(force, verbose)
+        if calls:
+            calls.result()
+            build_calls(force=True, compiled=True)
+    return LIB_PATH
+
+
+if __name__ == "__main__":  # "library": the C ABI alone, without torch
+    import sys
+    print((build_library if sys.argv[1:] == ["library"] else build)(force=True, verbose=True))
