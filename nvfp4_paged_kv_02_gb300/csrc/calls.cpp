@@ -21,7 +21,7 @@
 #include <cmath>
 #include <map>
 #include <string>
-#include <tuple>
+#include <utility>
 
 #include "../../include/nvfp4kv.h"
 
@@ -149,17 +149,17 @@ float* device_scale(const Args& a, int i, const at::Device& device) {
   refuse("k_scale/v_scale must be float32 CUDA tensors");
 }
 
-// Workspaces, one per (device, stream, kind): calls on one stream run one at a time, so they can share one; a
+// The attention's workspaces, one per (device, stream): calls on one stream run one at a time, so they can share one; a
 // larger one takes its place when a call needs it. A call that is being captured gets its own from the graph's
 // memory, so that a graph never depends on what later calls do with these. The GIL guards the map, which is
 // never destroyed (the process's end is no time to free device memory).
-at::Tensor scratch(const at::Device& device, cudaStream_t stream, int64_t bytes, bool counters) {
-  static auto* kept = new std::map<std::tuple<int, cudaStream_t, bool>, at::Tensor>();
+at::Tensor attention_workspace(const at::Device& device, cudaStream_t stream, int64_t bytes) {
+  static auto* kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>();
   const bool capturing = c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None;
-  at::Tensor* slot = capturing ? nullptr : &(*kept)[{device.index(), stream, counters}];
+  at::Tensor* slot = capturing ? nullptr : &(*kept)[{device.index(), stream}];
   if (slot && slot->defined() && slot->numel() >= bytes) return *slot;
   at::Tensor t = at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(device));
-  if (counters && cudaMemsetAsync(t.data_ptr(), 0, NVFP4_COUNTER_BYTES, stream) != cudaSuccess)
+  if (cudaMemsetAsync(t.data_ptr(), 0, NVFP4_COUNTER_BYTES, stream) != cudaSuccess)
     refuse("the workspace's counters could not be cleared");
   if (slot) *slot = t;
   return t;
@@ -330,7 +330,8 @@ PyObject* select_pages(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     nvfp4_status st = nvfp4_select_pages_workspace_bytes(fits32(r.n, "batch_size"), fits32(heads, "num_kv_heads"), t.width, &bytes);
     if (st != NVFP4_OK) return PyLong_FromLong(st);
     const cudaStream_t stream = stream_of(device);
-    const at::Tensor ws = scratch(device, stream, bytes, false);
+    // the scores, for this call: nothing later reads them, and they grow with the table's width
+    const at::Tensor ws = at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(device));
     st = nvfp4_select_pages(
         r.data, dtype_code(q), r.stride, fits32(r.heads, "num_qo_heads"), static_cast<int32_t>(heads),
         fits32(head_dim, "head_dim"), address(bounds, at::kHalf, device, "key_bounds"), bounds.size(0),
@@ -383,7 +384,7 @@ PyObject* attention(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     nvfp4_status st = nvfp4_paged_attention_workspace_bytes(Hq, g.heads, g.head_dim, &bytes);
     if (st != NVFP4_OK) return PyLong_FromLong(st);
     const cudaStream_t stream = stream_of(device);
-    const at::Tensor ws = scratch(device, stream, bytes, true);
+    const at::Tensor ws = attention_workspace(device, stream, bytes);
     const float sm = a.none(12) ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(g.head_dim))) : static_cast<float>(a.real(12));
     const float cap = static_cast<float>(a.real(13));
     const int32_t* len_ptr = static_cast<int32_t*>(address(lens, at::kInt, device, "seq_lens"));
