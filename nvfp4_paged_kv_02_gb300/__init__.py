@@ -629,7 +629,7 @@ def nvfp4_4over6_from_code(code: int) -> Optional[NVFP44Over6Config]:
 
 # These calls run once per layer and step, and small ones take the GPU less time than the argument checks
 # take in Python: they go to the library through nvfp4kv_calls (csrc/calls.cpp), which makes the checks, keeps
-# the workspaces and raises ValueError as the functions above do.
+# the attention's workspaces (one per stream, the 64 used last) and raises ValueError as the functions above do.
 
 def _pair(cache):
     """(K, V) of a tuple or of a stacked 5-D tensor with K/V on the second dimension."""

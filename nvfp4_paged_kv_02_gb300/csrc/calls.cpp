@@ -4,7 +4,7 @@
 // time than Python needs to read a dozen tensors' properties and to convert the arguments (25 us a
 // call on the host, measured; 5 to 8 us here). So this module does what the rest of the binding does in
 // Python: it checks shapes, types and strides, turns tensors into pointers, allocates outputs and
-// keeps the workspaces. No step of the work runs here.
+// keeps the attention's workspaces. No step of the work runs here.
 //
 // Functions take their arguments by position (the Python functions give them names and defaults),
 // raise ValueError for what the tensors' properties forbid, and return the outputs, or the status
@@ -18,10 +18,11 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
-#include <map>
 #include <string>
-#include <utility>
+#include <vector>
 
 #include "../../include/nvfp4kv.h"
 
@@ -149,20 +150,57 @@ float* device_scale(const Args& a, int i, const at::Device& device) {
   refuse("k_scale/v_scale must be float32 CUDA tensors");
 }
 
-// The attention's workspaces, one per (device, stream): calls on one stream run one at a time, so they can share one; a
-// larger one takes its place when a call needs it. A call that is being captured gets its own from the graph's
-// memory, so that a graph never depends on what later calls do with these. The GIL guards the map, which is
-// never destroyed (the process's end is no time to free device memory).
+// The attention's workspaces (its counters have to stay as the last call left them), one per (device, stream):
+// calls on one stream run one at a time, so they can share one; a larger one takes its place when a call needs
+// it. A stream goes by its id, which is never given again, not by its handle; cudaStreamPerThread is another
+// stream in each thread. At most kMostKept are kept: the one that was not used for longest goes back to torch's
+// allocator, which hands its memory to the same stream only, and so after the calls that use it. A call that is
+// being captured gets its own from the graph's memory, so that a graph never depends on what later calls do with
+// these. The GIL guards the list, which is never destroyed (the process's end is no time to free device memory).
+constexpr size_t kMostKept = 64;
+struct Kept {
+  int device;
+  unsigned long long stream;
+  uint64_t thread;
+  at::Tensor memory;
+};
+std::vector<Kept>& kept() {  // the last one used first
+  static auto* list = new std::vector<Kept>();
+  return *list;
+}
+uint64_t this_thread() {
+  static std::atomic<uint64_t> threads{0};
+  thread_local const uint64_t number = ++threads;
+  return number;
+}
+
 at::Tensor attention_workspace(const at::Device& device, cudaStream_t stream, int64_t bytes) {
-  static auto* kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>();
   const bool capturing = c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None;
-  at::Tensor* slot = capturing ? nullptr : &(*kept)[{device.index(), stream}];
-  if (slot && slot->defined() && slot->numel() >= bytes) return *slot;
-  at::Tensor t = at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(device));
-  if (cudaMemsetAsync(t.data_ptr(), 0, NVFP4_COUNTER_BYTES, stream) != cudaSuccess)
+  Kept k{device.index(), 0, stream == cudaStreamPerThread ? this_thread() : 0, {}};
+  if (!capturing && cudaStreamGetId(stream, &k.stream) != cudaSuccess) refuse("the current stream has no id");
+  auto find = [&] {
+    auto& list = kept();
+    return std::find_if(list.begin(), list.end(), [&](const Kept& x) {
+      return x.stream == k.stream && x.device == k.device && x.thread == k.thread;
+    });
+  };
+  if (!capturing) {
+    const auto at = find();
+    if (at != kept().end()) {
+      std::rotate(kept().begin(), at, at + 1);
+      if (kept().front().memory.numel() >= bytes) return kept().front().memory;
+    }
+  }
+  k.memory = at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(device));
+  if (cudaMemsetAsync(k.memory.data_ptr(), 0, NVFP4_COUNTER_BYTES, stream) != cudaSuccess)
     refuse("the workspace's counters could not be cleared");
-  if (slot) *slot = t;
-  return t;
+  if (!capturing) {
+    const auto at = find();
+    if (at != kept().end()) kept().erase(at);
+    kept().insert(kept().begin(), k);
+    if (kept().size() > kMostKept) kept().pop_back();
+  }
+  return k.memory;
 }
 
 cudaStream_t stream_of(const at::Device& device) { return c10::cuda::getCurrentCUDAStream(device.index()).stream(); }
@@ -411,11 +449,29 @@ PyObject* attention(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   });
 }
 
+// The attention's workspaces that are kept, the last one used first: (device, stream's id, thread of a
+// per-thread stream, bytes).
+PyObject* workspaces(PyObject*, PyObject* const*, Py_ssize_t n) {
+  return guarded(n, 0, []() -> PyObject* {
+    PyObject* list = PyList_New(0);
+    for (const Kept& k : kept()) {
+      PyObject* item = list ? Py_BuildValue("iKKL", k.device, k.stream, static_cast<unsigned long long>(k.thread),
+                                            static_cast<long long>(k.memory.numel()))
+                            : nullptr;
+      if (!item || PyList_Append(list, item) < 0) Py_CLEAR(list);
+      Py_XDECREF(item);
+      if (!list) break;
+    }
+    return list;
+  });
+}
+
 PyMethodDef kMethods[] = {
     {"qk_norm_rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(qk_norm_rope_append)), METH_FASTCALL, nullptr},
     {"page_key_bounds", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(page_key_bounds)), METH_FASTCALL, nullptr},
     {"select_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(select_pages)), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(attention)), METH_FASTCALL, nullptr},
+    {"workspaces", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(workspaces)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "nvfp4kv_calls", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
