@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -214,18 +215,19 @@ PyObject* pair(const at::Tensor& x, const at::Tensor& y) {
   return r;
 }
 
+// No exception leaves a call: torch's own become what torch raises for them (OutOfMemoryError among them).
 template <typename F>
 PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F body) {
+  HANDLE_TH_ERRORS
   try {
     if (given != wanted) refuse("wrong number of arguments");
     return body();
   } catch (const Refused& e) {
     PyErr_SetString(PyExc_ValueError, e.what.c_str());
   } catch (PyObject*) {  // set already
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
   }
   return nullptr;
+  END_HANDLE_TH_ERRORS
 }
 
 // query, key, value, q_weight, k_weight, cos_sin, batch_indices, positions, k codes, v codes, k scales, v scales,
