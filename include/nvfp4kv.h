@@ -553,8 +553,12 @@ nvfp4_status nvfp4_paged_attention_workspace_bytes(int32_t num_qo_heads, int32_t
  * live block scale shows in the outputs that the formula has it in, and in no others. What the
  * slots past a request's end hold is of no consequence. The new token's own key and value are
  * in the cache already (append first).
- * Scores and sums are binary32; K and V are exact; a weight exp(x_t - m) is rounded to
- * binary16 before it multiplies V. The result does not depend on scheduling.
+ * K and V are exact. Query rows are taken in binary16 after a power of two has scaled them (what
+ * is below 2^-38 of a row's largest element is lost). A weight exp(x_t - m) is rounded to binary16
+ * before it multiplies V: 2^-11 relative; the sum that it is divided by, which lse comes from too,
+ * is of the weights before that rounding. Products are accumulated in binary32 by matrix
+ * instructions, which do not round every step to nearest. The result does not depend on scheduling,
+ * nor a head's on the other heads' or requests' queries.
  *   query         device [batch_size, num_qo_heads, head_dim] of dtype, tokens query_row_stride
  *                 elements apart; 16-byte aligned, stride a multiple of 8.
  *   out           device, contiguous [batch_size, num_qo_heads, head_dim] of dtype, 16-byte
