@@ -524,8 +524,9 @@ nvfp4_status nvfp4_select_pages_workspace_bytes(int32_t batch_size, int32_t num_
  *   workspace      device, workspace_bytes >= nvfp4_select_pages_workspace_bytes, 16-byte
  *                  aligned; holds anything; one call at a time.
  * Requirements: num_qo_heads a multiple of num_kv_heads, head_dim a multiple of 16 and at most
- * 256, batch_size at most 16384, max_pages_per_request at most 2^30 and batch_size times an
- * eighth of it at most 2^31 - 1, max_selected >= 1, num_sink_pages, num_recent_pages >= 0. */
+ * 256, num_pages at most 2^31 - 1, batch_size at most 16384, max_pages_per_request at most 2^30
+ * and batch_size times an eighth of it at most 2^31 - 1, max_selected >= 1, num_sink_pages,
+ * num_recent_pages >= 0. */
 nvfp4_status nvfp4_select_pages(const void* query, int32_t dtype, int64_t query_row_stride,
                                 int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
                                 const void* key_bounds, int64_t num_pages, int32_t page_size,
@@ -570,9 +571,9 @@ nvfp4_status nvfp4_paged_attention_workspace_bytes(int32_t num_qo_heads, int32_t
  *                 One call at a time (as the work-distribution workspace).
  *   The other arguments are those of nvfp4_dequantize_paged.
  * Requirements: num_qo_heads a multiple of num_kv_heads, head_dim a multiple of 16 and at most
- * 256, batch_size at most 16384, sm_scale finite, logits_soft_cap finite and >= 0; batch_size *
- * num_qo_heads times the positions that a request can have (by the table's width, or by
- * max_selected) at most about 2^43. */
+ * 256, batch_size at most 16384, at most 2^31 - 1 pages in the pool, sm_scale finite,
+ * logits_soft_cap finite and >= 0; batch_size * num_qo_heads times the positions that a request
+ * can have (by the table's width, or by max_selected) at most about 2^43. */
 nvfp4_status nvfp4_paged_attention_decode(
     const void* query, int32_t dtype, int64_t query_row_stride, int32_t num_qo_heads,
     nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache, int32_t page_size,

@@ -2,6 +2,7 @@
 // FlashInfer materializer's launcher makes -- dtypes, ranks, inner strides, 16-byte
 // alignment and shared extents -- plus the scale values passed by value), then one
 // launch sequence on the caller's stream.
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -784,6 +785,12 @@ nvfp4_status check_tables(const std::string& f, int32_t table_dtype, int32_t max
   return NVFP4_OK;
 }
 
+// The kernels that read tables into registers hold a page's index in 32 bits.
+nvfp4_status check_pool(const std::string& f, int64_t num_pages) {
+  if (num_pages > INT32_MAX) return fail(NVFP4_ERR_UNSUPPORTED, f + ": more than 2^31 - 1 pages");
+  return NVFP4_OK;
+}
+
 // The selection counts lists, groups of eight pages and a request's pages in 32 bits, its workspace's bytes in 64.
 nvfp4_status check_select_size(const std::string& f, int64_t batch_size, int64_t H, int64_t max_pages) {
   if (batch_size * H > INT32_MAX) return fail(NVFP4_ERR_UNSUPPORTED, f + ": more than 2^31 - 1 lists");
@@ -978,6 +985,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_select_pages(
     if (max_selected < 1) return fail(NVFP4_ERR_INVALID_ARG, f + ": max_selected must be >= 1");
     if (num_pages < 0 || num_sink_pages < 0 || num_recent_pages < 0)
       return fail(NVFP4_ERR_INVALID_ARG, f + ": negative size");
+    if (nvfp4_status st = check_pool(f, num_pages)) return st;
     if (nvfp4_status st = check_select_size(f, batch_size, num_kv_heads, max_pages_per_request)) return st;
     if (batch_size == 0) return NVFP4_OK;
     if (nvfp4_status st = check_rows(f, "query", query, query_row_stride,
@@ -1060,6 +1068,7 @@ nvfp4_status attention_impl(
     return fail(NVFP4_ERR_INVALID_ARG, f + ": logits_soft_cap must be finite and >= 0");
   if (nvfp4_status st = check_cache(fn, "k_cache", k_cache, page_size, num_kv_heads, head_dim)) return st;
   if (nvfp4_status st = check_cache(fn, "v_cache", v_cache, page_size, num_kv_heads, head_dim)) return st;
+  if (nvfp4_status st = check_pool(f, std::min(k_cache.num_pages, v_cache.num_pages))) return st;
   if (batch_size == 0) return NVFP4_OK;
   // A CTA counts its places (units of 32 tokens and nine more of each list) in 32 bits.
   const int64_t reach = sparse ? static_cast<int64_t>(max_selected) * page_size

@@ -1022,7 +1022,7 @@ nvfp4_status launch_attention(AttentionArgs a, cudaStream_t stream) {
   a.chunks = (a.G + 8 * nt - 1) / (8 * nt);
   a.chunk_heads = (a.G + a.chunks - 1) / a.chunks;
   const int64_t pool = a.kc.num_pages < a.vc.num_pages ? a.kc.num_pages : a.vc.num_pages;
-  a.pool_pages = pool > INT32_MAX ? static_cast<uint32_t>(INT32_MAX) : static_cast<uint32_t>(pool);
+  a.pool_pages = static_cast<uint32_t>(pool);
   const int64_t strides[4] = {a.kc.data_page_stride, a.vc.data_page_stride, a.kc.sf_page_stride, a.vc.sf_page_stride};
   for (int64_t s : strides)
     if (s > static_cast<int64_t>(UINT32_MAX)) return fail(NVFP4_ERR_UNSUPPORTED, "nvfp4_paged_attention_decode: a page stride above 4 GiB");

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 import nvfp4_paged_kv_02_gb300 as nv
-from tests.test_decode_ops_refusals import UNS, attend, err, select
+from tests.test_decode_ops_refusals import UNS, attend, cache, err, select
 
 TABLE = 2 ** 31 - 1
 
@@ -51,3 +51,12 @@ def test_attention_counts_every_list_of_a_wide_batch(lib):
     # below the limit the next check answers (here: no query)
     assert attend(lib, q=None, B=16384, maxp=2 ** 19 - 2 ** 10) == nv.ERR_INVALID_ARG and "query" in err(lib)
     assert attend(lib, q=None, B=1, maxp=TABLE) == nv.ERR_INVALID_ARG and "query" in err(lib)
+
+
+def test_page_indices_are_32_bits(lib):
+    huge = cache(pages=2 ** 31)
+    assert select(lib, pages=2 ** 31) == UNS and "pages" in err(lib)
+    assert attend(lib, kc=huge, vc=huge) == UNS and "pages" in err(lib)
+    assert attend(lib, kc=huge, vc=huge, S=4, sel=1 << 20) == UNS and "pages" in err(lib)
+    # the smaller of the two caches counts; the next check answers (here: no query)
+    assert attend(lib, kc=huge, q=None) == nv.ERR_INVALID_ARG and "query" in err(lib)
