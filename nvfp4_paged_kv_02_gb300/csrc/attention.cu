@@ -11,12 +11,14 @@
 // clock. A tile that goes through shared memory as binary16 for tcgen05.mma would have to be
 // decoded to registers and written back first; mma.sync takes the decoded registers as they
 // are, and its 1024 multiply-adds a clock and SM (measured) are three times what G <= 8 needs.
-// The budget is instructions: some 720 of a warp for 32 tokens of 128 elements, 2.8 a lane and
-// element, of which decoding, scaling and multiplying take 1.7. On large calls they bound it, on
-// small ones the start (lengths, their scan, the first pages: 4 us), one unit's latency and the
-// joins. At 8 KV heads of 128: 430 K tokens of 128 requests, G = 4: 111 us (4.4 TB/s); 117 K tokens
-// of 64 requests, G = 8: 41 us (3.1); one request of 131 K tokens, G = 4: 47 us (3.2); 16 requests of
-// 30 tokens 7.7 us. The tensor pipe is 16 % busy.
+// It takes some 690 instructions of a warp for 32 tokens of 128 elements, 2.7 a lane and element, of
+// which decoding, scaling and multiplying are 1.7. On large calls nothing is full: 59 % of the issue
+// slots, 51 % of the ALU pipe, 22 % of the tensor pipe, 4.4 of 6.8 TB/s; 162 registers admit twelve
+// warps to an SM, and each of them looks up pages, copies and computes in turn. On small calls it is
+// the start (lengths, their scan, the first pages: 4 us), one unit's latency and the joins. At 8 KV heads
+// of 128, in calls back to back: 430 K tokens of 128 requests, G = 4: 111 us (4.4 TB/s); 110 K tokens of
+// 64 requests, G = 8: 42 us (3.1); one request of 131 K tokens, G = 4: 47.5 us (3.2); 16 requests of 30
+// tokens 8.4 us (7.7 in a graph).
 //
 // Work. A unit is 32 tokens of one (request, KV head, chunk of up to 8 NT query heads). All
 // units of a launch, in that order, are cut into equal runs, one for each CTA, so that ragged
@@ -40,8 +42,8 @@
 // binary32 and of the weights before that rounding. What the rounding saves: a second product
 // with the weights' low parts (binary32 in effect) takes 124 us instead of 111 (430 K tokens), 50 instead of
 // 47.5 (one request of 131 K); a sum of the rounded weights beside the other one 113.6 and 48.7. What
-// it costs: outputs in binary16 are 2.9e-4 (root of the mean square, relative) from 64 bits on that request,
-// where weights in binary32 leave 2.05e-4, the output's own rounding; in bf16 it does not show.
+// it costs: outputs in binary16 are 2.8e-4 (root of the mean square, relative) from 64 bits on that request,
+// where weights in binary32 leave 2.1e-4, the output's own rounding; in bf16 it does not show.
 // Sums. The matrix instructions accumulate in binary32 registers, in an order of their own and without
 // rounding every step to nearest: a few 2^-24 of the sum of the magnitudes for 16 products.
 // Output. O^T = V^T P^T: A is V^T (16 of d), B is P^T, which movmatrix makes of S^T. A
@@ -64,8 +66,8 @@ constexpr int kMaxCtasPerSm = 4;
 constexpr int kSegmentCost = 9;
 constexpr size_t kMostSmem = 224 * 1024;  // dynamic; the CTA's limit less its static arrays
 // A segment of so few units is the run's that it begins in: cutting it costs a join (3 us) and saves
-// less. 512 lists of 64 to 400 tokens: 15.2 us (8: 17.2), of 384: 19.3 (20.7); one request of 500
-// tokens (16 units): 9.9 us cut (16: 10.4), 32 lists of 512: 11.2 (12.7).
+// less. 512 lists of 20 to 400 tokens: 15 us (with 8 here: 17), of 384: 19.3 (20.7); one request of 500
+// tokens (16 units): 9.1 us in a graph, cut (with 16 here 0.5 more), 32 lists of 512: 11.2 (12.7).
 constexpr int kWholeUnits = 12;
 constexpr float kWeightBias = 8.0f;
 constexpr float kSlack = 7.0f;

@@ -375,9 +375,10 @@ __global__ void __launch_bounds__((kRingWarps + 1) * 32, 3) page_key_bounds_ring
 // A lane's bounds come through its own ring of stages in shared memory (cp.async; no other lane
 // reads them, so a wait is all the synchronization there is). The lanes' parts of a unit's sums are
 // joined together at its end: 17 shuffles for eight pages and four heads of 128 elements, 32 if each
-// row of pages is joined by itself. Reading the bounds, 4 D bytes a page and head, is the floor;
-// instructions bound it, the 2 G D multiply-adds (packed two by two) first among them. With the
-// selection, at D = 128: 512 lists of 549 pages on average, G = 4, 31 us (2.95 TB/s of bounds); 512
+// row of pages is joined by itself. Reading the bounds, 4 D bytes a page and head, is the floor.
+// 158 registers (G <= 4) admit twelve warps to an SM, 232 (G <= 8) eight; they wait for their copies most,
+// and 45 and 41 % of the issue slots are used, the 2 G D multiply-adds (packed two by two) first among the
+// instructions. With the selection, at D = 128, in calls back to back: 512 lists of 346 pages on average, G = 4, 31 us (2.95 TB/s of bounds); 512
 // lists of 2270 pages 138 us (4.3); 32 lists of 7200 pages, G = 8, 55 us (2.1). Two lanes to a page
 // would need no shuffles but takes 16 % longer: the rows then lie 4 D bytes apart in shared memory.
 
@@ -588,8 +589,9 @@ __global__ void __launch_bounds__(kScoreWarps * 32, GC == 4 ? 3 : 2) page_scores
 // One CTA for each list. The k-th largest key is found by its digits, from the highest bit in
 // which the keys differ: a histogram of a digit in shared memory, the bin that holds the k-th,
 // and so on inside that bin, until the bin is wanted as a whole. Then one pass in page order
-// writes the pages above it and the first ones equal to it. Its barriers bound it, some 4 us a
-// wave: 512 lists of up to 1024 pages take 4.6 us less in CTAs of 128 threads than of 512 (31.0 and
+// writes the pages above it and the first ones equal to it. It is a chain of short steps with a barrier
+// or two between them: by itself, from cold caches, 9 us for 512 lists of up to 1024 pages and 11 us for 32
+// lists of 7200, which leave four fifths of the SMs idle. 512 lists of up to 1024 pages take 4.6 us less in CTAs of 128 threads than of 512 (31.0 and
 // 35.6 us with the scores), 16 lists of the same length 1.2 us more (12.0 and 10.8).
 
 constexpr int kSelectThreads = 512, kShortThreads = 128;
