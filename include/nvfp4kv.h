@@ -19,7 +19,8 @@
  * and, additions of this library, the operators of a decode step that works on such a cache:
  *   - norm and rotation of the query and key rows with the append in the same pass
  *   - bounds of each page's keys, and the pages that they promise the largest scores for
- *   - attention of one new token per request, over all pages or over selected ones
+ *   - attention of one new token per request, over all pages, over a window with the first tokens, or
+ *     over selected pages
  *
  * Number formats: E2M1 codes (grid {0,0.5,1,1.5,2,3,4,6}, 4 bits, two per byte, element
  * 2k in the low nibble); E4M3 (e4m3fn) block scales stored as bytes, one per 16
@@ -474,6 +475,30 @@ nvfp4_status nvfp4_qk_norm_rope_append_paged(
     const nvfp4_4over6_config* recipe, void* query_out, int64_t query_out_row_stride,
     int32_t* dev_status, void* stream);
 
+/* nvfp4_qk_norm_rope_append_paged for tokens with a position on each of several axes (time, height and
+ * width of an image's or video's patches): pair k of token i has
+ *   c = cos_sin[p][k], s = cos_sin[p][rotary_dim/2 + k], p = rotary_positions[pair_axes[k]][i]
+ * and `positions` says only where the rows go in the cache.
+ *   rotary_positions device int32 [num_rotary_axes, nnz], contiguous.
+ *   num_rotary_axes  1 to 8.
+ *   pair_axes        device uint8 [rotary_dim / 2], 4-byte aligned. A position that a pair goes by and that
+ *                    is outside the table is reported (NVFP4_DEV_BAD_POSITION) and nothing of its token is
+ *                    written; an axis that is not below num_rotary_axes counts as such for every token.
+ *   The other arguments, the operations and their order are those of nvfp4_qk_norm_rope_append_paged. */
+nvfp4_status nvfp4_qk_norm_rope_axes_append_paged(
+    const void* query, const void* key, const void* value, int32_t dtype, int64_t nnz,
+    int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, int64_t query_row_stride,
+    int64_t key_row_stride, int64_t value_row_stride, const void* q_weight,
+    const void* k_weight, float eps, const float* cos_sin, int64_t num_positions,
+    int32_t rotary_dim, int32_t rotary_interleaved, const int32_t* rotary_positions,
+    int32_t num_rotary_axes, const uint8_t* pair_axes, const int32_t* batch_indices,
+    const int32_t* positions, nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache,
+    int32_t page_size, int32_t kv_layout, const int32_t* kv_indices, int64_t num_kv_indices,
+    const int32_t* kv_indptr, const int32_t* kv_last_page_len, int32_t batch_size,
+    float k_scale, float v_scale, const float* k_scale_dev, const float* v_scale_dev,
+    const nvfp4_4over6_config* recipe, void* query_out, int64_t query_out_row_stride,
+    int32_t* dev_status, void* stream);
+
 /* Element-wise bounds of the keys of pages: for every logical page of request b that holds a
  * position of [first_positions[b], seq_lens[b]), with its physical page p and its live slots
  * t (positions below seq_lens[b]):
@@ -582,6 +607,18 @@ nvfp4_status nvfp4_paged_attention_decode(
     int32_t batch_size, const float* k_scale, const float* v_scale, float sm_scale,
     float logits_soft_cap, int32_t window_left, void* out, float* lse, int32_t* dev_status,
     void* workspace, int64_t workspace_bytes, void* stream);
+
+/* nvfp4_paged_attention_decode with first tokens that stay visible: with window_left >= 0 the live
+ * positions are t < seq_lens[b] with t >= seq_lens[b] - 1 - window_left or t < num_sink_tokens. Without a
+ * window every position is live, and num_sink_tokens (>= 0) changes nothing. */
+nvfp4_status nvfp4_paged_attention_decode_sinks(
+    const void* query, int32_t dtype, int64_t query_row_stride, int32_t num_qo_heads,
+    nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache, int32_t page_size,
+    int32_t num_kv_heads, int32_t head_dim, int32_t kv_layout, const void* block_tables,
+    int32_t table_dtype, int32_t max_pages_per_request, const int32_t* seq_lens,
+    int32_t batch_size, const float* k_scale, const float* v_scale, float sm_scale,
+    float logits_soft_cap, int32_t window_left, int32_t num_sink_tokens, void* out, float* lse,
+    int32_t* dev_status, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* nvfp4_paged_attention_decode over selected pages: request b's KV head h attends to the live
  * positions (t < seq_lens[b]) of its logical pages selected_pages[b, h, 0 .. num_selected[b,

@@ -18,10 +18,11 @@ Operations (FlashInfer documentation pages):
   nvfp4_4over6_from_code         (the recipe as one int64)
 
 Operators of a decode step over such a cache (additions of this library):
-  nvfp4_qk_norm_rope_append_paged      per-head RMS norm and rotation of q and k, and the append
+  nvfp4_qk_norm_rope_append_paged      per-head RMS norm and rotation of q and k (by positions of one axis or of
+                                       several: nvfp4_rotary_axes), and the append
   nvfp4_page_key_bounds                element-wise bounds of each page's keys
   nvfp4_select_pages                   the pages whose bounds promise the largest scores
-  nvfp4_paged_attention_decode         attention of one new token per request
+  nvfp4_paged_attention_decode         attention of one new token per request (sliding windows, first tokens that stay)
   nvfp4_sparse_paged_attention_decode  the same over selected pages
 """
 
@@ -46,7 +47,7 @@ __all__ = [
     "paged_caches", "LIB_PATH", "nvfp4_kv_quantize", "nvfp4_kv_dequantize",
     "nvfp4_4over6_code", "nvfp4_4over6_from_code", "nvfp4_qk_norm_rope_append_paged",
     "nvfp4_page_key_bounds", "nvfp4_select_pages", "nvfp4_paged_attention_decode",
-    "nvfp4_sparse_paged_attention_decode",
+    "nvfp4_sparse_paged_attention_decode", "nvfp4_rotary_axes",
 ]
 
 LIB_PATH = _build.LIB_PATH
@@ -167,6 +168,10 @@ def load() -> ctypes.CDLL:
         L.nvfp4_qk_norm_rope_append_paged.argtypes = [
             vp, vp, vp, i32, i64, i32, i32, i32, i64, i64, i64, vp, vp, f32, vp, i64, i32, i32, vp,
             vp, _Cache, _Cache, i32, i32, vp, i64, vp, vp, i32, f32, f32, vp, vp, vp, vp, i64, vp, vp]
+        L.nvfp4_qk_norm_rope_axes_append_paged.restype = i32
+        L.nvfp4_qk_norm_rope_axes_append_paged.argtypes = [
+            vp, vp, vp, i32, i64, i32, i32, i32, i64, i64, i64, vp, vp, f32, vp, i64, i32, i32, vp, i32, vp, vp,
+            vp, _Cache, _Cache, i32, i32, vp, i64, vp, vp, i32, f32, f32, vp, vp, vp, vp, i64, vp, vp]
         L.nvfp4_page_key_bounds.restype = i32
         L.nvfp4_page_key_bounds.argtypes = [
             _Cache, i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, vp, vp, vp]
@@ -182,6 +187,10 @@ def load() -> ctypes.CDLL:
         L.nvfp4_paged_attention_decode.argtypes = [
             vp, i32, i64, i32, _Cache, _Cache, i32, i32, i32, i32, vp, i32, i32, vp, i32, vp, vp, f32,
             f32, i32, vp, vp, vp, vp, i64, vp]
+        L.nvfp4_paged_attention_decode_sinks.restype = i32
+        L.nvfp4_paged_attention_decode_sinks.argtypes = [
+            vp, i32, i64, i32, _Cache, _Cache, i32, i32, i32, i32, vp, i32, i32, vp, i32, vp, vp, f32,
+            f32, i32, i32, vp, vp, vp, vp, i64, vp]
         L.nvfp4_sparse_paged_attention_decode.restype = i32
         L.nvfp4_sparse_paged_attention_decode.argtypes = [
             vp, i32, i64, i32, _Cache, _Cache, i32, i32, i32, i32, vp, i32, i32, vp, i32, vp, vp, i32,
@@ -656,19 +665,40 @@ def nvfp4_qk_norm_rope_append_paged(query: torch.Tensor, key: torch.Tensor, valu
                                     rotary_interleaved: bool = False,
                                     nvfp4_4over6: Optional[NVFP44Over6Config] = None,
                                     out: Optional[torch.Tensor] = None,
-                                    dev_status: Optional[torch.Tensor] = None) -> torch.Tensor:
+                                    dev_status: Optional[torch.Tensor] = None,
+                                    rotary_positions: Optional[torch.Tensor] = None,
+                                    rotary_axes: Optional[torch.Tensor] = None) -> torch.Tensor:
     """RMS norm of each head's query and key rows (weights q_weight, k_weight [D]; None: no norm),
     rotation by cos_sin[position] (float32 [positions, rotary_dim]: cosines, then sines; None: no
     rotation), and quantize-append of the key and value rows, in one launch. query [nnz, Hq, D], key
     and value [nnz, H, D] may be slices of one tensor. Returns the query rows (`out`, which may be
-    `query`). The other arguments are those of nvfp4_quantize_append_paged."""
+    `query`). With rotary_positions (int32 [axes, nnz]) a token has a position on each of up to eight axes,
+    and pair k of the rotation goes by the one on axis rotary_axes[k] (uint8 [rotary_dim / 2], see
+    nvfp4_rotary_axes); `positions` then only says where the rows go in the cache. The other arguments are
+    those of nvfp4_quantize_append_paged."""
     k, v = _pair(paged_kv_cache)
     ks, vs = _pair(kv_cache_sf)
     r = None if nvfp4_4over6 is None else nvfp4_4over6._values()
     return _done("nvfp4_qk_norm_rope_append_paged", _calls().qk_norm_rope_append(
         query, key, value, q_weight, k_weight, cos_sin, batch_indices, positions, k, v, ks, vs, kv_indices,
         kv_indptr, kv_last_page_len, k_scale, v_scale, _layout(kv_layout), eps, rotary_interleaved, r, out,
-        dev_status))
+        dev_status, rotary_positions, rotary_axes))
+
+
+def nvfp4_rotary_axes(sections: Sequence[int], in_turn: bool = False,
+                      device: Union[str, int, torch.device] = "cuda") -> torch.Tensor:
+    """The axis of each rotary pair (uint8 [sum(sections)]) from the number of pairs of each axis: one axis' pairs
+    after the other's, or with `in_turn` pair by pair (0, 1, 2, 0, 1, 2, ...) while an axis has pairs left."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 8 or min(left) < 0:
+        raise ValueError("sections must be the pairs of one to eight axes")
+    axes = []
+    if in_turn:
+        for k in range(max(left)):
+            axes += [a for a, n in enumerate(left) if k < n]
+    else:
+        axes = [a for a, n in enumerate(left) for _ in range(n)]
+    return torch.tensor(axes, dtype=torch.uint8, device=device)
 
 
 
@@ -708,16 +738,18 @@ def nvfp4_paged_attention_decode(query: torch.Tensor, paged_kv_cache, kv_cache_s
                                  sm_scale: Optional[float] = None, logits_soft_cap: float = 0.0,
                                  window_left: int = -1, out: Optional[torch.Tensor] = None,
                                  lse: Optional[torch.Tensor] = None,
-                                 dev_status: Optional[torch.Tensor] = None):
+                                 dev_status: Optional[torch.Tensor] = None,
+                                 num_sink_tokens: int = 0):
     """Attention of one new token per request, query [B, Hq, D], over the paged cache's first
-    seq_lens[b] positions (the last window_left + 1 of them when window_left >= 0). k_scale, v_scale: the
+    seq_lens[b] positions (the last window_left + 1 of them when window_left >= 0, and with num_sink_tokens
+    the first ones, which then stay visible to the left of the window). k_scale, v_scale: the
     global decode scales, 1-element float32 CUDA tensors; sm_scale: D ** -0.5 unless given. Returns (out
     [B, Hq, D], lse float32 [B, Hq], natural logarithm); a request without positions gets 0 and -inf."""
     k, v = _pair(paged_kv_cache)
     ks, vs = _pair(kv_cache_sf)
     return _done("nvfp4_paged_attention_decode", _calls().attention(
         query, k, v, ks, vs, block_tables, seq_lens, None, None, k_scale, v_scale, _layout(kv_layout), sm_scale,
-        logits_soft_cap, window_left, out, lse, dev_status))
+        logits_soft_cap, window_left, out, lse, dev_status, num_sink_tokens))
 
 
 
@@ -736,4 +768,4 @@ def nvfp4_sparse_paged_attention_decode(query: torch.Tensor, paged_kv_cache, kv_
     ks, vs = _pair(kv_cache_sf)
     return _done("nvfp4_sparse_paged_attention_decode", _calls().attention(
         query, k, v, ks, vs, block_tables, seq_lens, selected_pages, num_selected, k_scale, v_scale,
-        _layout(kv_layout), sm_scale, logits_soft_cap, -1, out, lse, dev_status))
+        _layout(kv_layout), sm_scale, logits_soft_cap, -1, out, lse, dev_status, 0))

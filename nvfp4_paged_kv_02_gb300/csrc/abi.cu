@@ -809,6 +809,116 @@ nvfp4_status check_rows(const std::string& f, const char* name, const void* p, i
   return NVFP4_OK;
 }
 
+// Shared body of the two norm, rotation and append entry points.
+nvfp4_status norm_rope_append_impl(
+    const char* fn, bool axes, const int32_t* rotary_positions, int32_t num_axes, const uint8_t* pair_axes,
+    const void* query, const void* key, const void* value, int32_t dtype, int64_t nnz,
+    int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, int64_t query_row_stride,
+    int64_t key_row_stride, int64_t value_row_stride, const void* q_weight,
+    const void* k_weight, float eps, const float* cos_sin, int64_t num_positions,
+    int32_t rotary_dim, int32_t rotary_interleaved, const int32_t* batch_indices,
+    const int32_t* positions, nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache,
+    int32_t page_size, int32_t kv_layout, const int32_t* kv_indices, int64_t num_kv_indices,
+    const int32_t* kv_indptr, const int32_t* kv_last_page_len, int32_t batch_size,
+    float k_scale, float v_scale, const float* k_scale_dev, const float* v_scale_dev,
+    const nvfp4_4over6_config* recipe, void* query_out, int64_t query_out_row_stride,
+    int32_t* dev_status, void* stream) {
+  const std::string f(fn);
+  if (nvfp4_status st = check_recipe(recipe)) return st;
+  if (nvfp4_status st = check_geometry(fn, page_size, num_kv_heads, head_dim, kv_layout)) return st;
+  if (nvfp4_status st = check_dtype(f, dtype)) return st;
+  if (num_qo_heads < 1) return fail(NVFP4_ERR_INVALID_ARG, f + ": num_qo_heads must be >= 1");
+  if (head_dim > 512) return fail(NVFP4_ERR_UNSUPPORTED, f + ": head_dim above 512");
+  if (nnz < 0 || batch_size < 0 || num_positions < 0)
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": negative size");
+  if (!(std::isfinite(eps) && eps >= 0.0f)) return fail(NVFP4_ERR_INVALID_ARG, f + ": eps must be finite and >= 0");
+  if (rotary_dim < 0 || rotary_dim % 16 != 0 || rotary_dim > head_dim)
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": rotary_dim must be a multiple of 16 between 0 and head_dim");
+  if (rotary_interleaved != 0 && rotary_interleaved != 1)
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": rotary_interleaved must be 0 or 1");
+  if (axes && (num_axes < 1 || num_axes > kMaxRotaryAxes))
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": num_rotary_axes must be between 1 and " + std::to_string(kMaxRotaryAxes));
+  if ((k_scale_dev == nullptr) != (v_scale_dev == nullptr))
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": give both scales in device memory or both by value");
+  if (!k_scale_dev && (!(std::isfinite(k_scale) && k_scale > 0.0f) || !(std::isfinite(v_scale) && v_scale > 0.0f)))
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": k_scale and v_scale must be positive finite");
+  if (!aligned(k_scale_dev, 4) || !aligned(v_scale_dev, 4))
+    return fail(NVFP4_ERR_ALIGNMENT, f + ": device scales must be 4-byte aligned");
+  if (nvfp4_status st = check_cache(fn, "k_cache", k_cache, page_size, num_kv_heads, head_dim)) return st;
+  if (nvfp4_status st = check_cache(fn, "v_cache", v_cache, page_size, num_kv_heads, head_dim)) return st;
+  if (nnz == 0) return NVFP4_OK;
+  const int64_t q_row = static_cast<int64_t>(num_qo_heads) * head_dim;
+  const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (nvfp4_status st = check_rows(f, "query", query, query_row_stride, q_row)) return st;
+  if (nvfp4_status st = check_rows(f, "key", key, key_row_stride, kv_row)) return st;
+  if (nvfp4_status st = check_rows(f, "value", value, value_row_stride, kv_row)) return st;
+  if (nvfp4_status st = check_rows(f, "query_out", query_out, query_out_row_stride, q_row)) return st;
+  if (query_out == query && query_out_row_stride != query_row_stride)
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": query_out in place needs query's row stride");
+  if (!batch_indices || !positions || !kv_indptr || (!kv_indices && num_kv_indices > 0) ||
+      (rotary_dim > 0 && (!cos_sin || (axes && (!rotary_positions || !pair_axes)))))
+    return fail(NVFP4_ERR_INVALID_ARG, f + ": null device pointer");
+  if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(cos_sin, 16))
+    return fail(NVFP4_ERR_ALIGNMENT, f + ": weights and cos_sin must be 16-byte aligned");
+  if (axes && (!aligned(rotary_positions, 4) || !aligned(pair_axes, 4)))
+    return fail(NVFP4_ERR_ALIGNMENT, f + ": rotary_positions and pair_axes must be 4-byte aligned");
+  if (batch_size == 0) return fail(NVFP4_ERR_INVALID_ARG, f + ": rows given but batch_size is 0");
+  if (num_kv_indices < 0) return fail(NVFP4_ERR_INVALID_ARG, f + ": num_kv_indices must be >= 0");
+  if (num_qo_heads + 2 * static_cast<int64_t>(num_kv_heads) > INT32_MAX / 2 ||
+      nnz > (int64_t(1) << 40) / (num_qo_heads + 2 * static_cast<int64_t>(num_kv_heads)))
+    return fail(NVFP4_ERR_UNSUPPORTED, f + ": more than 2^40 rows");
+  NormRopeArgs a{};
+  a.ap.k = static_cast<const uint8_t*>(key);
+  a.ap.v = static_cast<const uint8_t*>(value);
+  a.ap.k_row_bytes = key_row_stride * 2;
+  a.ap.v_row_bytes = value_row_stride * 2;
+  a.ap.nnz = nnz;
+  a.ap.H = num_kv_heads;
+  a.ap.D = head_dim;
+  a.ap.nb = head_dim / 16;
+  a.ap.div_ps = make_div(page_size);
+  a.ap.batch_indices = batch_indices;
+  a.ap.positions = positions;
+  a.ap.kc = k_cache;
+  a.ap.vc = v_cache;
+  a.ap.ps = page_size;
+  a.ap.layout = kv_layout;
+  a.ap.kv_indices = kv_indices;
+  a.ap.num_kv_indices = num_kv_indices;
+  a.ap.kv_indptr = kv_indptr;
+  a.ap.kv_last_page_len = kv_last_page_len;
+  a.ap.batch_size = batch_size;
+  a.ap.gs[0] = k_scale;
+  a.ap.gs[1] = v_scale;
+  a.ap.gs_dev[0] = k_scale_dev;
+  a.ap.gs_dev[1] = v_scale_dev;
+  a.ap.cap_a = nvfp4_e4m3_max(recipe);
+  a.ap.neg_zero = 0x80000000u;
+  a.ap.status = dev_status;
+  a.q = static_cast<const uint8_t*>(query);
+  a.q_row_bytes = query_row_stride * 2;
+  a.q_out = static_cast<uint8_t*>(query_out);
+  a.q_out_row_bytes = query_out_row_stride * 2;
+  a.Hq = num_qo_heads;
+  a.q_weight = static_cast<const uint8_t*>(q_weight);
+  a.k_weight = static_cast<const uint8_t*>(k_weight);
+  a.eps = eps;
+  a.inv_d = static_cast<float>(1.0 / head_dim);
+  a.cos_sin = cos_sin;
+  a.num_positions = num_positions;
+  a.rotary_dim = rotary_dim;
+  if (axes && rotary_dim > 0) {
+    a.axis_positions = rotary_positions;
+    a.pair_axes = pair_axes;
+    a.axes = num_axes;
+  }
+  a.interleaved = rotary_interleaved;
+  while ((16 << a.log2_T) < head_dim) ++a.log2_T;
+  int mode = 0;
+  if (recipe) mode = 1 + (recipe->err_mode == NVFP4_ERR_MSE ? 1 : 0) + (recipe->err_use_fast_math ? 2 : 0);
+  return launch_norm_rope_append(a, dtype == NVFP4_BF16, mode, static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -825,93 +935,40 @@ NVFP4_EXPORT nvfp4_status nvfp4_qk_norm_rope_append_paged(
     float k_scale, float v_scale, const float* k_scale_dev, const float* v_scale_dev,
     const nvfp4_4over6_config* recipe, void* query_out, int64_t query_out_row_stride,
     int32_t* dev_status, void* stream) {
-  return guarded([&]() -> nvfp4_status {
-    const char* fn = "nvfp4_qk_norm_rope_append_paged";
-    const std::string f(fn);
-    if (nvfp4_status st = check_recipe(recipe)) return st;
-    if (nvfp4_status st = check_geometry(fn, page_size, num_kv_heads, head_dim, kv_layout)) return st;
-    if (nvfp4_status st = check_dtype(f, dtype)) return st;
-    if (num_qo_heads < 1) return fail(NVFP4_ERR_INVALID_ARG, f + ": num_qo_heads must be >= 1");
-    if (head_dim > 512) return fail(NVFP4_ERR_UNSUPPORTED, f + ": head_dim above 512");
-    if (nnz < 0 || batch_size < 0 || num_positions < 0)
-      return fail(NVFP4_ERR_INVALID_ARG, f + ": negative size");
-    if (!(std::isfinite(eps) && eps >= 0.0f)) return fail(NVFP4_ERR_INVALID_ARG, f + ": eps must be finite and >= 0");
-    if (rotary_dim < 0 || rotary_dim % 16 != 0 || rotary_dim > head_dim)
-      return fail(NVFP4_ERR_INVALID_ARG, f + ": rotary_dim must be a multiple of 16 between 0 and head_dim");
-    if (rotary_interleaved != 0 && rotary_interleaved != 1)
-      return fail(NVFP4_ERR_INVALID_ARG, f + ": rotary_interleaved must be 0 or 1");
-    if ((k_scale_dev == nullptr) != (v_scale_dev == nullptr))
-      return fail(NVFP4_ERR_INVALID_ARG, f + ": give both scales in device memory or both by value");
-    if (!k_scale_dev && (!(std::isfinite(k_scale) && k_scale > 0.0f) || !(std::isfinite(v_scale) && v_scale > 0.0f)))
-      return fail(NVFP4_ERR_INVALID_ARG, f + ": k_scale and v_scale must be positive finite");
-    if (!aligned(k_scale_dev, 4) || !aligned(v_scale_dev, 4))
-      return fail(NVFP4_ERR_ALIGNMENT, f + ": device scales must be 4-byte aligned");
-    if (nvfp4_status st = check_cache(fn, "k_cache", k_cache, page_size, num_kv_heads, head_dim)) return st;
-    if (nvfp4_status st = check_cache(fn, "v_cache", v_cache, page_size, num_kv_heads, head_dim)) return st;
-    if (nnz == 0) return NVFP4_OK;
-    const int64_t q_row = static_cast<int64_t>(num_qo_heads) * head_dim;
-    const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
-    if (nvfp4_status st = check_rows(f, "query", query, query_row_stride, q_row)) return st;
-    if (nvfp4_status st = check_rows(f, "key", key, key_row_stride, kv_row)) return st;
-    if (nvfp4_status st = check_rows(f, "value", value, value_row_stride, kv_row)) return st;
-    if (nvfp4_status st = check_rows(f, "query_out", query_out, query_out_row_stride, q_row)) return st;
-    if (query_out == query && query_out_row_stride != query_row_stride)
-      return fail(NVFP4_ERR_INVALID_ARG, f + ": query_out in place needs query's row stride");
-    if (!batch_indices || !positions || !kv_indptr || (!kv_indices && num_kv_indices > 0) ||
-        (rotary_dim > 0 && !cos_sin))
-      return fail(NVFP4_ERR_INVALID_ARG, f + ": null device pointer");
-    if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(cos_sin, 16))
-      return fail(NVFP4_ERR_ALIGNMENT, f + ": weights and cos_sin must be 16-byte aligned");
-    if (batch_size == 0) return fail(NVFP4_ERR_INVALID_ARG, f + ": rows given but batch_size is 0");
-    if (num_kv_indices < 0) return fail(NVFP4_ERR_INVALID_ARG, f + ": num_kv_indices must be >= 0");
-    if (num_qo_heads + 2 * static_cast<int64_t>(num_kv_heads) > INT32_MAX / 2 ||
-        nnz > (int64_t(1) << 40) / (num_qo_heads + 2 * static_cast<int64_t>(num_kv_heads)))
-      return fail(NVFP4_ERR_UNSUPPORTED, f + ": more than 2^40 rows");
-    NormRopeArgs a{};
-    a.ap.k = static_cast<const uint8_t*>(key);
-    a.ap.v = static_cast<const uint8_t*>(value);
-    a.ap.k_row_bytes = key_row_stride * 2;
-    a.ap.v_row_bytes = value_row_stride * 2;
-    a.ap.nnz = nnz;
-    a.ap.H = num_kv_heads;
-    a.ap.D = head_dim;
-    a.ap.nb = head_dim / 16;
-    a.ap.div_ps = make_div(page_size);
-    a.ap.batch_indices = batch_indices;
-    a.ap.positions = positions;
-    a.ap.kc = k_cache;
-    a.ap.vc = v_cache;
-    a.ap.ps = page_size;
-    a.ap.layout = kv_layout;
-    a.ap.kv_indices = kv_indices;
-    a.ap.num_kv_indices = num_kv_indices;
-    a.ap.kv_indptr = kv_indptr;
-    a.ap.kv_last_page_len = kv_last_page_len;
-    a.ap.batch_size = batch_size;
-    a.ap.gs[0] = k_scale;
-    a.ap.gs[1] = v_scale;
-    a.ap.gs_dev[0] = k_scale_dev;
-    a.ap.gs_dev[1] = v_scale_dev;
-    a.ap.cap_a = nvfp4_e4m3_max(recipe);
-    a.ap.neg_zero = 0x80000000u;
-    a.ap.status = dev_status;
-    a.q = static_cast<const uint8_t*>(query);
-    a.q_row_bytes = query_row_stride * 2;
-    a.q_out = static_cast<uint8_t*>(query_out);
-    a.q_out_row_bytes = query_out_row_stride * 2;
-    a.Hq = num_qo_heads;
-    a.q_weight = static_cast<const uint8_t*>(q_weight);
-    a.k_weight = static_cast<const uint8_t*>(k_weight);
-    a.eps = eps;
-    a.inv_d = static_cast<float>(1.0 / head_dim);
-    a.cos_sin = cos_sin;
-    a.num_positions = num_positions;
-    a.rotary_dim = rotary_dim;
-    a.interleaved = rotary_interleaved;
-    while ((16 << a.log2_T) < head_dim) ++a.log2_T;
-    int mode = 0;
-    if (recipe) mode = 1 + (recipe->err_mode == NVFP4_ERR_MSE ? 1 : 0) + (recipe->err_use_fast_math ? 2 : 0);
-    return launch_norm_rope_append(a, dtype == NVFP4_BF16, mode, static_cast<cudaStream_t>(stream));
+  return guarded([&] {
+    return norm_rope_append_impl(
+        "nvfp4_qk_norm_rope_append_paged", false, nullptr, 0, nullptr,
+        query, key, value, dtype, nnz, num_qo_heads, num_kv_heads, head_dim,
+        query_row_stride, key_row_stride, value_row_stride, q_weight, k_weight, eps,
+        cos_sin, num_positions, rotary_dim, rotary_interleaved, batch_indices,
+        positions, k_cache, v_cache, page_size, kv_layout, kv_indices, num_kv_indices,
+        kv_indptr, kv_last_page_len, batch_size, k_scale, v_scale, k_scale_dev,
+        v_scale_dev, recipe, query_out, query_out_row_stride, dev_status, stream);
+  });
+}
+
+NVFP4_EXPORT nvfp4_status nvfp4_qk_norm_rope_axes_append_paged(
+    const void* query, const void* key, const void* value, int32_t dtype, int64_t nnz,
+    int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, int64_t query_row_stride,
+    int64_t key_row_stride, int64_t value_row_stride, const void* q_weight,
+    const void* k_weight, float eps, const float* cos_sin, int64_t num_positions,
+    int32_t rotary_dim, int32_t rotary_interleaved, const int32_t* rotary_positions,
+    int32_t num_rotary_axes, const uint8_t* pair_axes, const int32_t* batch_indices,
+    const int32_t* positions, nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache,
+    int32_t page_size, int32_t kv_layout, const int32_t* kv_indices, int64_t num_kv_indices,
+    const int32_t* kv_indptr, const int32_t* kv_last_page_len, int32_t batch_size,
+    float k_scale, float v_scale, const float* k_scale_dev, const float* v_scale_dev,
+    const nvfp4_4over6_config* recipe, void* query_out, int64_t query_out_row_stride,
+    int32_t* dev_status, void* stream) {
+  return guarded([&] {
+    return norm_rope_append_impl(
+        "nvfp4_qk_norm_rope_axes_append_paged", true, rotary_positions, num_rotary_axes, pair_axes,
+        query, key, value, dtype, nnz, num_qo_heads, num_kv_heads, head_dim,
+        query_row_stride, key_row_stride, value_row_stride, q_weight, k_weight, eps,
+        cos_sin, num_positions, rotary_dim, rotary_interleaved, batch_indices,
+        positions, k_cache, v_cache, page_size, kv_layout, kv_indices, num_kv_indices,
+        kv_indptr, kv_last_page_len, batch_size, k_scale, v_scale, k_scale_dev,
+        v_scale_dev, recipe, query_out, query_out_row_stride, dev_status, stream);
   });
 }
 
@@ -1052,8 +1109,8 @@ nvfp4_status attention_impl(
     const void* block_tables, int32_t table_dtype, int32_t max_pages, const int32_t* seq_lens,
     int32_t batch_size, bool sparse, const int32_t* selected, const int32_t* num_selected,
     int32_t max_selected, const float* k_scale, const float* v_scale, float sm_scale,
-    float soft_cap, int32_t window_left, void* out, float* lse, int32_t* dev_status,
-    void* workspace, int64_t workspace_bytes, void* stream) {
+    float soft_cap, int32_t window_left, int32_t num_sink_tokens, void* out, float* lse,
+    int32_t* dev_status, void* workspace, int64_t workspace_bytes, void* stream) {
   const std::string f(fn);
   if (nvfp4_status st = check_geometry(fn, page_size, num_kv_heads, head_dim, kv_layout)) return st;
   if (nvfp4_status st = check_dtype(f, dtype)) return st;
@@ -1066,6 +1123,7 @@ nvfp4_status attention_impl(
   if (!std::isfinite(sm_scale)) return fail(NVFP4_ERR_INVALID_ARG, f + ": sm_scale must be finite");
   if (!(std::isfinite(soft_cap) && soft_cap >= 0.0f))
     return fail(NVFP4_ERR_INVALID_ARG, f + ": logits_soft_cap must be finite and >= 0");
+  if (num_sink_tokens < 0) return fail(NVFP4_ERR_INVALID_ARG, f + ": num_sink_tokens must be >= 0");
   if (nvfp4_status st = check_cache(fn, "k_cache", k_cache, page_size, num_kv_heads, head_dim)) return st;
   if (nvfp4_status st = check_cache(fn, "v_cache", v_cache, page_size, num_kv_heads, head_dim)) return st;
   if (nvfp4_status st = check_pool(f, std::min(k_cache.num_pages, v_cache.num_pages))) return st;
@@ -1113,6 +1171,7 @@ nvfp4_status attention_impl(
   a.sm_scale = sm_scale;
   a.soft_cap = soft_cap;
   a.window_left = window_left;
+  a.sink = num_sink_tokens;
   a.out = static_cast<uint8_t*>(out);
   a.lse = lse;
   a.status = dev_status;
@@ -1137,7 +1196,25 @@ NVFP4_EXPORT nvfp4_status nvfp4_paged_attention_decode(
                           num_qo_heads, k_cache, v_cache, page_size, num_kv_heads, head_dim,
                           kv_layout, block_tables, table_dtype, max_pages_per_request, seq_lens,
                           batch_size, false, nullptr, nullptr, 0, k_scale, v_scale, sm_scale,
-                          logits_soft_cap, window_left, out, lse, dev_status, workspace,
+                          logits_soft_cap, window_left, 0, out, lse, dev_status, workspace,
+                          workspace_bytes, stream);
+  });
+}
+
+NVFP4_EXPORT nvfp4_status nvfp4_paged_attention_decode_sinks(
+    const void* query, int32_t dtype, int64_t query_row_stride, int32_t num_qo_heads,
+    nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache, int32_t page_size,
+    int32_t num_kv_heads, int32_t head_dim, int32_t kv_layout, const void* block_tables,
+    int32_t table_dtype, int32_t max_pages_per_request, const int32_t* seq_lens,
+    int32_t batch_size, const float* k_scale, const float* v_scale, float sm_scale,
+    float logits_soft_cap, int32_t window_left, int32_t num_sink_tokens, void* out, float* lse,
+    int32_t* dev_status, void* workspace, int64_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    return attention_impl("nvfp4_paged_attention_decode_sinks", query, dtype, query_row_stride,
+                          num_qo_heads, k_cache, v_cache, page_size, num_kv_heads, head_dim,
+                          kv_layout, block_tables, table_dtype, max_pages_per_request, seq_lens,
+                          batch_size, false, nullptr, nullptr, 0, k_scale, v_scale, sm_scale,
+                          logits_soft_cap, window_left, num_sink_tokens, out, lse, dev_status, workspace,
                           workspace_bytes, stream);
   });
 }
@@ -1156,7 +1233,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_sparse_paged_attention_decode(
                           num_qo_heads, k_cache, v_cache, page_size, num_kv_heads, head_dim,
                           kv_layout, block_tables, table_dtype, max_pages_per_request, seq_lens,
                           batch_size, true, selected_pages, num_selected, max_selected, k_scale,
-                          v_scale, sm_scale, logits_soft_cap, -1, out, lse, dev_status,
+                          v_scale, sm_scale, logits_soft_cap, -1, 0, out, lse, dev_status,
                           workspace, workspace_bytes, stream);
   });
 }

@@ -4,6 +4,7 @@
 //   x_t = sm_scale * gs_k * sum_d q[d] (e2m1 * S)_K[t, d]      (soft cap c: c tanh(x_t / c))
 //   out = gs_v * sum_t exp(x_t - m) (e2m1 * S)_V[t, :] / l,    m = max x_t, l = sum exp(x_t - m)
 //   lse = m + log(l)
+// (live: t < len; with a window w also t >= len - 1 - w, or t < sink, the first tokens that stay)
 // in one pass with a running maximum and sum. No live token: out = 0, lse = -inf.
 //
 // What bounds it is reading the cache: 9/8 byte for an element of K and of V together, against
@@ -117,9 +118,10 @@ __device__ __forceinline__ float soft_capped(float x, float cap) {
 
 // ---- which units ---------------------------------------------------------------------------
 
-// The live range of request b: tokens [lo, len).
+// The live range of request b: tokens [lo, len), and with a window the first `sink` ones. Its units are the
+// `first_units` that hold those, and from the unit that holds lo on (`gap` units are passed over).
 struct Span {
-  int32_t lo, len;
+  int32_t lo, len, sink, first_units, gap;
 };
 __device__ __forceinline__ Span span_of(const AttentionArgs& a, int32_t b) {
   const int64_t reach = a.max_pages * a.ps;
@@ -127,6 +129,9 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& a, int32_t b) {
   Span s;
   s.len = n > reach ? static_cast<int32_t>(reach) : n;
   s.lo = a.window_left >= 0 ? max(0, s.len - 1 - a.window_left) : 0;
+  s.sink = min(a.sink, s.lo);
+  s.first_units = static_cast<int32_t>((static_cast<uint32_t>(s.sink) + kUnit - 1) / kUnit);
+  s.gap = max(s.lo / kUnit - s.first_units, 0);  // (0: the last of the first units may hold lo too)
   return s;
 }
 
@@ -137,7 +142,7 @@ __device__ __forceinline__ int32_t units_of(const AttentionArgs& a, int32_t b, i
     return (n * a.ps + kUnit - 1) / kUnit;
   }
   const Span s = span_of(a, b);
-  return s.len > 0 ? (s.len - 1) / kUnit + 1 - s.lo / kUnit : 0;
+  return s.len > 0 ? (s.len - 1) / kUnit + 1 - s.gap : 0;
 }
 
 // What a segment counts for when the runs are cut: its units, and kSegmentCost for its queries,
@@ -414,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
     lk_live = false;
     if (!lk_unit) return;
     // a token, or a slot of the selected pages
-    const int32_t p = static_cast<int32_t>(static_cast<uint32_t>((a.selected ? 0 : span.lo / kUnit) + pu) * kUnit + lane);
+    const int32_t p = static_cast<int32_t>(static_cast<uint32_t>((a.selected || pu < span.first_units ? 0 : span.gap) + pu) * kUnit + lane);
     int32_t col = div_q32(p, a.div_ps);
     const int32_t slot = p - col * a.ps;
     if (a.selected) {
@@ -425,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
         return;
       }
       if (static_cast<int64_t>(col) * a.ps + slot >= span.len) return;
-    } else if (p < span.lo || p >= span.len) {
+    } else if ((p < span.lo && p >= span.sink) || p >= span.len) {
       return;
     }
     const int32_t* entry = reinterpret_cast<const int32_t*>(list + (static_cast<int64_t>(col) << (a.table64 ? 3 : 2)));

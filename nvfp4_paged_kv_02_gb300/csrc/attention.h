@@ -25,7 +25,7 @@ struct AttentionArgs {
   const float* k_scale;
   const float* v_scale;
   float sm_scale, soft_cap;
-  int32_t window_left;
+  int32_t window_left, sink;  // with a window: the first `sink` positions too
   uint8_t* out;
   float* lse;  // may be null
   int32_t* status;

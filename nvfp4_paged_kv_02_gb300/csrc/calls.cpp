@@ -232,9 +232,9 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F body) {
 
 // query, key, value, q_weight, k_weight, cos_sin, batch_indices, positions, k codes, v codes, k scales, v scales,
 // kv_indices, kv_indptr, kv_last_page_len, k_scale, v_scale, layout, eps, interleaved, recipe (None or (e4m3_max,
-// err_mode, fast)), out, dev_status
+// err_mode, fast)), out, dev_status, rotary_positions, rotary_axes
 PyObject* qk_norm_rope_append(PyObject*, PyObject* const* argv, Py_ssize_t n) {
-  return guarded(n, 23, [&]() -> PyObject* {
+  return guarded(n, 25, [&]() -> PyObject* {
     const Args a{argv};
     const at::Tensor& q = first(a.tensor(0, "query"));
     const at::Device device = q.device();
@@ -296,16 +296,34 @@ PyObject* qk_norm_rope_append(PyObject*, PyObject* const* argv, Py_ssize_t n) {
       o = rows_of(out, type, device, "out", qr.heads, g.head_dim);
       if (o.n != qr.n) refuse("out must have query's shape");
     }
-    const nvfp4_status st = nvfp4_qk_norm_rope_append_paged(
-        qr.data, kr.data, vr.data, code, qr.n, fits32(qr.heads, "num_qo_heads"), g.heads, g.head_dim, qr.stride,
-        kr.stride, vr.stride, w[0], w[1], static_cast<float>(a.real(18)), table, table_rows, rotary,
-        PyObject_IsTrue(argv[19]) == 1, static_cast<int32_t*>(address(bi, at::kInt, device, "batch_indices")),
-        static_cast<int32_t*>(address(pos, at::kInt, device, "positions")), k.c, v.c, g.page_size, layout,
-        static_cast<int32_t*>(address(indices, at::kInt, device, "kv_indices")), indices.numel(),
-        static_cast<int32_t*>(address(indptr, at::kInt, device, "kv_indptr")),
-        address<int32_t>(a, 14, at::kInt, device, "kv_last_page_len", true), fits32(batch, "batch_size"), ks, vs, kd, vd,
-        has_recipe ? &recipe : nullptr, o.data, o.stride, address<int32_t>(a, 22, at::kInt, device, "dev_status", true),
-        stream_of(device));
+    const int32_t Hq = fits32(qr.heads, "num_qo_heads"), requests = fits32(batch, "batch_size");
+    const float eps = static_cast<float>(a.real(18));
+    const int32_t interleaved = PyObject_IsTrue(argv[19]) == 1;
+    const int32_t* bi_ptr = static_cast<int32_t*>(address(bi, at::kInt, device, "batch_indices"));
+    const int32_t* pos_ptr = static_cast<int32_t*>(address(pos, at::kInt, device, "positions"));
+    const int32_t* idx_ptr = static_cast<int32_t*>(address(indices, at::kInt, device, "kv_indices"));
+    const int32_t* ptr_ptr = static_cast<int32_t*>(address(indptr, at::kInt, device, "kv_indptr"));
+    const int32_t* last_ptr = address<int32_t>(a, 14, at::kInt, device, "kv_last_page_len", true);
+    int32_t* status = address<int32_t>(a, 22, at::kInt, device, "dev_status", true);
+    const nvfp4_4over6_config* r = has_recipe ? &recipe : nullptr;
+    nvfp4_status st;
+    if (a.none(23) && a.none(24)) {
+      st = nvfp4_qk_norm_rope_append_paged(qr.data, kr.data, vr.data, code, qr.n, Hq, g.heads, g.head_dim, qr.stride, kr.stride,
+                                           vr.stride, w[0], w[1], eps, table, table_rows, rotary, interleaved, bi_ptr, pos_ptr,
+                                           k.c, v.c, g.page_size, layout, idx_ptr, indices.numel(), ptr_ptr, last_ptr, requests,
+                                           ks, vs, kd, vd, r, o.data, o.stride, status, stream_of(device));
+    } else {
+      if (a.none(23) || a.none(24)) refuse("rotary_positions and rotary_axes go together");
+      const at::Tensor &ap = a.tensor(23, "rotary_positions"), &ax = a.tensor(24, "rotary_axes");
+      if (ap.dim() != 2 || ap.size(1) != qr.n) refuse("rotary_positions must be [axes, n] with a column for each row");
+      if (ax.numel() != rotary / 2) refuse("rotary_axes must have an entry for each of cos_sin's rotary_dim / 2 pairs");
+      st = nvfp4_qk_norm_rope_axes_append_paged(
+          qr.data, kr.data, vr.data, code, qr.n, Hq, g.heads, g.head_dim, qr.stride, kr.stride, vr.stride, w[0], w[1], eps,
+          table, table_rows, rotary, interleaved, static_cast<int32_t*>(address(ap, at::kInt, device, "rotary_positions")),
+          fits32(ap.size(0), "axes"), static_cast<uint8_t*>(address(ax, at::kByte, device, "rotary_axes")), bi_ptr, pos_ptr,
+          k.c, v.c, g.page_size, layout, idx_ptr, indices.numel(), ptr_ptr, last_ptr, requests, ks, vs, kd, vd, r, o.data,
+          o.stride, status, stream_of(device));
+    }
     if (st != NVFP4_OK) return PyLong_FromLong(st);
     return THPVariable_Wrap(out);
   });
@@ -386,9 +404,9 @@ PyObject* select_pages(PyObject*, PyObject* const* argv, Py_ssize_t n) {
 }
 
 // query, k codes, v codes, k scales, v scales, block_tables, seq_lens, selected, count (None: all pages), k_scale,
-// v_scale, layout, sm_scale (None: head_dim ** -0.5), soft cap, window_left, out, lse, dev_status
+// v_scale, layout, sm_scale (None: head_dim ** -0.5), soft cap, window_left, out, lse, dev_status, num_sink_tokens
 PyObject* attention(PyObject*, PyObject* const* argv, Py_ssize_t n) {
-  return guarded(n, 18, [&]() -> PyObject* {
+  return guarded(n, 19, [&]() -> PyObject* {
     const Args a{argv};
     const at::Tensor& q = first(a.tensor(0, "query"));
     const at::Device device = q.device();
@@ -432,9 +450,15 @@ PyObject* attention(PyObject*, PyObject* const* argv, Py_ssize_t n) {
     float* lse_ptr = static_cast<float*>(address(lse, at::kFloat, device, "lse"));
     int32_t* status = address<int32_t>(a, 17, at::kInt, device, "dev_status", true);
     if (a.none(7)) {
-      st = nvfp4_paged_attention_decode(r.data, code, r.stride, Hq, k.c, v.c, g.page_size, g.heads, g.head_dim, layout,
-                                        t.data, t.type, t.width, len_ptr, batch, gk, gv, sm, cap,
-                                        a.int32(14, "window_left"), out_ptr, lse_ptr, status, ws.data_ptr(), ws.numel(), stream);
+      const int32_t window = a.int32(14, "window_left"), sinks = a.int32(18, "num_sink_tokens");
+      if (sinks == 0)
+        st = nvfp4_paged_attention_decode(r.data, code, r.stride, Hq, k.c, v.c, g.page_size, g.heads, g.head_dim, layout,
+                                          t.data, t.type, t.width, len_ptr, batch, gk, gv, sm, cap, window, out_ptr, lse_ptr,
+                                          status, ws.data_ptr(), ws.numel(), stream);
+      else
+        st = nvfp4_paged_attention_decode_sinks(r.data, code, r.stride, Hq, k.c, v.c, g.page_size, g.heads, g.head_dim,
+                                                layout, t.data, t.type, t.width, len_ptr, batch, gk, gv, sm, cap, window,
+                                                sinks, out_ptr, lse_ptr, status, ws.data_ptr(), ws.numel(), stream);
     } else {
       const at::Tensor &sel = a.tensor(7, "selected_pages"), &num = a.tensor(8, "num_selected");
       if (sel.dim() != 3 || sel.size(0) != r.n || sel.size(1) != g.heads || num.dim() != 2 || num.size(0) != r.n ||

@@ -76,6 +76,7 @@ nvfp4_status launch_append(const AppendArgs& a, bool bf16, int mode, bool vec256
                            cudaStream_t stream);
 
 // ---- norm, rotation and append -----------------------------------------------------------
+constexpr int kMaxRotaryAxes = 8;
 struct NormRopeArgs {
   AppendArgs ap;  // the key and value rows and where they go
   const uint8_t* q;
@@ -89,6 +90,9 @@ struct NormRopeArgs {
   const float* cos_sin;  // [num_positions, rotary_dim]
   int64_t num_positions;
   int32_t rotary_dim, interleaved;
+  const int32_t* axis_positions;  // [axes, nnz], or null: the rotation goes by `positions`
+  const uint8_t* pair_axes;       // [rotary_dim / 2]
+  int32_t axes;
   int32_t log2_T;  // lanes of a row
   // set at launch: steps of a token's query rows and of its key (value) rows, and the parts that
   // a token's steps are dealt out in

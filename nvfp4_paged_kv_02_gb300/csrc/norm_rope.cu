@@ -5,7 +5,8 @@
 //   r = 1 / sqrt(sum(x^2) * (1/D) + eps),  y = (x * r) * w
 //   pairs (y_a, y_b) of the first R elements:  (y_a c - y_b s,  y_b c + y_a s)
 // with (c, s) from the row of the table at the token's position; the rest of y passes through.
-// Pairs are (i, i + R/2), or (2i, 2i+1) when interleaved. The result is rounded once to the
+// Pairs are (i, i + R/2), or (2i, 2i+1) when interleaved. A token may have a position on each of several
+// axes (time, height, width): pair i then goes by the position on its axis. The result is rounded once to the
 // input type; a key row then goes through the append's block rule (append.cu), as the rounded
 // row would if it were handed to the append. Value rows are quantized as they are.
 //
@@ -13,6 +14,9 @@
 // squares, so that the codes (which jump at the format's borders) are reproducible: eight
 // squares t[i] += t[i+4], t[i+2], t[i+1]; the two groups of eight that rotate together are
 // added; the D/16 pair sums, filled up with zeros to a power of two, add by halves.
+//
+// AXES: positions of several axes. A lane's pairs are four and four neighbours; where four are of one axis
+// (sections of a multiple of four) they are one load as before.
 //
 // T = D/16 rounded up to a power of two lanes work on one row; lane j holds the two groups of
 // eight elements that rotate together: groups j and j + R/16 below R/16, else 2j and 2j+1. A
@@ -129,7 +133,7 @@ __device__ __forceinline__ void norm_rope(const NormRopeArgs& a, const Turn& tur
 // of 128, fp16, 4over6), 142 against 155 (24 and six). Where steps are full, choosing by lane would cost: 184 against 162
 // (eight heads, bf16). Five CTAs to an SM serve the standard recipe's mixed steps (62 against 68 us);
 // the same cap costs the others (66 against 62).
-template <bool BF16, int MODE, bool MIXED>
+template <bool BF16, int MODE, bool MIXED, bool AXES>
 __global__ void __launch_bounds__(kThreads, MIXED && MODE == 0 ? 5 : 0) norm_rope_append_kernel(const NormRopeArgs a) {
   __shared__ Tables tab;
   __shared__ __align__(16) uint4 s_rows[kThreads / 32][64];  // a warp's rows, as groups of eight
@@ -146,6 +150,16 @@ __global__ void __launch_bounds__(kThreads, MIXED && MODE == 0 ? 5 : 0) norm_rop
   turn.turns = j < nr;
   turn.ga = j < nt ? (j < nr ? j : 2 * j) : 0;
   turn.gb = j < nt ? (j < nr ? j + nr : 2 * j + 1) : 0;
+  const int ca = a.interleaved ? 4 * turn.ga : 8 * j, cb = a.interleaved ? 4 * turn.gb : 8 * j + 4;  // its pairs: four from each
+  uint32_t axes_a = 0, axes_b = 0;
+  bool bad_axes = false;
+  if (AXES && turn.turns) {
+    axes_a = __ldg(reinterpret_cast<const uint32_t*>(a.pair_axes + ca));
+    axes_b = __ldg(reinterpret_cast<const uint32_t*>(a.pair_axes + cb));
+#pragma unroll
+    for (int e = 0; e < 32; e += 8)
+      bad_axes = bad_axes || (axes_a >> e & 0xFFu) >= a.axes || (axes_b >> e & 0xFFu) >= a.axes;
+  }
   const int32_t k_end = a.q_steps + (H + per_step - 1) / per_step;  // steps from here on have value rows only
   const int64_t items = a.ap.nnz * a.parts;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp; item < items;
@@ -153,19 +167,57 @@ __global__ void __launch_bounds__(kThreads, MIXED && MODE == 0 ? 5 : 0) norm_rop
     const int64_t i = div_q(item, a.div_parts);
     const int32_t from = static_cast<int32_t>(item - i * a.parts) * a.steps_per_part;
     const int32_t to = min(from + a.steps_per_part, a.q_steps + a.kv_steps);
-    const int32_t pos = __ldg(a.ap.positions + i);
-    if (nr > 0 && (pos < 0 || pos >= a.num_positions)) {
-      if (lane == 0) flag(a.ap.status, NVFP4_DEV_BAD_POSITION);
-      continue;
-    }
-    if (turn.turns && from < k_end) {
-      const float* cs = a.cos_sin + static_cast<int64_t>(pos) * a.rotary_dim;
-      const float* sn = cs + a.rotary_dim / 2;
-      const int ca = a.interleaved ? 4 * turn.ga : 8 * j, cb = a.interleaved ? 4 * turn.gb : 8 * j + 4;
-      load4(cs + ca, turn.c);
-      load4(cs + cb, turn.c + 4);
-      load4(sn + ca, turn.s);
-      load4(sn + cb, turn.s + 4);
+    if (AXES) {
+      // a row of the table for each axis: four pairs of one axis are a 16-byte load, mixed ones four loads
+      bool in = !bad_axes;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t of = k ? axes_b : axes_a;
+        const bool same = of == (of & 0xFFu) * 0x01010101u;
+        int32_t p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[e] = 0;
+          if (turn.turns && !bad_axes && (e == 0 || !same))
+            p[e] = __ldg(a.axis_positions + static_cast<int64_t>(of >> (8 * e) & 0xFFu) * a.ap.nnz + i);
+          if (p[e] < 0 || p[e] >= a.num_positions) {
+            in = false;
+            p[e] = 0;
+          }
+        }
+        if (!turn.turns || from >= k_end || !in) continue;
+        const float* cs = a.cos_sin + (k ? cb : ca);
+        if (same) {
+          cs += static_cast<int64_t>(p[0]) * a.rotary_dim;
+          load4(cs, turn.c + 4 * k);
+          load4(cs + a.rotary_dim / 2, turn.s + 4 * k);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float* at = cs + static_cast<int64_t>(p[e]) * a.rotary_dim + e;
+            turn.c[4 * k + e] = __ldg(at);
+            turn.s[4 * k + e] = __ldg(at + a.rotary_dim / 2);
+          }
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, !in)) {
+        if (lane == 0) flag(a.ap.status, NVFP4_DEV_BAD_POSITION);
+        continue;
+      }
+    } else {
+      const int32_t pos = __ldg(a.ap.positions + i);
+      if (nr > 0 && (pos < 0 || pos >= a.num_positions)) {
+        if (lane == 0) flag(a.ap.status, NVFP4_DEV_BAD_POSITION);
+        continue;
+      }
+      if (turn.turns && from < k_end) {
+        const float* cs = a.cos_sin + static_cast<int64_t>(pos) * a.rotary_dim;
+        const float* sn = cs + a.rotary_dim / 2;
+        load4(cs + ca, turn.c);
+        load4(cs + cb, turn.c + 4);
+        load4(sn + ca, turn.s);
+        load4(sn + cb, turn.s + 4);
+      }
     }
     if (from < a.q_steps) {
       uint4 wa{}, wb{};
@@ -269,11 +321,11 @@ __global__ void __launch_bounds__(kThreads, MIXED && MODE == 0 ? 5 : 0) norm_rop
   }
 }
 
-template <bool BF16, int MODE>
+template <bool BF16, int MODE, bool AXES>
 nvfp4_status launch_t(NormRopeArgs a, cudaStream_t stream) {
   const int per_step = 32 >> a.log2_T;
-  const auto kern = a.ap.H % per_step != 0 ? norm_rope_append_kernel<BF16, MODE, true>
-                                           : norm_rope_append_kernel<BF16, MODE, false>;
+  const auto kern = a.ap.H % per_step != 0 ? norm_rope_append_kernel<BF16, MODE, true, AXES>
+                                           : norm_rope_append_kernel<BF16, MODE, false, AXES>;
   int64_t cap;
   if (nvfp4_status st = resident_ctas(reinterpret_cast<const void*>(kern), kThreads, 0, 32,
                                       "nvfp4_qk_norm_rope_append_paged", &cap))
@@ -294,14 +346,14 @@ nvfp4_status launch_t(NormRopeArgs a, cudaStream_t stream) {
   return check_launch("nvfp4_qk_norm_rope_append_paged");
 }
 
-template <bool BF16>
+template <bool BF16, bool AXES>
 nvfp4_status launch_m(const NormRopeArgs& a, int mode, cudaStream_t s) {
   switch (mode) {
-    case 0: return launch_t<BF16, 0>(a, s);
-    case 1: return launch_t<BF16, 1>(a, s);
-    case 2: return launch_t<BF16, 2>(a, s);
-    case 3: return launch_t<BF16, 3>(a, s);
-    default: return launch_t<BF16, 4>(a, s);
+    case 0: return launch_t<BF16, 0, AXES>(a, s);
+    case 1: return launch_t<BF16, 1, AXES>(a, s);
+    case 2: return launch_t<BF16, 2, AXES>(a, s);
+    case 3: return launch_t<BF16, 3, AXES>(a, s);
+    default: return launch_t<BF16, 4, AXES>(a, s);
   }
 }
 
@@ -309,7 +361,9 @@ nvfp4_status launch_m(const NormRopeArgs& a, int mode, cudaStream_t s) {
 
 nvfp4_status launch_norm_rope_append(const NormRopeArgs& a, bool bf16, int mode,
                                      cudaStream_t stream) {
-  return bf16 ? launch_m<true>(a, mode, stream) : launch_m<false>(a, mode, stream);
+  if (a.axis_positions)
+    return bf16 ? launch_m<true, true>(a, mode, stream) : launch_m<false, true>(a, mode, stream);
+  return bf16 ? launch_m<true, false>(a, mode, stream) : launch_m<false, false>(a, mode, stream);
 }
 
 }  // namespace nvfp4
