@@ -20,7 +20,7 @@
  *   - norm and rotation of the query and key rows with the append in the same pass
  *   - bounds of each page's keys, and the pages that they promise the largest scores for
  *   - attention of one new token per request, over all pages, over a window with the first tokens, or
- *     over selected pages
+ *     over selected pages; and of several (prompts, chunks, drafts)
  *
  * Number formats: E2M1 codes (grid {0,0.5,1,1.5,2,3,4,6}, 4 bits, two per byte, element
  * 2k in the low nibble); E4M3 (e4m3fn) block scales stored as bytes, one per 16
@@ -635,6 +635,52 @@ nvfp4_status nvfp4_sparse_paged_attention_decode(
     int32_t batch_size, const int32_t* selected_pages, const int32_t* num_selected,
     int32_t max_selected, const float* k_scale, const float* v_scale, float sm_scale,
     float logits_soft_cap, void* out, float* lse, int32_t* dev_status, void* workspace,
+    int64_t workspace_bytes, void* stream);
+
+/* ---- prompts ------------------------------------------------------------------------------ */
+
+/* Bytes of the workspace of nvfp4_paged_attention_prefill (some 40 MB). */
+nvfp4_status nvfp4_paged_attention_prefill_workspace_bytes(int32_t head_dim, int64_t* bytes);
+
+/* Attention of the last tokens of each request (a prompt, a chunk of one, drafts to be verified) over a paged
+ * NVFP4 cache that holds their keys and values already (append first). Rows [qo_indptr[b], qo_indptr[b+1]) of
+ * query are the last n tokens of request b, token i of them at position p = seq_lens[b] - n + i. For its query
+ * head j of KV head h = j / (num_qo_heads / num_kv_heads), over the live positions t:
+ *   x_t = sm_scale * k_scale * sum_d q_d K[t, d]     (K, V: e2m1 * S)
+ *   with logits_soft_cap c > 0:  x_t = c tanh(x_t / c)
+ *   out = v_scale * sum_t exp(x_t) V[t, :] / sum_t exp(x_t),   lse = log sum_t exp(x_t)
+ * Live are the positions t < seq_lens[b]; with causal = 1 only t <= p; with window_left >= 0 only
+ * t >= p - window_left or t < num_sink_tokens. Positions on a page outside the pool are left out
+ * (NVFP4_DEV_BAD_PAGE). A row with no live position gets out = 0 and lse = -inf (a request with more query
+ * tokens than positions has such rows under causal), and so does a row whose live scores are all -inf. NaN in a
+ * query row or in a live block scale shows in the outputs that the formula has it in, and in no others. What the
+ * slots past a request's end hold is of no consequence. Rows of no request are left as they were. An entry of
+ * qo_indptr outside [0, nnz] or below the one before it is reported (NVFP4_DEV_BAD_BATCH) and taken as the nearest
+ * that is not.
+ * K and V are exact; query rows, weights and sums are rounded and accumulated as by nvfp4_paged_attention_decode.
+ * The result does not depend on scheduling, nor a row's on the other rows' values.
+ *   query         device [nnz, num_qo_heads, head_dim] of dtype, tokens query_row_stride elements apart;
+ *                 16-byte aligned, stride a multiple of 8.
+ *   qo_indptr     device int32 [batch_size + 1].
+ *   causal        0 or 1.
+ *   out           device, contiguous [nnz, num_qo_heads, head_dim] of dtype, 16-byte aligned.
+ *   lse           device float [nnz, num_qo_heads], or NULL.
+ *   dev_status    NVFP4_DEV_TIMEOUT besides the others, if a wait of the kernel's warps for one another ran out.
+ *   workspace     device, workspace_bytes >= nvfp4_paged_attention_prefill_workspace_bytes, 16-byte aligned; holds
+ *                 anything past its first NVFP4_COUNTER_BYTES bytes, which are not touched (so a workspace of the
+ *                 decode calls that is large enough serves too). One call at a time.
+ *   The other arguments are those of nvfp4_paged_attention_decode.
+ * Requirements: num_qo_heads a multiple of num_kv_heads, head_dim a multiple of 16 and at most 256, batch_size at
+ * most 16384, at most 2^31 - 1 pages in the pool, query tokens and positions of a request, at most 2^37 query
+ * rows (nnz * num_qo_heads), sm_scale finite, logits_soft_cap finite and >= 0, num_sink_tokens >= 0. */
+nvfp4_status nvfp4_paged_attention_prefill(
+    const void* query, int32_t dtype, int64_t nnz, int64_t query_row_stride, int32_t num_qo_heads,
+    const int32_t* qo_indptr, nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache,
+    int32_t page_size, int32_t num_kv_heads, int32_t head_dim, int32_t kv_layout,
+    const void* block_tables, int32_t table_dtype, int32_t max_pages_per_request,
+    const int32_t* seq_lens, int32_t batch_size, const float* k_scale, const float* v_scale,
+    int32_t causal, float sm_scale, float logits_soft_cap, int32_t window_left,
+    int32_t num_sink_tokens, void* out, float* lse, int32_t* dev_status, void* workspace,
     int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus

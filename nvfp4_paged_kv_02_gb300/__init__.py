@@ -24,6 +24,7 @@ Operators of a decode step over such a cache (additions of this library):
   nvfp4_select_pages                   the pages whose bounds promise the largest scores
   nvfp4_paged_attention_decode         attention of one new token per request (sliding windows, first tokens that stay)
   nvfp4_sparse_paged_attention_decode  the same over selected pages
+  nvfp4_paged_attention_prefill        attention of the last tokens of each request: prompts, chunks, drafts
 """
 
 from __future__ import annotations
@@ -48,6 +49,7 @@ __all__ = [
     "nvfp4_4over6_code", "nvfp4_4over6_from_code", "nvfp4_qk_norm_rope_append_paged",
     "nvfp4_page_key_bounds", "nvfp4_select_pages", "nvfp4_paged_attention_decode",
     "nvfp4_sparse_paged_attention_decode", "nvfp4_rotary_axes",
+    "nvfp4_paged_attention_prefill",
 ]
 
 LIB_PATH = _build.LIB_PATH
@@ -187,6 +189,12 @@ def load() -> ctypes.CDLL:
         L.nvfp4_paged_attention_decode.argtypes = [
             vp, i32, i64, i32, _Cache, _Cache, i32, i32, i32, i32, vp, i32, i32, vp, i32, vp, vp, f32,
             f32, i32, vp, vp, vp, vp, i64, vp]
+        L.nvfp4_paged_attention_prefill_workspace_bytes.restype = i32
+        L.nvfp4_paged_attention_prefill_workspace_bytes.argtypes = [i32, vp]
+        L.nvfp4_paged_attention_prefill.restype = i32
+        L.nvfp4_paged_attention_prefill.argtypes = [
+            vp, i32, i64, i64, i32, vp, _Cache, _Cache, i32, i32, i32, i32, vp, i32, i32, vp, i32, vp, vp, i32,
+            f32, f32, i32, i32, vp, vp, vp, vp, i64, vp]
         L.nvfp4_paged_attention_decode_sinks.restype = i32
         L.nvfp4_paged_attention_decode_sinks.argtypes = [
             vp, i32, i64, i32, _Cache, _Cache, i32, i32, i32, i32, vp, i32, i32, vp, i32, vp, vp, f32,
@@ -769,3 +777,24 @@ def nvfp4_sparse_paged_attention_decode(query: torch.Tensor, paged_kv_cache, kv_
     return _done("nvfp4_sparse_paged_attention_decode", _calls().attention(
         query, k, v, ks, vs, block_tables, seq_lens, selected_pages, num_selected, k_scale, v_scale,
         _layout(kv_layout), sm_scale, logits_soft_cap, -1, out, lse, dev_status, 0))
+
+
+def nvfp4_paged_attention_prefill(query: torch.Tensor, paged_kv_cache, kv_cache_sf, qo_indptr: torch.Tensor,
+                                  block_tables: torch.Tensor, seq_lens: torch.Tensor, k_scale: torch.Tensor,
+                                  v_scale: torch.Tensor, kv_layout: str = "NHD", causal: bool = True,
+                                  sm_scale: Optional[float] = None, logits_soft_cap: float = 0.0,
+                                  window_left: int = -1, num_sink_tokens: int = 0,
+                                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                                  dev_status: Optional[torch.Tensor] = None):
+    """Attention of the last tokens of each request (a prompt, a chunk of one, drafts), query [nnz, Hq, D],
+    over the paged cache's first seq_lens[b] positions, which hold the new tokens' keys and values already.
+    Rows qo_indptr[b] .. qo_indptr[b + 1] (int32 [B + 1]) are request b's last tokens. With `causal` a token
+    sees the positions up to its own; with window_left >= 0 only the last window_left + 1 of those, and the
+    first num_sink_tokens. Returns (out [nnz, Hq, D], lse float32 [nnz, Hq], natural logarithm); a row that
+    sees no position gets 0 and -inf, rows of no request are left as they were (give `out` and `lse`, if it
+    matters). The other arguments are those of nvfp4_paged_attention_decode."""
+    k, v = _pair(paged_kv_cache)
+    ks, vs = _pair(kv_cache_sf)
+    return _done("nvfp4_paged_attention_prefill", _calls().prefill(
+        query, k, v, ks, vs, qo_indptr, block_tables, seq_lens, k_scale, v_scale, _layout(kv_layout), causal, sm_scale,
+        logits_soft_cap, window_left, num_sink_tokens, out, lse, dev_status))

@@ -1238,4 +1238,92 @@ NVFP4_EXPORT nvfp4_status nvfp4_sparse_paged_attention_decode(
   });
 }
 
+NVFP4_EXPORT nvfp4_status nvfp4_paged_attention_prefill_workspace_bytes(int32_t head_dim, int64_t* bytes) {
+  return guarded([&]() -> nvfp4_status {
+    const std::string f = "nvfp4_paged_attention_prefill_workspace_bytes";
+    if (head_dim < 16 || head_dim % 16 != 0)
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": head_dim must be a positive multiple of 16");
+    if (head_dim > kAttnMaxHeadDim) return fail(NVFP4_ERR_UNSUPPORTED, f + ": head_dim above 256");
+    if (!bytes) return fail(NVFP4_ERR_INVALID_ARG, f + ": bytes is null");
+    *bytes = prefill_workspace_bytes(head_dim);
+    return NVFP4_OK;
+  });
+}
+
+NVFP4_EXPORT nvfp4_status nvfp4_paged_attention_prefill(
+    const void* query, int32_t dtype, int64_t nnz, int64_t query_row_stride, int32_t num_qo_heads,
+    const int32_t* qo_indptr, nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache,
+    int32_t page_size, int32_t num_kv_heads, int32_t head_dim, int32_t kv_layout,
+    const void* block_tables, int32_t table_dtype, int32_t max_pages_per_request,
+    const int32_t* seq_lens, int32_t batch_size, const float* k_scale, const float* v_scale,
+    int32_t causal, float sm_scale, float logits_soft_cap, int32_t window_left,
+    int32_t num_sink_tokens, void* out, float* lse, int32_t* dev_status, void* workspace,
+    int64_t workspace_bytes, void* stream) {
+  return guarded([&]() -> nvfp4_status {
+    const char* fn = "nvfp4_paged_attention_prefill";
+    const std::string f(fn);
+    if (nvfp4_status st = check_geometry(fn, page_size, num_kv_heads, head_dim, kv_layout)) return st;
+    if (nvfp4_status st = check_dtype(f, dtype)) return st;
+    if (nvfp4_status st = check_query_heads(f, num_qo_heads, num_kv_heads)) return st;
+    if (head_dim > kAttnMaxHeadDim) return fail(NVFP4_ERR_UNSUPPORTED, f + ": head_dim above 256");
+    if (nvfp4_status st = check_tables(f, table_dtype, max_pages_per_request, batch_size)) return st;
+    if (nnz < 0) return fail(NVFP4_ERR_INVALID_ARG, f + ": negative size");
+    if (causal != 0 && causal != 1) return fail(NVFP4_ERR_INVALID_ARG, f + ": causal must be 0 or 1");
+    if (!std::isfinite(sm_scale)) return fail(NVFP4_ERR_INVALID_ARG, f + ": sm_scale must be finite");
+    if (!(std::isfinite(logits_soft_cap) && logits_soft_cap >= 0.0f))
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": logits_soft_cap must be finite and >= 0");
+    if (num_sink_tokens < 0) return fail(NVFP4_ERR_INVALID_ARG, f + ": num_sink_tokens must be >= 0");
+    if (nvfp4_status st = check_cache(fn, "k_cache", k_cache, page_size, num_kv_heads, head_dim)) return st;
+    if (nvfp4_status st = check_cache(fn, "v_cache", v_cache, page_size, num_kv_heads, head_dim)) return st;
+    if (nvfp4_status st = check_pool(f, std::min(k_cache.num_pages, v_cache.num_pages))) return st;
+    if (nnz == 0 || batch_size == 0) return NVFP4_OK;
+    // Query tokens are counted in 32 bits, segments of rows and positions too.
+    const int64_t reach = static_cast<int64_t>(max_pages_per_request) * page_size;
+    if (nnz > INT32_MAX || nnz > (int64_t(1) << 37) / num_qo_heads || reach > INT32_MAX)
+      return fail(NVFP4_ERR_UNSUPPORTED, f + ": more than 2^31 - 1 query tokens or positions of a request, or 2^37 query rows");
+    const int64_t row = static_cast<int64_t>(num_qo_heads) * head_dim;
+    if (nvfp4_status st = check_rows(f, "query", query, query_row_stride, row)) return st;
+    if (nvfp4_status st = check_rows(f, "out", out, row, row)) return st;
+    if (!qo_indptr || !seq_lens || !k_scale || !v_scale || (!block_tables && max_pages_per_request > 0))
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": null device pointer");
+    if (!aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(lse, 4))
+      return fail(NVFP4_ERR_ALIGNMENT, f + ": scales and lse must be 4-byte aligned");
+    if (workspace_bytes < prefill_workspace_bytes(head_dim) || !workspace)
+      return fail(NVFP4_ERR_INVALID_ARG, f + ": the workspace is smaller than nvfp4_paged_attention_prefill_workspace_bytes");
+    if (!aligned(workspace, 16)) return fail(NVFP4_ERR_ALIGNMENT, f + ": workspace must be 16-byte aligned");
+    PrefillArgs a{};
+    a.q = static_cast<const uint8_t*>(query);
+    a.q_row_bytes = query_row_stride * 2;
+    a.nnz = nnz;
+    a.kc = k_cache;
+    a.vc = v_cache;
+    a.ps = page_size;
+    a.Hq = num_qo_heads;
+    a.H = num_kv_heads;
+    a.G = num_qo_heads / num_kv_heads;
+    a.D = head_dim;
+    a.layout = kv_layout;
+    a.B = batch_size;
+    a.bf16 = dtype == NVFP4_BF16;
+    a.table64 = table_dtype == NVFP4_I64;
+    a.causal = causal;
+    a.div_ps = make_div(page_size);
+    a.qo_indptr = qo_indptr;
+    a.block_tables = block_tables;
+    a.max_pages = max_pages_per_request;
+    a.seq_lens = seq_lens;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.sm_scale = sm_scale;
+    a.soft_cap = logits_soft_cap;
+    a.window_left = window_left;
+    a.sink = num_sink_tokens;
+    a.out = static_cast<uint8_t*>(out);
+    a.lse = lse;
+    a.status = dev_status;
+    a.workspace = workspace;
+    return launch_prefill(a, static_cast<cudaStream_t>(stream));
+  });
+}
+
 }  // extern "C"

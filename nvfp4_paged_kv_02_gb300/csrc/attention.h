@@ -1,5 +1,5 @@
 // attention.h -- arguments of the operators that read a paged NVFP4 cache with a query:
-// page bounds, page selection and attention of one new token per request.
+// page bounds, page selection, attention of one new token per request and of several.
 #pragma once
 
 #include "internal.h"
@@ -40,6 +40,36 @@ struct AttentionArgs {
 // Device memory that a launch needs, whatever the lengths.
 int64_t attention_workspace_bytes(int32_t Hq, int32_t H, int32_t D);
 nvfp4_status launch_attention(AttentionArgs a, cudaStream_t stream);
+
+struct PrefillArgs {
+  const uint8_t* q;
+  int64_t q_row_bytes, nnz;
+  nvfp4_paged_cache kc, vc;
+  int32_t ps, Hq, H, G, D, layout, B;
+  int32_t bf16, table64, causal;
+  Div div_ps;
+  const int32_t* qo_indptr;  // [B + 1]
+  const void* block_tables;
+  int64_t max_pages;
+  const int32_t* seq_lens;
+  const float* k_scale;
+  const float* v_scale;
+  float sm_scale, soft_cap;
+  int32_t window_left, sink;
+  uint8_t* out;
+  float* lse;  // may be null
+  int32_t* status;
+  void* workspace;
+  // set at launch
+  int64_t pool_pages, parts_offset;
+  PipeTest pipe;
+};
+// In the workspace, for each run: the segment that it begins and others continue, up to run `last` (-1: none).
+struct PrefillCut {
+  int32_t b, t, h, last;
+};
+int64_t prefill_workspace_bytes(int32_t D);
+nvfp4_status launch_prefill(PrefillArgs a, cudaStream_t stream);
 
 struct BoundsArgs {
   nvfp4_paged_cache kc;

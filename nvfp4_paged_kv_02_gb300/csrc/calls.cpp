@@ -475,6 +475,60 @@ PyObject* attention(PyObject*, PyObject* const* argv, Py_ssize_t n) {
   });
 }
 
+// query, k codes, v codes, k scales, v scales, qo_indptr, block_tables, seq_lens, k_scale, v_scale, layout, causal,
+// sm_scale (None: head_dim ** -0.5), soft cap, window_left, num_sink_tokens, out, lse, dev_status
+PyObject* prefill(PyObject*, PyObject* const* argv, Py_ssize_t n) {
+  return guarded(n, 19, [&]() -> PyObject* {
+    const Args a{argv};
+    const at::Tensor& q = first(a.tensor(0, "query"));
+    const at::Device device = q.device();
+    const c10::cuda::CUDAGuard on(device);
+    const auto type = q.scalar_type();
+    const int32_t code = dtype_code(q);
+    const Cache k = cache_of(a.tensor(1, "k_cache"), a.tensor(3, "k scales"), device);
+    const Cache v = cache_of(a.tensor(2, "v_cache"), a.tensor(4, "v scales"), device);
+    if (k.a != v.a || k.b != v.b || k.last != v.last) refuse("the K and V caches must have the same page shape");
+    const int32_t layout = a.int32(10, "kv_layout");
+    const Geometry g = geometry_of(k, layout);
+    const Rows r = rows_of(q, type, device, "query", -1, g.head_dim);
+    const at::Tensor &indptr = a.tensor(5, "qo_indptr"), &lens = a.tensor(7, "seq_lens");
+    const int64_t batch = lens.numel();
+    if (indptr.numel() != batch + 1) refuse("qo_indptr must have one entry more than seq_lens");
+    const Tables t = tables_of(a.tensor(6, "block_tables"), batch, device);
+    const float *gk = device_scale(a, 8, device), *gv = device_scale(a, 9, device);
+    at::Tensor out, lse;
+    if (a.none(16)) {
+      out = at::empty({r.n, r.heads, g.head_dim}, q.options());
+    } else {
+      out = a.tensor(16, "out");
+      if (out.dim() != 3 || out.size(0) != r.n || out.size(1) != r.heads || out.size(2) != g.head_dim)
+        refuse("out must be [nnz, num_qo_heads, head_dim]");
+    }
+    if (a.none(17)) {
+      lse = at::empty({r.n, r.heads}, q.options().dtype(at::kFloat));
+    } else {
+      lse = a.tensor(17, "lse");
+      if (lse.dim() != 2 || lse.size(0) != r.n || lse.size(1) != r.heads) refuse("lse must be [nnz, num_qo_heads]");
+    }
+    int64_t bytes = 0;
+    nvfp4_status st = nvfp4_paged_attention_prefill_workspace_bytes(g.head_dim, &bytes);
+    if (st != NVFP4_OK) return PyLong_FromLong(st);
+    const cudaStream_t stream = stream_of(device);
+    const at::Tensor ws = attention_workspace(device, stream, bytes);
+    const float sm = a.none(12) ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(g.head_dim))) : static_cast<float>(a.real(12));
+    st = nvfp4_paged_attention_prefill(
+        r.data, code, r.n, r.stride, fits32(r.heads, "num_qo_heads"),
+        static_cast<int32_t*>(address(indptr, at::kInt, device, "qo_indptr")), k.c, v.c, g.page_size, g.heads, g.head_dim, layout,
+        t.data, t.type, t.width, static_cast<int32_t*>(address(lens, at::kInt, device, "seq_lens")), fits32(batch, "batch_size"),
+        gk, gv, PyObject_IsTrue(argv[11]) == 1, sm, static_cast<float>(a.real(13)), a.int32(14, "window_left"),
+        a.int32(15, "num_sink_tokens"), address(out, type, device, "out"),
+        static_cast<float*>(address(lse, at::kFloat, device, "lse")), address<int32_t>(a, 18, at::kInt, device, "dev_status", true),
+        ws.data_ptr(), ws.numel(), stream);
+    if (st != NVFP4_OK) return PyLong_FromLong(st);
+    return pair(out, lse);
+  });
+}
+
 // The attention's workspaces that are kept, the last one used first: (device, stream's id, thread of a
 // per-thread stream, bytes).
 PyObject* workspaces(PyObject*, PyObject* const*, Py_ssize_t n) {
@@ -497,6 +551,7 @@ PyMethodDef kMethods[] = {
     {"page_key_bounds", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(page_key_bounds)), METH_FASTCALL, nullptr},
     {"select_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(select_pages)), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(attention)), METH_FASTCALL, nullptr},
+    {"prefill", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(prefill)), METH_FASTCALL, nullptr},
     {"workspaces", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(workspaces)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -1,0 +1,110 @@
+// tcgen05.cuh -- fifth-generation tensor core forms for sm_103a: tensor memory, matrix products of binary16
+// tiles with binary32 sums, and their completion on an mbarrier.
+//
+// Tiles in shared memory are stored in atoms of 64 elements (128 bytes) a row, eight rows (1024 bytes) to a
+// swizzle group, the 16-byte chunks of row r exchanged by XOR with r % 8. The same bytes serve as a K-major
+// operand (rows are M or N, the 64 elements are K) and as an MN-major one (rows are K).
+#pragma once
+
+#include <cstdint>
+
+#include "pipeline.cuh"
+
+namespace nvfp4 {
+
+constexpr uint32_t kTmemColumns = 512;
+
+// The registers of a warpgroup's threads from here on (all of its warps call it): fewer, or more, which waits until
+// others have given theirs up.
+template <int N, bool MORE>
+__device__ __forceinline__ void set_registers() {
+  if (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// All 32 lanes of one warp; the address goes to shared memory. Waits while another CTA of the SM holds columns.
+__device__ __forceinline__ void tmem_alloc(uint32_t* address) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(address)),
+               "n"(kTmemColumns) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t address) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(address), "n"(kTmemColumns));
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Ordinary stores to shared memory become visible to the tensor cores.
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// A shared-memory operand in 128-byte swizzle atoms. `mn_stride`: bytes between atoms of 64 along M or N (of an
+// MN-major operand; a K-major one does not use it). Eight rows are 1024 bytes apart.
+__device__ __forceinline__ uint64_t smem_operand(uint32_t address, uint32_t mn_stride) {
+  return static_cast<uint64_t>((address & 0x3FFFFu) >> 4) | static_cast<uint64_t>(mn_stride >> 4) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+
+// Instruction descriptor: binary16 operands, binary32 sums, 128 x N; b_mn: B is MN-major.
+__device__ __forceinline__ uint32_t mma_shape(uint32_t n, bool b_mn) {
+  return 1u << 4 | (b_mn ? 1u << 16 : 0u) | (n >> 3) << 17 | (128u >> 4) << 24;
+}
+
+// D (tensor memory) = A B + (sum ? D : 0) over 16 elements of K; one thread issues it.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool sum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(shape),
+      "r"(static_cast<uint32_t>(sum)) : "memory");
+}
+// The same with A in tensor memory (two binary16 elements to a column).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool sum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(shape),
+      "r"(static_cast<uint32_t>(sum)) : "memory");
+}
+// An arrival on `bar` when every product that this thread has issued is done.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// 32 or 16 columns of this warp's 32 lanes, a column to a register. Loads are asynchronous: the registers hold the
+// values after tmem_wait, which takes them so that no use of them comes before it.
+#define NVFP4_R8(v, i) "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3]), "=f"(v[i + 4]), "=f"(v[i + 5]), "=f"(v[i + 6]), "=f"(v[i + 7])
+#define NVFP4_RW8(v, i) "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7])
+#define NVFP4_IN8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+#define NVFP4_INF8(v, i) "f"(v[i]), "f"(v[i + 1]), "f"(v[i + 2]), "f"(v[i + 3]), "f"(v[i + 4]), "f"(v[i + 5]), "f"(v[i + 6]), "f"(v[i + 7])
+__device__ __forceinline__ void tmem_load(float (&v)[32], uint32_t address) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : NVFP4_R8(v, 0), NVFP4_R8(v, 8), NVFP4_R8(v, 16), NVFP4_R8(v, 24) : "r"(address));
+}
+__device__ __forceinline__ void tmem_load(float (&v)[16], uint32_t address) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : NVFP4_R8(v, 0), NVFP4_R8(v, 8) : "r"(address));
+}
+__device__ __forceinline__ void tmem_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : NVFP4_RW8(v, 0), NVFP4_RW8(v, 8), NVFP4_RW8(v, 16), NVFP4_RW8(v, 24) :: "memory");
+}
+__device__ __forceinline__ void tmem_wait(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : NVFP4_RW8(v, 0), NVFP4_RW8(v, 8) :: "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t address, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::
+          NVFP4_IN8(v, 0), NVFP4_IN8(v, 8), "r"(address) : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t address, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::
+          NVFP4_INF8(v, 0), NVFP4_INF8(v, 8), "r"(address) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+#undef NVFP4_R8
+#undef NVFP4_RW8
+#undef NVFP4_IN8
+#undef NVFP4_INF8
+
+}  // namespace nvfp4
