@@ -671,8 +671,9 @@ nvfp4_status nvfp4_paged_attention_prefill_workspace_bytes(int32_t head_dim, int
  *                 decode calls that is large enough serves too). One call at a time.
  *   The other arguments are those of nvfp4_paged_attention_decode.
  * Requirements: num_qo_heads a multiple of num_kv_heads, head_dim a multiple of 16 and at most 256, batch_size at
- * most 16384, at most 2^31 - 1 pages in the pool, query tokens and positions of a request, at most 2^37 query
- * rows (nnz * num_qo_heads), sm_scale finite, logits_soft_cap finite and >= 0, num_sink_tokens >= 0. */
+ * most 16384, at most 2^31 - 1 pages in the pool, at most 2^31 - 512 query rows of a KV head (nnz * num_qo_heads /
+ * num_kv_heads) and positions of a request (max_pages_per_request * page_size), page strides of at most 4 GiB,
+ * sm_scale finite, logits_soft_cap finite and >= 0, num_sink_tokens >= 0. */
 nvfp4_status nvfp4_paged_attention_prefill(
     const void* query, int32_t dtype, int64_t nnz, int64_t query_row_stride, int32_t num_qo_heads,
     const int32_t* qo_indptr, nvfp4_paged_cache k_cache, nvfp4_paged_cache v_cache,

@@ -1277,10 +1277,10 @@ NVFP4_EXPORT nvfp4_status nvfp4_paged_attention_prefill(
     if (nvfp4_status st = check_cache(fn, "v_cache", v_cache, page_size, num_kv_heads, head_dim)) return st;
     if (nvfp4_status st = check_pool(f, std::min(k_cache.num_pages, v_cache.num_pages))) return st;
     if (nnz == 0 || batch_size == 0) return NVFP4_OK;
-    // Query tokens are counted in 32 bits, segments of rows and positions too.
-    const int64_t reach = static_cast<int64_t>(max_pages_per_request) * page_size;
-    if (nnz > INT32_MAX || nnz > (int64_t(1) << 37) / num_qo_heads || reach > INT32_MAX)
-      return fail(NVFP4_ERR_UNSUPPORTED, f + ": more than 2^31 - 1 query tokens or positions of a request, or 2^37 query rows");
+    // A KV head's query rows are counted in 32 bits, positions too (with a tile's slack).
+    const int64_t reach = static_cast<int64_t>(max_pages_per_request) * page_size, most = (int64_t(1) << 31) - 512;
+    if (nnz > most / (num_qo_heads / num_kv_heads) || reach > most)
+      return fail(NVFP4_ERR_UNSUPPORTED, f + ": more than 2^31 - 512 query rows of a KV head or positions of a request");
     const int64_t row = static_cast<int64_t>(num_qo_heads) * head_dim;
     if (nvfp4_status st = check_rows(f, "query", query, query_row_stride, row)) return st;
     if (nvfp4_status st = check_rows(f, "out", out, row, row)) return st;
@@ -1308,6 +1308,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_paged_attention_prefill(
     a.table64 = table_dtype == NVFP4_I64;
     a.causal = causal;
     a.div_ps = make_div(page_size);
+    a.div_g = make_div(a.G);
     a.qo_indptr = qo_indptr;
     a.block_tables = block_tables;
     a.max_pages = max_pages_per_request;

@@ -47,7 +47,7 @@ struct PrefillArgs {
   nvfp4_paged_cache kc, vc;
   int32_t ps, Hq, H, G, D, layout, B;
   int32_t bf16, table64, causal;
-  Div div_ps;
+  Div div_ps, div_g;
   const int32_t* qo_indptr;  // [B + 1]
   const void* block_tables;
   int64_t max_pages;
@@ -62,6 +62,7 @@ struct PrefillArgs {
   void* workspace;
   // set at launch
   int64_t pool_pages, parts_offset;
+  uint32_t k_stride, v_stride, k_sf_stride, v_sf_stride;  // page strides, bytes
   PipeTest pipe;
 };
 // In the workspace, for each run: the segment that it begins and others continue, up to run `last` (-1: none).

@@ -16,11 +16,11 @@
 // parts of one that is go to the workspace, and a second kernel adds them in the runs' order: results do not
 // depend on timing.
 //
-// A CTA (one to an SM) has three kinds of warps, which wait for one another on mbarriers only:
-//   load     (8 warps, in two groups that take every second tile) pages are looked up, codes and scales loaded two
-//            tiles ahead into registers, decoded to e2m1 * S, exact in binary16, and written to shared memory in
-//            the tensor cores' order;
-//   product  (one thread) S = Q K^T and O += P V by tcgen05.mma, sums in tensor memory;
+// A CTA (one to an SM) has four kinds of warps, which wait for one another on mbarriers only:
+//   page     (3 warps, in turn) walk the run's tiles, look up the pages and leave each tile's places in a ring;
+//   load     (8 warps) codes and scales are copied to shared memory a tile or two ahead, decoded to e2m1 * S, exact
+//            in binary16, and written in the tensor cores' order;
+//   product  (one warp) S = Q K^T and O += P V by tcgen05.mma, sums in tensor memory;
 //   softmax  (8 warps, a row to a thread) S from tensor memory, its running maximum and sum, P in binary16 back to
 //            tensor memory over S; at a segment's end O to the output. They also bring the next queries.
 // Two streams keep the tensor cores busy while the other one is at its weights: the two halves of 256 rows over the
@@ -41,16 +41,15 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kSoftmaxWarps = 8;
-constexpr int kLoadWarps = 4;   // of a group
-constexpr int kLoadGroups = 2;
-constexpr int kProductWarp = kSoftmaxWarps + kLoadGroups * kLoadWarps;
-constexpr int kWarps = kProductWarp + 4;  // (three of the last warpgroup have nothing to do)
-// Registers of a thread of each warpgroup: the launch's 96 for 640 threads, dealt out again. 2 x 144 + 2 x 72 + 48 =
-// 5 x 96.
-constexpr int kLaunchRegisters = 96, kSoftmaxRegisters = 144, kLoadRegisters = 72, kProductRegisters = 48;
-static_assert(2 * kSoftmaxRegisters + 2 * kLoadRegisters + kProductRegisters <= 5 * kLaunchRegisters, "more than the launch has");
+constexpr int kLoadWarps = 8;
+constexpr int kProductWarp = kSoftmaxWarps + kLoadWarps;
+constexpr int kPageWarps = 3;
+constexpr int kWarps = kProductWarp + 1 + kPageWarps;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMeta = 4;          // tiles whose masks are kept
+// Registers of a thread of each warpgroup: the launch's 96 for 640 threads, dealt out again.
+constexpr int kLaunchRegisters = 96, kSoftmaxRegisters = 136, kLoadRegisters = 64, kOtherRegisters = 80;
+static_assert(2 * kSoftmaxRegisters + 2 * kLoadRegisters + kOtherRegisters <= 5 * kLaunchRegisters, "more than the launch has");
+constexpr int kRing = 8;          // tiles whose places are kept
 constexpr int kSegmentCost = 2;   // what a segment's queries and outputs count for, in tiles
 constexpr int kWholeUnits = 8;    // a segment of so few tiles is not cut
 
@@ -61,7 +60,11 @@ struct Shape {
   static constexpr int kRows = 128 * MT;
   static constexpr int kQBytes = 128 * DP * 2;       // of 128 rows
   static constexpr int kTileBytes = BN * DP * 2;
-  static constexpr int kK = MT * kQBytes, kV = kK + 2 * kTileBytes, kBytes = kV + 2 * kTileBytes;
+  // codes and scales as they are: of kRaw tiles (and one more of scales), K and V
+  static constexpr int kRaw = MT * DP == 256 ? 1 : 2;
+  static constexpr int kCodeBytes = BN * DP / 2, kScaleBytes = BN * DP / 16;
+  static constexpr int kK = MT * kQBytes, kCodes = kK + 4 * kTileBytes, kScales = kCodes + kRaw * 2 * kCodeBytes;
+  static constexpr int kBytes = kScales + (kRaw + 1) * 2 * kScaleBytes;
   static constexpr int kWarpTokens = BN / kLoadWarps;
   static constexpr uint32_t kO = 2 * BN;             // columns of tensor memory: two of S, then O
 };
@@ -82,9 +85,8 @@ __device__ __forceinline__ Request request_of(const PrefillArgs& a, int32_t b) {
 struct Sight {
   int32_t hi, lo, sink;
 };
-__device__ __forceinline__ Sight sight_of(const PrefillArgs& a, const Request& q, int64_t r0, int64_t r1) {
-  const int32_t first = q.L - q.n + static_cast<int32_t>(quotient64(r0, a.G));
-  const int32_t last = q.L - q.n + static_cast<int32_t>(quotient64(r1 - 1, a.G));
+__device__ __forceinline__ Sight sight_of(const PrefillArgs& a, const Request& q, int32_t r0, int32_t r1) {
+  const int32_t first = q.L - q.n + div_q32(r0, a.div_g), last = q.L - q.n + div_q32(r1 - 1, a.div_g);
   Sight s;
   s.hi = a.causal ? max(last + 1, 0) : q.L;
   s.lo = a.window_left >= 0 && first > a.window_left ? min(first - a.window_left, s.hi) : 0;
@@ -107,15 +109,15 @@ struct Segment {
 
 template <class S>
 __device__ __forceinline__ void fill(const PrefillArgs& a, Segment& s) {
-  const int64_t rows = static_cast<int64_t>(s.q.n) * a.G, r0 = static_cast<int64_t>(s.t) * S::kRows;
-  s.see = sight_of(a, s.q, r0, min(rows, r0 + S::kRows));
+  const int32_t rows = s.q.n * a.G, r0 = s.t * S::kRows;
+  s.see = sight_of(a, s.q, r0, min(rows - r0, S::kRows) + r0);
   s.first_units = (s.see.sink + S::BN - 1) / S::BN;
   s.gap = max(s.see.lo / S::BN - s.first_units, 0);
   s.units = s.see.hi > 0 ? (s.see.hi - 1) / S::BN + 1 - s.gap : 0;
 }
 template <class S>
 __device__ __forceinline__ int32_t tiles_of(const PrefillArgs& a, const Request& q) {
-  return static_cast<int32_t>((static_cast<int64_t>(q.n) * a.G + S::kRows - 1) / S::kRows);
+  return static_cast<int32_t>((static_cast<uint32_t>(q.n * a.G) + S::kRows - 1) / S::kRows);
 }
 __device__ __forceinline__ int32_t places_of(int32_t units) { return units + kSegmentCost; }
 // The next segment (the caller knows that there is one).
@@ -124,7 +126,7 @@ __device__ __forceinline__ void next_segment(const PrefillArgs& a, Segment& s) {
   s.start += places_of(s.units);
   if (++s.h < a.H) return;
   s.h = 0;
-  if (static_cast<int64_t>(++s.t) * S::kRows >= static_cast<int64_t>(s.q.n) * a.G) {
+  if (++s.t >= tiles_of<S>(a, s.q)) {
     s.t = 0;
     do s.q = request_of(a, ++s.b);
     while (s.q.n == 0);
@@ -147,16 +149,29 @@ __device__ __forceinline__ Portion portion_of(const Segment& s, int64_t run) {
 }
 
 struct Barriers {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], q_full, o_step, merge, done;
+  uint64_t full[4], empty[4];  // K's two stages, then V's
+  uint64_t s_full[2], p_full[2], o_full[2], q_full[2], o_step, merge, done;
+  uint64_t ring_full[kRing], ring_empty[kRing];
 };
+// One tile of the run, as the page warps leave it to the others. `stream`: bits 0 and 1, the streams whose rows see
+// it; 2 and 3, it is their first of the portion; 4 and 5, their last; 6 and 7, they have one; 8, set. `rest`: tiles of the
+// portion after it.
+struct Tile {
+  uint2 where[128];           // page (kNoPage: none) and row in it of each position
+  uint32_t live[4];           // positions that are on a page of the pool, 32 to a word
+  uint32_t nan[kLoadWarps];   // a load warp's V scales hold NaN
+  uint16_t nan_blocks[128];   // which blocks of a position (where its warp's nan is set)
+  uint32_t stream;
+  int32_t rest, first;        // first: of its portion
+};
+constexpr uint32_t kNoPage = 0xFFFFFFFFu;
+constexpr int32_t kEnd = -1;          // `rest` after the last tile
 struct Shared {
   Barriers bar;
+  Tile ring[kRing];
   Segment first;                      // the run's
   uint32_t tmem;
   int32_t dead;                       // a wait has run out
-  uint32_t live[kMeta][kLoadWarps];   // positions of a tile that are on a page of the pool
-  uint32_t nan[kMeta][kLoadWarps];    // a warp's V scales hold NaN
-  uint16_t nan_blocks[kMeta][128];    // which blocks of a position (where its warp's nan is set)
   float factor[256];                  // of the query rows
   float m[128], l[128];               // of the second stream
   uint32_t poison[128];
@@ -196,7 +211,7 @@ __device__ __forceinline__ int64_t scan_cta(int64_t v, int64_t* s_scan) {
 
 __device__ __forceinline__ uint32_t low_bits(int32_t n) { return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1); }
 
-// E: elements of a row that a lane decodes, 32 (two blocks, 16-byte loads) or 16.
+// E: elements of a row that a lane decodes, 32 (two blocks; 16-byte copies of codes and 4-byte ones of scales) or 16.
 template <int DP, int MT, int E>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs a) {
   using S = Shape<DP, MT>;
@@ -251,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
       for (int32_t f = f0;;) {
         fill<S>(a, s);
         if (stop() || ++f == f1) break;
-        if (static_cast<int64_t>(++s.t) * S::kRows >= static_cast<int64_t>(s.q.n) * a.G) {
+        if (++s.t >= tiles_of<S>(a, s.q)) {
           s.t = 0;
           do s.q = request_of(a, ++s.b);
           while (s.q.n == 0);
@@ -292,18 +307,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
   Barriers& bar = sh.bar;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar.k_full + i, kLoadWarps);
-      mbar_init(bar.v_full + i, kLoadWarps);
-      mbar_init(bar.k_empty + i, 1);
-      mbar_init(bar.v_empty + i, 1);
+      mbar_init(bar.full + i, kLoadWarps);
+      mbar_init(bar.full + 2 + i, kLoadWarps);
+      mbar_init(bar.empty + i, 1);
+      mbar_init(bar.empty + 2 + i, 1);
       mbar_init(bar.s_full + i, 1);
       mbar_init(bar.p_full + i, 4);
       mbar_init(bar.o_full + i, 1);
     }
-    mbar_init(&bar.q_full, kOne ? 4 : kSoftmaxWarps);
+    mbar_init(bar.q_full, kTurns ? kSoftmaxWarps : 4);
+    mbar_init(bar.q_full + 1, 4);  // (of the second half)
     mbar_init(&bar.o_step, 1);
     mbar_init(&bar.merge, kSoftmaxWarps);
     mbar_init(&bar.done, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(bar.ring_full + i, 1);
+      mbar_init(bar.ring_empty + i, 1);
+    }
     sh.dead = 0;
     fence_mbar_init();
   }
@@ -313,328 +333,407 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  // A bounded wait; when it runs out, or another role's has, everyone returns.
-  auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
-    for (uint32_t i = 0; i < limit; ++i) {
-      if (mbar_try_wait(b, parity)) return true;
-      if ((i & 15) == 15 && *static_cast<volatile int32_t*>(&sh.dead)) return false;
-    }
-    if (!*static_cast<volatile int32_t*>(&sh.dead)) flag(a.status, NVFP4_DEV_TIMEOUT);
-    *static_cast<volatile int32_t*>(&sh.dead) = 1;
-    return false;
+  // A warp's bounded wait; when it runs out, or another's has, all of the CTA's warps return.
+  volatile int32_t* const dead = &sh.dead;
+  auto wait_warp = [&](uint64_t* b, uint32_t parity) -> bool {
+    for (uint32_t i = 0; !__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity)); ++i)
+      if (__any_sync(0xFFFFFFFFu, i == limit || *dead != 0)) {
+        *dead = 1;
+        return false;
+      }
+    return true;
   };
-  auto wait_warp = [&](uint64_t* b, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, wait(b, parity)); };
   auto more = [&](const Segment& s) { return s.start + places_of(s.units) < run; };
   const int D = a.D;
   const uint32_t base = smem_addr(smem);
 
-  if (warp >= kProductWarp) {
+  if (warp >= kProductWarp) set_registers<kOtherRegisters, false>();
+  if (warp == kProductWarp) {
     // ---- product ----
-    set_registers<kProductRegisters, false>();
-    if (warp == kProductWarp && lane == 0) {
-      const uint32_t shape_s = mma_shape(BN, false), shape_o = mma_shape(D, true);
-      uint32_t unit = 0, q_count = 0;       // tiles so far, segments so far
-      uint32_t p_count[2] = {0, 0};
-      auto issue_s = [&](int half, int buf, uint32_t g) {
-        const uint32_t q = base + half * S::kQBytes, k = base + S::kK + (g & 1) * S::kTileBytes;
-        for (int i = 0; i < D / 16; ++i)
-          mma_ss(tmem + buf * BN, smem_operand(q + (i >> 2) * 16384 + (i & 3) * 32, 16),
-                 smem_operand(k + (i >> 2) * (BN * 128) + (i & 3) * 32, 16), shape_s, i > 0);
+    const uint32_t shape_s = mma_shape(BN, false), shape_o = mma_shape(D, true);
+    const uint32_t q_op = smem_operand(base, 16), k_op = smem_operand(base + S::kK, 16);
+    const uint32_t v_op = smem_operand(base + S::kK + 2 * S::kTileBytes, BN * 128);
+    uint32_t q_counts = 0, p_counts = 0;  // a bit for each: parities
+    auto commit = [&](uint64_t* b) {
+      if (elected()) mma_commit(b);
+      __syncwarp();
+    };
+    auto issue_s = [&](int half, int buf, uint32_t g) {
+      const uint32_t q = q_op + half * (S::kQBytes / 16), k = k_op + (g & 1) * (S::kTileBytes / 16), d = tmem + buf * BN;
+      if (elected()) {
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i)
+          if (16 * i < D) mma_ss(d, q + (i >> 2) * 1024 + (i & 3) * 2, k + (i >> 2) * (BN * 8) + (i & 3) * 2, shape_s, i > 0);
         mma_commit(bar.s_full + buf);
-      };
-      auto issue_o = [&](int stream, int buf, uint32_t g, bool sum) {
-        const uint32_t v = base + S::kV + (g & 1) * S::kTileBytes;
-        for (int i = 0; i < BN / 16; ++i)
-          mma_ts(tmem + S::kO + stream * DP, tmem + buf * BN + 8 * i, smem_operand(v + i * 2048, BN * 128), shape_o, sum || i > 0);
-      };
-      auto k_ready = [&](uint32_t g) { return wait(bar.k_full + (g & 1), (g >> 1) & 1); };
-      auto v_ready = [&](uint32_t g) { return wait(bar.v_full + (g & 1), (g >> 1) & 1); };
-      auto p_ready = [&](int buf) {
-        if (!wait(bar.p_full + buf, p_count[buf]++ & 1)) return false;
-        tc_fence_after();
-        return true;
-      };
-      Segment s = sh.first;
-      for (bool ok = true; ok;) {
-        const Portion part = portion_of(s, run);
-        const int32_t n = part.end - part.u;
-        if (n > 0) {
-          auto tile = [&](int32_t k) {  // position of the portion's tile k
-            const int32_t u = part.u + k;
-            return (u < s.first_units ? u : u + s.gap) * BN;
-          };
-          ok = wait(&bar.q_full, q_count++ & 1);
-          if (ok) tc_fence_after();
-          if constexpr (kTwo) {
-            const int64_t rows = static_cast<int64_t>(s.q.n) * a.G, r0 = static_cast<int64_t>(s.t) * S::kRows;
-            Sight see[2];
-            int32_t last[2];  // a half's last tile
-            for (int i = 0; i < 2; ++i) {
-              see[i] = {0, 0, 0};
-              if (r0 + 128 * i < rows) see[i] = sight_of(a, s.q, r0 + 128 * i, min(rows, r0 + 128 * i + 128));
-              last[i] = n - 1;
-              while (last[i] >= 0 && !sees<BN>(see[i], tile(last[i]))) --last[i];
-            }
-            bool sum[2] = {false, false};
-            ok = ok && k_ready(unit);
-            if (ok) {
-              tc_fence_after();
-              for (int i = 0; i < 2; ++i)
-                if (sees<BN>(see[i], tile(0))) issue_s(i, i, unit);
-              mma_commit(bar.k_empty + (unit & 1));
-            }
-            for (int32_t k = 0; ok && k < n; ++k) {
-              const uint32_t g = unit + k;
-              bool has_k = false;
-              ok = v_ready(g);
-              for (int i = 0; ok && i < 2; ++i) {
-                if (sees<BN>(see[i], tile(k))) {
-                  ok = p_ready(i);
-                  if (!ok) break;
-                  issue_o(i, i, g, sum[i]);
-                  sum[i] = true;
-                  if (k == last[i]) mma_commit(bar.o_full + i);
-                }
-                if (i == 1) mma_commit(bar.v_empty + (g & 1));
-                if (k + 1 < n && (i == 1 || sees<BN>(see[i], tile(k + 1)))) {
-                  if (!has_k) {
-                    ok = has_k = k_ready(g + 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                  }
-                  if (sees<BN>(see[i], tile(k + 1))) issue_s(i, i, g + 1);
-                  if (i == 1) mma_commit(bar.k_empty + ((g + 1) & 1));
-                }
-              }
-            }
-          } else {
-            // (in one stream, S of the next tile goes ahead of O of this one; in two, S of the one after the next
-            // follows O of this one, whose P it overwrites)
-            constexpr int kAhead = 2;
-            for (int32_t k = 0; ok && k < n + kAhead; ++k) {
-              auto start_s = [&](int32_t j) {
-                if (!k_ready(unit + j)) return false;
-                tc_fence_after();
-                issue_s(0, j & 1, unit + j);
-                mma_commit(bar.k_empty + ((unit + j) & 1));
-                return true;
-              };
-              if (kOne) {
-                if (k < n) ok = start_s(k);
-              } else if (k < 2 && k < n) {
-                ok = start_s(k);
-              }
-              const int32_t j = kOne ? k - 1 : k - 2;  // the tile whose O is next
-              if (!ok || j < 0 || j >= n) continue;
-              const uint32_t g = unit + j;
-              ok = v_ready(g) && p_ready(j & 1);
-              if (!ok) break;
-              tc_fence_after();
-              issue_o(kOne ? 0 : j & 1, j & 1, g, kOne ? j > 0 : j > 1);
-              mma_commit(bar.v_empty + (g & 1));
-              if (kOne) mma_commit(&bar.o_step);
-              if (kOne ? j == n - 1 : j >= n - 2) mma_commit(bar.o_full + (kOne ? 0 : j & 1));
-              if (!kOne && j + 2 < n) ok = start_s(j + 2);
-            }
-          }
-          unit += n;
-        }
-        if (!more(s)) break;
-        next_segment<S>(a, s);
       }
-      // nothing of this CTA is under way any more when it ends
-      mma_commit(&bar.done);
-      for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(&bar.done, 0); ++i) {}
+      __syncwarp();
+    };
+    auto issue_o = [&](int stream, int buf, uint32_t g, bool sum) {
+      const uint32_t v = v_op + (g & 1) * (S::kTileBytes / 16), d = tmem + S::kO + stream * DP, p = tmem + buf * BN;
+      if (elected()) {
+#pragma unroll
+        for (int i = 0; i < BN / 16; ++i) mma_ts(d, p + 8 * i, v + i * 128, shape_o, sum || i > 0);
+      }
+      __syncwarp();
+    };
+    auto k_ready = [&](uint32_t g) {
+      const bool ok = wait_warp(bar.full + (g & 1), (g >> 1) & 1);
+      tc_fence_after();
+      return ok;
+    };
+    auto v_ready = [&](uint32_t g) { return wait_warp(bar.full + 2 + (g & 1), (g >> 1) & 1); };
+    auto q_ready = [&](int half) {
+      const bool ok = wait_warp(bar.q_full + half, q_counts >> half & 1);
+      q_counts ^= 1u << half;
+      return ok;
+    };
+    auto p_ready = [&](int buf) {
+      const bool ok = wait_warp(bar.p_full + buf, p_counts >> buf & 1);
+      p_counts ^= 1u << buf;
+      tc_fence_after();
+      return ok;
+    };
+    auto tile_ready = [&](uint32_t g) { return wait_warp(bar.ring_full + g % kRing, g / kRing & 1); };
+    auto tile = [&](uint32_t g) -> const Tile& { return sh.ring[g % kRing]; };
+    auto pass_on = [&](uint32_t g) {
+      if (lane == 0) mbar_arrive(bar.ring_empty + g % kRing);
+      __syncwarp();
+    };
+    if constexpr (kTwo) {
+      // Steps: O of tile g in both halves, and S of the next tile, each behind the O whose P it overwrites. A
+      // portion's first step has no O, its last one no S.
+      uint32_t g = 0, now = 0;  // now: the flags of g, 0 in a first step
+      int32_t rest = 0;
+      for (bool ok = true; ok;) {
+        const uint32_t ahead = now ? g + 1 : g;
+        uint32_t next = 0;
+        if (!now || rest > 0) {
+          if (!tile_ready(ahead) || tile(ahead).rest == kEnd) break;
+          next = tile(ahead).stream;
+        }
+        if (now) ok = v_ready(g);
+        if (next && !now) ok = ok && k_ready(ahead);
+#pragma unroll 1
+        for (int i = 0; ok && i < 2; ++i) {
+          if (now >> i & 1) {
+            ok = p_ready(i);
+            if (!ok) break;
+            issue_o(i, i, g, !(now >> (2 + i) & 1));
+            if (now >> (4 + i) & 1) commit(bar.o_full + i);
+          }
+          if (next && now && i == 0) ok = k_ready(ahead);
+          if (ok && !now && (next >> (6 + i) & 1)) ok = q_ready(i);
+          if (ok && (next >> i & 1)) issue_s(i, i, ahead);
+        }
+        if (!ok) break;
+        if (now) {
+          commit(bar.empty + 2 + (g & 1));
+          pass_on(g);
+        }
+        if (next) {
+          commit(bar.empty + (ahead & 1));
+          rest = tile(ahead).rest;
+        }
+        if (now) ++g;
+        now = next;
+      }
+    } else {
+      // In one stream S of the next tile goes ahead of O of this one; in two, S of the one after the next follows O
+      // of this one, whose P it overwrites.
+      constexpr int kAhead = kOne ? 1 : 2;
+      uint32_t started = 0;  // tiles whose S has been issued
+      int turn = 0;          // of the tile's buffers, from a portion's first tile on
+      for (uint32_t g = 0; tile_ready(g); ++g) {
+        const int32_t rest = tile(g).rest;
+        if (rest == kEnd) break;
+        const uint32_t now = tile(g).stream;
+        bool ok = true;
+        if (tile(g).first) {
+          turn = 0;
+          ok = q_ready(0);
+        }
+        // the tiles of this portion that are due
+        const uint32_t due = kTurns && !tile(g).first ? g + 1 : g + min(rest, 1) + 1;
+#pragma unroll 1
+        for (; ok && started < due; ++started) {
+          ok = tile_ready(started) && k_ready(started);
+          if (!ok) break;
+          issue_s(0, (turn + (started - g)) & 1, started);
+          commit(bar.empty + (started & 1));
+        }
+        if (!ok || !v_ready(g) || !p_ready(turn)) break;
+        issue_o(kOne ? 0 : turn, turn, g, !(now >> (kOne ? 2 : 2 + turn) & 1));
+        commit(bar.empty + 2 + (g & 1));
+        if (kOne) commit(&bar.o_step);
+        if (now >> 4 & 3) commit(bar.o_full + (kOne ? 0 : turn));
+        if (kTurns && rest > 1) {
+          if (!tile_ready(g + kAhead) || !k_ready(g + kAhead)) break;
+          issue_s(0, turn, g + kAhead);
+          commit(bar.empty + ((g + kAhead) & 1));
+          started = g + kAhead + 1;
+        }
+        turn ^= 1;
+        pass_on(g);
+      }
+    }
+    // nothing of this CTA is under way any more when it ends
+    commit(&bar.done);
+    for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(&bar.done, 0); ++i) {}
+  } else if (warp > kProductWarp) {
+    // ---- page ----
+    const int turn = warp - kProductWarp - 1;
+    Segment s = sh.first;
+    Portion part{0, 0, false};
+    int32_t k = turn, n = 0;       // this warp's tile of the portion's n
+    uint32_t g = turn;
+    Sight see[2];
+    int32_t last[2];
+    auto position = [&](int32_t i) {  // of the portion's tile i
+      const int32_t u = part.u + i;
+      return (u < s.first_units ? u : u + s.gap) * BN;
+    };
+    auto enter = [&] {
+      part = portion_of(s, run);
+      n = part.end - part.u;
+      if (!kTwo || n <= 0) return;
+      const int32_t r0 = s.t * S::kRows, rows = min(s.q.n * a.G - r0, S::kRows);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        see[i] = {0, 0, 0};
+        if (128 * i < rows) see[i] = sight_of(a, s.q, r0 + 128 * i, r0 + min(rows, 128 * i + 128));
+        last[i] = n - 1;
+        while (last[i] >= 0 && !sees<BN>(see[i], position(last[i]))) --last[i];
+      }
+    };
+    enter();
+    for (;; g += kPageWarps) {
+      bool any = true;
+      while (k >= n) {
+        if (!more(s)) {
+          any = false;
+          break;
+        }
+        k -= n;
+        next_segment<S>(a, s);
+        enter();
+      }
+      Tile& out = sh.ring[g % kRing];
+      if (!wait_warp(bar.ring_empty + g % kRing, (g / kRing & 1) ^ 1)) break;
+      if (any) {
+        const int32_t t0 = position(k);
+#pragma unroll 1
+        for (int j = 0; j < BN / 32; ++j) {
+          const int32_t t = t0 + 32 * j + lane;
+          uint2 where = make_uint2(kNoPage, 0);
+          if (t < s.see.hi && t < s.q.L && (t >= s.see.lo || t < s.see.sink)) {
+            const int32_t col = div_q32(t, a.div_ps), slot = t - col * a.ps;
+            const int64_t at = s.b * a.max_pages + col;
+            const int64_t p = a.table64 ? __ldg(static_cast<const int64_t*>(a.block_tables) + at)
+                                        : static_cast<int64_t>(__ldg(static_cast<const int32_t*>(a.block_tables) + at));
+            if (p >= 0 && p < a.pool_pages) where.x = static_cast<uint32_t>(p);
+            else flag(a.status, NVFP4_DEV_BAD_PAGE);
+            where.y = a.layout == NVFP4_NHD ? slot * a.H + s.h : s.h * a.ps + slot;
+          }
+          out.where[32 * j + lane] = where;
+          const uint32_t word = __ballot_sync(0xFFFFFFFFu, where.x != kNoPage);
+          if (lane == 0) out.live[j] = word;
+        }
+        if (lane == 0) {
+          uint32_t stream = 256;
+          if constexpr (kTwo) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (last[i] >= 0) stream |= 64u << i;
+              if (!sees<BN>(see[i], t0)) continue;
+              bool before = false;  // an earlier tile of the portion
+              for (int32_t e = 0; e < k && !before; ++e) before = sees<BN>(see[i], position(e));
+              stream |= 1u << i | (before ? 0u : 4u << i) | (k == last[i] ? 16u << i : 0u);
+            }
+          } else if constexpr (kTurns) {
+            stream |= 1u << (k & 1) | (k < 2 ? 4u << (k & 1) : 0u) | (k + 2 >= n ? 16u << (k & 1) : 0u);
+          } else {
+            stream |= 1u | (k == 0 ? 4u : 0u) | (k + 1 == n ? 16u : 0u);
+          }
+          out.stream = stream;
+          out.rest = n - 1 - k;
+          out.first = k == 0;
+        }
+      } else if (lane == 0) {
+        out.rest = kEnd;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.ring_full + g % kRing);
+      if (!any) break;
+      k += kPageWarps;
     }
   } else if (warp >= kSoftmaxWarps) {
     // ---- load ----
     set_registers<kLoadRegisters, false>();
+    // A warp's positions are its own from the copies on: only the tiles that it writes are shared.
     constexpr int TW = S::kWarpTokens;
     constexpr int kLanes = DP / E;             // of a row
     constexpr int kStep = 32 / kLanes;         // rows at a time
     constexpr int kItems = TW / kStep;         // of a lane, in a tile
-    constexpr int kWords = E / 8;
-    const int group = (warp - kSoftmaxWarps) / kLoadWarps, w = (warp - kSoftmaxWarps) % kLoadWarps;
-    const int my_row = lane / kLanes, my_part = lane % kLanes;
+    constexpr int kRaw = S::kRaw;
+    static_assert(kItems >= 1 && TW * DP / 64 <= 32, "a warp's scales are a word to a lane");
+    const int w = warp - kSoftmaxWarps;
+    const int my_row = w * TW + lane / kLanes, my_part = lane % kLanes;
     const bool in_row = my_part * E < D;
-    Segment s = sh.first;
-    Portion part = portion_of(s, run);
-    int32_t u = part.u + group, end = part.end;
-    uint32_t unit = group;
-    bool any = true;
-    // to a tile of this group, or past the run's end
-    auto settle = [&] {
-      while (u >= end) {
-        if (!more(s)) {
-          any = false;
-          return;
-        }
-        const int32_t rest = u - end;
-        next_segment<S>(a, s);
-        part = portion_of(s, run);
-        u = part.u + rest;
-        end = part.end;
-      }
-    };
-    constexpr uint32_t kDead = 0xFFFFFFFFu;
-    uint32_t page = kDead, row = 0;  // of position `lane` of this warp's part of the tile looked up
-    bool ahead = false;
-    auto look_up = [&] {
-      ahead = any;
-      page = kDead;
-      if (!any) return;
-      const int32_t t = (u < s.first_units ? u : u + s.gap) * BN + w * TW + lane;
-      if (lane < TW && t < s.see.hi && t < s.q.L && (t >= s.see.lo || t < s.see.sink)) {
-        const int32_t col = div_q32(t, a.div_ps), slot = t - col * a.ps;
-        const int64_t at = s.b * a.max_pages + col;
-        const int64_t p = a.table64 ? __ldg(static_cast<const int64_t*>(a.block_tables) + at)
-                                    : static_cast<int64_t>(__ldg(static_cast<const int32_t*>(a.block_tables) + at));
-        if (p >= 0 && p < a.pool_pages) page = static_cast<uint32_t>(p);
-        else flag(a.status, NVFP4_DEV_BAD_PAGE);
-        row = a.layout == NVFP4_NHD ? slot * a.H + s.h : s.h * a.ps + slot;
-      }
-    };
-    uint32_t kr[kItems][kWords], vr[kItems][kWords], ks[kItems], vs[kItems];
-    uint32_t live = 0;
-    auto load_codes = [&](const nvfp4_paged_cache& c, uint32_t (&r)[kItems][kWords]) {
+    const int nb = D / 16;
+    // scales: 4 bytes to a lane (E = 32), copied; else one by one through registers, from issue to issue
+    const int scale_row = w * TW + (E == 32 ? lane / (DP / 64) : 0), scale_word = lane % (DP / 64);
+    const bool scale_lane = lane < TW * (DP / 64) && scale_word * 4 < nb;
+    constexpr int kBytesEach = TW * (DP / 16) / 32;  // of a lane
+    uint32_t carried[2] = {0, 0};
+    auto code_slot = [&](uint32_t g, int kv) { return base + S::kCodes + ((g % kRaw) * 2 + kv) * S::kCodeBytes; };
+    auto scale_slot = [&](uint32_t g, int kv) { return S::kScales + ((g % (kRaw + 1)) * 2 + kv) * S::kScaleBytes; };
+    auto issue_scales = [&](uint32_t g) {
+      const Tile& tile = sh.ring[g % kRing];
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        const uint32_t p = __shfl_sync(0xFFFFFFFFu, page, i * kStep + my_row), rw = __shfl_sync(0xFFFFFFFFu, row, i * kStep + my_row);
-        const bool in = p != kDead && in_row;
-        const uint8_t* src = c.data + static_cast<uint64_t>(p) * c.data_page_stride + static_cast<uint64_t>(rw) * (D / 2) + my_part * (E / 2);
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint8_t* const sf = kv ? a.vc.sf : a.kc.sf;
+        const uint32_t stride = kv ? a.v_sf_stride : a.k_sf_stride;
         if constexpr (E == 32) {
-          const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(src)) : uint4{};
-          r[i][0] = x.x; r[i][1] = x.y; r[i][2] = x.z; r[i][3] = x.w;
+          if (scale_lane) {
+            const uint2 at = tile.where[scale_row];
+            const bool in = at.x != kNoPage;
+            cp_async<4>(base + scale_slot(g, kv) + scale_row * (DP / 16) + 4 * scale_word,
+                        in ? sf + static_cast<uint64_t>(at.x) * stride + static_cast<uint64_t>(at.y) * nb + 4 * scale_word : sf, in);
+          }
         } else {
-          const uint2 x = in ? __ldg(reinterpret_cast<const uint2*>(src)) : uint2{};
-          r[i][0] = x.x; r[i][1] = x.y;
+          carried[kv] = 0;
+#pragma unroll
+          for (int i = 0; i < kBytesEach; ++i) {
+            const int n = lane * kBytesEach + i, row = w * TW + n / (DP / 16), block = n % (DP / 16);
+            const uint2 at = tile.where[row];
+            if (at.x != kNoPage && block < nb)
+              carried[kv] |= static_cast<uint32_t>(__ldg(sf + static_cast<uint64_t>(at.x) * stride + static_cast<uint64_t>(at.y) * nb + block)) << (8 * i);
+          }
         }
       }
     };
-    auto load_scales = [&](const nvfp4_paged_cache& c, uint32_t (&r)[kItems]) {
+    // the carried scales of tile g to their slots
+    auto put_scales = [&](uint32_t g) {
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        const uint32_t p = __shfl_sync(0xFFFFFFFFu, page, i * kStep + my_row), rw = __shfl_sync(0xFFFFFFFFu, row, i * kStep + my_row);
-        const bool in = p != kDead && in_row;
-        const uint8_t* src = c.sf + static_cast<uint64_t>(p) * c.sf_page_stride + static_cast<uint64_t>(rw) * (D / 16) + my_part * (E / 16);
-        if constexpr (E == 32) r[i] = in ? static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(src))) : 0u;
-        else r[i] = in ? static_cast<uint32_t>(__ldg(src)) : 0u;
-      }
+      for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int i = 0; i < kBytesEach; ++i)
+          smem[scale_slot(g, kv) + w * TW * (DP / 16) + lane * kBytesEach + i] = static_cast<uint8_t>(carried[kv] >> (8 * i));
     };
-    // Decoded rows to a tile's atoms. Lanes of a row whose chunks would meet in the same banks store them in
-    // another order (DP = 128: 8 lanes are two rows of two atoms; 256: one row of four).
-    auto store = [&](uint32_t tile, const uint32_t (&r)[kItems][kWords], const uint32_t (&sc)[kItems]) {
+    auto issue_codes = [&](uint32_t g, int kv) {
+      const uint2* where = sh.ring[g % kRing].where + my_row;
+      const uint8_t* const codes = (kv ? a.vc.data : a.kc.data) + my_part * (E / 2);
+      const uint32_t stride = kv ? a.v_stride : a.k_stride, dst = code_slot(g, kv) + my_row * (DP / 2) + my_part * (E / 2);
       if (!in_row) return;
 #pragma unroll
       for (int i = 0; i < kItems; ++i) {
-        const int rw = w * TW + i * kStep + my_row;
+        const uint2 at = where[i * kStep];
+        const bool in = at.x != kNoPage;
+        cp_async<E / 2>(dst + i * kStep * (DP / 2),
+                        in ? codes + static_cast<uint64_t>(at.x) * stride + static_cast<uint64_t>(at.y) * static_cast<uint32_t>(D / 2) : codes, in);
+      }
+    };
+    // NaN scales of V, for the softmax (they are taken as 0 in the tile)
+    auto find_nan = [&](uint32_t g) {
+      Tile& tile = sh.ring[g % kRing];
+      uint32_t bad = 0;
+      const uint8_t* const sf = smem + scale_slot(g, 1) + my_row * (DP / 16) + my_part * (E / 16);
+      auto scale_of = [&](int i) -> uint32_t {
+        return !in_row ? 0u : (E == 32 ? *reinterpret_cast<const uint16_t*>(sf + i * kStep * (DP / 16)) : sf[i * kStep * (DP / 16)]);
+      };
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) bad |= ((scale_of(i) & 0x7F7Fu) + 0x0101u) & 0x8080u;
+      const bool any = __any_sync(0xFFFFFFFFu, bad != 0);
+      if (any) {
+#pragma unroll 1
+        for (int i = 0; i < kItems; ++i) {
+          const uint32_t x = scale_of(i);
+          uint32_t blocks = 0;
+          for (int b = 0; b < E / 16; ++b)
+            if ((x >> (8 * b) & 0x7Fu) == 0x7Fu) blocks |= 1u << (my_part * (E / 16) + b);
+          for (int o = 1; o < kLanes; o <<= 1) blocks |= __shfl_xor_sync(0xFFFFFFFFu, blocks, o);
+          if (my_part == 0) tile.nan_blocks[my_row + i * kStep] = static_cast<uint16_t>(blocks);
+        }
+      }
+      if (lane == 0) tile.nan[w] = any;
+    };
+    // Decoded rows to a tile's atoms. Lanes of a row whose chunks would meet in the same banks store them in
+    // another order (DP = 128: 8 lanes are two rows of two atoms; 256: one row of four).
+    auto decode = [&](uint32_t g, int kv) {
+      if (!in_row) return;
+      const uint32_t tile = base + S::kK + (2 * kv + (g & 1)) * S::kTileBytes;
+      const uint8_t* const codes = smem + (code_slot(g, kv) - base) + my_row * (DP / 2) + my_part * (E / 2);
+      const uint8_t* const sf = smem + scale_slot(g, kv) + my_row * (DP / 16) + my_part * (E / 16);
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        const int row = my_row + i * kStep;
+        uint32_t sc = E == 32 ? *reinterpret_cast<const uint16_t*>(sf + i * kStep * (DP / 16)) : sf[i * kStep * (DP / 16)] * 0x0101u;
+        if (kv) sc &= ~((((sc & 0x7F7Fu) + 0x0101u) & 0x8080u) / 128 * 255);
+        const uint32_t s2 = f16x2_from_e4m3x2(sc);
+        auto put = [&](uint32_t word, uint32_t scale, uint32_t dst) {
+          uint32_t x[4];
+          f16x2x4_from_e2m1x8(word, x[0], x[1], x[2], x[3]);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(hmul2_rn(x[0], scale)), "r"(hmul2_rn(x[1], scale)),
+                       "r"(hmul2_rn(x[2], scale)), "r"(hmul2_rn(x[3], scale)) : "memory");
+        };
         if constexpr (E == 32) {
           const int atom = my_part >> 1;
-          const uint32_t at = tile + atom * (BN * 128) + rw * 128;
+          const uint32_t at = tile + atom * (BN * 128) + row * 128;
           const int turn = DP == 128 ? 2 * (atom & 1) : (DP == 256 ? atom : 0);
-          const uint32_t s2 = f16x2_from_e4m3x2(sc[i]);
-          const uint32_t s_lo = low_twice(s2), s_hi = high_twice(s2);
+          const uint4 raw = *reinterpret_cast<const uint4*>(codes + i * kStep * (DP / 2));
+          const bool two = turn & 2, one = turn & 1;
+          uint32_t r[4] = {two ? raw.z : raw.x, two ? raw.w : raw.y, two ? raw.x : raw.z, two ? raw.y : raw.w};
+          if (DP == 256) {
+            const uint32_t q[4] = {r[0], r[1], r[2], r[3]};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int c = j ^ turn;  // the chunk of this lane's four that it stores now
-            uint32_t word = r[i][j], scale = j < 2 ? s_lo : s_hi;
-            if (DP == 128) {
-              word = turn ? r[i][j ^ 2] : word;
-              scale = turn ? (j < 2 ? s_hi : s_lo) : scale;
-            } else if (DP == 256) {
-              const uint32_t x0 = turn & 1 ? r[i][j ^ 1] : word, x1 = turn & 1 ? r[i][j ^ 3] : r[i][j ^ 2];
-              word = turn & 2 ? x1 : x0;
-              scale = turn & 2 ? (j < 2 ? s_hi : s_lo) : scale;
-            }
-            uint32_t x[4];
-            f16x2x4_from_e2m1x8(word, x[0], x[1], x[2], x[3]);
-            const uint32_t dst = at + (((4 * (my_part & 1) + c) ^ (rw & 7)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(hmul2_rn(x[0], scale)), "r"(hmul2_rn(x[1], scale)),
-                         "r"(hmul2_rn(x[2], scale)), "r"(hmul2_rn(x[3], scale)) : "memory");
+            for (int j = 0; j < 4; ++j) r[j] = one ? q[j ^ 1] : q[j];
           }
+          const uint32_t s_lo = two ? high_twice(s2) : low_twice(s2), s_hi = two ? low_twice(s2) : high_twice(s2);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) put(r[j], j < 2 ? s_lo : s_hi, at + (((4 * (my_part & 1) + (j ^ turn)) ^ (row & 7)) << 4));
         } else {
-          const uint32_t at = tile + (my_part >> 2) * (BN * 128) + rw * 128;
-          const uint32_t scale = f16x2_from_e4m3x2(sc[i] * 0x0101u);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t x[4];
-            f16x2x4_from_e2m1x8(r[i][j], x[0], x[1], x[2], x[3]);
-            const uint32_t dst = at + (((2 * (my_part & 3) + j) ^ (rw & 7)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(hmul2_rn(x[0], scale)), "r"(hmul2_rn(x[1], scale)),
-                         "r"(hmul2_rn(x[2], scale)), "r"(hmul2_rn(x[3], scale)) : "memory");
+          const uint32_t at = tile + (my_part >> 2) * (BN * 128) + row * 128;
+          const uint2 raw = *reinterpret_cast<const uint2*>(codes + i * kStep * (DP / 2));
+          put(raw.x, s2, at + (((2 * (my_part & 3)) ^ (row & 7)) << 4));
+          put(raw.y, s2, at + (((2 * (my_part & 3) + 1) ^ (row & 7)) << 4));
+        }
+      }
+    };
+    bool live[kRaw + 1] = {};  // whether tiles g .. g + kRaw are there
+    bool ok = !a.pipe.stall;   // (a test: nothing comes, and every wait runs out)
+#pragma unroll 1
+    for (int32_t g = -kRaw; ok; ++g) {
+      const uint32_t ahead = g + kRaw;
+      const bool due = g >= 0 && live[0];
+      if (g >= 0 && !due) break;
+      if (E != 32 && ahead > 0 && live[kRaw - 1]) put_scales(ahead - 1);
+      live[kRaw] = (g < 0 ? ahead == 0 || live[kRaw - 1] : live[kRaw - 1]) &&
+                   wait_warp(bar.ring_full + ahead % kRing, ahead / kRing & 1) && sh.ring[ahead % kRing].rest != kEnd;
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        if (due) {
+          cp_async_wait<2 * kRaw - 1>();
+          __syncwarp();
+          if (kv == 0) find_nan(g);
+          if (!wait_warp(bar.empty + 2 * kv + (g & 1), ((g >> 1) & 1) ^ 1)) {
+            ok = false;
+            break;
           }
+          decode(g, kv);
+          fence_async_proxy();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar.full + 2 * kv + (g & 1));
         }
-      }
-    };
-    auto publish = [&](uint64_t* full) {
-      fence_async_proxy();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full);
-    };
-    settle();
-    look_up();
-    if (ahead) {
-      live = __ballot_sync(0xFFFFFFFFu, page != kDead);
-      load_codes(a.kc, kr);
-      load_scales(a.kc, ks);
-      load_scales(a.vc, vs);
-      load_codes(a.vc, vr);
-    }
-    bool have = ahead;
-    if (have) {
-      u += kLoadGroups;
-      settle();
-      look_up();
-    }
-    while (have) {
-      if (a.pipe.stall) break;  // (a test: nothing comes, and every wait runs out)
-      const uint32_t stage = unit & 1, parity = ((unit >> 1) & 1) ^ 1, meta = unit & (kMeta - 1);
-      if (!wait_warp(bar.k_empty + stage, parity)) break;
-      // what the softmax has to know of this tile; NaN scales of V are taken out
-      uint32_t bad = 0;
-#pragma unroll
-      for (int i = 0; i < kItems; ++i) bad |= ((vs[i] & 0x7F7Fu) + 0x0101u) & 0x8080u;
-      const bool any_nan = __any_sync(0xFFFFFFFFu, bad != 0);
-      if (any_nan) {
-#pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-          uint32_t blocks = 0;
-          for (int k = 0; k < E / 16; ++k)
-            if ((vs[i] >> (8 * k) & 0x7Fu) == 0x7Fu) {
-              blocks |= 1u << (my_part * (E / 16) + k);
-              vs[i] &= ~(0xFFu << (8 * k));
-            }
-          for (int o = 1; o < kLanes; o <<= 1) blocks |= __shfl_xor_sync(0xFFFFFFFFu, blocks, o);
-          if (my_part == 0) sh.nan_blocks[meta][w * TW + i * kStep + my_row] = static_cast<uint16_t>(blocks);
+        if (live[kRaw]) {
+          if (kv == 0) issue_scales(ahead);
+          issue_codes(ahead, kv);
         }
+        cp_async_commit();
       }
-      if (lane == 0) {
-        sh.live[meta][w] = live;
-        sh.nan[meta][w] = any_nan;
-      }
-      store(base + S::kK + stage * S::kTileBytes, kr, ks);
-      publish(bar.k_full + stage);
-      uint32_t vs_now[kItems];
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) vs_now[i] = vs[i];
-      if (ahead) {
-        live = __ballot_sync(0xFFFFFFFFu, page != kDead);
-        load_codes(a.kc, kr);
-        load_scales(a.kc, ks);
-        load_scales(a.vc, vs);
-      }
-      if (!wait_warp(bar.v_empty + stage, parity)) break;
-      store(base + S::kV + stage * S::kTileBytes, vr, vs_now);
-      publish(bar.v_full + stage);
-      have = ahead;
-      if (have) {
-        load_codes(a.vc, vr);
-        u += kLoadGroups;
-        settle();
-        look_up();
-      }
-      unit += kLoadGroups;
+      for (int i = 0; i < kRaw; ++i) live[i] = live[i + 1];
     }
+    cp_async_wait<0>();
   } else {
     // ---- softmax ----
     set_registers<kSoftmaxRegisters, true>();
@@ -642,27 +741,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
     const int stream = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;  // this warp's lanes of tensor memory
     const float gk = __ldg(a.k_scale), gv = __ldg(a.v_scale);
-    const float cap = a.soft_cap;
-    uint32_t unit = 0, q_count = 0, o_count = 0, merges = 0, steps = 0;
+    const float cap = a.soft_cap, unit = a.sm_scale * gk;
+    uint32_t tiles = 0, q_count = 0, o_count = 0, merges = 0, steps = 0;
     uint32_t s_count[2] = {0, 0};
     Segment s = sh.first;
     for (;;) {
       const Portion part = portion_of(s, run);
       const int32_t n = part.end - part.u;
-      const int64_t rows = static_cast<int64_t>(s.q.n) * a.G, r0 = static_cast<int64_t>(s.t) * S::kRows;
-      const int local = (kTwo ? 128 * stream : 0) + quarter * 32 + lane;  // this thread's row of the segment
-      const bool alive = r0 + local < rows;
-      const int64_t token = quotient64(r0 + local, a.G);
-      const int32_t head = static_cast<int32_t>(r0 + local - token * a.G);
+      const int32_t r0 = s.t * S::kRows, rows = min(s.q.n * a.G - r0, S::kRows);  // the segment's first, and their count
+      const int local = (kTwo ? 128 * stream : 0) + quarter * 32 + lane;          // this thread's row of them
+      const bool alive = local < rows;
+      const int32_t token = div_q32(alive ? r0 + local : 0, a.div_g), head = (alive ? r0 + local : 0) - token * a.G;
       uint8_t* const out = a.out + ((s.q.q0 + token) * a.Hq + static_cast<int64_t>(s.h) * a.G + head) * D * 2;
       float* const lse = a.lse ? a.lse + (s.q.q0 + token) * a.Hq + static_cast<int64_t>(s.h) * a.G + head : nullptr;
       if (n == 0 && part.mine && stream == (kTwo ? stream : 0) && alive) {  // nothing that any row sees
         for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(out)[i] = uint4{};
         if (lse) *lse = -INFINITY;
       }
+      Sight see{0, 0, 0};  // of this stream's rows
+      bool mine = n > 0;   // it has tiles in the portion
+      if constexpr (kTwo) {
+        if (128 * stream < rows) see = sight_of(a, s.q, r0 + 128 * stream, r0 + min(rows, 128 * stream + 128));
+        int32_t u = part.end;
+        for (mine = false; u > part.u && !mine; --u) mine = sees<BN>(see, (u - 1 < s.first_units ? u - 1 : u - 1 + s.gap) * BN);
+      }
       if (n > 0) {
         // -- the queries: in binary16, each row scaled by a power of two --
-        {
+        if (mine) {
           const int width = D / 8;
           int log_t = 0;
           while ((1 << log_t) < width) ++log_t;
@@ -670,20 +775,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           const int per_warp = kTurns ? 16 : 32;
           const int q_row = kTurns ? warp * 16 : (kTwo ? warp * 32 : quarter * 32);  // this warp's first
 #pragma unroll 1
-          for (int i0 = 0; i0 < per_warp; i0 += 4 * step) {
-            uint4 raw[4];
+          for (int i0 = 0; i0 < per_warp; i0 += 8 * step) {
+            uint4 raw[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 8; ++k) {
               const int i = q_row + i0 + k * step + (lane >> log_t);
               raw[k] = uint4{};
-              if (i0 + k * step < per_warp && r0 + i < rows && j < width) {
-                const int64_t tk = quotient64(r0 + i, a.G);
+              if (i0 + k * step < per_warp && i < rows && j < width) {
+                const int32_t tk = div_q32(r0 + i, a.div_g);
                 const int64_t hd = static_cast<int64_t>(s.h) * a.G + (r0 + i - tk * a.G);
                 raw[k] = __ldg(reinterpret_cast<const uint4*>(a.q + (s.q.q0 + tk) * a.q_row_bytes + hd * D * 2) + j);
               }
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 8; ++k) {
               if (i0 + k * step >= per_warp) break;
               const int i = q_row + i0 + k * step + (lane >> log_t);
               const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
@@ -695,10 +800,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
                 top = max3(top, fabsf(v[2 * e]), fabsf(v[2 * e + 1]));
               }
               for (int o = T >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-              const int e2 = top > 0.0f && top <= FLT_MAX ? ilogbf(top) - 14 : 0;
-              float f = ldexpf(a.sm_scale, e2) * gk;
-              // 2^-e2 as two factors (it may be out of range by itself), with f's sign: f is not negative from
-              // here on, and a maximum of scores is one of logits; f = 0 is a query of zeros
+              const int exponent = max(static_cast<int>(__float_as_uint(top) >> 23), 1) - 127;
+              const int e2 = top > 0.0f && top <= FLT_MAX ? exponent - 14 : 0;
+              // 2^e2 and 2^-e2 as two factors (they may be out of range by themselves), with f's sign: f is not
+              // negative from here on, and a maximum of scores is one of logits; f = 0 is a query of zeros
+              float f = unit * __int_as_float((127 + e2 / 2) << 23) * __int_as_float((127 + (e2 - e2 / 2)) << 23);
               float f1 = __int_as_float((127 - e2 / 2) << 23);
               const float f2 = __int_as_float((127 - (e2 - e2 / 2)) << 23);
               if (f < 0.0f) f1 = -f1;
@@ -717,22 +823,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           }
           fence_async_proxy();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.q_full);
-          if (!wait_warp(&bar.q_full, q_count++ & 1)) break;
+          uint64_t* const full = bar.q_full + (kTwo ? stream : 0);
+          if (lane == 0) mbar_arrive(full);
+          if (!wait_warp(full, q_count++ & 1)) break;
         }
         // -- this row --
-        const float f = sh.factor[local];
-        const float unit2 = cap > 0.0f ? kLog2e : f * kLog2e;  // what turns x into base-2 logarithms
-        const int32_t p = s.q.L - s.q.n + static_cast<int32_t>(token);
+        const float f = mine ? sh.factor[local] : 1.0f;
+        const float unit2 = f * kLog2e;  // what turns a sum of products into base-2 logarithms
+        // cap tanh(x / cap) of x = f v, by 1 - 2 / (e^(2x/cap) + 1): absolute error a few 2^-24 of the cap
+        const float turn2 = cap > 0.0f ? f / cap * (2.0f * kLog2e) : 0.0f;
+        auto capped = [&](float v) { return cap * __fmaf_rn(-2.0f, rcp(ex2(v * turn2) + 1.0f), 1.0f); };
+        const int32_t p = s.q.L - s.q.n + token;
         const int32_t hi = !alive ? 0 : (a.causal ? min(max(p + 1, 0), s.q.L) : s.q.L);
         const int32_t lo = a.window_left >= 0 && p > a.window_left ? p - a.window_left : 0;
         const int32_t sink = a.window_left >= 0 ? a.sink : 0;
         const bool busy = __any_sync(0xFFFFFFFFu, alive);
         const int32_t all_hi = __reduce_min_sync(0xFFFFFFFFu, alive ? hi : INT32_MAX);
         const int32_t all_lo = __reduce_max_sync(0xFFFFFFFFu, alive ? lo : 0);
-        Sight see{0, 0, 0};  // of this stream's rows
-        if (kTwo && r0 + 128 * stream < rows)
-          see = sight_of(a, s.q, r0 + 128 * stream, min(rows, r0 + 128 * stream + 128));
         float m = -INFINITY, l = 0.0f;
         uint32_t poison = 0;
         bool started = false, ok = true;
@@ -744,44 +851,42 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           ok = wait_warp(bar.s_full + buf, s_count[buf]++ & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t meta = (unit + k) & (kMeta - 1);
+          const Tile& tile = sh.ring[(tiles + k) % kRing];
           const uint32_t s_at = tmem + lanes + buf * BN;
           if (busy) {
-            // which positions: a word for 32 of them
-            uint32_t words[BN / 32];
-            bool full = t0 + BN <= all_hi && (t0 >= all_lo || t0 + BN <= sink);
-#pragma unroll
-            for (int c = 0; c < BN / 32; ++c) {
-              words[c] = S::kWarpTokens == 32 ? sh.live[meta][c] : sh.live[meta][2 * c] | sh.live[meta][2 * c + 1] << 16;
-              full = full && words[c] == ~0u;
-            }
-            if (!full) {
-#pragma unroll
-              for (int c = 0; c < BN / 32; ++c) {
-                const int32_t t = t0 + 32 * c;
-                words[c] &= low_bits(hi - t) & (~low_bits(lo - t) | low_bits(sink - t));
-              }
-            }
+            const bool full = t0 + BN <= all_hi && (t0 >= all_lo || t0 + BN <= sink) &&
+                              (BN == 128 ? tile.live[0] & tile.live[1] & tile.live[2] & tile.live[3] : tile.live[0] & tile.live[1]) == ~0u;
             auto weigh = [&](auto masked_, auto capped_) {
               constexpr bool kMasked = decltype(masked_)::value, kCapped = decltype(capped_)::value;
-              constexpr int NC = BN / 32;
-              float v[2][32];
-              tmem_load(v[0], s_at);
-              tmem_wait(v[0]);
-              float top = -INFINITY;
+              constexpr int NC = BN / 32;  // words of 32 positions
+              float x[32], y[32], tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              auto seen = [&](int c) -> uint32_t {  // which of a word's
+                const int32_t t = t0 + 32 * c;
+                return tile.live[c] & low_bits(hi - t) & (~low_bits(lo - t) | low_bits(sink - t));
+              };
+              auto take = [&](float (&v)[32], int c) {
+                tmem_loaded(v);
+                const uint32_t word = kMasked ? seen(c) : 0u;
 #pragma unroll
-              for (int c = 0; c < NC; ++c) {
-                float (&x)[32] = v[c & 1];
-                tmem_load(v[(c + 1) & 1], s_at + (c + 1 < NC ? 32 * (c + 1) : 0));  // (the first again, for the weights)
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  const float x0 = kMasked && !(words[c] >> i & 1u) ? -INFINITY : x[i];
-                  const float x1 = kMasked && !(words[c] >> (i + 1) & 1u) ? -INFINITY : x[i + 1];
-                  top = max3(top, x0, x1);
+                for (int e = 0; e < 32; e += 2) {
+                  const float v0 = kMasked && !(word >> e & 1u) ? -INFINITY : v[e];
+                  const float v1 = kMasked && !(word >> (e + 1) & 1u) ? -INFINITY : v[e + 1];
+                  tops[e / 2 % 4] = max3(tops[e / 2 % 4], v0, v1);
                 }
-                tmem_wait(v[(c + 1) & 1]);
+              };
+              tmem_load(x, s_at);
+              tmem_wait();
+#pragma unroll 1
+              for (int c = 0; c < NC; c += 2) {
+                tmem_load(y, s_at + 32 * (c + 1));
+                take(x, c);
+                tmem_wait();
+                tmem_load(x, c + 2 < NC ? s_at + 32 * (c + 2) : s_at);  // (at last the first again, for the weights)
+                take(y, c + 1);
+                tmem_wait();
               }
-              top = (kCapped ? soft_capped(top * f, cap) : top) * unit2;
+              float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+              top = kCapped ? capped(top) * kLog2e : top * unit2;
               const bool rises = top > m + kSlack;  // (by row: a result does not depend on other rows)
               if (__any_sync(0xFFFFFFFFu, rises)) {
                 const float g = rises ? ex2(m - top) : 1.0f;
@@ -791,40 +896,49 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
                   if (kOne && !wait_warp(&bar.o_step, (steps - 1) & 1)) return false;
                   tc_fence_after();
                   const uint32_t o_at = tmem + lanes + S::kO + (kOne ? 0 : stream * DP);
+#pragma unroll 1
                   for (int d = 0; d < D; d += 16) {
                     float o[16];
                     tmem_load(o, o_at + d);
-                    tmem_wait(o);
+                    tmem_wait();
+                    tmem_loaded(o);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] *= g;
+                    for (int e = 0; e < 16; ++e) o[e] *= g;
                     tmem_store(o_at + d, o);
                   }
                 }
               }
               const float off = m == -INFINITY ? 0.0f : kWeightBias - m;
-              float sums[4] = {0, 0, 0, 0};
+              float sum[4] = {0, 0, 0, 0};
+              auto put = [&](float (&v)[32], int c) {
+                tmem_loaded(v);
+                const uint32_t word = kMasked ? seen(c) : 0u;
+                uint32_t p[16];
 #pragma unroll
-              for (int c = 0; c < NC; ++c) {
-                float (&x)[32] = v[(NC + c) & 1];
-                if (c + 1 < NC) tmem_load(v[(NC + c + 1) & 1], s_at + 32 * (c + 1));
-                uint32_t y[16];
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  float p01[2];
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    float z = kCapped ? soft_capped(x[i + e] * f, cap) : x[i + e];
-                    if (kMasked && !(words[c] >> (i + e) & 1u)) z = -INFINITY;
-                    p01[e] = ex2(__fmaf_rn(z, unit2, off));
-                    sums[(i + e) & 3] += p01[e];
+                for (int e = 0; e < 32; e += 2) {
+                  float v0 = kCapped ? capped(v[e]) : v[e], v1 = kCapped ? capped(v[e + 1]) : v[e + 1];
+                  if (kMasked) {
+                    v0 = word >> e & 1u ? v0 : -INFINITY;
+                    v1 = word >> (e + 1) & 1u ? v1 : -INFINITY;
                   }
-                  y[i / 2] = f16x2_from_f32(p01[0], p01[1]);
+                  fma2(v0, v1, kCapped ? kLog2e : unit2, off);
+                  v0 = ex2(v0);
+                  v1 = ex2(v1);
+                  add2(sum[e % 4], sum[e % 4 + 1], v0, v1);
+                  p[e / 2] = f16x2_from_f32(v0, v1);
                 }
-                if (kCapped) __syncwarp();
-                tmem_store(s_at + 16 * c, y);
-                if (c + 1 < NC) tmem_wait(v[(NC + c + 1) & 1]);
+                tmem_store(s_at + 16 * c, p);
+              };
+#pragma unroll 1
+              for (int c = 0; c < NC; c += 2) {
+                tmem_load(y, s_at + 32 * (c + 1));
+                put(x, c);
+                tmem_wait();
+                if (c + 2 < NC) tmem_load(x, s_at + 32 * (c + 2));
+                put(y, c + 1);
+                tmem_wait();
               }
-              l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+              l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
               return true;
             };
             using T = std::true_type;
@@ -834,10 +948,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
             if (!ok) break;
             // blocks of V that are NaN, where this row sees them
             for (int w = 0; w < kLoadWarps; ++w) {
-              if (!sh.nan[meta][w]) continue;
+              if (!tile.nan[w]) continue;
               for (int i = 0; i < S::kWarpTokens; ++i) {
                 const int c = w * S::kWarpTokens + i, t = t0 + c;
-                if (t < hi && (t >= lo || t < sink)) poison |= sh.nan_blocks[meta][c];
+                if (t < hi && (t >= lo || t < sink)) poison |= tile.nan_blocks[c];
               }
             }
             __syncwarp();
@@ -884,19 +998,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           const float w0 = (two ? g0 : 1.0f) * scale, w1 = g1 * scale;
           float* const part_o = whole ? nullptr : part_of(a, blockIdx.x, s.start < 0 ? 0 : 1, S::kRows, DP);
           const uint32_t o_at = tmem + lanes + S::kO + (kOne || kTurns ? 0 : stream * DP);
+#pragma unroll 1
           for (int d = 0; d < D; d += 16) {
             float o[16] = {};
             __syncwarp();
             if (started) {
               tmem_load(o, o_at + d);
-              tmem_wait(o);
+              tmem_wait();
+              tmem_loaded(o);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] *= w0;
             if (two) {
               float x[16];
               tmem_load(x, o_at + DP + d);
-              tmem_wait(x);
+              tmem_wait();
+              tmem_loaded(x);
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] += w1 * x[i];
             }
@@ -928,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           }
           tc_fence_before();  // (these reads come before the next segment's products)
         }
-        unit += n;
+        tiles += n;
       }
       if (!more(s)) break;
       next_segment<S>(a, s);
@@ -942,6 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && sh.dead) flag(a.status, NVFP4_DEV_TIMEOUT);
   if (warp == kProductWarp) {
     tc_fence_after();
     tmem_free(tmem);
@@ -958,12 +1076,12 @@ __global__ void __launch_bounds__(256) join_kernel(const PrefillArgs a) {
   if (c.last < 0) return;
   const Request q = request_of(a, c.b);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = a.D;
-  const int64_t rows = static_cast<int64_t>(q.n) * a.G, r0 = static_cast<int64_t>(c.t) * S::kRows;
+  const int32_t r0 = c.t * S::kRows, rows = q.n * a.G - r0;
   const int64_t first = blockIdx.x;
   const float gv = __ldg(a.v_scale);
   for (int k = 0; k < 4; ++k) {
     const int local = blockIdx.y * kJoinRows + warp * 4 + k;
-    if (r0 + local >= rows) return;
+    if (local >= rows) return;
     auto part = [&](int64_t i) { return part_of(a, i, i == first ? 1 : 0, S::kRows, DP); };
     float top = -INFINITY;
     for (int64_t i = first + lane; i <= c.last; i += 32) top = fmaxf(top, part(i)[S::kRows * DP + local]);
@@ -987,7 +1105,7 @@ __global__ void __launch_bounds__(256) join_kernel(const PrefillArgs a) {
       }
     }
     const float f = sum == 0.0f ? 0.0f : gv / sum;
-    const int64_t token = quotient64(r0 + local, a.G);
+    const int32_t token = div_q32(r0 + local, a.div_g);
     const int64_t row = (q.q0 + token) * a.Hq + static_cast<int64_t>(c.h) * a.G + (r0 + local - token * a.G);
 #pragma unroll
     for (int e = 0; e < (DP + 127) / 128; ++e) {
@@ -1022,9 +1140,9 @@ nvfp4_status launch_t(PrefillArgs a, cudaStream_t stream) {
 
 template <int DP, int MT>
 nvfp4_status launch_e(const PrefillArgs& a, cudaStream_t s) {
-  // 16-byte loads of codes and 2-byte loads of scales
-  auto even = [](const nvfp4_paged_cache& c) { return reinterpret_cast<uintptr_t>(c.sf) % 2 == 0 && c.sf_page_stride % 2 == 0; };
-  return a.D % 32 == 0 && even(a.kc) && even(a.vc) ? launch_t<DP, MT, 32>(a, s) : launch_t<DP, MT, 16>(a, s);
+  // 16-byte copies of codes and 4-byte copies of scales
+  auto even = [](const nvfp4_paged_cache& c) { return reinterpret_cast<uintptr_t>(c.sf) % 4 == 0 && c.sf_page_stride % 4 == 0; };
+  return a.D % 64 == 0 && even(a.kc) && even(a.vc) ? launch_t<DP, MT, 32>(a, s) : launch_t<DP, MT, 16>(a, s);
 }
 
 }  // namespace
@@ -1036,6 +1154,13 @@ int64_t prefill_workspace_bytes(int32_t D) {
 
 nvfp4_status launch_prefill(PrefillArgs a, cudaStream_t stream) {
   a.pool_pages = a.kc.num_pages < a.vc.num_pages ? a.kc.num_pages : a.vc.num_pages;
+  const int64_t strides[4] = {a.kc.data_page_stride, a.vc.data_page_stride, a.kc.sf_page_stride, a.vc.sf_page_stride};
+  for (int64_t s : strides)
+    if (s > static_cast<int64_t>(UINT32_MAX)) return fail(NVFP4_ERR_UNSUPPORTED, "nvfp4_paged_attention_prefill: a page stride above 4 GiB");
+  a.k_stride = static_cast<uint32_t>(strides[0]);
+  a.v_stride = static_cast<uint32_t>(strides[1]);
+  a.k_sf_stride = static_cast<uint32_t>(strides[2]);
+  a.v_sf_stride = static_cast<uint32_t>(strides[3]);
   a.pipe = pipe_test_from_env();
   // 256 rows of a segment share the decoded tiles; requests of fewer rows than 128 have no use for them
   const bool two = a.nnz * a.G > static_cast<int64_t>(a.B) * 128;

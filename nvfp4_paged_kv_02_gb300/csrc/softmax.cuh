@@ -1,4 +1,4 @@
-// softmax.cuh -- what the attention kernels share: the arithmetic of weights, the cut of a launch's work into
+// softmax.cuh -- what the attention kernels share: asynchronous copies, the arithmetic of weights, the cut of a launch's work into
 // equal runs, and a block of the cache as binary16.
 #pragma once
 
@@ -14,6 +14,21 @@ constexpr float kWeightBias = 8.0f;
 constexpr float kSlack = 7.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Asynchronous copies to shared memory; not live: nothing is read, the destination is zero-filled.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool live) {
+  const int n = live ? BYTES : 0;  // 0: nothing is read, the destination is zero-filled
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -24,6 +39,21 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float soft_capped(float x, float cap) {
   const float e = ex2(x / cap * (2.0f * kLog2e));
   return cap * (1.0f - 2.0f / (e + 1.0f));
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// (x0, x1) = (x0, x1) * a + b, and (s0, s1) += (x0, x1), in one instruction each.
+__device__ __forceinline__ void fma2(float& x0, float& x1, float a, float b) {
+  asm("{\n\t.reg .b64 x, a, b;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 a, {%2, %2};\n\tmov.b64 b, {%3, %3};\n\t"
+      "fma.rn.f32x2 x, x, a, b;\n\tmov.b64 {%0, %1}, x;\n\t}" : "+f"(x0), "+f"(x1) : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add2(float& s0, float& s1, float x0, float x1) {
+  asm("{\n\t.reg .b64 s, x;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 x, {%2, %3};\n\tadd.rn.f32x2 s, s, x;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}" : "+f"(s0), "+f"(s1) : "f"(x0), "f"(x1));
 }
 
 // a / b, by 32-bit division where both are small.

@@ -37,31 +37,40 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 // Ordinary stores to shared memory become visible to the tensor cores.
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// A shared-memory operand in 128-byte swizzle atoms. `mn_stride`: bytes between atoms of 64 along M or N (of an
-// MN-major operand; a K-major one does not use it). Eight rows are 1024 bytes apart.
-__device__ __forceinline__ uint64_t smem_operand(uint32_t address, uint32_t mn_stride) {
-  return static_cast<uint64_t>((address & 0x3FFFFu) >> 4) | static_cast<uint64_t>(mn_stride >> 4) << 16 |
-         static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+// The low word of a shared-memory operand in 128-byte swizzle atoms. `mn_stride`: bytes between atoms of 64 along M
+// or N (of an MN-major operand; a K-major one does not use it). An address further on by n bytes adds n / 16.
+__device__ __forceinline__ uint32_t smem_operand(uint32_t address, uint32_t mn_stride) {
+  return (address & 0x3FFFFu) >> 4 | (mn_stride >> 4) << 16;
 }
+// The high word: eight rows are 1024 bytes apart.
+constexpr uint32_t kOperandHigh = 1024 >> 4 | 1u << 14 | 2u << 29;
 
 // Instruction descriptor: binary16 operands, binary32 sums, 128 x N; b_mn: B is MN-major.
 __device__ __forceinline__ uint32_t mma_shape(uint32_t n, bool b_mn) {
   return 1u << 4 | (b_mn ? 1u << 16 : 0u) | (n >> 3) << 17 | (128u >> 4) << 24;
 }
 
+// True in one lane of the warp, always the same one: products are issued in warp-uniform code by it, so that their
+// operands go to uniform registers without more ado.
+__device__ __forceinline__ bool elected() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 // D (tensor memory) = A B + (sum ? D : 0) over 16 elements of K; one thread issues it.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool sum) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool sum) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(shape),
-      "r"(static_cast<uint32_t>(sum)) : "memory");
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(shape),
+      "r"(static_cast<uint32_t>(sum)), "n"(kOperandHigh) : "memory");
 }
 // The same with A in tensor memory (two binary16 elements to a column).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool sum) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool sum) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(shape),
-      "r"(static_cast<uint32_t>(sum)) : "memory");
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(shape),
+      "r"(static_cast<uint32_t>(sum)), "n"(kOperandHigh) : "memory");
 }
 // An arrival on `bar` when every product that this thread has issued is done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -69,7 +78,7 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 }
 
 // 32 or 16 columns of this warp's 32 lanes, a column to a register. Loads are asynchronous: the registers hold the
-// values after tmem_wait, which takes them so that no use of them comes before it.
+// values after tmem_wait, and tmem_loaded after it keeps uses of them from going ahead of it.
 #define NVFP4_R8(v, i) "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3]), "=f"(v[i + 4]), "=f"(v[i + 5]), "=f"(v[i + 6]), "=f"(v[i + 7])
 #define NVFP4_RW8(v, i) "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7])
 #define NVFP4_IN8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
@@ -85,12 +94,11 @@ __device__ __forceinline__ void tmem_load(float (&v)[16], uint32_t address) {
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : NVFP4_R8(v, 0), NVFP4_R8(v, 8) : "r"(address));
 }
-__device__ __forceinline__ void tmem_wait(float (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : NVFP4_RW8(v, 0), NVFP4_RW8(v, 8), NVFP4_RW8(v, 16), NVFP4_RW8(v, 24) :: "memory");
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_loaded(float (&v)[32]) {
+  asm volatile("" : NVFP4_RW8(v, 0), NVFP4_RW8(v, 8), NVFP4_RW8(v, 16), NVFP4_RW8(v, 24));
 }
-__device__ __forceinline__ void tmem_wait(float (&v)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : NVFP4_RW8(v, 0), NVFP4_RW8(v, 8) :: "memory");
-}
+__device__ __forceinline__ void tmem_loaded(float (&v)[16]) { asm volatile("" : NVFP4_RW8(v, 0), NVFP4_RW8(v, 8)); }
 __device__ __forceinline__ void tmem_store(uint32_t address, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::

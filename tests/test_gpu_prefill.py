@@ -353,3 +353,10 @@ def test_refusals_by_the_tensors(gpu_lib):
         call(0, ok[0], num_sink_tokens=-1)
     out, lse = call(0, ok[0][:0])
     assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+@pytest.mark.parametrize("window", [-1, 30])
+def test_many_segments_with_an_empty_half(gpu_lib, window):
+    """288 rows a KV head: the second segment's second half has none; several segments to a CTA."""
+    new, lens = [72] * 130, [72 + 3 * i for i in range(130)]
+    _both(gpu_lib, 17, new, lens, 2, 4, 64, 16, HND, BF16, window_left=window, num_sink_tokens=2)

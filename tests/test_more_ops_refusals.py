@@ -91,8 +91,8 @@ def prefill(lib, **kw):
     (dict(out=None), INV, "out is null"), (dict(out=FAKE + 8), ALI, "out"), (dict(lse=FAKE + 2), ALI, "lse"), (dict(ks=FAKE + 1), ALI, "scales"),
     (dict(ptr=None), INV, "null"), (dict(lens=None), INV, "null"), (dict(bt=None), INV, "null"), (dict(vs=None), INV, "null"),
     (dict(kc=cache(data=FAKE + 8)), ALI, "k_cache"), (dict(vc=cache(dstride=10)), INV, "v_cache"), (dict(kc=cache(pages=1 << 31), vc=cache(pages=1 << 31)), UNS, "pages"),
-    (dict(nnz=1 << 31), UNS, "query tokens"), (dict(nnz=(1 << 31) - 1, Hq=128, H=128, qs=1 << 14, kc=cache(H=128), vc=cache(H=128)), UNS, "query rows"),
-    (dict(maxp=(1 << 31) - 1), UNS, "positions"), (dict(ws=None), INV, "workspace"), (dict(wsb=1000), INV, "workspace"), (dict(ws=FAKE + 8), ALI, "workspace"),
+    (dict(nnz=1 << 31), UNS, "query rows"), (dict(nnz=1 << 29), UNS, "query rows"),
+    (dict(maxp=(1 << 31) - 1), UNS, "positions"), (dict(maxp=1 << 27), UNS, "positions"), (dict(ws=None), INV, "workspace"), (dict(wsb=1000), INV, "workspace"), (dict(ws=FAKE + 8), ALI, "workspace"),
 ])
 def test_prefill_refuses(lib, kw, code, text):
     assert prefill(lib, **kw) == code
