@@ -17,9 +17,10 @@
 // depend on timing.
 //
 // A CTA (one to an SM) has four kinds of warps, which wait for one another on mbarriers only:
-//   page     (3 warps, in turn) walk the run's tiles, look up the pages and leave each tile's places in a ring;
-//   load     (8 warps) codes and scales are copied to shared memory a tile or two ahead, decoded to e2m1 * S, exact
-//            in binary16, and written in the tensor cores' order;
+//   page     (3 warps, in turn) walk the run's tiles, look up the pages and leave in a ring what the others need to
+//            know of a tile;
+//   decode   (8 warps, some rows of a tile to each) copy codes and scales to shared memory a tile or two ahead, and
+//            turn them into e2m1 * S, exact in binary16, in the tensor cores' order;
 //   product  (one warp) S = Q K^T and O += P V by tcgen05.mma, sums in tensor memory;
 //   softmax  (8 warps, a row to a thread) S from tensor memory, its running maximum and sum, P in binary16 back to
 //            tensor memory over S; at a segment's end O to the output. They also bring the next queries.
@@ -41,16 +42,16 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kSoftmaxWarps = 8;
-constexpr int kLoadWarps = 8;
-constexpr int kProductWarp = kSoftmaxWarps + kLoadWarps;
+constexpr int kDecodeWarps = 8;
+constexpr int kProductWarp = kSoftmaxWarps + kDecodeWarps;
 constexpr int kPageWarps = 3;
 constexpr int kWarps = kProductWarp + 1 + kPageWarps;
 constexpr int kThreads = kWarps * 32;
 // Registers of a thread of each warpgroup: the launch's 96 for 640 threads, dealt out again.
-constexpr int kLaunchRegisters = 96, kSoftmaxRegisters = 136, kLoadRegisters = 64, kOtherRegisters = 80;
-static_assert(2 * kSoftmaxRegisters + 2 * kLoadRegisters + kOtherRegisters <= 5 * kLaunchRegisters, "more than the launch has");
+constexpr int kLaunchRegisters = 96, kSoftmaxRegisters = 136, kDecodeRegisters = 64, kOtherRegisters = 80;
+static_assert(2 * kSoftmaxRegisters + 2 * kDecodeRegisters + kOtherRegisters <= 5 * kLaunchRegisters, "more than the launch has");
 constexpr int kRing = 8;          // tiles whose places are kept
-constexpr int kSegmentCost = 2;   // what a segment's queries and outputs count for, in tiles
+constexpr int kSegmentCost = 4;   // what a segment's queries and outputs count for, in tiles
 constexpr int kWholeUnits = 8;    // a segment of so few tiles is not cut
 
 // DP: head_dim rounded up to 64, 128 or 256. MT: 128 rows of a segment, or twice as many.
@@ -65,7 +66,7 @@ struct Shape {
   static constexpr int kCodeBytes = BN * DP / 2, kScaleBytes = BN * DP / 16;
   static constexpr int kK = MT * kQBytes, kCodes = kK + 4 * kTileBytes, kScales = kCodes + kRaw * 2 * kCodeBytes;
   static constexpr int kBytes = kScales + (kRaw + 1) * 2 * kScaleBytes;
-  static constexpr int kWarpTokens = BN / kLoadWarps;
+  static constexpr int kWarpTokens = BN / kDecodeWarps;
   static constexpr uint32_t kO = 2 * BN;             // columns of tensor memory: two of S, then O
 };
 
@@ -149,20 +150,20 @@ __device__ __forceinline__ Portion portion_of(const Segment& s, int64_t run) {
 }
 
 struct Barriers {
-  uint64_t full[4], empty[4];  // K's two stages, then V's
+  uint64_t full[4], empty[4];          // K's two stages, then V's
   uint64_t s_full[2], p_full[2], o_full[2], q_full[2], o_step, merge, done;
   uint64_t ring_full[kRing], ring_empty[kRing];
 };
 // One tile of the run, as the page warps leave it to the others. `stream`: bits 0 and 1, the streams whose rows see
-// it; 2 and 3, it is their first of the portion; 4 and 5, their last; 6 and 7, they have one; 8, set. `rest`: tiles of the
-// portion after it.
+// it; 2 and 3, it is their first of the portion; 4 and 5, their last; 6 and 7, they have one; 8, set; 9, all of its
+// positions are on pages of the pool. `rest`: tiles of the portion after it.
 struct Tile {
-  uint2 where[128];           // page (kNoPage: none) and row in it of each position
-  uint32_t live[4];           // positions that are on a page of the pool, 32 to a word
-  uint32_t nan[kLoadWarps];   // a load warp's V scales hold NaN
-  uint16_t nan_blocks[128];   // which blocks of a position (where its warp's nan is set)
+  uint2 where[128];              // page (kNoPage: none) and row in it of each position
+  uint32_t live[4];              // positions that are on a page of the pool, 32 to a word
+  uint8_t nan[kDecodeWarps];     // a decode warp's V scales hold NaN (eight, read at once)
+  uint16_t nan_blocks[128];      // which blocks of a position (where its warp's nan is set)
   uint32_t stream;
-  int32_t rest, first;        // first: of its portion
+  int32_t rest, first;           // first: of its portion
 };
 constexpr uint32_t kNoPage = 0xFFFFFFFFu;
 constexpr int32_t kEnd = -1;          // `rest` after the last tile
@@ -170,6 +171,7 @@ struct Shared {
   Barriers bar;
   Tile ring[kRing];
   Segment first;                      // the run's
+  Segment next[kSoftmaxWarps];        // a softmax warp's
   uint32_t tmem;
   int32_t dead;                       // a wait has run out
   float factor[256];                  // of the query rows
@@ -307,8 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
   Barriers& bar = sh.bar;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar.full + i, kLoadWarps);
-      mbar_init(bar.full + 2 + i, kLoadWarps);
+      mbar_init(bar.full + i, kDecodeWarps);
+      mbar_init(bar.full + 2 + i, kDecodeWarps);
       mbar_init(bar.empty + i, 1);
       mbar_init(bar.empty + 2 + i, 1);
       mbar_init(bar.s_full + i, 1);
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
   // A warp's bounded wait; when it runs out, or another's has, all of the CTA's warps return.
   volatile int32_t* const dead = &sh.dead;
   auto wait_warp = [&](uint64_t* b, uint32_t parity) -> bool {
-    for (uint32_t i = 0; !__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity)); ++i)
+    for (uint32_t i = 0; !__all_sync(0xFFFFFFFFu, mbar_wait_nap(b, parity)); ++i)
       if (__any_sync(0xFFFFFFFFu, i == limit || *dead != 0)) {
         *dead = 1;
         return false;
@@ -350,135 +352,127 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
   if (warp >= kProductWarp) set_registers<kOtherRegisters, false>();
   if (warp == kProductWarp) {
     // ---- product ----
-    const uint32_t shape_s = mma_shape(BN, false), shape_o = mma_shape(D, true);
-    const uint32_t q_op = smem_operand(base, 16), k_op = smem_operand(base + S::kK, 16);
-    const uint32_t v_op = smem_operand(base + S::kK + 2 * S::kTileBytes, BN * 128);
-    uint32_t q_counts = 0, p_counts = 0;  // a bit for each: parities
-    auto commit = [&](uint64_t* b) {
-      if (elected()) mma_commit(b);
-      __syncwarp();
-    };
-    auto issue_s = [&](int half, int buf, uint32_t g) {
-      const uint32_t q = q_op + half * (S::kQBytes / 16), k = k_op + (g & 1) * (S::kTileBytes / 16), d = tmem + buf * BN;
-      if (elected()) {
+    const uint32_t leader = elected();
+    {
+      const uint32_t shape_s = mma_shape(BN, false), shape_o = mma_shape(D, true);
+      const uint32_t q_op = smem_operand(base, 16), k_op = smem_operand(base + S::kK, 16);
+      const uint32_t v_op = smem_operand(base + S::kK + 2 * S::kTileBytes, BN * 128);
+      uint32_t q_counts = 0, p_counts = 0;  // a bit for each: parities
+      auto issue_s = [&](int half, int buf, uint32_t g) {
+        const uint32_t q = q_op + half * (S::kQBytes / 16), k = k_op + (g & 1) * (S::kTileBytes / 16), d = tmem + buf * BN;
 #pragma unroll
         for (int i = 0; i < DP / 16; ++i)
-          if (16 * i < D) mma_ss(d, q + (i >> 2) * 1024 + (i & 3) * 2, k + (i >> 2) * (BN * 8) + (i & 3) * 2, shape_s, i > 0);
-        mma_commit(bar.s_full + buf);
-      }
-      __syncwarp();
-    };
-    auto issue_o = [&](int stream, int buf, uint32_t g, bool sum) {
-      const uint32_t v = v_op + (g & 1) * (S::kTileBytes / 16), d = tmem + S::kO + stream * DP, p = tmem + buf * BN;
-      if (elected()) {
+          if (16 * i < D) mma_ss(leader, d, q + (i >> 2) * 1024 + (i & 3) * 2, k + (i >> 2) * (BN * 8) + (i & 3) * 2, shape_s, i > 0);
+        mma_commit(leader, bar.s_full + buf);
+      };
+      auto issue_o = [&](int stream, int buf, uint32_t g, bool sum) {
+        const uint32_t v = v_op + (g & 1) * (S::kTileBytes / 16), d = tmem + S::kO + stream * DP, p = tmem + buf * BN;
 #pragma unroll
-        for (int i = 0; i < BN / 16; ++i) mma_ts(d, p + 8 * i, v + i * 128, shape_o, sum || i > 0);
-      }
-      __syncwarp();
-    };
-    auto k_ready = [&](uint32_t g) {
-      const bool ok = wait_warp(bar.full + (g & 1), (g >> 1) & 1);
-      tc_fence_after();
-      return ok;
-    };
-    auto v_ready = [&](uint32_t g) { return wait_warp(bar.full + 2 + (g & 1), (g >> 1) & 1); };
-    auto q_ready = [&](int half) {
-      const bool ok = wait_warp(bar.q_full + half, q_counts >> half & 1);
-      q_counts ^= 1u << half;
-      return ok;
-    };
-    auto p_ready = [&](int buf) {
-      const bool ok = wait_warp(bar.p_full + buf, p_counts >> buf & 1);
-      p_counts ^= 1u << buf;
-      tc_fence_after();
-      return ok;
-    };
-    auto tile_ready = [&](uint32_t g) { return wait_warp(bar.ring_full + g % kRing, g / kRing & 1); };
-    auto tile = [&](uint32_t g) -> const Tile& { return sh.ring[g % kRing]; };
-    auto pass_on = [&](uint32_t g) {
-      if (lane == 0) mbar_arrive(bar.ring_empty + g % kRing);
-      __syncwarp();
-    };
-    if constexpr (kTwo) {
-      // Steps: O of tile g in both halves, and S of the next tile, each behind the O whose P it overwrites. A
-      // portion's first step has no O, its last one no S.
-      uint32_t g = 0, now = 0;  // now: the flags of g, 0 in a first step
-      int32_t rest = 0;
-      for (bool ok = true; ok;) {
-        const uint32_t ahead = now ? g + 1 : g;
-        uint32_t next = 0;
-        if (!now || rest > 0) {
-          if (!tile_ready(ahead) || tile(ahead).rest == kEnd) break;
-          next = tile(ahead).stream;
-        }
-        if (now) ok = v_ready(g);
-        if (next && !now) ok = ok && k_ready(ahead);
-#pragma unroll 1
-        for (int i = 0; ok && i < 2; ++i) {
-          if (now >> i & 1) {
-            ok = p_ready(i);
-            if (!ok) break;
-            issue_o(i, i, g, !(now >> (2 + i) & 1));
-            if (now >> (4 + i) & 1) commit(bar.o_full + i);
+        for (int i = 0; i < BN / 16; ++i) mma_ts(leader, d, p + 8 * i, v + i * 128, shape_o, sum || i > 0);
+      };
+      auto k_ready = [&](uint32_t g) {
+        const bool ok = wait_warp(bar.full + (g & 1), (g >> 1) & 1);
+        tc_fence_after();
+        return ok;
+      };
+      auto v_ready = [&](uint32_t g) { return wait_warp(bar.full + 2 + (g & 1), (g >> 1) & 1); };
+      auto q_ready = [&](int half) {
+        const bool ok = wait_warp(bar.q_full + half, q_counts >> half & 1);
+        q_counts ^= 1u << half;
+        return ok;
+      };
+      auto p_ready = [&](int buf) {
+        const bool ok = wait_warp(bar.p_full + buf, p_counts >> buf & 1);
+        p_counts ^= 1u << buf;
+        tc_fence_after();
+        return ok;
+      };
+      auto tile_ready = [&](uint32_t g) { return wait_warp(bar.ring_full + g % kRing, g / kRing & 1); };
+      auto tile = [&](uint32_t g) -> const Tile& { return sh.ring[g % kRing]; };
+      auto pass_on = [&](uint32_t g) { if (leader) mbar_arrive(bar.ring_empty + g % kRing); };
+      if constexpr (kTwo) {
+        // Steps: O of tile g in both halves, and S of the next tile, each behind the O whose P it overwrites. A
+        // portion's first step has no O, its last one no S.
+        uint32_t g = 0, now = 0;  // now: the flags of g, 0 in a first step
+        int32_t rest = 0;
+        for (bool ok = true; ok;) {
+          const uint32_t ahead = now ? g + 1 : g;
+          uint32_t next = 0;
+          int32_t next_rest = 0;
+          if (!now || rest > 0) {
+            if (!tile_ready(ahead)) break;
+            next_rest = uniform(tile(ahead).rest);
+            next = uniform(tile(ahead).stream);
+            if (next_rest == kEnd) break;
           }
-          if (next && now && i == 0) ok = k_ready(ahead);
-          if (ok && !now && (next >> (6 + i) & 1)) ok = q_ready(i);
-          if (ok && (next >> i & 1)) issue_s(i, i, ahead);
+          ok = now ? v_ready(g) : k_ready(ahead);
+#pragma unroll 1
+          for (int i = 0; ok && i < 2; ++i) {
+            if (now >> i & 1) {
+              ok = p_ready(i);
+              if (!ok) break;
+              issue_o(i, i, g, !(now >> (2 + i) & 1));
+              if (now >> (4 + i) & 1) mma_commit(leader, bar.o_full + i);
+            }
+            if (next && now && i == 0) ok = k_ready(ahead);
+            if (ok && !now && (next >> (6 + i) & 1)) ok = q_ready(i);
+            if (ok && (next >> i & 1)) issue_s(i, i, ahead);
+          }
+          if (!ok) break;
+          if (now) {
+            mma_commit(leader, bar.empty + 2 + (g & 1));
+            pass_on(g);
+            ++g;
+          }
+          if (next) mma_commit(leader, bar.empty + (ahead & 1));
+          rest = next_rest;
+          now = next;
         }
-        if (!ok) break;
-        if (now) {
-          commit(bar.empty + 2 + (g & 1));
+      } else {
+        // In one stream S of the next tile goes ahead of O of this one; in two, S of the one after the next follows
+        // O of this one, whose P it overwrites.
+        constexpr int kAhead = kOne ? 1 : 2;
+        uint32_t started = 0;  // tiles whose S has been issued
+        int turn = 0;          // of the tile's buffers, from a portion's first tile on
+        for (uint32_t g = 0; tile_ready(g); ++g) {
+          const int32_t rest = uniform(tile(g).rest);
+          if (rest == kEnd) break;
+          const uint32_t now = uniform(tile(g).stream);
+          bool ok = true;
+          const bool first = uniform(tile(g).first);
+          if (first) {
+            turn = 0;
+            ok = q_ready(0);
+          }
+          // the tiles of this portion that are due
+          const uint32_t due = kTurns && !first ? g + 1 : g + min(rest, 1) + 1;
+#pragma unroll 1
+          for (; ok && started < due; ++started) {
+            ok = tile_ready(started) && k_ready(started);
+            if (!ok) break;
+            issue_s(0, (turn + (started - g)) & 1, started);
+            mma_commit(leader, bar.empty + (started & 1));
+          }
+          if (!ok || !v_ready(g) || !p_ready(turn)) break;
+          issue_o(kOne ? 0 : turn, turn, g, !(now >> (kOne ? 2 : 2 + turn) & 1));
+          mma_commit(leader, bar.empty + 2 + (g & 1));
+          if (kOne) mma_commit(leader, &bar.o_step);
+          if (now >> 4 & 3) mma_commit(leader, bar.o_full + (kOne ? 0 : turn));
+          if (kTurns && rest > 1) {
+            if (!tile_ready(g + kAhead) || !k_ready(g + kAhead)) break;
+            issue_s(0, turn, g + kAhead);
+            mma_commit(leader, bar.empty + ((g + kAhead) & 1));
+            started = g + kAhead + 1;
+          }
+          turn ^= 1;
           pass_on(g);
         }
-        if (next) {
-          commit(bar.empty + (ahead & 1));
-          rest = tile(ahead).rest;
-        }
-        if (now) ++g;
-        now = next;
       }
-    } else {
-      // In one stream S of the next tile goes ahead of O of this one; in two, S of the one after the next follows O
-      // of this one, whose P it overwrites.
-      constexpr int kAhead = kOne ? 1 : 2;
-      uint32_t started = 0;  // tiles whose S has been issued
-      int turn = 0;          // of the tile's buffers, from a portion's first tile on
-      for (uint32_t g = 0; tile_ready(g); ++g) {
-        const int32_t rest = tile(g).rest;
-        if (rest == kEnd) break;
-        const uint32_t now = tile(g).stream;
-        bool ok = true;
-        if (tile(g).first) {
-          turn = 0;
-          ok = q_ready(0);
-        }
-        // the tiles of this portion that are due
-        const uint32_t due = kTurns && !tile(g).first ? g + 1 : g + min(rest, 1) + 1;
-#pragma unroll 1
-        for (; ok && started < due; ++started) {
-          ok = tile_ready(started) && k_ready(started);
-          if (!ok) break;
-          issue_s(0, (turn + (started - g)) & 1, started);
-          commit(bar.empty + (started & 1));
-        }
-        if (!ok || !v_ready(g) || !p_ready(turn)) break;
-        issue_o(kOne ? 0 : turn, turn, g, !(now >> (kOne ? 2 : 2 + turn) & 1));
-        commit(bar.empty + 2 + (g & 1));
-        if (kOne) commit(&bar.o_step);
-        if (now >> 4 & 3) commit(bar.o_full + (kOne ? 0 : turn));
-        if (kTurns && rest > 1) {
-          if (!tile_ready(g + kAhead) || !k_ready(g + kAhead)) break;
-          issue_s(0, turn, g + kAhead);
-          commit(bar.empty + ((g + kAhead) & 1));
-          started = g + kAhead + 1;
-        }
-        turn ^= 1;
-        pass_on(g);
-      }
+      // nothing of this CTA is under way any more when it ends
+      mma_commit(leader, &bar.done);
+      for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(&bar.done, 0); ++i) {}
     }
-    // nothing of this CTA is under way any more when it ends
-    commit(&bar.done);
-    for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(&bar.done, 0); ++i) {}
+    __syncwarp();
   } else if (warp > kProductWarp) {
     // ---- page ----
     const int turn = warp - kProductWarp - 1;
@@ -521,6 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
       if (!wait_warp(bar.ring_empty + g % kRing, (g / kRing & 1) ^ 1)) break;
       if (any) {
         const int32_t t0 = position(k);
+        bool whole = true;
 #pragma unroll 1
         for (int j = 0; j < BN / 32; ++j) {
           const int32_t t = t0 + 32 * j + lane;
@@ -536,10 +531,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           }
           out.where[32 * j + lane] = where;
           const uint32_t word = __ballot_sync(0xFFFFFFFFu, where.x != kNoPage);
+          whole = whole && word == ~0u;
           if (lane == 0) out.live[j] = word;
         }
         if (lane == 0) {
-          uint32_t stream = 256;
+          uint32_t stream = whole ? 768 : 256;
           if constexpr (kTwo) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -567,8 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
       k += kPageWarps;
     }
   } else if (warp >= kSoftmaxWarps) {
-    // ---- load ----
-    set_registers<kLoadRegisters, false>();
+    // ---- decode ----
+    set_registers<kDecodeRegisters, false>();
     // A warp's positions are its own from the copies on: only the tiles that it writes are shared.
     constexpr int TW = S::kWarpTokens;
     constexpr int kLanes = DP / E;             // of a row
@@ -664,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
       const uint32_t tile = base + S::kK + (2 * kv + (g & 1)) * S::kTileBytes;
       const uint8_t* const codes = smem + (code_slot(g, kv) - base) + my_row * (DP / 2) + my_part * (E / 2);
       const uint8_t* const sf = smem + scale_slot(g, kv) + my_row * (DP / 16) + my_part * (E / 16);
-#pragma unroll
+#pragma unroll 2
       for (int i = 0; i < kItems; ++i) {
         const int row = my_row + i * kStep;
         uint32_t sc = E == 32 ? *reinterpret_cast<const uint16_t*>(sf + i * kStep * (DP / 16)) : sf[i * kStep * (DP / 16)] * 0x0101u;
@@ -744,8 +740,36 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
     const float cap = a.soft_cap, unit = a.sm_scale * gk;
     uint32_t tiles = 0, q_count = 0, o_count = 0, merges = 0, steps = 0;
     uint32_t s_count[2] = {0, 0};
-    Segment s = sh.first;
-    for (;;) {
+    // -- the queries --
+    // A warp brings its own rows: as they are, by asynchronous copies to where the products will read them, and
+    // then turns them in place into binary16, each row scaled by a power of two. kPer lanes share a row.
+    constexpr int kPer = kTurns ? 2 : 1;
+    const int q_row = kTurns ? warp * 16 : (kTwo ? warp * 32 : quarter * 32);  // this warp's first
+    const int width = D / 8;                                                  // 16-byte chunks of a row
+    auto chunk = [&](int row, int j) -> uint8_t* {
+      const int r = row & 127;
+      return smem + (row >> 7) * S::kQBytes + (j >> 3) * 16384 + r * 128 + (((j & 7) ^ (r & 7)) << 4);
+    };
+    auto fetch = [&](const Segment& s) {
+      int log_t = 0;
+      while ((1 << log_t) < width) ++log_t;
+      const int j = lane & ((1 << log_t) - 1), step = 32 >> log_t;
+      const int32_t first = s.t * S::kRows, rows = s.q.n * a.G - first;
+      if (j < width) {
+#pragma unroll 1
+        for (int i = q_row + (lane >> log_t); i < q_row + 32 / kPer; i += step) {
+          const bool in = i < rows;
+          const int32_t row = in ? first + i : first, tk = div_q32(row, a.div_g);
+          const int64_t hd = static_cast<int64_t>(s.h) * a.G + (row - tk * a.G);
+          cp_async<16>(smem_addr(chunk(i, j)), a.q + (s.q.q0 + tk) * a.q_row_bytes + hd * D * 2 + 16 * j, in);
+        }
+      }
+      cp_async_commit();
+    };
+    fetch(sh.first);
+    for (bool begun = false;; begun = true) {
+      const Segment s = begun ? sh.next[warp] : sh.first;
+      const bool final = !more(s);
       const Portion part = portion_of(s, run);
       const int32_t n = part.end - part.u;
       const int32_t r0 = s.t * S::kRows, rows = min(s.q.n * a.G - r0, S::kRows);  // the segment's first, and their count
@@ -758,69 +782,76 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
         for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(out)[i] = uint4{};
         if (lse) *lse = -INFINITY;
       }
-      Sight see{0, 0, 0};  // of this stream's rows
-      bool mine = n > 0;   // it has tiles in the portion
+      // this stream's tiles of the portion: the first `sinks`, and [k0, k1)
+      int32_t sinks = 0, k0 = 0, k1 = n;
       if constexpr (kTwo) {
+        Sight see{0, 0, 0};
         if (128 * stream < rows) see = sight_of(a, s.q, r0 + 128 * stream, r0 + min(rows, 128 * stream + 128));
-        int32_t u = part.end;
-        for (mine = false; u > part.u && !mine; --u) mine = sees<BN>(see, (u - 1 < s.first_units ? u - 1 : u - 1 + s.gap) * BN);
+        const int32_t to = max(s.first_units - part.u, 0);  // the portion's first tile past the segment's first units
+        auto tile_at = [&](int32_t t) {  // of the portion, that holds position t or comes after it
+          const int32_t u = t / BN;
+          return (u < s.first_units ? u : max(u - s.gap, s.first_units)) - part.u;
+        };
+        k1 = see.hi > 0 ? min(max(tile_at(see.hi - 1) + 1, 0), n) : 0;
+        k0 = see.hi > 0 ? min(max(tile_at(see.lo), 0), n) : 0;
+        sinks = min(min(max((see.sink + BN - 1) / BN - part.u, 0), to), min(k0, n));
+      }
+      const bool mine = sinks > 0 || k0 < k1;   // it has tiles in the portion
+      if (final) {
+        // the run's last segment, if others continue it
+        if (tid == 0 && s.units > kWholeUnits && s.start >= 0 && s.start < run && s.start + s.units > run) {
+          PrefillCut* const cuts = reinterpret_cast<PrefillCut*>(static_cast<uint8_t*>(a.workspace) + NVFP4_COUNTER_BYTES);
+          cuts[blockIdx.x] = {s.b, s.t, s.h, static_cast<int32_t>(cut.run_of(c0 + s.start + s.units - 1))};
+        }
+      } else {  // (kept in shared memory: the registers are for the scores)
+        Segment next = s;
+        next_segment<S>(a, next);
+        __syncwarp();
+        if (lane == 0) sh.next[warp] = next;
+        __syncwarp();
       }
       if (n > 0) {
-        // -- the queries: in binary16, each row scaled by a power of two --
         if (mine) {
-          const int width = D / 8;
-          int log_t = 0;
-          while ((1 << log_t) < width) ++log_t;
-          const int T = 1 << log_t, j = lane & (T - 1), step = 32 >> log_t;
-          const int per_warp = kTurns ? 16 : 32;
-          const int q_row = kTurns ? warp * 16 : (kTwo ? warp * 32 : quarter * 32);  // this warp's first
+          cp_async_wait<0>();
+          __syncwarp();
+          const int row = q_row + lane / kPer;
+          float top = 0.0f;
 #pragma unroll 1
-          for (int i0 = 0; i0 < per_warp; i0 += 8 * step) {
-            uint4 raw[8];
+          for (int j = lane % kPer; j < width; j += kPer) {
+            const uint4 raw = *reinterpret_cast<const uint4*>(chunk(row, j));
+            const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int i = q_row + i0 + k * step + (lane >> log_t);
-              raw[k] = uint4{};
-              if (i0 + k * step < per_warp && i < rows && j < width) {
-                const int32_t tk = div_q32(r0 + i, a.div_g);
-                const int64_t hd = static_cast<int64_t>(s.h) * a.G + (r0 + i - tk * a.G);
-                raw[k] = __ldg(reinterpret_cast<const uint4*>(a.q + (s.q.q0 + tk) * a.q_row_bytes + hd * D * 2) + j);
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (i0 + k * step >= per_warp) break;
-              const int i = q_row + i0 + k * step + (lane >> log_t);
-              const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-              float v[8], top = 0.0f;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                v[2 * e] = a.bf16 ? __uint_as_float(x[e] << 16) : f32_from_f16_lo(x[e]);
-                v[2 * e + 1] = a.bf16 ? f32_from_bf16_hi(x[e]) : f32_from_f16_hi(x[e]);
-                top = max3(top, fabsf(v[2 * e]), fabsf(v[2 * e + 1]));
-              }
-              for (int o = T >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-              const int exponent = max(static_cast<int>(__float_as_uint(top) >> 23), 1) - 127;
-              const int e2 = top > 0.0f && top <= FLT_MAX ? exponent - 14 : 0;
-              // 2^e2 and 2^-e2 as two factors (they may be out of range by themselves), with f's sign: f is not
-              // negative from here on, and a maximum of scores is one of logits; f = 0 is a query of zeros
-              float f = unit * __int_as_float((127 + e2 / 2) << 23) * __int_as_float((127 + (e2 - e2 / 2)) << 23);
-              float f1 = __int_as_float((127 - e2 / 2) << 23);
-              const float f2 = __int_as_float((127 - (e2 - e2 / 2)) << 23);
-              if (f < 0.0f) f1 = -f1;
-              if (f == 0.0f) f1 = 0.0f;
-              f = f == 0.0f ? 1.0f : fabsf(f);
-              if (j < width) {
-                uint32_t y[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = f16x2_from_f32(v[2 * e] * f1 * f2, v[2 * e + 1] * f1 * f2);
-                const int r = i & 127;
-                const uint32_t dst = base + (i >> 7) * S::kQBytes + (j >> 3) * 16384 + r * 128 + (((j & 7) ^ (r & 7)) << 4);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
-              }
-              if (j == 0) sh.factor[i] = f;
+            for (int e = 0; e < 4; ++e) {
+              const float v0 = a.bf16 ? __uint_as_float(x[e] << 16) : f32_from_f16_lo(x[e]);
+              const float v1 = a.bf16 ? f32_from_bf16_hi(x[e]) : f32_from_f16_hi(x[e]);
+              top = max3(top, fabsf(v0), fabsf(v1));
             }
           }
+          if (kPer == 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          const int exponent = max(static_cast<int>(__float_as_uint(top) >> 23), 1) - 127;
+          const int e2 = top > 0.0f && top <= FLT_MAX ? exponent - 14 : 0;
+          // 2^e2 and 2^-e2 as two factors (they may be out of range by themselves), with f's sign: f is not
+          // negative from here on, and a maximum of scores is one of logits; f = 0 is a query of zeros
+          float f = unit * __int_as_float((127 + e2 / 2) << 23) * __int_as_float((127 + (e2 - e2 / 2)) << 23);
+          float f1 = __int_as_float((127 - e2 / 2) << 23);
+          const float f2 = __int_as_float((127 - (e2 - e2 / 2)) << 23);
+          if (f < 0.0f) f1 = -f1;
+          if (f == 0.0f) f1 = 0.0f;
+          f = f == 0.0f ? 1.0f : fabsf(f);
+#pragma unroll 1
+          for (int j = lane % kPer; j < width; j += kPer) {
+            uint4* const at = reinterpret_cast<uint4*>(chunk(row, j));
+            const uint4 raw = *at;
+            uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float v0 = a.bf16 ? __uint_as_float(x[e] << 16) : f32_from_f16_lo(x[e]);
+              const float v1 = a.bf16 ? f32_from_bf16_hi(x[e]) : f32_from_f16_hi(x[e]);
+              x[e] = f16x2_from_f32(v0 * f1 * f2, v1 * f1 * f2);
+            }
+            *at = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+          sh.factor[row] = f;
           fence_async_proxy();
           __syncwarp();
           uint64_t* const full = bar.q_full + (kTwo ? stream : 0);
@@ -846,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
         for (int32_t k = kTurns ? stream : 0; k < n; k += kTurns ? 2 : 1) {
           const int32_t u = part.u + k;
           const int32_t t0 = (u < s.first_units ? u : u + s.gap) * BN;
-          if (kTwo && !sees<BN>(see, t0)) continue;
+          if (kTwo && !(k < sinks || (k >= k0 && k < k1))) continue;
           const int buf = kTwo ? stream : k & 1;
           ok = wait_warp(bar.s_full + buf, s_count[buf]++ & 1);
           if (!ok) break;
@@ -854,8 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           const Tile& tile = sh.ring[(tiles + k) % kRing];
           const uint32_t s_at = tmem + lanes + buf * BN;
           if (busy) {
-            const bool full = t0 + BN <= all_hi && (t0 >= all_lo || t0 + BN <= sink) &&
-                              (BN == 128 ? tile.live[0] & tile.live[1] & tile.live[2] & tile.live[3] : tile.live[0] & tile.live[1]) == ~0u;
+            const bool full = t0 + BN <= all_hi && (t0 >= all_lo || t0 + BN <= sink) && (tile.stream & 512);
             auto weigh = [&](auto masked_, auto capped_) {
               constexpr bool kMasked = decltype(masked_)::value, kCapped = decltype(capped_)::value;
               constexpr int NC = BN / 32;  // words of 32 positions
@@ -947,11 +977,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
             else ok = full ? weigh(F{}, F{}) : weigh(T{}, F{});
             if (!ok) break;
             // blocks of V that are NaN, where this row sees them
-            for (int w = 0; w < kLoadWarps; ++w) {
-              if (!tile.nan[w]) continue;
-              for (int i = 0; i < S::kWarpTokens; ++i) {
-                const int c = w * S::kWarpTokens + i, t = t0 + c;
-                if (t < hi && (t >= lo || t < sink)) poison |= tile.nan_blocks[c];
+            if (*reinterpret_cast<const uint64_t*>(tile.nan)) {
+#pragma unroll 1
+              for (int c = 0; c < BN; ++c) {
+                const int32_t t = t0 + c;
+                if (tile.nan[c / S::kWarpTokens] && t < hi && (t >= lo || t < sink)) poison |= tile.nan_blocks[c];
               }
             }
             __syncwarp();
@@ -988,6 +1018,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
             poison |= sh.poison[local];
           }
         }
+        // the products of this segment's queries are done: the next ones may come
+        cp_async_wait<0>();
+        if (!final) fetch(sh.next[warp]);
         if (busy && (!kTurns || stream == 0)) {
           const bool whole = part.u == 0 && part.end == s.units;
           const float top = fmaxf(m, m1);
@@ -999,8 +1032,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           float* const part_o = whole ? nullptr : part_of(a, blockIdx.x, s.start < 0 ? 0 : 1, S::kRows, DP);
           const uint32_t o_at = tmem + lanes + S::kO + (kOne || kTurns ? 0 : stream * DP);
 #pragma unroll 1
-          for (int d = 0; d < D; d += 16) {
-            float o[16] = {};
+          for (int d = 0; d < D; d += 32) {  // (head_dim may end in the middle: what lies past it is not stored)
+            float o[32] = {};
             __syncwarp();
             if (started) {
               tmem_load(o, o_at + d);
@@ -1008,31 +1041,36 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
               tmem_loaded(o);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= w0;
+            for (int i = 0; i < 32; ++i) o[i] *= w0;
             if (two) {
-              float x[16];
+              float x[32];
               tmem_load(x, o_at + DP + d);
               tmem_wait();
               tmem_loaded(x);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] += w1 * x[i];
+              for (int i = 0; i < 32; ++i) o[i] += w1 * x[i];
             }
-            if (poison >> (d / 16) & 1u) {
+            if (poison >> (d / 16) & 3u) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = NAN;
+              for (int i = 0; i < 32; ++i) o[i] = poison >> (d / 16 + i / 16) & 1u ? NAN : o[i];
             }
             if (alive && whole) {
-              uint32_t y[8];
+              uint4* const dst = reinterpret_cast<uint4*>(out + d * 2);
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                y[i] = a.bf16 ? bf16x2_from_f32(o[2 * i], o[2 * i + 1]) : f16x2_from_f32(o[2 * i], o[2 * i + 1]);
-              uint4* dst = reinterpret_cast<uint4*>(out + d * 2);
-              dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-              dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+              for (int k = 0; k < 4; ++k) {
+                uint32_t y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float v0 = o[8 * k + 2 * i], v1 = o[8 * k + 2 * i + 1];
+                  y[i] = a.bf16 ? bf16x2_from_f32(v0, v1) : f16x2_from_f32(v0, v1);
+                }
+                if (k < 2 || d + 16 < D) dst[k] = make_uint4(y[0], y[1], y[2], y[3]);
+              }
             } else if (alive) {
               float4* dst = reinterpret_cast<float4*>(part_o + static_cast<int64_t>(local) * DP + d);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              for (int i = 0; i < 8; ++i)
+                if (i < 4 || d + 16 < D) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
           }
           if (alive) {
@@ -1046,15 +1084,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           tc_fence_before();  // (these reads come before the next segment's products)
         }
         tiles += n;
+      } else if (!final) {
+        cp_async_wait<0>();
+        fetch(sh.next[warp]);
       }
-      if (!more(s)) break;
-      next_segment<S>(a, s);
+      if (final) break;
+      __syncwarp();
     }
-    // the run's last segment, if others continue it
-    if (tid == 0 && s.units > kWholeUnits && s.start >= 0 && s.start < run && s.start + s.units > run) {
-      PrefillCut* const cuts = reinterpret_cast<PrefillCut*>(static_cast<uint8_t*>(a.workspace) + NVFP4_COUNTER_BYTES);
-      cuts[blockIdx.x] = {s.b, s.t, s.h, static_cast<int32_t>(cut.run_of(c0 + s.start + s.units - 1))};
-    }
+    cp_async_wait<0>();
     }
   }
   tc_fence_before();

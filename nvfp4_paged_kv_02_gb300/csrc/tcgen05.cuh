@@ -14,6 +14,20 @@ namespace nvfp4 {
 
 constexpr uint32_t kTmemColumns = 512;
 
+// Whether a phase is complete; if not, the thread may sleep for some microseconds before it says so.
+constexpr uint32_t kNap = 10000;  // ns
+__device__ __forceinline__ bool mbar_wait_nap(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "n"(kNap)
+      : "memory");
+  return ok != 0;
+}
+
 // The registers of a warpgroup's threads from here on (all of its warps call it): fewer, or more, which waits until
 // others have given theirs up.
 template <int N, bool MORE>
@@ -50,31 +64,35 @@ __device__ __forceinline__ uint32_t mma_shape(uint32_t n, bool b_mn) {
   return 1u << 4 | (b_mn ? 1u << 16 : 0u) | (n >> 3) << 17 | (128u >> 4) << 24;
 }
 
-// True in one lane of the warp, always the same one: products are issued in warp-uniform code by it, so that their
-// operands go to uniform registers without more ado.
-__device__ __forceinline__ bool elected() {
+// True in one lane of the warp. Products are issued in code that the whole warp runs, and by that lane alone: so their
+// operands are computed in uniform registers, where the instruction takes them.
+__device__ __forceinline__ uint32_t elected() {
   uint32_t one;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-  return one != 0;
+  return one;
 }
+// The same value in all lanes, and known to be.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_or_sync(0xFFFFFFFFu, v); }
 
-// D (tensor memory) = A B + (sum ? D : 0) over 16 elements of K; one thread issues it.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool sum) {
+// D (tensor memory) = A B + (sum ? D : 0) over 16 elements of K, by the lane where `leader` is set.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, uint32_t sum) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(shape),
-      "r"(static_cast<uint32_t>(sum)), "n"(kOperandHigh) : "memory");
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\tmov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b),
+      "r"(shape), "r"(sum), "n"(kOperandHigh), "r"(leader) : "memory");
 }
 // The same with A in tensor memory (two binary16 elements to a column).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool sum) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, uint32_t sum) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(shape),
-      "r"(static_cast<uint32_t>(sum)), "n"(kOperandHigh) : "memory");
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(shape), "r"(sum),
+      "n"(kOperandHigh), "r"(leader) : "memory");
 }
-// An arrival on `bar` when every product that this thread has issued is done.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+// An arrival on `bar` when every product that the leader has issued is done.
+__device__ __forceinline__ void mma_commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)), "r"(leader) : "memory");
 }
 
 // 32 or 16 columns of this warp's 32 lanes, a column to a register. Loads are asynchronous: the registers hold the
