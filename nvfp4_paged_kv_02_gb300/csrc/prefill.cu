@@ -51,7 +51,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kLaunchRegisters = 96, kSoftmaxRegisters = 136, kDecodeRegisters = 64, kOtherRegisters = 80;
 static_assert(2 * kSoftmaxRegisters + 2 * kDecodeRegisters + kOtherRegisters <= 5 * kLaunchRegisters, "more than the launch has");
 constexpr int kRing = 8;          // tiles whose places are kept
-constexpr int kSegmentCost = 4;   // what a segment's queries and outputs count for, in tiles
+constexpr int kSegmentCost = 5;   // what a segment's queries and outputs count for, in tiles
 constexpr int kWholeUnits = 8;    // a segment of so few tiles is not cut
 
 // DP: head_dim rounded up to 64, 128 or 256. MT: 128 rows of a segment, or twice as many.
@@ -157,13 +157,15 @@ struct Barriers {
 // One tile of the run, as the page warps leave it to the others. `stream`: bits 0 and 1, the streams whose rows see
 // it; 2 and 3, it is their first of the portion; 4 and 5, their last; 6 and 7, they have one; 8, set; 9, all of its
 // positions are on pages of the pool. `rest`: tiles of the portion after it.
-struct Tile {
+struct __align__(16) Tile {
   uint2 where[128];              // page (kNoPage: none) and row in it of each position
   uint32_t live[4];              // positions that are on a page of the pool, 32 to a word
-  uint8_t nan[kDecodeWarps];     // a decode warp's V scales hold NaN (eight, read at once)
-  uint16_t nan_blocks[128];      // which blocks of a position (where its warp's nan is set)
+  uint8_t nan[kDecodeWarps];     // a decode warp's V scales hold NaN (eight, read with the next two at once)
   uint32_t stream;
-  int32_t rest, first;           // first: of its portion
+  int32_t rest;
+  uint16_t nan_blocks[128];      // which blocks of a position (where its warp's nan is set)
+  int32_t first;                 // of its portion
+  int32_t unused[3];             // (a multiple of 16 bytes)
 };
 constexpr uint32_t kNoPage = 0xFFFFFFFFu;
 constexpr int32_t kEnd = -1;          // `rest` after the last tile
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
     return true;
   };
   auto more = [&](const Segment& s) { return s.start + places_of(s.units) < run; };
-  const int D = a.D;
+  const int D = E == 32 && DP <= 128 ? DP : a.D;
   const uint32_t base = smem_addr(smem);
 
   if (warp >= kProductWarp) set_registers<kOtherRegisters, false>();
@@ -883,9 +885,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           if (!ok) break;
           tc_fence_after();
           const Tile& tile = sh.ring[(tiles + k) % kRing];
+          const uint4 about = *reinterpret_cast<const uint4*>(tile.nan);  // nan, stream, rest
           const uint32_t s_at = tmem + lanes + buf * BN;
           if (busy) {
-            const bool full = t0 + BN <= all_hi && (t0 >= all_lo || t0 + BN <= sink) && (tile.stream & 512);
+            const bool full = t0 + BN <= all_hi && (t0 >= all_lo || t0 + BN <= sink) && (about.z & 512);
             auto weigh = [&](auto masked_, auto capped_) {
               constexpr bool kMasked = decltype(masked_)::value, kCapped = decltype(capped_)::value;
               constexpr int NC = BN / 32;  // words of 32 positions
@@ -977,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
             else ok = full ? weigh(F{}, F{}) : weigh(T{}, F{});
             if (!ok) break;
             // blocks of V that are NaN, where this row sees them
-            if (*reinterpret_cast<const uint64_t*>(tile.nan)) {
+            if (about.x | about.y) {
 #pragma unroll 1
               for (int c = 0; c < BN; ++c) {
                 const int32_t t = t0 + c;
