@@ -95,20 +95,39 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 struct Span {
   int32_t lo, len, sink, first_units, gap;
 };
-__device__ __forceinline__ Span span_of(const AttentionArgs& a, int32_t b) {
+__device__ __forceinline__ Span span_of(const AttentionArgs& a, int32_t b, int32_t tokens = 1) {
   const int64_t reach = a.max_pages * a.ps;
   const int32_t n = max(__ldg(a.seq_lens + b), 0);
   Span s;
   s.len = n > reach ? static_cast<int32_t>(reach) : n;
-  s.lo = a.window_left >= 0 ? max(0, s.len - 1 - a.window_left) : 0;
+  const int32_t first = s.len - tokens;  // the first query token's position
+  s.lo = a.window_left >= 0 ? max(0, first - min(a.window_left, s.len)) : 0;
   s.sink = min(a.sink, s.lo);
   s.first_units = static_cast<int32_t>((static_cast<uint32_t>(s.sink) + kUnit - 1) / kUnit);
   s.gap = max(s.lo / kUnit - s.first_units, 0);  // (0: the last of the first units may hold lo too)
   return s;
 }
 
+// ROWS: the query tokens [q0, q0 + n) of request b, if their rows are for this kernel (n = 0: they are not).
+struct Tokens {
+  int64_t q0;
+  int32_t n;
+};
+__device__ __forceinline__ Tokens tokens_of(const AttentionArgs& a, int32_t b) {
+  const int64_t p0 = min(max(static_cast<int64_t>(__ldg(a.qo_indptr + b)), int64_t(0)), a.nnz);
+  const int64_t p1 = min(max(static_cast<int64_t>(__ldg(a.qo_indptr + b + 1)), p0), a.nnz);
+  return {p0, (p1 - p0) * a.G <= a.most_rows ? static_cast<int32_t>(p1 - p0) : 0};
+}
+
 // Units of one (request, head): of its tokens, or of the slots of its selected pages.
+template <bool ROWS>
 __device__ __forceinline__ int32_t units_of(const AttentionArgs& a, int32_t b, int32_t h) {
+  if constexpr (ROWS) {
+    const Tokens q = tokens_of(a, b);
+    if (q.n == 0) return 0;
+    const Span s = span_of(a, b, q.n);
+    return s.len > 0 ? (s.len - 1) / kUnit + 1 - s.gap : 0;
+  }
   if (a.selected) {
     const int32_t n = min(max(__ldg(a.num_selected + static_cast<int64_t>(b) * a.H + h), 0), a.max_selected);
     return (n * a.ps + kUnit - 1) / kUnit;
@@ -121,26 +140,28 @@ __device__ __forceinline__ int32_t units_of(const AttentionArgs& a, int32_t b, i
 // its join and its output. Those trailing places of a segment hold no work.
 __device__ __forceinline__ int32_t places_of(int32_t units) { return units > 0 ? units + kSegmentCost : 0; }
 
+template <bool ROWS>
 __device__ __forceinline__ int64_t places_of_request(const AttentionArgs& a, int32_t b) {
   int64_t n = 0;
   if (a.selected) {
-    for (int32_t h = 0; h < a.H; ++h) n += places_of(units_of(a, b, h));
+    for (int32_t h = 0; h < a.H; ++h) n += places_of(units_of<ROWS>(a, b, h));
   } else {
-    n = static_cast<int64_t>(places_of(units_of(a, b, 0))) * a.H;
+    n = static_cast<int64_t>(places_of(units_of<ROWS>(a, b, 0))) * a.H;
   }
   return n * a.chunks;
 }
 
 // cum[e] = places of the requests up to the end of group e (of 1 << a.log2_group in order, a.groups of
 // them); every thread calls it, ends with a barrier.
+template <bool ROWS>
 __device__ __forceinline__ void scan_places(const AttentionArgs& a, int64_t* cum, int64_t* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.groups + kThreads - 1) / kThreads;
   const int lo = tid * per, hi = min(a.groups, lo + per);
   int64_t local = 0;
   for (int e = lo; e < hi; ++e) {
-    local += places_of_request(a, e << a.log2_group);
-    for (int b = (e << a.log2_group) + 1; b < min(a.B, (e + 1) << a.log2_group); ++b) local += places_of_request(a, b);
+    local += places_of_request<ROWS>(a, e << a.log2_group);
+    for (int b = (e << a.log2_group) + 1; b < min(a.B, (e + 1) << a.log2_group); ++b) local += places_of_request<ROWS>(a, b);
     cum[e] = local;
   }
   int64_t v = local;
@@ -163,6 +184,7 @@ struct Segment {
   int32_t b, h, chunk, units, start;
 };
 
+template <bool ROWS>
 __device__ __forceinline__ Segment find_segment(const AttentionArgs& a, const int64_t* cum, int64_t place) {
   int32_t lo = 0, hi = a.groups - 1;
   while (lo < hi) {
@@ -173,15 +195,15 @@ __device__ __forceinline__ Segment find_segment(const AttentionArgs& a, const in
   Segment s{lo << a.log2_group, 0, 0, 0, 0};
   int64_t start = lo > 0 ? cum[lo - 1] : 0;
   if (a.log2_group > 0) {  // the request in its group
-    for (int64_t n; place >= start + (n = places_of_request(a, s.b)); ++s.b) start += n;
+    for (int64_t n; place >= start + (n = places_of_request<ROWS>(a, s.b)); ++s.b) start += n;
   }
-  s.units = units_of(a, s.b, 0);
+  s.units = units_of<ROWS>(a, s.b, 0);
   if (a.selected) {
     for (;;) {
       const int64_t head = static_cast<int64_t>(places_of(s.units)) * a.chunks;
       if (place < start + head || s.h + 1 == a.H) break;
       start += head;
-      s.units = units_of(a, s.b, ++s.h);
+      s.units = units_of<ROWS>(a, s.b, ++s.h);
     }
   } else {
     const int64_t head = static_cast<int64_t>(places_of(s.units)) * a.chunks;
@@ -194,6 +216,7 @@ __device__ __forceinline__ Segment find_segment(const AttentionArgs& a, const in
 }
 
 // The next segment that has units (the caller knows that there is one).
+template <bool ROWS>
 __device__ __forceinline__ void next_segment(const AttentionArgs& a, Segment& s) {
   s.start += places_of(s.units);
   if (++s.chunk < a.chunks) return;
@@ -203,7 +226,7 @@ __device__ __forceinline__ void next_segment(const AttentionArgs& a, Segment& s)
       s.h = 0;
       ++s.b;
     }
-    s.units = s.b < a.B ? units_of(a, s.b, s.h) : 1;
+    s.units = s.b < a.B ? units_of<ROWS>(a, s.b, s.h) : 1;
   } while (s.units == 0);
 }
 
@@ -231,9 +254,11 @@ constexpr int kStages = 3;
 // ---- the kernel ------------------------------------------------------------------------------
 
 // NW: words of codes that a lane holds of a V row (D <= 64 NW). NT: eights of query heads.
+// ROWS: of several query tokens of each request, which see different positions; a row in place of a query head is
+// a (token, head) pair, row r of KV head h is token r / G and head h G + r % G. Requests of up to most_rows rows.
 // FULL: D = 64 NW and scale rows that cp.async can copy; otherwise any D, and scales of any
 // alignment, which go through registers.
-template <int NW, int NT, bool FULL>
+template <int NW, int NT, bool FULL, bool ROWS>
 __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attention_kernel(const AttentionArgs a) {
   using T = Tile<NW>;
   constexpr int NS = kStages;
@@ -250,20 +275,28 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
   const int r = lane >> 2, c = lane & 3;
   const int D = FULL ? 64 * NW : a.D;
   const float gk = __ldg(a.k_scale), gv = __ldg(a.v_scale);
-  scan_places(a, cum, s_scan);
+  scan_places<ROWS>(a, cum, s_scan);
 
   // heads without live tokens get zeros
   auto write_zeros = [&] {
     for (int32_t b = blockIdx.x; b < a.B; b += gridDim.x) {
       const int64_t reach = a.max_pages * a.ps;
       if (tid == 0 && __ldg(a.seq_lens + b) > reach) flag(a.status, NVFP4_DEV_LEN_CLAMPED);
-      if (!a.selected && units_of(a, b, 0) > 0) continue;
+      if (!a.selected && units_of<ROWS>(a, b, 0) > 0) continue;
+      if constexpr (ROWS) {
+        const Tokens q = tokens_of(a, b);
+        const int64_t row = q.q0 * a.Hq, rows = static_cast<int64_t>(q.n) * a.Hq;
+        uint2* o = reinterpret_cast<uint2*>(a.out + row * D * 2);
+        for (int64_t i = tid; i < rows * D / 4; i += kThreads) o[i] = make_uint2(0, 0);
+        for (int64_t i = tid; i < rows && a.lse; i += kThreads) a.lse[row + i] = -INFINITY;
+      } else {
       for (int32_t h = 0; h < a.H; ++h) {
-        if (units_of(a, b, h) > 0) continue;
+        if (units_of<ROWS>(a, b, h) > 0) continue;
         const int64_t row = static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(h) * a.G;
         uint2* o = reinterpret_cast<uint2*>(a.out + row * D * 2);
         for (int i = tid; i < a.G * D / 4; i += kThreads) o[i] = make_uint2(0, 0);
         for (int i = tid; i < a.G && a.lse; i += kThreads) a.lse[row + i] = -INFINITY;
+      }
       }
     }
   };
@@ -289,17 +322,32 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
   }
 
   auto more = [&](const Segment& s) { return s.start + places_of(s.units) < run; };
-  Segment cs = find_segment(a, cum, c0);  // the consumer's segment
+  Segment cs = find_segment<ROWS>(a, cum, c0);  // the consumer's segment
   // the run begins in the segment's empty places, or in a segment that is not cut
   if (cs.start + cs.units <= 0 || (cs.start < 0 && cs.units <= kWholeUnits)) {
     if (!more(cs)) {
       write_zeros();
       return;
     }
-    next_segment(a, cs);
+    next_segment<ROWS>(a, cs);
   }
   uint32_t raw[NT][8 * NW];  // the coming segment's query rows, as they are
   auto load_queries = [&](const Segment& s) {
+    if constexpr (ROWS) {
+      const Tokens tk = tokens_of(a, s.b);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = 8 * nt + r, token = row / a.G;
+        const uint8_t* q = a.q + (tk.q0 + token) * a.q_row_bytes + ((static_cast<int64_t>(s.h) * a.G + row - token * a.G) * D + 16 * NW * c) * 2;
+#pragma unroll
+        for (int i = 0; i < 2 * NW; ++i) {
+          const bool in = token < tk.n && 16 * NW * c + 8 * i < D;
+          const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(q) + i) : uint4{};
+          raw[nt][4 * i] = x.x; raw[nt][4 * i + 1] = x.y; raw[nt][4 * i + 2] = x.z; raw[nt][4 * i + 3] = x.w;
+        }
+      }
+      return;
+    }
     const int head0 = s.chunk * a.chunk_heads, heads = min(a.chunk_heads, a.G - head0);
     const uint8_t* q = a.q + s.b * a.q_row_bytes +
                        ((static_cast<int64_t>(s.h) * a.G + head0 + r) * D + 16 * NW * c) * 2;
@@ -328,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
   auto enter = [&] {
     portion(ps, pu, pend);
     pu += warp;
-    span = span_of(a, ps.b);
+    span = span_of(a, ps.b, ROWS ? tokens_of(a, ps.b).n : 1);
     list = static_cast<const uint8_t*>(a.block_tables) + (ps.b * a.max_pages << (a.table64 ? 3 : 2));
     if (a.selected)
       slots = min(max(__ldg(a.num_selected + static_cast<int64_t>(ps.b) * a.H + ps.h), 0), a.max_selected) * a.ps;
@@ -336,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
   enter();
   auto settle = [&] {  // to a unit of this warp, or past the run's end (pu >= pend)
     while (pu >= pend && more(ps)) {
-      next_segment(a, ps);
+      next_segment<ROWS>(a, ps);
       enter();
     }
   };
@@ -515,7 +563,15 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
     }
     return v;
   };
-  auto write_out = [&](int64_t row, int heads, int parts) {
+  // (ROWS: `row` is the request's first token, `h` the KV head)
+  auto write_out = [&](int64_t row, int heads, int parts, int32_t h) {
+    auto at = [&](int head) -> int64_t {
+      if constexpr (ROWS) {
+        const int token = head / a.G;
+        return (row + token) * a.Hq + static_cast<int64_t>(h) * a.G + head - token * a.G;
+      }
+      return row + head;
+    };
     for (int i = tid; i < heads * D / 4; i += kThreads) {
       const int head = i / (D / 4), d = i % (D / 4) * 4;
       const float4 v = joined(head, d, parts);
@@ -523,10 +579,10 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
       uint2 w;
       w.x = a.bf16 ? bf16x2_from_f32(v.x * f, v.y * f) : f16x2_from_f32(v.x * f, v.y * f);
       w.y = a.bf16 ? bf16x2_from_f32(v.z * f, v.w * f) : f16x2_from_f32(v.z * f, v.w * f);
-      *reinterpret_cast<uint2*>(a.out + ((row + head) * D + d) * 2) = w;
+      *reinterpret_cast<uint2*>(a.out + (at(head) * D + d) * 2) = w;
     }
     if (a.lse && tid < heads)
-      a.lse[row + tid] = s_sum[tid] == 0.0f ? -INFINITY
+      a.lse[at(tid)] = s_sum[tid] == 0.0f ? -INFINITY
                                             : (s_top[tid] - kWeightBias) * (1.0f / kLog2e) + logf(s_sum[tid]);
   };
   // Parts of shared segments: run i's slot 0 if the segment began before the run, else its slot 1.
@@ -541,8 +597,31 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
   for (;;) {
     // the segment's query heads
     const int head0 = cs.chunk * a.chunk_heads;
-    const int heads = min(a.chunk_heads, a.G - head0);
+    int heads = min(a.chunk_heads, a.G - head0);
     const int64_t q_row = static_cast<int64_t>(cs.h) * a.G + head0;
+    // ROWS: what this lane's rows see (t < row_hi, and t >= row_lo or t < sink); units below `plain` and at or past
+    // `open` (or of first tokens) are all rows' alike
+    Span seen{};
+    int64_t q_first = 0;
+    int32_t row_hi[NT][2], row_lo[NT][2], plain = 0, open = 0;
+    if constexpr (ROWS) {
+      const Tokens tk = tokens_of(a, cs.b);
+      heads = tk.n * a.G;
+      q_first = tk.q0;
+      seen = span_of(a, cs.b, tk.n);
+      const int32_t first = seen.len - tk.n;
+      auto lo_of = [&](int32_t p) { return a.window_left >= 0 && p > a.window_left ? p - a.window_left : 0; };
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int32_t p = first + min((8 * nt + 2 * c + k) / a.G, tk.n - 1);
+          row_hi[nt][k] = a.causal ? p + 1 : seen.len;
+          row_lo[nt][k] = lo_of(p);
+        }
+      plain = a.causal ? first + 1 : seen.len;
+      open = lo_of(seen.len - 1);
+    }
     uint32_t qf[NT][4 * NW][2];
     float factor[NT][2];  // base-2 logarithm units of a score (before the cap: natural ones)
 #pragma unroll
@@ -678,6 +757,49 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
             for (int nt = 0; nt < NT; ++nt) x[k / 2][nt][k % 2 * 2] = x[k / 2][nt][k % 2 * 2 + 1] = -INFINITY;
           }
       }
+      uint32_t nan_rows[NT][2];  // blocks of V that are NaN where a row sees them
+      bool nan_seen = false;
+      if constexpr (ROWS) {
+        const int32_t base = (cu < seen.first_units ? cu : cu + seen.gap) * kUnit;
+        if (base + kUnit > plain || (base < open && base + kUnit > seen.sink)) {
+          auto sees = [&](int32_t t, int nt, int k) {
+            return t < row_hi[nt][k] && (t >= row_lo[nt][k] || t < a.sink);
+          };
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (!sees(base + 8 * k + t0, nt, e)) x[k / 2][nt][k % 2 * 2 + e] = -INFINITY;
+          // A weight of 0 does not keep a NaN of V from a row that does not see it: NaN scales are taken out of the
+          // stage here, and put into the sums of the rows that do.
+          uint8_t* const sr = const_cast<uint8_t*>(st) + T::kVs + lane * T::kScales;
+          uint32_t blocks = 0;
+#pragma unroll
+          for (int e = 0; e < 4 * NW; ++e)
+            if ((sr[e] & 0x7Fu) == 0x7Fu && (mask >> lane & 1u)) blocks |= 1u << e;
+          nan_seen = __any_sync(0xFFFFFFFFu, blocks != 0);
+          if (nan_seen) {
+#pragma unroll
+            for (int e = 0; e < 4 * NW; ++e)
+              if (blocks >> e & 1u) sr[e] = 0;
+            __syncwarp();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) nan_rows[nt][e] = 0;
+            for (int from = 0; from < kUnit; ++from) {
+              const uint32_t theirs = __shfl_sync(0xFFFFFFFFu, blocks, from);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (sees(base + from, nt, e)) nan_rows[nt][e] |= theirs;
+            }
+          }
+        }
+      }
       // The maximum follows the scores only when one is more than kSlack above it: until then a
       // weight is at most 2^(kWeightBias + kSlack), which binary16 holds.
       float top[NT][2];
@@ -783,13 +905,25 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
           }
         }
       }
+      if (ROWS && nan_seen) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+              if (nan_rows[nt][k] >> ((NW * r + w) >> 1) & 1u) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nt][w][i][k] = o[nt][w][i][k + 2] = NAN;
+              }
+      }
     }
 
     // the next segment's queries arrive while this one is joined
     const Segment done = cs;
     const bool last_segment = !more(cs);
     if (!last_segment) {
-      next_segment(a, cs);
+      next_segment<ROWS>(a, cs);
       load_queries(cs);
     }
 
@@ -818,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
     __syncthreads();
     join_stats(kWarps);
     if (whole) {
-      write_out(static_cast<int64_t>(done.b) * a.Hq + q_row, heads, kWarps);
+      write_out(ROWS ? q_first : static_cast<int64_t>(done.b) * a.Hq + q_row, heads, kWarps, done.h);
     } else {
       // this run's part of a segment that others share: the last of them will join the parts, at its
       // end, so that nobody waits here for the count (a run shares at most its first and its last)
@@ -864,7 +998,8 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
     for (int n = 0; n < shared; ++n) {
       if (!s_shared[n].join) continue;
       const int32_t first = s_shared[n].first, last = s_shared[n].last, head0 = s_shared[n].chunk * a.chunk_heads;
-      const int heads = min(a.chunk_heads, a.G - head0);
+      const Tokens tk = ROWS ? tokens_of(a, s_shared[n].b) : Tokens{0, 0};
+      const int heads = ROWS ? tk.n * a.G : min(a.chunk_heads, a.G - head0);
       // The last of them adds all up, in the runs' order, with kBatch parts' loads under way at once:
       // this is a chain of trips to L2, at the kernel's end. Few parts: all threads go over all of
       // them; many: every warp over a fourth.
@@ -910,17 +1045,17 @@ __global__ void __launch_bounds__(kThreads, NW <= 2 && NT == 1 ? 3 : 1) attentio
       }
       __syncthreads();
       join_stats(teams);
-      write_out(static_cast<int64_t>(s_shared[n].b) * a.Hq + static_cast<int64_t>(s_shared[n].h) * a.G + head0, heads,
-                teams);
+      write_out(ROWS ? tk.q0 : static_cast<int64_t>(s_shared[n].b) * a.Hq + static_cast<int64_t>(s_shared[n].h) * a.G + head0,
+                heads, teams, s_shared[n].h);
       __syncthreads();
     }
   }
   write_zeros();
 }
 
-template <int NW, int NT, bool FULL>
+template <int NW, int NT, bool FULL, bool ROWS>
 nvfp4_status launch_t(AttentionArgs a, cudaStream_t stream) {
-  const auto kern = attention_kernel<NW, NT, FULL>;
+  const auto kern = attention_kernel<NW, NT, FULL, ROWS>;
   const size_t fixed = kWarps * kStages * Tile<NW>::kBytes + kWarps * 8 * NT * (64 * NW + 4) * 4;
   // an entry of the scan for each request; where they do not fit (above some 10,600 requests with head_dim
   // above 192, 15,100 above 128), for two
@@ -941,7 +1076,8 @@ nvfp4_status launch_t(AttentionArgs a, cudaStream_t stream) {
 
 template <int NW, int NT>
 nvfp4_status launch_f(const AttentionArgs& a, bool full, cudaStream_t s) {
-  return full ? launch_t<NW, NT, true>(a, s) : launch_t<NW, NT, false>(a, s);
+  if (a.qo_indptr) return full ? launch_t<NW, NT, true, true>(a, s) : launch_t<NW, NT, false, true>(a, s);
+  return full ? launch_t<NW, NT, true, false>(a, s) : launch_t<NW, NT, false, false>(a, s);
 }
 
 // Query heads that one pass over the cache serves: eight, or sixteen where the accumulators of
@@ -957,8 +1093,8 @@ int64_t attention_workspace_bytes(int32_t Hq, int32_t H, int32_t D) {
 }
 
 nvfp4_status launch_attention(AttentionArgs a, cudaStream_t stream) {
-  const int nt = eights_of(a.G, a.D), nw = (a.D + 63) / 64;
-  a.chunks = (a.G + 8 * nt - 1) / (8 * nt);
+  const int nt = a.qo_indptr ? a.most_rows / 8 : eights_of(a.G, a.D), nw = (a.D + 63) / 64;
+  a.chunks = a.qo_indptr ? 1 : (a.G + 8 * nt - 1) / (8 * nt);
   a.chunk_heads = (a.G + a.chunks - 1) / a.chunks;
   const int64_t pool = a.kc.num_pages < a.vc.num_pages ? a.kc.num_pages : a.vc.num_pages;
   a.pool_pages = static_cast<uint32_t>(pool);

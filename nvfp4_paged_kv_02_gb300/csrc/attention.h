@@ -30,6 +30,11 @@ struct AttentionArgs {
   float* lse;  // may be null
   int32_t* status;
   void* workspace;
+  // several query tokens of each request, in requests of at most most_rows (8 or 16) rows of a KV head (attention of
+  // the last tokens): rows of query by qo_indptr; or null
+  const int32_t* qo_indptr;
+  int64_t nnz;
+  int32_t causal, most_rows;
   // set at launch
   int32_t chunks, chunk_heads;  // passes over a KV head's query heads, and the heads of one
   uint32_t pool_pages;          // pages that both caches have
@@ -62,6 +67,7 @@ struct PrefillArgs {
   void* workspace;
   // set at launch
   int64_t pool_pages, parts_offset;
+  int32_t few_rows;  // requests of so few rows are another kernel's
   uint32_t k_stride, v_stride, k_sf_stride, v_sf_stride;  // page strides, bytes
   PipeTest pipe;
 };

@@ -79,7 +79,8 @@ __device__ __forceinline__ Request request_of(const PrefillArgs& a, int32_t b) {
   const int64_t p1 = min(max(static_cast<int64_t>(__ldg(a.qo_indptr + b + 1)), p0), a.nnz);
   const int64_t reach = a.max_pages * a.ps;
   const int32_t n = max(__ldg(a.seq_lens + b), 0);
-  return {p0, static_cast<int32_t>(p1 - p0), n > reach ? static_cast<int32_t>(reach) : n};
+  const int32_t tokens = (p1 - p0) * a.G <= a.few_rows ? 0 : static_cast<int32_t>(p1 - p0);
+  return {p0, tokens, n > reach ? static_cast<int32_t>(reach) : n};
 }
 
 // Positions that rows [r0, r1) of a request see: t < hi and (t >= lo or t < sink).
@@ -1202,6 +1203,28 @@ nvfp4_status launch_prefill(PrefillArgs a, cudaStream_t stream) {
   a.k_sf_stride = static_cast<uint32_t>(strides[2]);
   a.v_sf_stride = static_cast<uint32_t>(strides[3]);
   a.pipe = pipe_test_from_env();
+  // Where requests have few rows on average (drafts, or single tokens among them), those that have go to the kernel
+  // of single tokens, which reads a cache faster than rows of 128 can be made of it: 64 requests of four tokens, four
+  // query heads to a KV head, 105 K positions: 117 us here, 83 with both launches. Tables of up to 1024 positions stay
+  // here: the second launch costs more (five requests of 1 to 9 tokens over up to 86 positions: 14 us, with both 27).
+  a.few_rows = 0;
+  const int64_t all = a.nnz * a.G, sixteen = a.D <= 128 ? 16 : 8;
+  if (all <= sixteen * a.B && a.max_pages * a.ps > 1024) {
+    AttentionArgs f{};
+    f.q = a.q; f.q_row_bytes = a.q_row_bytes;
+    f.kc = a.kc; f.vc = a.vc;
+    f.ps = a.ps; f.Hq = a.Hq; f.H = a.H; f.G = a.G; f.D = a.D; f.layout = a.layout; f.B = a.B;
+    f.bf16 = a.bf16; f.table64 = a.table64;
+    f.div_ps = a.div_ps;
+    f.block_tables = a.block_tables; f.max_pages = a.max_pages; f.seq_lens = a.seq_lens;
+    f.k_scale = a.k_scale; f.v_scale = a.v_scale;
+    f.sm_scale = a.sm_scale; f.soft_cap = a.soft_cap;
+    f.window_left = a.window_left; f.sink = a.sink;
+    f.out = a.out; f.lse = a.lse; f.status = a.status; f.workspace = a.workspace;
+    f.qo_indptr = a.qo_indptr; f.nnz = a.nnz; f.causal = a.causal;
+    f.most_rows = a.few_rows = sixteen == 16 && all > 8 * static_cast<int64_t>(a.B) ? 16 : 8;
+    if (nvfp4_status st = launch_attention(f, stream)) return st;
+  }
   // 256 rows of a segment share the decoded tiles; requests of fewer rows than 128 have no use for them
   const bool two = a.nnz * a.G > static_cast<int64_t>(a.B) * 128;
   if (a.D > 128) return launch_e<256, 1>(a, stream);

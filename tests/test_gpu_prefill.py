@@ -43,8 +43,8 @@ def _ref(c, q, indptr, sm=None, **kw):
     return PR.attention(PR.with_f32_scales(c), q.double().numpy(), indptr, q.shape[-1] ** -0.5 if sm is None else sm, **kw)
 
 
-def _both(nv, seed, new, lens, H, G, D, ps, layout, dtype, want_status=0, **kw):
-    c = R.make_paged(seed, lens, H, D, ps, layout)
+def _both(nv, seed, new, lens, H, G, D, ps, layout, dtype, want_status=0, width=None, **kw):
+    c = R.make_paged(seed, lens, H, D, ps, layout, width=width)
     q = _query(seed, sum(new), H * G, D, dtype)
     indptr = _indptr(new)
     out, lse, status = _run(nv, c, q, indptr, **kw)
@@ -313,7 +313,7 @@ def test_many_requests(gpu_lib):
 def test_a_wait_that_runs_out(gpu_lib):
     """The tiles are withheld: the call comes back, reports it, and the next call is right."""
     c = R.make_paged(15, [300, 700], 2, 128, 16, HND)
-    for new, D in (([300, 20], 128), ([2, 3], 128), ([50, 3], 256)):
+    for new, D in (([300, 20], 128), ([20, 30], 128), ([50, 3], 256)):
         c = R.make_paged(15, [300, 700], 2, D, 16, HND)
         q = _query(15, sum(new), 4, D, BF16)
         os.environ["NVFP4KV_TEST_STALL_PIPELINE"] = "1"
@@ -360,3 +360,65 @@ def test_many_segments_with_an_empty_half(gpu_lib, window):
     """288 rows a KV head: the second segment's second half has none; several segments to a CTA."""
     new, lens = [72] * 130, [72 + 3 * i for i in range(130)]
     _both(gpu_lib, 17, new, lens, 2, 4, 64, 16, HND, BF16, window_left=window, num_sink_tokens=2)
+
+
+FEW = [
+    # few rows a request (and tables of more than 1024 positions): new, lens, H, G, D, ps, layout, dtype
+    ([1, 1, 1], [40, 1, 333], 2, 8, 128, 16, HND, BF16),
+    ([4] * 6, [31, 32, 33, 4, 700, 129], 2, 4, 128, 16, HND, BF16),      # drafts: sixteen rows
+    ([2, 5, 1, 0, 3], [1, 64, 100, 7, 2], 1, 3, 64, 12, NHD, F16),       # more tokens than positions among them
+    ([1, 1, 1, 1, 1, 40], [100, 30, 0, 400, 64, 300], 2, 2, 64, 16, HND, F16),   # a chunk beside single tokens
+    ([2, 1, 3, 300], [1500, 40, 9, 640], 1, 1, 96, 16, NHD, BF16),       # and a prompt beside drafts
+    ([3, 1, 3, 2], [200, 77, 5, 450], 2, 5, 80, 7, HND, BF16),
+    ([8, 1, 4], [260, 31, 700], 2, 1, 256, 16, HND, F16),
+    ([2, 4], [150, 90], 3, 2, 192, 8, NHD, BF16),
+    ([16, 3], [3000, 18], 1, 1, 32, 16, HND, F16),
+    ([2] * 90, [500 + i for i in range(90)], 4, 3, 64, 16, HND, BF16),   # lists that are cut
+]
+
+
+@pytest.mark.parametrize("m", range(len(MASKS)))
+@pytest.mark.parametrize("i", range(len(FEW)))
+def test_few_rows(gpu_lib, i, m):
+    _both(gpu_lib, 200 + i, *FEW[i], width=4000 // FEW[i][5], **MASKS[m])
+
+
+@pytest.mark.parametrize("window,sink", [(30, 33), (31, 32), (64, 1), (2, 70), (1000, 5)])
+def test_few_rows_windows_about_units(gpu_lib, window, sink):
+    _both(gpu_lib, window, [5, 3, 1], [400, 97, 32], 1, 2, 64, 16, HND, F16, width=100, window_left=window, num_sink_tokens=sink)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_few_rows_nan_shows_where_the_formula_has_it(gpu_lib, D):
+    new, lens = [3, 1, 4], [350, 90, 1200]
+    c = R.make_paged(18, lens, 2, D, 16, HND)
+    at = lambda b, t: (c.tables[b, t // 16], t % 16)  # noqa: E731
+    for b, t, h, block in ((0, 348, 0, 1), (0, 349, 1, 0), (2, 700, 1, 2), (2, 1197, 0, 3), (2, 1150, 0, 0)):
+        p, s = at(b, t)
+        c.vs[p, h, s, block] = 0x7F
+    p, s = at(2, 1198)
+    c.ks[p, 1, s, 0] = 0xFF
+    q = _query(18, sum(new), 4 if D == 128 else 2, D, BF16)
+    for kw in (dict(), dict(window_left=48, num_sink_tokens=3), dict(causal=False, window_left=47)):
+        out, lse, status = _run(gpu_lib, c, q, _indptr(new), **kw)
+        ref = _ref(c, q, _indptr(new), **kw)
+        assert np.isnan(ref[0]).any() and not np.isnan(ref[0]).all(-1).all()
+        PR.check(out, lse, ref, BF16)
+        assert status == 0
+
+
+def test_few_rows_captured_and_replayed(gpu_lib):
+    """Under a graph a request grows from few rows to many and back."""
+    c = R.make_paged(19, [1500, 900, 40], 2, 128, 16, HND)
+    q = _query(19, 12, 8, 128, BF16)
+    args = list(_args(c, q, _indptr([4, 4, 4])))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = gpu_lib.nvfp4_paged_attention_prefill(*args)
+    for new, now in (([4, 4, 4], [1500, 900, 40]), ([1, 11, 0], [1400, 299, 0]), ([0, 4, 8], [3, 880, 17])):
+        args[3].copy_(torch.as_tensor(_indptr(new)))
+        args[5].copy_(torch.tensor(now))
+        graph.replay()
+        torch.cuda.synchronize()
+        short = R.Paged(**{**c.__dict__, "lens": np.array(now, np.int32)})
+        PR.check(out, lse, _ref(short, q, _indptr(new)), BF16)
