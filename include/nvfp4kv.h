@@ -666,9 +666,10 @@ nvfp4_status nvfp4_paged_attention_prefill_workspace_bytes(int32_t head_dim, int
  *   out           device, contiguous [nnz, num_qo_heads, head_dim] of dtype, 16-byte aligned.
  *   lse           device float [nnz, num_qo_heads], or NULL.
  *   dev_status    NVFP4_DEV_TIMEOUT besides the others, if a wait of the kernel's warps for one another ran out.
- *   workspace     device, workspace_bytes >= nvfp4_paged_attention_prefill_workspace_bytes, 16-byte aligned; holds
- *                 anything past its first NVFP4_COUNTER_BYTES bytes, which are not touched (so a workspace of the
- *                 decode calls that is large enough serves too). One call at a time.
+ *   workspace     device, workspace_bytes >= nvfp4_paged_attention_prefill_workspace_bytes, 16-byte aligned. Its
+ *                 first NVFP4_COUNTER_BYTES bytes are zero before its first use and left zero by every call,
+ *                 whatever its sizes; the rest holds anything (a workspace of the decode calls that is large enough
+ *                 serves too). One call at a time.
  *   The other arguments are those of nvfp4_paged_attention_decode.
  * Requirements: num_qo_heads a multiple of num_kv_heads, head_dim a multiple of 16 and at most 256, batch_size at
  * most 16384, at most 2^31 - 1 pages in the pool, at most 2^31 - 512 query rows of a KV head (nnz * num_qo_heads /

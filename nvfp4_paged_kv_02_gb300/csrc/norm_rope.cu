@@ -132,9 +132,11 @@ __device__ __forceinline__ void norm_rope(const NormRopeArgs& a, const Turn& tur
 // us against 74 with key and value rows in steps of their own (32,764 tokens, eight query heads and one KV head
 // of 128, fp16, 4over6), 142 against 155 (24 and six). Where steps are full, choosing by lane would cost: 184 against 162
 // (eight heads, bf16). Five CTAs to an SM serve the standard recipe's mixed steps (62 against 68 us);
-// the same cap costs the others (66 against 62).
+// the same cap costs the others (66 against 62). AXES: five CTAs too, 171 us against 181 (32,764 tokens, bf16, three
+// axes in sections of 16, 24 and 24 pairs) and 196 against 203 (fp16, 4over6, the axes of 32 pairs in turn, where a pair's
+// cosine and sine are loads of their own).
 template <bool BF16, int MODE, bool MIXED, bool AXES>
-__global__ void __launch_bounds__(kThreads, MIXED && MODE == 0 ? 5 : 0) norm_rope_append_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, AXES || (MIXED && MODE == 0) ? 5 : 0) norm_rope_append_kernel(const NormRopeArgs a) {
   __shared__ Tables tab;
   __shared__ __align__(16) uint4 s_rows[kThreads / 32][64];  // a warp's rows, as groups of eight
   float gs[2];
