@@ -396,19 +396,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
       if constexpr (kTwo) {
         // Steps: O of tile g in both halves, and S of the next tile, each behind the O whose P it overwrites. A
         // portion's first step has no O, its last one no S.
+        // (A stage of K that is full says that its tile is in the ring: only a portion's first tile, which may be the
+        // run's end instead, is waited for there.)
         uint32_t g = 0, now = 0;  // now: the flags of g, 0 in a first step
         int32_t rest = 0;
         for (bool ok = true; ok;) {
           const uint32_t ahead = now ? g + 1 : g;
+          const bool more_s = !now || rest > 0;
           uint32_t next = 0;
-          int32_t next_rest = 0;
-          if (!now || rest > 0) {
-            if (!tile_ready(ahead)) break;
-            next_rest = uniform(tile(ahead).rest);
+          auto look = [&] {  // the next tile's stage and flags
+            ok = k_ready(ahead);
+            if (!ok) return;
+            rest = uniform(tile(ahead).rest);
             next = uniform(tile(ahead).stream);
-            if (next_rest == kEnd) break;
+          };
+          if (!now) {
+            if (!tile_ready(ahead) || static_cast<int32_t>(uniform(tile(ahead).rest)) == kEnd) break;
+            look();
+          } else {
+            ok = v_ready(g);
           }
-          ok = now ? v_ready(g) : k_ready(ahead);
 #pragma unroll 1
           for (int i = 0; ok && i < 2; ++i) {
             if (now >> i & 1) {
@@ -417,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
               issue_o(i, i, g, !(now >> (2 + i) & 1));
               if (now >> (4 + i) & 1) mma_commit(leader, bar.o_full + i);
             }
-            if (next && now && i == 0) ok = k_ready(ahead);
+            if (now && more_s && i == 0) look();
             if (ok && !now && (next >> (6 + i) & 1)) ok = q_ready(i);
             if (ok && (next >> i & 1)) issue_s(i, i, ahead);
           }
@@ -428,7 +435,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
             ++g;
           }
           if (next) mma_commit(leader, bar.empty + (ahead & 1));
-          rest = next_rest;
           now = next;
         }
       } else {
