@@ -24,9 +24,10 @@ LIB_PATH = os.path.join(HERE, "libnvfp4kv.so")
 CALLS_PATH = os.path.join(HERE, "nvfp4kv_calls.so")
 CALLS_SOURCE = "calls.cpp"
 SOURCES = ["abi.cu", "append.cu", "dequant.cu", "materialize.cu", "global_scale.cu",
-           "norm_rope.cu", "attention.cu", "pages.cu", "prefill.cu"]
+           "norm_rope.cu", "attention.cu", "pages.cu", "prefill.cu",
+           "attention_sinks.cu", "attention_tokens.cu"]
 HEADERS = ["device.cuh", "internal.h", "scan.cuh", "pipeline.cuh", "quantize.cuh",
-           "attention.h", "softmax.cuh", "tcgen05.cuh"]
+           "attention.h", "attention.cuh", "softmax.cuh", "tcgen05.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-fmad=false", "--extended-lambda",
               "-Xcompiler", "-fPIC,-fvisibility=hidden,-O2", "-I", os.path.join(ROOT, "include")]

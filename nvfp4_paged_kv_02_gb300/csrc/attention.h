@@ -45,6 +45,9 @@ struct AttentionArgs {
 // Device memory that a launch needs, whatever the lengths.
 int64_t attention_workspace_bytes(int32_t Hq, int32_t H, int32_t D);
 nvfp4_status launch_attention(AttentionArgs a, cudaStream_t stream);
+// its kinds, in translation units of their own (nw: head_dim / 64, rounded up; nt: eights of rows)
+nvfp4_status launch_attention_sinks(const AttentionArgs& a, int nw, int nt, bool full, cudaStream_t stream);
+nvfp4_status launch_attention_tokens(const AttentionArgs& a, int nw, int nt, bool full, cudaStream_t stream);
 
 struct PrefillArgs {
   const uint8_t* q;

@@ -28,8 +28,23 @@
 // same tiles, or the same 128 rows over every second tile, joined at the end. head_dim above 128 leaves tensor
 // memory for one stream: there S of the next tile is computed meanwhile.
 //
+// What bounds it. 256 rows of 128 elements take the tensor cores 2048 cycles for a tile of 128 positions, and the CTA
+// some 4400: the chain of a stream (S from tensor memory, its maximum, 128 exponentials to a row, P back; O of it; the
+// next S: 2900 cycles of a softmax warp, 1000 of the tensor cores, the rest hand-overs), half of which the other
+// stream's products fill. One prompt of 12,345 tokens, 32 query heads and 8 KV heads of 128: 1158 us (1079 TFLOP/s; at
+// the measured 1947 it would be 641), the tensor pipe busy for 46 %, 57 % of the issue slots, 41 % of the ALU pipe. Eight
+// chunks of up to 2048 tokens over up to 10 K positions: 207 us (749 TFLOP/s); four prompts of up to 7879 tokens with
+// a window of 1023 and 64 first tokens, 32 query heads on 4: 720 (642); 16 requests of up to 1024 tokens of images with
+// heads of 256 and capped logits: 177 (345). A segment's beginning and end cost 15 to 20 K cycles, which the short ones
+// of a window feel. What mattered most was that the loops over tiles stay in the instruction cache (they were 3225 us
+// for the first prompt when unrolled wide: 28 % of the requests missed) and spill nothing: 227 KB of shared memory
+// leave the other cache too little to hold what is spilled.
+// Two warps for the products, one to a stream, are slower (1403 us against 1203 then: the streams fall into step, and
+// want the tensor cores and the exponentials at the same times); so are copies by the page warps (1870), rows of S
+// held whole in registers (2230, with spills), and decoding warps with K or V to themselves (images 203 against 184).
+//
 // Queries are scaled row by row by a power of two into binary16 (what is below 2^-38 of a row's largest element is
-// lost), weights are rounded to binary16 (2^-11 relative), as in attention.cu, and so are the running maximum and
+// lost), weights are rounded to binary16 (2^-11 relative), as in attention.cuh, and so are the running maximum and
 // sum kept. A NaN block scale of V is taken as 0 in the product and the outputs that see it are set to NaN: a weight
 // of 0 would not keep it from rows that do not.
 #include "attention.h"
@@ -51,8 +66,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kLaunchRegisters = 96, kSoftmaxRegisters = 136, kDecodeRegisters = 64, kOtherRegisters = 80;
 static_assert(2 * kSoftmaxRegisters + 2 * kDecodeRegisters + kOtherRegisters <= 5 * kLaunchRegisters, "more than the launch has");
 constexpr int kRing = 8;          // tiles whose places are kept
-constexpr int kSegmentCost = 5;   // what a segment's queries and outputs count for, in tiles
-constexpr int kWholeUnits = 8;    // a segment of so few tiles is not cut
+constexpr int kSegmentCost = 5;   // what a segment's queries and outputs count for, in tiles (2: 1543 us for the long prompt, 4: 1203)
+constexpr int kWholeUnits = 8;    // a segment of so few tiles is not cut (12: drafts 127 us against 116, a window 694 against 723)
 
 // DP: head_dim rounded up to 64, 128 or 256. MT: 128 rows of a segment, or twice as many.
 template <int DP, int MT>
@@ -166,7 +181,6 @@ struct __align__(16) Tile {
   int32_t rest;
   uint16_t nan_blocks[128];      // which blocks of a position (where its warp's nan is set)
   int32_t first;                 // of its portion
-  int32_t unused[3];             // (a multiple of 16 bytes)
 };
 constexpr uint32_t kNoPage = 0xFFFFFFFFu;
 constexpr int32_t kEnd = -1;          // `rest` after the last tile
@@ -746,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
     const int stream = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;  // this warp's lanes of tensor memory
     const float gk = __ldg(a.k_scale), gv = __ldg(a.v_scale);
-    const float cap = a.soft_cap, unit = a.sm_scale * gk;
+    const float cap = a.soft_cap;
     uint32_t tiles = 0, q_count = 0, o_count = 0, merges = 0, steps = 0;
     uint32_t s_count[2] = {0, 0};
     // -- the queries --
@@ -841,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           const int e2 = top > 0.0f && top <= FLT_MAX ? exponent - 14 : 0;
           // 2^e2 and 2^-e2 as two factors (they may be out of range by themselves), with f's sign: f is not
           // negative from here on, and a maximum of scores is one of logits; f = 0 is a query of zeros
-          float f = unit * __int_as_float((127 + e2 / 2) << 23) * __int_as_float((127 + (e2 - e2 / 2)) << 23);
+          float f = (a.sm_scale * __int_as_float((127 + e2 / 2) << 23)) * (gk * __int_as_float((127 + (e2 - e2 / 2)) << 23));
           float f1 = __int_as_float((127 - e2 / 2) << 23);
           const float f2 = __int_as_float((127 - (e2 - e2 / 2)) << 23);
           if (f < 0.0f) f1 = -f1;
@@ -1113,9 +1127,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
   }
 }
 
-// The parts of the segment that run blockIdx.x begins and others continue, added in the runs' order; a warp takes
-// four of its rows, 32 rows to a CTA.
-constexpr int kJoinRows = 32;
+// The parts of the segment that run blockIdx.x begins and others continue, added in the runs' order, a row to a warp.
+constexpr int kJoinRows = 8;
 template <int DP, int MT>
 __global__ void __launch_bounds__(256) join_kernel(const PrefillArgs a) {
   using S = Shape<DP, MT>;
@@ -1126,14 +1139,15 @@ __global__ void __launch_bounds__(256) join_kernel(const PrefillArgs a) {
   const int32_t r0 = c.t * S::kRows, rows = q.n * a.G - r0;
   const int64_t first = blockIdx.x;
   const float gv = __ldg(a.v_scale);
-  for (int k = 0; k < 4; ++k) {
-    const int local = blockIdx.y * kJoinRows + warp * 4 + k;
+  for (int k = 0; k < kJoinRows / 8; ++k) {
+    const int local = blockIdx.y * kJoinRows + warp * (kJoinRows / 8) + k;
     if (local >= rows) return;
     auto part = [&](int64_t i) { return part_of(a, i, i == first ? 1 : 0, S::kRows, DP); };
     float top = -INFINITY;
     for (int64_t i = first + lane; i <= c.last; i += 32) top = fmaxf(top, part(i)[S::kRows * DP + local]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    // nothing above -inf: the sums are zeros, or NaN where every score was NaN, which has to stay
     const bool none = top == -INFINITY;
     float sum = 0.0f;
     float4 v[DP / 128 + 1] = {};

@@ -239,6 +239,15 @@ def test_scales_and_magnitudes(gpu_lib, sm, scale):
     PR.check(out, lse, _ref(c, q, _indptr([50, 10]), sm), BF16)
 
 
+@pytest.mark.parametrize("gk,sm,scale", [(1e-22, 1e-20, 1e37), (1e20, 1e15, 1e-36), (-0.002, 0.1, 1.0), (0.0, 0.1, 1.0)])
+def test_factors_whose_product_is_out_of_range(gpu_lib, gk, sm, scale):
+    c = R.make_paged(9, [280, 40], 2, 64, 16, HND)
+    c.gk = gk
+    q = _query(9, 60, 4, 64, BF16, scale)
+    out, lse, _ = _run(gpu_lib, c, q, _indptr([50, 10]), sm_scale=sm)
+    PR.check(out, lse, _ref(c, q, _indptr([50, 10]), float(np.float32(sm))), BF16)
+
+
 def test_growing_scores(gpu_lib):
     """The maximum rises all along a row, by more than the slack that it is given."""
     for D, G in ((64, 4), (128, 1), (256, 1)):
