@@ -431,3 +431,60 @@ def test_few_rows_captured_and_replayed(gpu_lib):
         torch.cuda.synchronize()
         short = R.Paged(**{**c.__dict__, "lens": np.array(now, np.int32)})
         PR.check(out, lse, _ref(short, q, _indptr(new)), BF16)
+
+
+@pytest.mark.parametrize("new,width", [([300, 40], None), ([3, 2], 100)])
+def test_caches_of_more_than_4_gib(gpu_lib, new, width):
+    """Pages 300 MB apart: offsets need 64 bits, for rows of 128 and for few."""
+    c = R.make_paged(20, [400, 90], 2, 64, 16, HND, width=width)
+    q = _query(20, sum(new), 4, 64, BF16)
+    dev = _dev(c, pad_data=300_000_000)
+    assert c.k.shape[0] * 300_000_000 > 1 << 32
+    out, lse, status = _run(gpu_lib, c, q, _indptr(new), dev)
+    PR.check(out, lse, _ref(c, q, _indptr(new)), BF16)
+    assert status == 0
+
+
+@pytest.mark.parametrize("width", [2, 70])
+def test_largest_batch(gpu_lib, width):
+    """16,384 requests, most of them without tokens, for rows of 128 and (tables of 1120 positions) for few."""
+    B = 16384
+    new = [1 + i % 4 if i % 911 == 0 else 0 for i in range(B)]
+    lens = [1 + i % 30 if i % 3 == 0 else 0 for i in range(B)]
+    _both(gpu_lib, 21, new, lens, 1, 2, 32, 16, HND, F16, width=width)
+    with pytest.raises(gpu_lib.NVFP4KVError, match="16384"):
+        c = R.make_paged(21, [1] * (B + 1), 1, 32, 16, HND)
+        gpu_lib.nvfp4_paged_attention_prefill(*_args(c, _query(21, B + 1, 2, 32, F16), np.arange(B + 2, dtype=np.int32)))
+
+
+def test_requests_that_share_pages(gpu_lib):
+    """A common prompt: two requests' tables name the same pages."""
+    c = R.make_paged(22, [160, 160, 200], 2, 64, 16, HND)
+    c.tables[1] = c.tables[0]
+    c.tables[2, :10] = c.tables[0, :10]
+    q = _query(22, 90, 4, 64, F16)
+    for new in ([30, 20, 40], [1, 2, 3]):
+        out, lse, status = _run(gpu_lib, c, q[:sum(new)], _indptr(new))
+        PR.check(out, lse, _ref(c, q[:sum(new)], _indptr(new)), F16)
+        assert status == 0
+
+
+def test_two_streams_at_once(gpu_lib):
+    """Calls that run beside each other have workspaces of their own."""
+    c = R.make_paged(23, [3000, 1700], 2, 128, 16, HND)
+    dev = _dev(c)
+    calls = []
+    for i, new in enumerate(([200, 64], [130, 1000], [4, 4], [900, 30])):
+        q = _query(30 + i, sum(new), 8, 128, BF16)
+        calls.append((q, _indptr(new), _args(c, q, _indptr(new), dev)))
+    alone = [gpu_lib.nvfp4_paged_attention_prefill(*a) for _, _, a in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        got = []
+        for s, (_, _, a) in zip(streams, calls):
+            with torch.cuda.stream(s):
+                got.append(gpu_lib.nvfp4_paged_attention_prefill(*a))
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(got, alone):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
