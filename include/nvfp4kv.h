@@ -656,7 +656,7 @@ nvfp4_status nvfp4_paged_attention_prefill_workspace_bytes(int32_t head_dim, int
  * query row or in a live block scale shows in the outputs that the formula has it in, and in no others. What the
  * slots past a request's end hold is of no consequence. Rows of no request are left as they were. An entry of
  * qo_indptr outside [0, nnz] or below the one before it is reported (NVFP4_DEV_BAD_BATCH) and taken as the nearest
- * that is not.
+ * that is not; the rows of requests after one that is below are left as they were or hold those of any of them.
  * K and V are exact; query rows, weights and sums are rounded and accumulated as by nvfp4_paged_attention_decode.
  * The result does not depend on scheduling, nor a row's on the other rows' values.
  *   query         device [nnz, num_qo_heads, head_dim] of dtype, tokens query_row_stride elements apart;

@@ -191,6 +191,7 @@ struct Shared {
   Segment next[kSoftmaxWarps];        // a softmax warp's
   uint32_t tmem;
   int32_t dead;                       // a wait has run out
+  int32_t last;                       // request that counts
   float factor[256];                  // of the query rows
   float m[128], l[128];               // of the second stream
   uint32_t poison[128];
@@ -251,9 +252,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
     int32_t* cum = reinterpret_cast<int32_t*>(smem);
     const int per = (a.B + kThreads - 1) / kThreads;
     const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
-    int32_t local = 0;
+    // Requests after an entry of qo_indptr that is below the one before it may share rows with others: they get
+    // none, and the tiles stay within 2^24 and one more for each request.
+    if (tid == 0) sh.last = a.B - 1;
+    int32_t local = 0, last = a.B - 1;
     for (int b = lo; b < hi; ++b) {
       const Request q = request_of(a, b);
+      if (__ldg(a.qo_indptr + b + 1) < __ldg(a.qo_indptr + b)) last = min(last, b);
       local += tiles_of<S>(a, q);
       cum[b] = local;
       if (blockIdx.x == 0) {
@@ -264,8 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
     }
     const int32_t before = static_cast<int32_t>(scan_cta(local, sh.scan)) - local;
     for (int b = lo; b < hi; ++b) cum[b] += before;
+    if (last < a.B - 1) atomicMin(&sh.last, last);
     __syncthreads();
-    const int32_t tiles = cum[a.B - 1];
+    const int32_t tiles = cum[sh.last];
     const int32_t per2 = (tiles + kThreads - 1) / kThreads;
     const int32_t f0 = static_cast<int32_t>(min(static_cast<int64_t>(tiles), static_cast<int64_t>(tid) * per2));
     const int32_t f1 = static_cast<int32_t>(min(static_cast<int64_t>(tiles), static_cast<int64_t>(f0) + per2));
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
     s.h = 0;
     // every tile of this thread's slice, until `stop` says so
     auto walk = [&](auto stop) {
-      int32_t x = 0, y = a.B - 1;
+      int32_t x = 0, y = sh.last;
       while (x < y) {
         const int32_t mid = (x + y) >> 1;
         if (cum[mid] > f0) y = mid;

@@ -488,3 +488,16 @@ def test_two_streams_at_once(gpu_lib):
         torch.cuda.synchronize()
         for (o, l), (wo, wl) in zip(got, alone):
             assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+def test_row_ranges_that_overlap(gpu_lib):
+    """After an entry below the one before it, requests may not take rows again: those before it keep theirs."""
+    B, n = 4001, 300
+    c = R.make_paged(24, [900] + [20] * (B - 1), 1, 64, 16, HND)
+    q = _query(24, n, 2, 64, F16)
+    indptr = np.array([0] + [n, 0] * (B // 2) + [n], np.int32)
+    assert indptr.size == B + 1
+    out, lse, status = _run(gpu_lib, c, q, indptr)
+    first = R.Paged(**{**c.__dict__, "B": 1, "tables": np.ascontiguousarray(c.tables[:1]), "lens": c.lens[:1]})
+    PR.check(out, lse, _ref(first, q, _indptr([n])), F16)
+    assert status == gpu_lib.DEV_BAD_BATCH
