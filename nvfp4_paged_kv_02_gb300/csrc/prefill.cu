@@ -48,6 +48,7 @@
 // sum kept. A NaN block scale of V is taken as 0 in the product and the outputs that see it are set to NaN: a weight
 // of 0 would not keep it from rows that do not.
 #include "attention.h"
+#include "prefill_tiles.h"
 #include "softmax.cuh"
 #include "tcgen05.cuh"
 
@@ -98,21 +99,10 @@ __device__ __forceinline__ Request request_of(const PrefillArgs& a, int32_t b) {
   return {p0, tokens, n > reach ? static_cast<int32_t>(reach) : n};
 }
 
-// Positions that rows [r0, r1) of a request see: t < hi and (t >= lo or t < sink).
-struct Sight {
-  int32_t hi, lo, sink;
-};
+// What rows [r0, r1) of a request see.
 __device__ __forceinline__ Sight sight_of(const PrefillArgs& a, const Request& q, int32_t r0, int32_t r1) {
   const int32_t first = q.L - q.n + div_q32(r0, a.div_g), last = q.L - q.n + div_q32(r1 - 1, a.div_g);
-  Sight s;
-  s.hi = a.causal ? max(last + 1, 0) : q.L;
-  s.lo = a.window_left >= 0 && first > a.window_left ? min(first - a.window_left, s.hi) : 0;
-  s.sink = min(a.sink, s.lo);
-  return s;
-}
-template <int BN>
-__device__ __forceinline__ bool sees(const Sight& s, int32_t t0) {  // some position of the tile at t0
-  return t0 < s.hi && (t0 + BN > s.lo || t0 < s.sink);
+  return sight_of_tokens(first, last, q.L, a.causal, a.window_left, a.sink);
 }
 
 // A segment, and the place of its first tile relative to the run's first.
@@ -124,13 +114,27 @@ struct Segment {
   int32_t first_units, gap;
 };
 
+// The units [u, end) of a segment that are this run's of `run` places; `mine`: it is, wholly, if it is not cut.
+struct Portion {
+  int32_t u, end;
+  bool mine;
+};
+
 template <class S>
 __device__ __forceinline__ void fill(const PrefillArgs& a, Segment& s) {
   const int32_t rows = s.q.n * a.G, r0 = s.t * S::kRows;
   s.see = sight_of(a, s.q, r0, min(rows - r0, S::kRows) + r0);
-  s.first_units = (s.see.sink + S::BN - 1) / S::BN;
-  s.gap = max(s.see.lo / S::BN - s.first_units, 0);
-  s.units = s.see.hi > 0 ? (s.see.hi - 1) / S::BN + 1 - s.gap : 0;
+  const Units u = units_of_sight<S::BN>(s.see);
+  s.first_units = u.first_units;
+  s.gap = u.gap;
+  s.units = u.units;
+}
+// The units of a portion that the 128 rows of half i of a segment see.
+template <class S>
+__device__ __forceinline__ Reach reach_of_half(const PrefillArgs& a, const Segment& s, const Portion& part, int i) {
+  const int32_t r0 = s.t * S::kRows, rows = min(s.q.n * a.G - r0, S::kRows);
+  const Sight see = 128 * i < rows ? sight_of(a, s.q, r0 + 128 * i, r0 + min(rows, 128 * i + 128)) : Sight{0, 0, 0};
+  return reach_of<S::BN>(see, s.first_units, s.gap, part.u, part.end - part.u);
 }
 template <class S>
 __device__ __forceinline__ int32_t tiles_of(const PrefillArgs& a, const Request& q) {
@@ -150,11 +154,6 @@ __device__ __forceinline__ void next_segment(const PrefillArgs& a, Segment& s) {
   }
   fill<S>(a, s);
 }
-// The units [u, end) of a segment that are this run's of `run` places; `mine`: it is, wholly, if it is not cut.
-struct Portion {
-  int32_t u, end;
-  bool mine;
-};
 __device__ __forceinline__ Portion portion_of(const Segment& s, int64_t run) {
   if (s.units <= kWholeUnits) {
     const bool mine = s.start >= 0 && s.start < run;
@@ -509,24 +508,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
     Portion part{0, 0, false};
     int32_t k = turn, n = 0;       // this warp's tile of the portion's n
     uint32_t g = turn;
-    Sight see[2];
-    int32_t last[2];
-    auto position = [&](int32_t i) {  // of the portion's tile i
-      const int32_t u = part.u + i;
-      return (u < s.first_units ? u : u + s.gap) * BN;
-    };
+    Reach reach[2];
     auto enter = [&] {
       part = portion_of(s, run);
       n = part.end - part.u;
       if (!kTwo || n <= 0) return;
-      const int32_t r0 = s.t * S::kRows, rows = min(s.q.n * a.G - r0, S::kRows);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        see[i] = {0, 0, 0};
-        if (128 * i < rows) see[i] = sight_of(a, s.q, r0 + 128 * i, r0 + min(rows, 128 * i + 128));
-        last[i] = n - 1;
-        while (last[i] >= 0 && !sees<BN>(see[i], position(last[i]))) --last[i];
-      }
+      for (int i = 0; i < 2; ++i) reach[i] = reach_of_half<S>(a, s, part, i);
     };
     enter();
     for (;; g += kPageWarps) {
@@ -543,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
       Tile& out = sh.ring[g % kRing];
       if (!wait_warp(bar.ring_empty + g % kRing, (g / kRing & 1) ^ 1)) break;
       if (any) {
-        const int32_t t0 = position(k);
+        const int32_t t0 = tile_of_unit<BN>(part.u + k, s.first_units, s.gap);
         bool whole = true;
 #pragma unroll 1
         for (int j = 0; j < BN / 32; ++j) {
@@ -568,11 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
           if constexpr (kTwo) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              if (last[i] >= 0) stream |= 64u << i;
-              if (!sees<BN>(see[i], t0)) continue;
-              bool before = false;  // an earlier tile of the portion
-              for (int32_t e = 0; e < k && !before; ++e) before = sees<BN>(see[i], position(e));
-              stream |= 1u << i | (before ? 0u : 4u << i) | (k == last[i] ? 16u << i : 0u);
+              if (reach[i].any()) stream |= 64u << i;
+              if (reach[i].has(k)) stream |= 1u << i | (k == reach[i].first() ? 4u << i : 0u) | (k == reach[i].last() ? 16u << i : 0u);
             }
           } else if constexpr (kTurns) {
             stream |= 1u << (k & 1) | (k < 2 ? 4u << (k & 1) : 0u) | (k + 2 >= n ? 16u << (k & 1) : 0u);
@@ -811,21 +796,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
         for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(out)[i] = uint4{};
         if (lse) *lse = -INFINITY;
       }
-      // this stream's tiles of the portion: the first `sinks`, and [k0, k1)
-      int32_t sinks = 0, k0 = 0, k1 = n;
-      if constexpr (kTwo) {
-        Sight see{0, 0, 0};
-        if (128 * stream < rows) see = sight_of(a, s.q, r0 + 128 * stream, r0 + min(rows, 128 * stream + 128));
-        const int32_t to = max(s.first_units - part.u, 0);  // the portion's first tile past the segment's first units
-        auto tile_at = [&](int32_t t) {  // of the portion, that holds position t or comes after it
-          const int32_t u = t / BN;
-          return (u < s.first_units ? u : max(u - s.gap, s.first_units)) - part.u;
-        };
-        k1 = see.hi > 0 ? min(max(tile_at(see.hi - 1) + 1, 0), n) : 0;
-        k0 = see.hi > 0 ? min(max(tile_at(see.lo), 0), n) : 0;
-        sinks = min(min(max((see.sink + BN - 1) / BN - part.u, 0), to), min(k0, n));
-      }
-      const bool mine = sinks > 0 || k0 < k1;   // it has tiles in the portion
+      Reach reach{0, 0, n};  // this stream's tiles of the portion
+      if constexpr (kTwo) reach = reach_of_half<S>(a, s, part, stream);
+      const bool mine = reach.any();
       if (final) {
         // the run's last segment, if others continue it
         if (tid == 0 && s.units > kWholeUnits && s.start >= 0 && s.start < run && s.start + s.units > run) {
@@ -904,9 +877,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
         uint32_t poison = 0;
         bool started = false, ok = true;
         for (int32_t k = kTurns ? stream : 0; k < n; k += kTurns ? 2 : 1) {
-          const int32_t u = part.u + k;
-          const int32_t t0 = (u < s.first_units ? u : u + s.gap) * BN;
-          if (kTwo && !(k < sinks || (k >= k0 && k < k1))) continue;
+          const int32_t t0 = tile_of_unit<BN>(part.u + k, s.first_units, s.gap);
+          if (kTwo && !reach.has(k)) continue;
           const int buf = kTwo ? stream : k & 1;
           ok = wait_warp(bar.s_full + buf, s_count[buf]++ & 1);
           if (!ok) break;
