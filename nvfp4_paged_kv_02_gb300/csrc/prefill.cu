@@ -52,6 +52,7 @@
 #include "softmax.cuh"
 #include "tcgen05.cuh"
 
+#include <algorithm>
 #include <cfloat>
 
 namespace nvfp4 {
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
   __shared__ Shared sh;
   uint8_t* const smem = smem_raw + (1024 - smem_addr(smem_raw) % 1024) % 1024;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t limit = a.pipe.wait_limit;
+  const uint32_t limit = a.pipe.wait_limit;  // (of naps)
 
   // -- the run: tiles of all requests, then places of all tiles --
   int64_t c0, run, ncta;
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillArgs 
       }
       // nothing of this CTA is under way any more when it ends
       mma_commit(leader, &bar.done);
-      for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(&bar.done, 0); ++i) {}
+      for (uint32_t i = 0; i < kNapLimit && !mbar_wait_nap(&bar.done, 0); ++i) {}
     }
     __syncwarp();
   } else if (warp > kProductWarp) {
@@ -1201,6 +1202,7 @@ nvfp4_status launch_prefill(PrefillArgs a, cudaStream_t stream) {
   a.k_sf_stride = static_cast<uint32_t>(strides[2]);
   a.v_sf_stride = static_cast<uint32_t>(strides[3]);
   a.pipe = pipe_test_from_env();
+  a.pipe.wait_limit = std::min(a.pipe.wait_limit, kNapLimit);
   // Where requests have few rows on average (drafts, or single tokens among them), those that have go to the kernel
   // of single tokens, which reads a cache faster than rows of 128 can be made of it: 64 requests of four tokens, four
   // query heads to a KV head, 105 K positions: 117 us here, 83 with both launches. Tables of up to 1024 positions stay
