@@ -135,6 +135,11 @@ __device__ __forceinline__ void norm_rope(const NormRopeArgs& a, const Turn& tur
 // the same cap costs the others (66 against 62). AXES: five CTAs too, 171 us against 181 (32,764 tokens, bf16, three
 // axes in sections of 16, 24 and 24 pairs) and 196 against 203 (fp16, 4over6, the axes of 32 pairs in turn, where a pair's
 // cosine and sine are loads of their own).
+// Where a lane's pairs begin is the same for all tokens, and is found before the loop over them; for bf16 and the recipes
+// with binary16 errors inside it, where ptxas gives these instances 96 registers (five CTAs) in place of 111 (four): 173
+// us against 193 (32,764 tokens, 32 query heads and eight KV heads of 128), with heads of 64 96 against 107, of 256 176
+// against 198. The other recipes are faster the other way (bf16, binary32 errors: 178 against 198). A launch bound of five
+// CTAs for all of them costs those that need none (169 against 162, standard recipe).
 template <bool BF16, int MODE, bool MIXED, bool AXES>
 __global__ void __launch_bounds__(kThreads, AXES || (MIXED && MODE == 0) ? 5 : 0) norm_rope_append_kernel(const NormRopeArgs a) {
   __shared__ Tables tab;
@@ -152,7 +157,13 @@ __global__ void __launch_bounds__(kThreads, AXES || (MIXED && MODE == 0) ? 5 : 0
   turn.turns = j < nr;
   turn.ga = j < nt ? (j < nr ? j : 2 * j) : 0;
   turn.gb = j < nt ? (j < nr ? j + nr : 2 * j + 1) : 0;
-  const int ca = a.interleaved ? 4 * turn.ga : 8 * j, cb = a.interleaved ? 4 * turn.gb : 8 * j + 4;  // its pairs: four from each
+  constexpr bool kInLoop = !AXES && BF16 && MODE >= 3;
+  int ca = 0, cb = 0;  // its pairs: four from each
+  auto find_pairs = [&] {
+    ca = a.interleaved ? 4 * turn.ga : 8 * j;
+    cb = a.interleaved ? 4 * turn.gb : 8 * j + 4;
+  };
+  if (!kInLoop) find_pairs();
   uint32_t axes_a = 0, axes_b = 0;
   bool bad_axes = false;
   if (AXES && turn.turns) {
@@ -215,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, AXES || (MIXED && MODE == 0) ? 5 : 0
       if (turn.turns && from < k_end) {
         const float* cs = a.cos_sin + static_cast<int64_t>(pos) * a.rotary_dim;
         const float* sn = cs + a.rotary_dim / 2;
+        if (kInLoop) find_pairs();
         load4(cs + ca, turn.c);
         load4(cs + cb, turn.c + 4);
         load4(sn + ca, turn.s);
