@@ -27,7 +27,8 @@ SOURCES = ["abi.cu", "append.cu", "dequant.cu", "materialize.cu", "global_scale.
            "norm_rope.cu", "attention.cu", "pages.cu", "prefill.cu",
            "attention_sinks.cu", "attention_tokens.cu"]
 HEADERS = ["device.cuh", "internal.h", "scan.cuh", "pipeline.cuh", "quantize.cuh",
-           "attention.h", "attention.cuh", "softmax.cuh", "tcgen05.cuh", "prefill_tiles.h"]
+           "attention.h", "attention.cuh", "softmax.cuh", "tcgen05.cuh", "prefill_tiles.h",
+           "attention_sizes.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-fmad=false", "--extended-lambda",
               "-Xcompiler", "-fPIC,-fvisibility=hidden,-O2", "-I", os.path.join(ROOT, "include")]

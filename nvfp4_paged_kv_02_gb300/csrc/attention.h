@@ -2,6 +2,7 @@
 // page bounds, page selection, attention of one new token per request and of several.
 #pragma once
 
+#include "attention_sizes.h"
 #include "internal.h"
 
 namespace nvfp4 {

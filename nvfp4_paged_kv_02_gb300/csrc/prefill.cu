@@ -1203,13 +1203,8 @@ nvfp4_status launch_prefill(PrefillArgs a, cudaStream_t stream) {
   a.v_sf_stride = static_cast<uint32_t>(strides[3]);
   a.pipe = pipe_test_from_env();
   a.pipe.wait_limit = std::min(a.pipe.wait_limit, kNapLimit);
-  // Where requests have few rows on average (drafts, or single tokens among them), those that have go to the kernel
-  // of single tokens, which reads a cache faster than rows of 128 can be made of it: 64 requests of four tokens, four
-  // query heads to a KV head, 105 K positions: 117 us here, 83 with both launches. Tables of up to 1024 positions stay
-  // here: the second launch costs more (five requests of 1 to 9 tokens over up to 86 positions: 14 us, with both 27).
-  a.few_rows = 0;
-  const int64_t all = a.nnz * a.G, sixteen = a.D <= 128 ? 16 : 8;
-  if (all <= sixteen * a.B && a.max_pages * a.ps > 1024) {
+  a.few_rows = few_rows_of(a.nnz * a.G, a.D, a.B, a.H, a.max_pages * a.ps);
+  if (a.few_rows > 0) {
     AttentionArgs f{};
     f.q = a.q; f.q_row_bytes = a.q_row_bytes;
     f.kc = a.kc; f.vc = a.vc;
@@ -1222,7 +1217,7 @@ nvfp4_status launch_prefill(PrefillArgs a, cudaStream_t stream) {
     f.window_left = a.window_left; f.sink = a.sink;
     f.out = a.out; f.lse = a.lse; f.status = a.status; f.workspace = a.workspace;
     f.qo_indptr = a.qo_indptr; f.nnz = a.nnz; f.causal = a.causal;
-    f.most_rows = a.few_rows = sixteen == 16 && all > 8 * static_cast<int64_t>(a.B) ? 16 : 8;
+    f.most_rows = a.few_rows;
     if (nvfp4_status st = launch_attention(f, stream)) return st;
   }
   // 256 rows of a segment share the decoded tiles; requests of fewer rows than 128 have no use for them
