@@ -154,11 +154,13 @@ float* device_scale(const Args& a, int i, const at::Device& device) {
 // The attention's workspaces (its counters have to stay as the last call left them), one per (device, stream):
 // calls on one stream run one at a time, so they can share one; a larger one takes its place when a call needs
 // it. A stream goes by its id, which is never given again, not by its handle; cudaStreamPerThread is another
-// stream in each thread. At most kMostKept are kept: the one that was not used for longest goes back to torch's
-// allocator, which hands its memory to the same stream only, and so after the calls that use it. A call that is
+// stream in each thread. At most kMostKept and kMostKeptBytes are kept (64 of the decode calls', which take up to 10 MB, or
+// 16 of the prompts', which take up to 41): those that were not used for longest go back to torch's
+// allocator, which hands their memory to the same stream only, and so after the calls that use it. A call that is
 // being captured gets its own from the graph's memory, so that a graph never depends on what later calls do with
 // these. The GIL guards the list, which is never destroyed (the process's end is no time to free device memory).
 constexpr size_t kMostKept = 64;
+constexpr int64_t kMostKeptBytes = int64_t(656) << 20;
 struct Kept {
   int device;
   unsigned long long stream;
@@ -199,7 +201,10 @@ at::Tensor attention_workspace(const at::Device& device, cudaStream_t stream, in
     const auto at = find();
     if (at != kept().end()) kept().erase(at);
     kept().insert(kept().begin(), k);
-    if (kept().size() > kMostKept) kept().pop_back();
+    int64_t held = 0;
+    for (const Kept& x : kept()) held += x.memory.numel();
+    for (; kept().size() > 1 && (kept().size() > kMostKept || held > kMostKeptBytes); kept().pop_back())
+      held -= kept().back().memory.numel();
   }
   return k.memory;
 }
