@@ -665,7 +665,8 @@ nvfp4_status nvfp4_paged_attention_prefill_workspace_bytes(int32_t head_dim, int
  *   causal        0 or 1.
  *   out           device, contiguous [nnz, num_qo_heads, head_dim] of dtype, 16-byte aligned.
  *   lse           device float [nnz, num_qo_heads], or NULL.
- *   dev_status    NVFP4_DEV_TIMEOUT besides the others, if a wait of the kernel's warps for one another ran out.
+ *   dev_status    NVFP4_DEV_TIMEOUT besides the others, if a wait of the kernel's warps for one another ran out (after
+ *                 half a second or so; out and lse are then not to be used).
  *   workspace     device, workspace_bytes >= nvfp4_paged_attention_prefill_workspace_bytes, 16-byte aligned. Its
  *                 first NVFP4_COUNTER_BYTES bytes are zero before its first use and left zero by every call,
  *                 whatever its sizes; the rest holds anything (a workspace of the decode calls that is large enough

@@ -14,7 +14,7 @@
 // are, and its 1024 multiply-adds a clock and SM (measured) are three times what G <= 8 needs.
 // It takes some 690 instructions of a warp for 32 tokens of 128 elements, 2.7 a lane and element, of
 // which decoding, scaling and multiplying are 1.7. On large calls nothing is full: 59 % of the issue
-// slots, 51 % of the ALU pipe, 22 % of the tensor pipe, 4.4 of 6.8 TB/s; 162 registers admit twelve
+// slots, 51 % of the ALU pipe, 22 % of the tensor pipe, 4.4 of 6.8 TB/s; 165 registers admit twelve
 // warps to an SM, and each of them looks up pages, copies and computes in turn. On small calls it is
 // the start (lengths, their scan, the first pages: 4 us), one unit's latency and the joins. At 8 KV heads
 // of 128, in calls back to back: 430 K tokens of 128 requests, G = 4: 111 us (4.4 TB/s); 110 K tokens of

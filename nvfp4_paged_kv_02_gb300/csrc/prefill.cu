@@ -31,22 +31,25 @@
 // What bounds it. 256 rows of 128 elements take the tensor cores 2048 cycles for a tile of 128 positions, and the CTA
 // some 4400: the chain of a stream (S from tensor memory, its maximum, 128 exponentials to a row, P back; O of it; the
 // next S: 2900 cycles of a softmax warp, 1000 of the tensor cores, the rest hand-overs), half of which the other
-// stream's products fill. One prompt of 12,345 tokens, 32 query heads and 8 KV heads of 128: 1158 us (1079 TFLOP/s; at
-// the measured 1947 it would be 641), the tensor pipe busy for 46 %, 57 % of the issue slots, 41 % of the ALU pipe. Eight
-// chunks of up to 2048 tokens over up to 10 K positions: 207 us (749 TFLOP/s); four prompts of up to 7879 tokens with
-// a window of 1023 and 64 first tokens, 32 query heads on 4: 720 (642); 16 requests of up to 1024 tokens of images with
-// heads of 256 and capped logits: 177 (345). A segment's beginning and end cost 15 to 20 K cycles, which the short ones
+// stream's products fill. One prompt of 12,345 tokens, 32 query heads and 8 KV heads of 128: 1158 us (1078 TFLOP/s; at
+// the measured 1947 it would be 641), the tensor pipe busy for 46 %, 57 % of the issue slots, 40 % of the ALU pipe. Eight
+// chunks of up to 2048 tokens over up to 10 K positions: 207 us (750 TFLOP/s); four prompts of up to 7879 tokens with
+// a window of 1023 and 64 first tokens, 32 query heads on 4: 714 (648); 16 requests of up to 1024 tokens of images with
+// heads of 256 and capped logits: 178 (343). A segment's beginning and end cost 15 to 20 K cycles, which the short ones
 // of a window feel. What mattered most was that the loops over tiles stay in the instruction cache (they were 3225 us
-// for the first prompt when unrolled wide: 28 % of the requests missed) and spill nothing: 227 KB of shared memory
-// leave the other cache too little to hold what is spilled.
+// for the first prompt when unrolled wide: 28 % of the requests missed) and that little is spilled (36 to 48 bytes a
+// thread, reloaded at 84 to 152): 227 KB of shared memory leave the other cache too little to hold more.
 // Two warps for the products, one to a stream, are slower (1403 us against 1203 then: the streams fall into step, and
 // want the tensor cores and the exponentials at the same times); so are copies by the page warps (1870), rows of S
 // held whole in registers (2230, with spills), and decoding warps with K or V to themselves (images 203 against 184).
 //
 // Queries are scaled row by row by a power of two into binary16 (what is below 2^-38 of a row's largest element is
-// lost), weights are rounded to binary16 (2^-11 relative), as in attention.cuh, and so are the running maximum and
-// sum kept. A NaN block scale of V is taken as 0 in the product and the outputs that see it are set to NaN: a weight
-// of 0 would not keep it from rows that do not.
+// lost). Weights are rounded to binary16 for the second product, as in attention.cuh: 2^-11 relative, and below 2^-22 of
+// the weight at the running maximum an absolute 2^-33 of that one. The maximum and the sum, of the weights before that
+// rounding, stay in binary32. What it costs: outputs in binary16 are 2.7e-4 (root of the mean square, relative) from 64
+// bits on the first prompt, where weights in binary32 leave 2.1e-4; in bf16 it does not show. A NaN block scale of V is
+// taken as 0 in the product and the outputs that see it are set to NaN: a weight of 0 would not keep it from rows that do
+// not.
 #include "attention.h"
 #include "prefill_tiles.h"
 #include "softmax.cuh"
