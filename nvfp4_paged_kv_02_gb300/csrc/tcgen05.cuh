@@ -15,7 +15,8 @@ namespace nvfp4 {
 constexpr uint32_t kTmemColumns = 512;
 
 // Whether a phase is complete; if not, the thread may sleep for some microseconds before it says so. A wait is given up
-// after kNapLimit naps: half a second (a nap takes 4 us, measured), and 1.3 s at most (what a warp waits for takes the others some ten microseconds).
+// after kNapLimit naps: half a second (a nap takes 4 us, measured), and 1.3 s at most (what a warp waits for takes the
+// others some ten microseconds).
 constexpr uint32_t kNap = 10000;  // ns
 constexpr uint32_t kNapLimit = 1u << 17;
 __device__ __forceinline__ bool mbar_wait_nap(uint64_t* bar, uint32_t parity) {
